@@ -427,6 +427,103 @@ va_status verify_attn_merge_partials(int32_t n, const va_tensor* o_parts, const 
                                      va_tensor* out, void* stream);
 
 /*
+ * va_rope - rotary position embedding of the append entry points.
+ *  cos_sin      [P, rot] fp32, row p: cos of the rot / 2 angles of position p,
+ *               then their sin; rot a multiple of 8, 8 <= rot <= 256 (64 on
+ *               the latent path). Rows 16-byte aligned. Only a head's first
+ *               rot columns turn.
+ *  positions    [total_q] int32, contiguous, or NULL: each token's position
+ *               is the one it is stored at, S - L + t. A position outside
+ *               [0, P) is read as the nearest inside.
+ *  interleaved  0: column i turns with column i + rot / 2; 1: column 2 i turns
+ *               with column 2 i + 1.
+ * A pair (x1, x2) becomes (x1 cos - x2 sin, x2 cos + x1 sin) in fp32, each
+ * product and the sum rounded by itself.
+ */
+typedef struct va_rope {
+  const va_tensor* cos_sin;
+  const va_tensor* positions;
+  int32_t interleaved;
+} va_rope;
+
+/*
+ * verify_attn_append_kv - rotates a batch's new queries and keys and stores
+ * its new keys and values in the paged cache: what runs before verify_attn.
+ * With L = cu_seqlens_q[b+1] - cu_seqlens_q[b] new tokens of sequence b and
+ * S = seqused_k[b] cached tokens (the new ones counted, as verify_attn's),
+ * new token t is stored at position S - L + t, i.e. in slot (S - L + t) % 16
+ * of page block_table[b, (S - L + t) / 16]. The two calls take the same
+ * block_table, cu_seqlens_q and seqused_k.
+ *
+ *  q, q_out     [total_q, Hq, 256] bf16, or both NULL. q_out is written with
+ *               the rotated q; it may be q itself (same address and strides),
+ *               and may not overlap any input otherwise.
+ *  k, v         [total_q, Hkv, 256] bf16; v is not rotated. q, k and v may be
+ *               views of one projection's output (innermost stride 1, rows
+ *               16-byte aligned).
+ *  rope         NULL: k is stored as it is (then q and q_out are NULL).
+ *  k_cache, v_cache  [num_blocks, 16, Hkv, 256] FP8_E4M3 or BF16, as verify_attn
+ *               reads them; written in place.
+ *  k_descale, v_descale  [1] fp32 or NULL (= 1.0): the stored value is
+ *               value / descale, rounded once from fp32 to nearest even (e4m3:
+ *               saturating at 448; NaN stays NaN).
+ *  k_scales, v_scales  [num_blocks, Hkv] fp32, any positive strides, or both
+ *               NULL: the cache is page-scaled (FP8_E4M3 only, no descales), as
+ *               verify_attn_scaled reads it: value = code * scales[page, head].
+ *               Written in place. Per page and KV head that gets new tokens:
+ *               need = the smallest 2^e, -64 <= e <= 64, with max|new| <=
+ *               448 * 2^e (NaN ignored). If the page's slot 0 is among the new
+ *               tokens its scale becomes need; otherwise the page holds older
+ *               tokens, its scale (read as clamped to [2^-64, 2^64]) becomes the
+ *               larger of itself and need, and where it grows the older tokens'
+ *               codes are rounded to it (exact between powers of two, except
+ *               below e4m3's normal range). Slots behind the new tokens are
+ *               left as they are.
+ *
+ * Tokens at negative positions (L > S) are neither stored nor rotated. Rows of
+ * q_out behind the last sequence are left as they were. Block-table entries
+ * outside [0, num_blocks) and positions past the table's width store nothing.
+ * Two sequences of a call may not append to the same page.
+ *
+ * One launch, asynchronous on stream; no workspace, no allocation, capturable.
+ * Errors before launching: VA_ERR_NULL (also one of q / q_out, or of k_scales /
+ * v_scales, without the other, or q without rope), VA_ERR_SHAPE, VA_ERR_DTYPE (also page scales
+ * over a BF16 cache), VA_ERR_LAYOUT, VA_ERR_UNSUPPORTED (head_dim other than
+ * 256, pages other than 16, rot out of range, descales beside page scales,
+ * more heads than a grid holds: Hkv + Hq / 4 > 65535); VA_ERR_CUDA for a failed
+ * launch.
+ */
+va_status verify_attn_append_kv(const va_tensor* q, const va_tensor* k, const va_tensor* v,
+                                const va_tensor* block_table, const va_tensor* cu_seqlens_q,
+                                const va_tensor* seqused_k, const va_rope* rope,
+                                const va_tensor* k_descale, const va_tensor* v_descale,
+                                va_tensor* k_scales, va_tensor* v_scales, va_tensor* q_out,
+                                va_tensor* k_cache, va_tensor* v_cache, void* stream);
+
+/*
+ * verify_attn_append_mla - the same for a latent cache (verify_attn_mla): new
+ * token t's row is [latent | rotated k_pe].
+ *
+ *  q_pe, q_pe_out  [total_q, Hq, 64] bf16, or both NULL: the queries' rope
+ *               parts. q_pe_out is usually the columns [512, 576) of the q that
+ *               verify_attn_mla takes, and q_pe may be that same view.
+ *  latent       [total_q, 512] bf16;  k_pe  [total_q, 64] bf16 (views of one
+ *               projection's output are fine).
+ *  rope         cos_sin [P, 64]; NULL: k_pe is stored as it is.
+ *  kv_cache     [num_blocks, 16, 1, 576] FP8_E4M3 or BF16, written in place.
+ *  descale      [1] fp32 or NULL: stored value = value / descale.
+ *  scales       [num_blocks, 1] fp32 or NULL: one scale a page for the whole
+ *               row, by the rule of verify_attn_append_kv; read by
+ *               verify_attn_mla_scaled.
+ * Otherwise as verify_attn_append_kv.
+ */
+va_status verify_attn_append_mla(const va_tensor* q_pe, const va_tensor* latent, const va_tensor* k_pe,
+                                 const va_tensor* block_table, const va_tensor* cu_seqlens_q,
+                                 const va_tensor* seqused_k, const va_rope* rope,
+                                 const va_tensor* descale, va_tensor* scales, va_tensor* q_pe_out,
+                                 va_tensor* kv_cache, void* stream);
+
+/*
  * verify_attn_last_device_error - reads and clears the device status word of
  * a workspace. This turns the pages' gates and asserts (sglang PR 36330 digest,
  * "Key code excerpts") into something a caller can check after launch: a

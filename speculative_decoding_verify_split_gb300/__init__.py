@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
+import threading
 from typing import Optional
 
 import torch
@@ -31,7 +33,8 @@ EXPORTS = ("verify_attn", "verify_attn_ex", "verify_attn_check", "verify_attn_pl
            "verify_attn_workspace_size", "verify_attn_status_string", "verify_attn_noalloc",
            "verify_attn_block_table_from_indptr", "verify_attn_opt", "verify_attn_mla",
            "verify_attn_mla_workspace_size", "verify_attn_partial", "verify_attn_merge_partials",
-           "verify_attn_last_device_error", "verify_attn_set_wait_limit")
+           "verify_attn_last_device_error", "verify_attn_set_wait_limit",
+           "verify_attn_append_kv", "verify_attn_append_mla")
 
 # Absorbed-MLA latent cache: row = [latent (MLA_NOPE) | rope key (MLA_PE)].
 MLA_NOPE, MLA_PE = 512, 64
@@ -117,6 +120,11 @@ def _lib():
         lib.verify_attn_last_device_error.restype = ctypes.c_int32
         lib.verify_attn_set_wait_limit.argtypes = [ctypes.c_uint64]
         lib.verify_attn_set_wait_limit.restype = ctypes.c_int32
+        V = ctypes.c_void_p   # descriptors packed by _pack, passed by address
+        lib.verify_attn_append_kv.argtypes = [V] * 15
+        lib.verify_attn_append_kv.restype = ctypes.c_int32
+        lib.verify_attn_append_mla.argtypes = [V] * 12
+        lib.verify_attn_append_mla.restype = ctypes.c_int32
         lib.verify_attn_status_string.argtypes = [ctypes.c_int32]
         lib.verify_attn_status_string.restype = ctypes.c_char_p
         _LIB = lib
@@ -148,6 +156,79 @@ def desc(t: Optional[torch.Tensor]):
 
 def _ref(d):
     return None if d is None else ctypes.byref(d)
+
+
+_DESC = struct.Struct("@Pii8q")     # one va_tensor
+_ROPE = struct.Struct("@PPi4x")     # one va_rope
+_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
+_MAX_DESCS = 16
+
+
+class _Packed(threading.local):
+    """This thread's descriptors of the call being made: ``_MAX_DESCS``
+    va_tensor and a va_rope behind them. Packing into one buffer costs a
+    fraction of a ctypes structure per tensor, which is what a small call's
+    time goes into."""
+
+    def __init__(self):
+        self.buf = ctypes.create_string_buffer(_DESC.size * _MAX_DESCS + _ROPE.size)
+        self.base = ctypes.addressof(self.buf)
+
+
+_packed = _Packed()
+assert _DESC.size == ctypes.sizeof(VaTensor)
+
+
+def _pack(*tensors):
+    """Addresses of the descriptors of ``tensors`` (None -> NULL), valid until
+    this thread's next call of it."""
+    buf, base, off, out = _packed.buf, _packed.base, 0, []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        code = _DTYPES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        shape = t.shape
+        n = len(shape)
+        if n > 4:
+            raise ValueError("at most 4 dimensions")
+        pad = _PAD[n]
+        _DESC.pack_into(buf, off, t.data_ptr(), code, n, *shape, *pad, *t.stride(), *pad)
+        out.append(base + off)
+        off += _DESC.size
+    return out
+
+
+def _pack_rope(cos_sin, positions, interleaved):
+    """Address of a va_rope over descriptors packed by _pack (None: no rotation)."""
+    if cos_sin is None:
+        if positions is not None:
+            raise ValueError("positions without cos_sin")
+        return None
+    off = _DESC.size * _MAX_DESCS
+    _ROPE.pack_into(_packed.buf, off, cos_sin, positions or 0, int(interleaved))
+    return _packed.base + off
+
+
+def _call(fn, where, device, stream, *args):
+    """fn(*args, stream) with ``device`` current; raises on an error status."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on a CUDA device, not {device}")
+    if torch.cuda.current_device() == device.index:
+        s = fn(*args, _stream_handle(stream, device))
+    else:
+        with torch.cuda.device(device):
+            s = fn(*args, _stream_handle(stream, device))
+    if s != VA_OK:
+        raise VerifyAttnError(s, where)
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on different devices: {device} and {t.device}")
 
 
 def _stream_handle(stream, device) -> int:
@@ -494,3 +575,44 @@ def merge_partials(parts, out=None, stream=None):
     if s != VA_OK:
         raise VerifyAttnError(s, "verify_attn_merge_partials")
     return out
+
+
+def append_kv(k, v, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, q=None, q_out=None,
+              cos_sin=None, positions=None, interleaved: bool = False, k_descale=None,
+              v_descale=None, k_scales=None, v_scales=None, stream=None):
+    """Rotates a batch's new queries and keys and stores its new keys and
+    values in the paged cache (see include/verify_attn.h): what runs before
+    ``verify_attn`` on the same block_table, cu_seqlens_q and seqused_k, or,
+    with k_scales / v_scales [num_blocks, Hkv] fp32, before
+    ``verify_attn_scaled``. Caches and scales are written in place. Returns
+    ``q_out`` (created if q is given without it; it may be q itself), or None."""
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _same_device(k.device, v, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, q, q_out,
+                 cos_sin, positions, k_descale, v_descale, k_scales, v_scales)
+    r = _pack(q, k, v, block_table, cu_seqlens_q, seqused_k, k_descale, v_descale, k_scales,
+              v_scales, q_out, k_cache, v_cache, cos_sin, positions)
+    rope = _pack_rope(r[13], r[14], interleaved)
+    _call(_lib().verify_attn_append_kv, "verify_attn_append_kv", k.device, stream, *r[:6], rope,
+          *r[6:13])
+    return q_out
+
+
+def append_mla(latent, k_pe, kv_cache, block_table, cu_seqlens_q, seqused_k, q_pe=None,
+               q_pe_out=None, cos_sin=None, positions=None, interleaved: bool = False,
+               descale=None, scales=None, stream=None):
+    """``append_kv`` for a latent cache (see include/verify_attn.h): stores
+    rows [latent | rotated k_pe] and rotates the queries' rope parts, before
+    ``verify_attn_mla`` (or, with scales [num_blocks, 1] fp32,
+    ``verify_attn_mla_scaled``). q_pe_out is usually ``q[..., 512:]``. Returns
+    ``q_pe_out``, or None."""
+    if q_pe is not None and q_pe_out is None:
+        q_pe_out = torch.empty(q_pe.shape, dtype=q_pe.dtype, device=q_pe.device)
+    _same_device(latent.device, k_pe, kv_cache, block_table, cu_seqlens_q, seqused_k, q_pe,
+                 q_pe_out, cos_sin, positions, descale, scales)
+    r = _pack(q_pe, latent, k_pe, block_table, cu_seqlens_q, seqused_k, descale, scales, q_pe_out,
+              kv_cache, cos_sin, positions)
+    rope = _pack_rope(r[10], r[11], interleaved)
+    _call(_lib().verify_attn_append_mla, "verify_attn_append_mla", latent.device, stream, *r[:6],
+          rope, *r[6:10])
+    return q_pe_out

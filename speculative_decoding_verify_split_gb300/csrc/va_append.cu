@@ -1,0 +1,487 @@
+// New tokens into the paged KV cache: rotary position embedding of q and k,
+// conversion to the cache's type, and the store into the pages that hold the
+// tokens' positions, in one launch.
+//
+//   pairs (x1, x2) of a head's first `rot` columns at position p:
+//     y1 = x1 cos(p, i) - x2 sin(p, i),  y2 = x2 cos(p, i) + x1 sin(p, i)
+//   stored = y (bf16), or round_e4m3(y / scale), saturating at 448.
+//
+// Token t of a sequence with L new and S cached tokens (the new ones among
+// them) is at position S - L + t. A unit of work is one page of one sequence:
+// the (at most 16) new tokens whose positions the page holds. A page belongs
+// to one CTA per KV head, so a page's scale (largest |value| over the page's
+// tokens) needs no atomics and the results do not depend on the launch order.
+// The units of sequence b are numbered from cu[b] / 16 + 2 b: L tokens touch
+// at most L / 16 + 2 pages, so the grid needs no device value, and a CTA finds
+// its sequence with one pass over cu_seqlens_q (each thread tests its own
+// sequences), a single round trip to memory that also brings the lengths.
+//
+// The products and their difference are rounded separately (no fused
+// multiply-add), so the stored bytes are those of the same formula in any
+// fp32 arithmetic.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "va_append.h"
+#include "va_fp8.cuh"
+
+namespace va {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kHeadsPerCta = 4;      // query heads of a page's tokens per CTA
+constexpr int kPeHeadsPerCta = 16;   // latent path: 64-wide query parts
+
+// How a cache holds its values.
+enum Kind { kBf16 = 0, kE4m3 = 1, kPageScaled = 2 };
+
+// One page of one sequence: tokens at positions [lo, hi) of page pg.
+struct Unit {
+  int b, tok0;     // sequence; row of the token at position lo
+  int64_t pg;      // page index in the sequence
+  int64_t lo, hi;
+};
+
+struct UnitShared {
+  int b, a, L, S;
+};
+
+// The unit of this CTA, or false if there is none. Contains barriers.
+__device__ __forceinline__ bool find_unit(const AppendParams& p, UnitShared* sh, Unit* out) {
+  if (threadIdx.x == 0) sh->b = -1;
+  __syncthreads();
+  // the previous kernel in the stream may write anything read below
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t u = blockIdx.x;
+  for (int b = threadIdx.x; b < p.num_seqs; b += kThreads) {
+    const int a = p.cu_q[b], e = p.cu_q[b + 1], s = p.seqused_k[b];
+    const int64_t g0 = (int64_t)(a / kPageSize) + 2 * (int64_t)b;
+    const int64_t g1 = (int64_t)(e / kPageSize) + 2 * ((int64_t)b + 1);
+    if (a >= 0 && g0 <= u && u < g1) {
+      const int end = e < p.total_q ? e : p.total_q;
+      sh->b = b;
+      sh->a = a;
+      sh->L = end - a;
+      sh->S = s;
+    }
+  }
+  __syncthreads();
+  const int b = sh->b;
+  if (b < 0) return false;
+  const int a = sh->a, L = sh->L;
+  const int64_t S = sh->S;
+  if (L <= 0) return false;
+  const int64_t pos0 = S - L;
+  const int64_t first = pos0 > 0 ? pos0 : 0;  // tokens before position 0 have no place
+  const int64_t i = u - ((int64_t)(a / kPageSize) + 2 * (int64_t)b);
+  out->b = b;
+  out->pg = first / kPageSize + i;
+  const int64_t pa = out->pg * kPageSize, pe = pa + kPageSize;
+  out->lo = pa > first ? pa : first;
+  out->hi = pe < S ? pe : S;
+  out->tok0 = a + (int)(out->lo - pos0);
+  return out->lo < out->hi;
+}
+
+// Row of the cos | sin table of token row tok at position x.
+__device__ __forceinline__ const float* table_row(const AppendParams& p, int tok, int64_t x) {
+  if (p.positions) x = p.positions[tok];
+  x = x < 0 ? 0 : (x >= p.max_pos ? p.max_pos - 1 : x);
+  return p.cos_sin + x * p.cs_s0;
+}
+
+__device__ __forceinline__ void unpack4(uint2 w, float* x) {
+  x[0] = __uint_as_float(w.x << 16);
+  x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+  x[2] = __uint_as_float(w.y << 16);
+  x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+
+// (x1, x2) -> (x1 c - x2 s, x2 c + x1 s), every operation rounded by itself.
+__device__ __forceinline__ void rotate(float& x1, float& x2, float c, float s) {
+  const float y1 = __fsub_rn(__fmul_rn(x1, c), __fmul_rn(x2, s));
+  const float y2 = __fadd_rn(__fmul_rn(x2, c), __fmul_rn(x1, s));
+  x1 = y1;
+  x2 = y2;
+}
+
+// Where a lane's eight columns of a 256-wide head lie: two groups of four at
+// o1 and o2. Halves: rotated lanes hold pairs (4 l + i, rot / 2 + 4 l + i),
+// the others the columns past `rot` in order. Interleaved: eight columns in a
+// row, pairs (2 i, 2 i + 1).
+struct Lane {
+  int o1, o2;
+  bool turn;  // these columns are rotated
+};
+
+template <bool INTER>
+__device__ __forceinline__ Lane lane_columns(int lane, int rot) {
+  Lane c;
+  if (INTER) {
+    c.o1 = 8 * lane;
+    c.o2 = c.o1 + 4;
+    c.turn = c.o1 < rot;
+  } else {
+    const int half = rot / 2;
+    c.turn = 4 * lane < half;
+    c.o1 = c.turn ? 4 * lane : rot + 2 * (4 * lane - half);
+    c.o2 = c.turn ? half + 4 * lane : c.o1 + 4;
+  }
+  return c;
+}
+
+template <bool INTER>
+__device__ __forceinline__ void rotate8(float* x, float4 c, float4 s) {
+  if (INTER) {
+    rotate(x[0], x[1], c.x, s.x);
+    rotate(x[2], x[3], c.y, s.y);
+    rotate(x[4], x[5], c.z, s.z);
+    rotate(x[6], x[7], c.w, s.w);
+  } else {
+    rotate(x[0], x[4], c.x, s.x);
+    rotate(x[1], x[5], c.y, s.y);
+    rotate(x[2], x[6], c.z, s.z);
+    rotate(x[3], x[7], c.w, s.w);
+  }
+}
+
+__device__ __forceinline__ uint2 to_bf16x4(const float* x) {
+  return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+}
+
+__device__ __forceinline__ uint32_t to_e4m3x4(const float* x, float scale) {
+  const uint32_t lo = pack_fp8x2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale));
+  const uint32_t hi = pack_fp8x2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale));
+  return lo | (hi << 16);
+}
+
+// Four codes under scale `had` as codes under scale `now`.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float had, float now) {
+  const float2 a = unpack_fp8x2(w & 0xFFFFu), b = unpack_fp8x2(w >> 16);
+  const float x[4] = {__fmul_rn(a.x, had), __fmul_rn(a.y, had), __fmul_rn(b.x, had), __fmul_rn(b.y, had)};
+  return to_e4m3x4(x, now);
+}
+
+// A page scale as it is read: finite and positive.
+__device__ __forceinline__ float usable_scale(float s) {
+  return fminf(fmaxf(s, kMinPageScale), kMaxPageScale);  // NaN -> the smallest
+}
+
+// The smallest 2^e, -64 <= e <= 64, with amax <= 448 * 2^e (448 = 1.75 * 2^8).
+__device__ __forceinline__ float scale_for(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  e = e < -64 ? -64 : (e > 64 ? 64 : e);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// ---- keys, values and queries of a GQA cache -----------------------------------
+//
+// blockIdx.y < hkv: the page's K rows (warps 0-3) and V rows (warps 4-7) of
+// one KV head, four slots of the page per warp. Above: the same tokens' rows
+// of kHeadsPerCta query heads, spread over the eight warps.
+template <int KIND, bool INTER>
+__global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams p) {
+  __shared__ UnitShared sh;
+  __shared__ float s_amax[kWarps];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Unit u;
+  if (!find_unit(p, &sh, &u)) return;  // CTA-uniform
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Lane col = lane_columns<INTER>(lane, p.rot);
+
+  if ((int)blockIdx.y >= p.hkv) {  // ---- query heads
+    const int h0 = ((int)blockIdx.y - p.hkv) * kHeadsPerCta;
+    const int nh = p.hq - h0 < kHeadsPerCta ? p.hq - h0 : kHeadsPerCta;
+    const int rows = (int)(u.hi - u.lo) * nh;
+    for (int r = warp; r < rows; r += kWarps) {
+      const int t = r / nh, h = h0 + r - t * nh;
+      const int tok = u.tok0 + t;
+      const uint16_t* src = p.q + (int64_t)tok * p.q_s0 + (int64_t)h * p.q_s1;
+      const uint2 w1 = *reinterpret_cast<const uint2*>(src + col.o1);
+      const uint2 w2 = *reinterpret_cast<const uint2*>(src + col.o2);
+      float x[8];
+      unpack4(w1, x);
+      unpack4(w2, x + 4);
+      if (col.turn) {
+        const float* cs = table_row(p, tok, u.lo + t) + 4 * lane;
+        rotate8<INTER>(x, *reinterpret_cast<const float4*>(cs), *reinterpret_cast<const float4*>(cs + p.rot / 2));
+      }
+      uint16_t* dst = p.q_out + (int64_t)tok * p.qo_s0 + (int64_t)h * p.qo_s1;
+      *reinterpret_cast<uint2*>(dst + col.o1) = to_bf16x4(x);
+      *reinterpret_cast<uint2*>(dst + col.o2) = to_bf16x4(x + 4);
+    }
+    return;
+  }
+
+  // ---- one KV head of the page
+  const int h = (int)blockIdx.y;
+  if (u.pg >= p.bt_width) return;
+  const int page = p.block_table[(int64_t)u.b * p.bt_s0 + u.pg * p.bt_s1];
+  if ((unsigned)page >= (unsigned)p.num_blocks) return;
+  const bool is_k = warp < kWarps / 2;
+  const int w4 = warp & 3;
+  const int s_lo = (int)(u.lo - u.pg * kPageSize), s_hi = (int)(u.hi - u.pg * kPageSize);
+  const uint16_t* src = (is_k ? p.k + (int64_t)h * p.k_s1 : p.v + (int64_t)h * p.v_s1);
+  const int64_t src_s0 = is_k ? p.k_s0 : p.v_s0;
+  const CacheView& c = is_k ? p.kc : p.vc;
+  const float* descale = is_k ? p.k_descale : p.v_descale;
+  const int64_t base = (int64_t)page * c.s0 + (int64_t)h * c.s2;
+
+  float x[4][8];
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int s = w4 + 4 * k;
+    if (s < s_lo || s >= s_hi) continue;  // warp-uniform
+    const int tok = u.tok0 + s - s_lo;
+    const uint16_t* row = src + (int64_t)tok * src_s0;
+    unpack4(*reinterpret_cast<const uint2*>(row + col.o1), x[k]);
+    unpack4(*reinterpret_cast<const uint2*>(row + col.o2), x[k] + 4);
+    if (is_k && col.turn) {
+      const float* cs = table_row(p, tok, u.pg * kPageSize + s) + 4 * lane;
+      rotate8<INTER>(x[k], *reinterpret_cast<const float4*>(cs), *reinterpret_cast<const float4*>(cs + p.rot / 2));
+    }
+    if (KIND == kPageScaled) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[k][i]));  // NaN counts as 0
+    }
+  }
+  float scale = 1.f;
+  bool divide = false;
+  if (KIND == kPageScaled) {
+    amax = warp_max(amax);
+    if (lane == 0) s_amax[warp] = amax;
+    __syncthreads();
+    const int w0 = is_k ? 0 : 4;
+    amax = fmaxf(fmaxf(s_amax[w0], s_amax[w0 + 1]), fmaxf(s_amax[w0 + 2], s_amax[w0 + 3]));
+    float* sp = c.scales + (int64_t)page * c.sc_s0 + (int64_t)h * c.sc_s1;
+    scale = scale_for(amax);
+    if (s_lo > 0) {  // the page's older tokens keep their scale, or are rounded to the larger one
+      const float had = usable_scale(*sp);
+      __syncthreads();  // every thread has read the old scale
+      scale = fmaxf(scale, had);
+      if (scale > had) {
+        unsigned char* dst = static_cast<unsigned char*>(c.data) + base;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int s = w4 + 4 * k;
+          if (s >= s_lo) continue;
+          uint32_t* d1 = reinterpret_cast<uint32_t*>(dst + (int64_t)s * c.s1 + col.o1);
+          uint32_t* d2 = reinterpret_cast<uint32_t*>(dst + (int64_t)s * c.s1 + col.o2);
+          const uint32_t a = *d1, b = *d2;
+          *d1 = rescale4(a, had, scale);
+          *d2 = rescale4(b, had, scale);
+        }
+      }
+    }
+    if (w4 == 0 && lane == 0) *sp = scale;
+  } else {
+    divide = descale != nullptr;
+    if (divide) scale = *descale;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int s = w4 + 4 * k;
+    if (s < s_lo || s >= s_hi) continue;
+    if (KIND == kBf16) {
+      if (divide) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[k][i] = __fdiv_rn(x[k][i], scale);
+      }
+      uint16_t* dst = static_cast<uint16_t*>(c.data) + base + (int64_t)s * c.s1;
+      *reinterpret_cast<uint2*>(dst + col.o1) = to_bf16x4(x[k]);
+      *reinterpret_cast<uint2*>(dst + col.o2) = to_bf16x4(x[k] + 4);
+    } else {
+      unsigned char* dst = static_cast<unsigned char*>(c.data) + base + (int64_t)s * c.s1;
+      *reinterpret_cast<uint32_t*>(dst + col.o1) = to_e4m3x4(x[k], scale);
+      *reinterpret_cast<uint32_t*>(dst + col.o2) = to_e4m3x4(x[k] + 4, scale);
+    }
+  }
+}
+
+// ---- rows of a latent cache ------------------------------------------------------
+//
+// blockIdx.y == 0: the page's rows [latent 512 | rope 64], two slots per
+// warp; a lane holds latent columns 8 l.. and 256 + 8 l.. and one rope pair.
+// Above: the tokens' 64-wide rope parts of kPeHeadsPerCta query heads, eight
+// lanes a row.
+template <int KIND, bool INTER>
+__global__ void __launch_bounds__(kThreads) va_append_mla_kernel(const AppendParams p) {
+  __shared__ UnitShared sh;
+  __shared__ float s_amax[kWarps];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Unit u;
+  if (!find_unit(p, &sh, &u)) return;  // CTA-uniform
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (blockIdx.y > 0) {  // ---- query heads
+    const int h0 = ((int)blockIdx.y - 1) * kPeHeadsPerCta;
+    const int nh = p.hq - h0 < kPeHeadsPerCta ? p.hq - h0 : kPeHeadsPerCta;
+    const int rows = (int)(u.hi - u.lo) * nh;
+    const int l8 = lane & 7;
+    const int o1 = INTER ? 8 * l8 : 4 * l8, o2 = INTER ? o1 + 4 : 32 + o1;
+    for (int r = warp * 4 + (lane >> 3); r < rows; r += kWarps * 4) {
+      const int t = r / nh, h = h0 + r - t * nh;
+      const int tok = u.tok0 + t;
+      const uint16_t* src = p.q + (int64_t)tok * p.q_s0 + (int64_t)h * p.q_s1;
+      float x[8];
+      unpack4(*reinterpret_cast<const uint2*>(src + o1), x);
+      unpack4(*reinterpret_cast<const uint2*>(src + o2), x + 4);
+      const float* cs = table_row(p, tok, u.lo + t) + 4 * l8;
+      rotate8<INTER>(x, *reinterpret_cast<const float4*>(cs), *reinterpret_cast<const float4*>(cs + kMlaPe / 2));
+      uint16_t* dst = p.q_out + (int64_t)tok * p.qo_s0 + (int64_t)h * p.qo_s1;
+      *reinterpret_cast<uint2*>(dst + o1) = to_bf16x4(x);
+      *reinterpret_cast<uint2*>(dst + o2) = to_bf16x4(x + 4);
+    }
+    return;
+  }
+
+  if (u.pg >= p.bt_width) return;
+  const int page = p.block_table[(int64_t)u.b * p.bt_s0 + u.pg * p.bt_s1];
+  if ((unsigned)page >= (unsigned)p.num_blocks) return;
+  const int s_lo = (int)(u.lo - u.pg * kPageSize), s_hi = (int)(u.hi - u.pg * kPageSize);
+  const CacheView& c = p.kc;
+  const int64_t base = (int64_t)page * c.s0;
+  // the lane's columns: eight latent ones at n1 and at n2, a rope pair at r1, r2
+  const int n1 = 8 * lane, n2 = 256 + 8 * lane;
+  const int r1 = INTER ? 2 * lane : lane, r2 = INTER ? r1 + 1 : lane + 32;
+
+  float x[2][16], y[2][2];
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int s = warp + kWarps * k;
+    if (s < s_lo || s >= s_hi) continue;  // warp-uniform
+    const int tok = u.tok0 + s - s_lo;
+    const uint16_t* lat = p.k + (int64_t)tok * p.k_s0;
+    const uint16_t* pe = p.v + (int64_t)tok * p.v_s0;
+    const uint4 a = *reinterpret_cast<const uint4*>(lat + n1), b = *reinterpret_cast<const uint4*>(lat + n2);
+    unpack4(make_uint2(a.x, a.y), x[k]);
+    unpack4(make_uint2(a.z, a.w), x[k] + 4);
+    unpack4(make_uint2(b.x, b.y), x[k] + 8);
+    unpack4(make_uint2(b.z, b.w), x[k] + 12);
+    y[k][0] = bf16_bits_to_float(pe[r1]);
+    y[k][1] = bf16_bits_to_float(pe[r2]);
+    if (p.cos_sin) {
+      const float* cs = table_row(p, tok, u.pg * kPageSize + s) + lane;
+      rotate(y[k][0], y[k][1], cs[0], cs[kMlaPe / 2]);
+    }
+    if (KIND == kPageScaled) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[k][i]));  // NaN counts as 0
+      amax = fmaxf(amax, fmaxf(fabsf(y[k][0]), fabsf(y[k][1])));
+    }
+  }
+  float scale = 1.f;
+  bool divide = false;
+  if (KIND == kPageScaled) {
+    amax = warp_max(amax);
+    if (lane == 0) s_amax[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_amax[w]);
+    float* sp = c.scales + (int64_t)page * c.sc_s0;
+    scale = scale_for(amax);
+    if (s_lo > 0) {
+      const float had = usable_scale(*sp);
+      __syncthreads();  // every thread has read the old scale
+      scale = fmaxf(scale, had);
+      if (scale > had) {
+        unsigned char* dst = static_cast<unsigned char*>(c.data) + base;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int s = warp + kWarps * k;
+          if (s >= s_lo) continue;
+          unsigned char* row = dst + (int64_t)s * c.s1;
+          uint2 a = *reinterpret_cast<uint2*>(row + n1), b = *reinterpret_cast<uint2*>(row + n2);
+          const uint32_t e = (uint32_t)row[kMlaNope + r1] | ((uint32_t)row[kMlaNope + r2] << 8);
+          a = make_uint2(rescale4(a.x, had, scale), rescale4(a.y, had, scale));
+          b = make_uint2(rescale4(b.x, had, scale), rescale4(b.y, had, scale));
+          *reinterpret_cast<uint2*>(row + n1) = a;
+          *reinterpret_cast<uint2*>(row + n2) = b;
+          const uint32_t f = rescale4(e, had, scale);
+          row[kMlaNope + r1] = (unsigned char)f;
+          row[kMlaNope + r2] = (unsigned char)(f >> 8);
+        }
+      }
+    }
+    if (warp == 0 && lane == 0) *sp = scale;
+  } else {
+    divide = p.k_descale != nullptr;
+    if (divide) scale = *p.k_descale;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int s = warp + kWarps * k;
+    if (s < s_lo || s >= s_hi) continue;
+    if (KIND == kBf16) {
+      if (divide) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[k][i] = __fdiv_rn(x[k][i], scale);
+        y[k][0] = __fdiv_rn(y[k][0], scale);
+        y[k][1] = __fdiv_rn(y[k][1], scale);
+      }
+      uint16_t* dst = static_cast<uint16_t*>(c.data) + base + (int64_t)s * c.s1;
+      const uint2 a = to_bf16x4(x[k]), b = to_bf16x4(x[k] + 4), d = to_bf16x4(x[k] + 8), e = to_bf16x4(x[k] + 12);
+      *reinterpret_cast<uint4*>(dst + n1) = make_uint4(a.x, a.y, b.x, b.y);
+      *reinterpret_cast<uint4*>(dst + n2) = make_uint4(d.x, d.y, e.x, e.y);
+      dst[kMlaNope + r1] = float_to_bf16_bits(y[k][0]);
+      dst[kMlaNope + r2] = float_to_bf16_bits(y[k][1]);
+    } else {
+      unsigned char* dst = static_cast<unsigned char*>(c.data) + base + (int64_t)s * c.s1;
+      *reinterpret_cast<uint2*>(dst + n1) = make_uint2(to_e4m3x4(x[k], scale), to_e4m3x4(x[k] + 4, scale));
+      *reinterpret_cast<uint2*>(dst + n2) = make_uint2(to_e4m3x4(x[k] + 8, scale), to_e4m3x4(x[k] + 12, scale));
+      const uint32_t f = pack_fp8x2(__fdiv_rn(y[k][0], scale), __fdiv_rn(y[k][1], scale));
+      dst[kMlaNope + r1] = (unsigned char)f;
+      dst[kMlaNope + r2] = (unsigned char)(f >> 8);
+    }
+  }
+}
+
+using KernelFn = void (*)(const AppendParams);
+
+template <int KIND>
+KernelFn pick(bool mla, bool inter) {
+  if (mla) return inter ? va_append_mla_kernel<KIND, true> : va_append_mla_kernel<KIND, false>;
+  return inter ? va_append_kernel<KIND, true> : va_append_kernel<KIND, false>;
+}
+
+}  // namespace
+
+int append_roles(bool mla, int64_t hkv, int64_t hq, int64_t* roles) {
+  const int64_t per = mla ? kPeHeadsPerCta : kHeadsPerCta;
+  *roles = (mla ? 1 : hkv) + (hq + per - 1) / per;
+  return *roles <= 65535;
+}
+
+cudaError_t launch_append(const AppendParams& p, bool mla, cudaStream_t stream) {
+  int64_t roles = 0;
+  const int64_t units = p.total_q / kPageSize + 2 * (int64_t)p.num_seqs;
+  if (!append_roles(mla, p.hkv, p.hq, &roles)) return cudaErrorInvalidValue;
+  const KernelFn fn = p.kc.scales ? pick<kPageScaled>(mla, p.interleaved)
+                      : p.kc.fp8  ? pick<kE4m3>(mla, p.interleaved)
+                                  : pick<kBf16>(mla, p.interleaved);
+  // a programmatic dependent of the stream's previous kernel, as the
+  // attention kernels are: it touches memory only after that kernel
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)units, (unsigned)roles);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+}  // namespace va

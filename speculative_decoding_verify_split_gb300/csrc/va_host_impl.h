@@ -15,7 +15,18 @@ struct Shapes {
   int32_t kv_dtype;
 };
 
-// Argument checks shared by every entry point (pure host code).
+// Elementary checks of a descriptor (pure host code): its element count, a
+// 16-byte-aligned address, its rank with non-negative extents and strides,
+// rows that can be read in 16-byte pieces, an optional fp32 scalar, and the
+// fp32 scales [num_blocks, hkv] of a page-scaled cache.
+int64_t numel(const va_tensor* t);
+bool aligned16(const void* p);
+bool dims_ok(const va_tensor* t, int ndim);
+bool rows_16b(const va_tensor* t);
+va_status check_descale(const va_tensor* t);
+va_status check_page_scales(const va_tensor* t, int64_t num_blocks, int64_t hkv);
+
+// Argument checks shared by every attention entry point (pure host code).
 va_status validate(const va_tensor* q, const va_tensor* k, const va_tensor* v,
                    const va_tensor* bt, const va_tensor* cu, const va_tensor* su,
                    int32_t max_seqlen_q, int32_t max_seqlen_k, const va_tensor* kd,

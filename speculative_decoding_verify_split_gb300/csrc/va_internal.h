@@ -27,6 +27,9 @@ __host__ __device__ constexpr int64_t mla_acc_index(int64_t piece, int row, int 
   return ((piece * (ldr / 4) + row / 4) * kMlaNope + col) * 4 + (row % 4);
 }
 constexpr int kPageSize = 16;
+// A page scale is read as if clamped to this range (NaN as the smallest).
+constexpr float kMinPageScale = 5.421010862427522e-20f;   // 2^-64
+constexpr float kMaxPageScale = 18446744073709551616.f;   // 2^64
 constexpr int kMaxRows = 64;  // G * max_seqlen_q packed rows per (sequence, KV head)
 
 // Everything a kernel needs, by value. Strides are in elements.
