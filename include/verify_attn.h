@@ -524,6 +524,54 @@ va_status verify_attn_append_mla(const va_tensor* q_pe, const va_tensor* latent,
                                  va_tensor* kv_cache, void* stream);
 
 /*
+ * verify_attn_scaled - verify attention over a page-scaled e4m3 cache: a key's
+ * stored codes stand for code * k_scales[page, head], a value's for
+ * code * v_scales[page, head] (verify_attn_append_kv writes such a cache).
+ * Otherwise the operation of verify_attn_opt:
+ *
+ *   s_j = softmax_scale * k_scales[p_j, h] * q . K_j   (then soft cap, mask, window)
+ *   out = sum_j softmax(s)_j * v_scales[p_j, h] * V_j,  p_j = key j's page
+ *
+ *  k_cache, v_cache  [num_blocks, 16, Hkv, 256] FP8_E4M3.
+ *  k_scales, v_scales  [num_blocks, Hkv] fp32, any positive strides; interleaved
+ *               ([num_blocks, Hkv, 2]) a page's two lie in one sector. Read as
+ *               clamped to [2^-64, 2^64] (NaN as 2^-64), so a scale of 0 makes
+ *               values of at most 448 * 2^-64. Only the scales of pages that
+ *               are read for their keys are read.
+ *  opts         NULL: no window, soft cap or sinks.
+ *  workspace    as verify_attn_ex (same size: verify_attn_workspace_size with
+ *               VA_FP8_E4M3), or NULL to use the library's own per-device workspace,
+ *               whose calls must be ordered on one stream; during stream
+ *               capture NULL is refused (VA_ERR_WORKSPACE).
+ * Accuracy: weights keep fp32 precision while the V scales of the pages a row
+ * sees lie within a factor of 2^96 of each other.
+ * Errors as verify_attn_opt; VA_ERR_NULL without scales, VA_ERR_DTYPE for a
+ * BF16 cache or scales that are not fp32, VA_ERR_SHAPE for scales of another
+ * shape, VA_ERR_LAYOUT for a zero stride or an address off 4 bytes.
+ */
+va_status verify_attn_scaled(const va_tensor* q, const va_tensor* k_cache, const va_tensor* v_cache,
+                             const va_tensor* k_scales, const va_tensor* v_scales,
+                             const va_tensor* block_table, const va_tensor* cu_seqlens_q,
+                             const va_tensor* seqused_k, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                             float softmax_scale, va_tensor* out, const va_options* opts,
+                             void* workspace, size_t workspace_bytes, int32_t num_splits,
+                             void* event_after_main, void* stream);
+
+/*
+ * verify_attn_mla_scaled - verify_attn_mla over a page-scaled e4m3 latent
+ * cache: scales [num_blocks, 1] fp32, one scale a page for its whole rows, as
+ * key and as value (verify_attn_append_mla writes such a cache). Workspace as
+ * verify_attn_mla (NULL is refused during stream capture); scales as
+ * verify_attn_scaled.
+ */
+va_status verify_attn_mla_scaled(const va_tensor* q, const va_tensor* kv_cache, const va_tensor* scales,
+                                 const va_tensor* block_table, const va_tensor* cu_seqlens_q,
+                                 const va_tensor* seqused_k, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                 float softmax_scale, va_tensor* out, void* workspace,
+                                 size_t workspace_bytes, int32_t num_splits, void* event_after_main,
+                                 void* stream);
+
+/*
  * verify_attn_last_device_error - reads and clears the device status word of
  * a workspace. This turns the pages' gates and asserts (sglang PR 36330 digest,
  * "Key code excerpts") into something a caller can check after launch: a

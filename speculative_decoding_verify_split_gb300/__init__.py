@@ -34,7 +34,8 @@ EXPORTS = ("verify_attn", "verify_attn_ex", "verify_attn_check", "verify_attn_pl
            "verify_attn_block_table_from_indptr", "verify_attn_opt", "verify_attn_mla",
            "verify_attn_mla_workspace_size", "verify_attn_partial", "verify_attn_merge_partials",
            "verify_attn_last_device_error", "verify_attn_set_wait_limit",
-           "verify_attn_append_kv", "verify_attn_append_mla")
+           "verify_attn_append_kv", "verify_attn_append_mla", "verify_attn_scaled",
+           "verify_attn_mla_scaled")
 
 # Absorbed-MLA latent cache: row = [latent (MLA_NOPE) | rope key (MLA_PE)].
 MLA_NOPE, MLA_PE = 512, 64
@@ -125,6 +126,13 @@ def _lib():
         lib.verify_attn_append_kv.restype = ctypes.c_int32
         lib.verify_attn_append_mla.argtypes = [V] * 12
         lib.verify_attn_append_mla.restype = ctypes.c_int32
+        lib.verify_attn_scaled.argtypes = [V] * 8 + [ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                                                     V, V, V, ctypes.c_size_t, ctypes.c_int32, V, V]
+        lib.verify_attn_scaled.restype = ctypes.c_int32
+        lib.verify_attn_mla_scaled.argtypes = [V] * 6 + [ctypes.c_int32, ctypes.c_int32,
+                                                         ctypes.c_float, V, V, ctypes.c_size_t,
+                                                         ctypes.c_int32, V, V]
+        lib.verify_attn_mla_scaled.restype = ctypes.c_int32
         lib.verify_attn_status_string.argtypes = [ctypes.c_int32]
         lib.verify_attn_status_string.restype = ctypes.c_char_p
         _LIB = lib
@@ -160,6 +168,7 @@ def _ref(d):
 
 _DESC = struct.Struct("@Pii8q")     # one va_tensor
 _ROPE = struct.Struct("@PPi4x")     # one va_rope
+_OPTIONS = struct.Struct("@ifP")    # one va_options
 _PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
 _MAX_DESCS = 16
 
@@ -212,15 +221,45 @@ def _pack_rope(cos_sin, positions, interleaved):
     return _packed.base + off
 
 
+def _pack_options(window_left, softcap, sinks):
+    """Address of a va_options over a descriptor packed by _pack (None: all off)."""
+    if window_left == -1 and not softcap and sinks is None:
+        return None
+    off = _DESC.size * _MAX_DESCS
+    _OPTIONS.pack_into(_packed.buf, off, int(window_left), float(softcap), sinks or 0)
+    return _packed.base + off
+
+
+def _call_workspace(workspace, nbytes, device, stream):
+    """(tensor, aligned address, bytes) of a call's workspace. Without one it is
+    allocated with torch for this call alone, on the call's stream, so that
+    calls on different streams, or captured into different graphs, share none."""
+    if workspace is None:
+        if stream is None:
+            workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    a = workspace.data_ptr()
+    off = (-a) % 256
+    return workspace, a + off, workspace.numel() * workspace.element_size() - off
+
+
+def _on_device(fn, device, *args):
+    """fn(*args) with ``device`` current."""
+    if device.type != "cuda" or torch.cuda.current_device() == device.index:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
 def _call(fn, where, device, stream, *args):
     """fn(*args, stream) with ``device`` current; raises on an error status."""
     if device.type != "cuda":
         raise ValueError(f"{where}: tensors must be on a CUDA device, not {device}")
-    if torch.cuda.current_device() == device.index:
-        s = fn(*args, _stream_handle(stream, device))
-    else:
-        with torch.cuda.device(device):
-            s = fn(*args, _stream_handle(stream, device))
+    s = _on_device(fn, device, *args, _stream_handle(stream, device))
     if s != VA_OK:
         raise VerifyAttnError(s, where)
 
@@ -616,3 +655,53 @@ def append_mla(latent, k_pe, kv_cache, block_table, cu_seqlens_q, seqused_k, q_p
     _call(_lib().verify_attn_append_mla, "verify_attn_append_mla", latent.device, stream, *r[:6],
           rope, *r[6:10])
     return q_pe_out
+
+
+def verify_attn_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_seqlens_q,
+                       seqused_k, max_seqlen_q: int, max_seqlen_k: int, softmax_scale: float,
+                       out=None, window_left: int = -1, softcap: float = 0.0, sinks=None,
+                       workspace: Optional[torch.Tensor] = None, num_splits: int = 0, stream=None,
+                       event_after_main=None):
+    """Verify attention over a page-scaled e4m3 cache (see include/verify_attn.h):
+    scales [num_blocks, Hkv] fp32 for K and for V, as ``append_kv`` writes
+    them, with the variants of ``verify_attn_opt``. ``workspace`` (a uint8
+    device tensor, zeroed before its first use if its status word is to be
+    read) None: one of the call's own, from torch's allocator."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _same_device(q.device, k_cache, v_cache, k_scales, v_scales, block_table, cu_seqlens_q,
+                 seqused_k, out, sinks, workspace)
+    n = 0      # where the arguments have no plan, the call says why
+    if workspace is None and q.dim() == 3 and k_cache.dim() == 4 and seqused_k.dim() == 1:
+        n = _on_device(_lib().verify_attn_workspace_size, q.device, seqused_k.shape[0],
+                       k_cache.shape[2], q.shape[1], int(max_seqlen_q), int(max_seqlen_k),
+                       VA_FP8_E4M3, int(num_splits))
+    keep, addr, nbytes = _call_workspace(workspace, n, q.device, stream)
+    r = _pack(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_seqlens_q, seqused_k, out, sinks)
+    _call(_lib().verify_attn_scaled, "verify_attn_scaled", q.device, stream, *r[:8],
+          int(max_seqlen_q), int(max_seqlen_k), float(softmax_scale), r[8],
+          _pack_options(window_left, softcap, r[9]), addr, nbytes, int(num_splits),
+          _event_handle(event_after_main))
+    return out
+
+
+def verify_attn_mla_scaled(q, kv_cache, scales, block_table, cu_seqlens_q, seqused_k,
+                           max_seqlen_q: int, max_seqlen_k: int, softmax_scale: float, out=None,
+                           workspace: Optional[torch.Tensor] = None, num_splits: int = 0,
+                           stream=None, event_after_main=None):
+    """``verify_attn_mla`` over a page-scaled e4m3 latent cache (see
+    include/verify_attn.h): scales [num_blocks, 1] fp32, as ``append_mla``
+    writes them. ``workspace`` as for ``verify_attn_scaled``."""
+    if out is None:
+        out = torch.empty(q.shape[0], q.shape[1], MLA_NOPE, dtype=torch.bfloat16, device=q.device)
+    _same_device(q.device, kv_cache, scales, block_table, cu_seqlens_q, seqused_k, out, workspace)
+    n = 0
+    if workspace is None and q.dim() == 3 and seqused_k.dim() == 1:
+        n = _on_device(_lib().verify_attn_mla_workspace_size, q.device, seqused_k.shape[0],
+                       q.shape[1], int(max_seqlen_q), int(max_seqlen_k), int(num_splits))
+    keep, addr, nbytes = _call_workspace(workspace, n, q.device, stream)
+    r = _pack(q, kv_cache, scales, block_table, cu_seqlens_q, seqused_k, out)
+    _call(_lib().verify_attn_mla_scaled, "verify_attn_mla_scaled", q.device, stream, *r[:6],
+          int(max_seqlen_q), int(max_seqlen_k), float(softmax_scale), r[6], addr, nbytes,
+          int(num_splits), _event_handle(event_after_main))
+    return out

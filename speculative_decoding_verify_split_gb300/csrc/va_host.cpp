@@ -279,12 +279,22 @@ va_status validate_options(const va_options* opts, const Shapes& sh) {
   return VA_OK;
 }
 
+static void set_page_scales(Params* p, const PageScales* s) {
+  if (!s) return;
+  p->k_scales = static_cast<const float*>(s->k->data);
+  p->ks_s0 = s->k->stride[0];
+  p->ks_s1 = s->k->stride[1];
+  p->v_scales = static_cast<const float*>(s->v->data);
+  p->vs_s0 = s->v->stride[0];
+  p->vs_s1 = s->v->stride[1];
+}
+
 va_status launch(const va_tensor* q, const va_tensor* k, const va_tensor* v, const va_tensor* bt,
                  const va_tensor* cu, const va_tensor* su, int32_t max_q, int32_t max_k,
                  float scale, const va_tensor* kd, const va_tensor* vd, va_tensor* out,
                  const Shapes& sh, const va_plan& plan, void* ws, size_t ws_bytes,
                  cudaEvent_t ev_mid, cudaStream_t stream, const va_options* opts,
-                 const PartialOut* part) {
+                 const PartialOut* part, const PageScales* scales) {
   if (sh.total_q == 0 || sh.num_seqs == 0) return VA_OK;  // no output rows
   if ((size_t)plan.workspace_bytes > ws_bytes || !ws) return VA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return VA_ERR_WORKSPACE;
@@ -346,6 +356,7 @@ va_status launch(const va_tensor* q, const va_tensor* k, const va_tensor* v, con
     p.lse_s0 = part->lse->stride[0];
     p.lse_s1 = part->lse->stride[1];
   }
+  set_page_scales(&p, scales);
   const WorkspaceLayout lay = workspace_layout(plan.num_work, plan.num_splits, plan.max_rows);
   char* base = static_cast<char*>(ws);
   p.ws_meta = reinterpret_cast<int32_t*>(base + lay.meta_off);
@@ -472,7 +483,7 @@ va_status launch_mla(const va_tensor* q, const va_tensor* kv, const va_tensor* b
                      const va_tensor* su, int32_t max_q, int32_t max_k, float scale,
                      const va_tensor* kd, const va_tensor* vd, va_tensor* out, const Shapes& sh,
                      const va_plan& plan, void* ws, size_t ws_bytes, cudaEvent_t ev_mid,
-                     cudaStream_t stream) {
+                     cudaStream_t stream, const PageScales* scales) {
   if (sh.total_q == 0 || sh.num_seqs == 0) return VA_OK;
   if ((size_t)plan.workspace_bytes > ws_bytes || !ws) return VA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return VA_ERR_WORKSPACE;
@@ -514,6 +525,7 @@ va_status launch_mla(const va_tensor* q, const va_tensor* kv, const va_tensor* b
   p.piece_cost = p.kv_fp8 ? kMlaPieceCostTiles : kMlaPieceCostTilesBf16;
   p.dv = kMlaNope;
   p.wait_limit_ns = wait_limit_ns();
+  set_page_scales(&p, scales);
   const WorkspaceLayout lay =
       workspace_layout(plan.num_work, plan.num_splits, mla_row_stride(plan.max_rows), kMlaNope);
   char* base = static_cast<char*>(ws);
@@ -549,6 +561,15 @@ static va_status library_workspace(DeviceState* st, size_t bytes, cudaStream_t s
   if (cudaMemsetAsync(st->ws, 0, 256, stream) != cudaSuccess) return VA_ERR_CUDA;
   st->ws_bytes = bytes;
   return VA_OK;
+}
+
+// The library's workspace may be replaced by a later call, so its address must
+// not be baked into a graph: a page-scaled call being captured needs the
+// caller's workspace.
+static va_status refuse_capture(cudaStream_t stream) {
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return VA_ERR_CUDA;
+  return cap == cudaStreamCaptureStatusNone ? VA_OK : VA_ERR_WORKSPACE;
 }
 
 va_status current_device_sms(int* sms) {
@@ -603,13 +624,19 @@ static va_status run_call(const va_tensor* q, const va_tensor* k_cache, const va
                           float softmax_scale, const va_tensor* k_descale,
                           const va_tensor* v_descale, va_tensor* out, const va_options* opts,
                           void* workspace, size_t workspace_bytes, bool own_ws, int32_t num_splits,
-                          cudaEvent_t ev_mid, cudaStream_t stream) {
+                          cudaEvent_t ev_mid, cudaStream_t stream, const PageScales* scales = nullptr) {
   Shapes sh;
   va_status s = validate(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, max_seqlen_q,
                          max_seqlen_k, k_descale, v_descale, out, &sh);
   if (s != VA_OK) return s;
   s = validate_options(opts, sh);
   if (s != VA_OK) return s;
+  if (scales) {
+    if (sh.kv_dtype != VA_FP8_E4M3) return VA_ERR_DTYPE;
+    s = check_page_scales(scales->k, sh.num_blocks, sh.hkv);
+    if (s == VA_OK) s = check_page_scales(scales->v, sh.num_blocks, sh.hkv);
+    if (s != VA_OK) return s;
+  }
   if (num_splits < 0) return VA_ERR_UNSUPPORTED;
   std::unique_lock<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
@@ -621,6 +648,8 @@ static va_status run_call(const va_tensor* q, const va_tensor* k_cache, const va
   if (s != VA_OK) return s;
   if (own_ws) {
     if (sh.total_q == 0 || sh.num_seqs == 0) return VA_OK;
+    if (scales) s = refuse_capture(stream);
+    if (s != VA_OK) return s;
     s = library_workspace(st, (size_t)plan.workspace_bytes, stream);
     if (s != VA_OK) return s;
     workspace = st->ws;
@@ -630,7 +659,7 @@ static va_status run_call(const va_tensor* q, const va_tensor* k_cache, const va
   }
   return launch(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, max_seqlen_q,
                 max_seqlen_k, softmax_scale, k_descale, v_descale, out, sh, plan, workspace,
-                workspace_bytes, ev_mid, stream, opts);
+                workspace_bytes, ev_mid, stream, opts, nullptr, scales);
 }
 
 VA_EXPORT va_status verify_attn_ex(const va_tensor* q, const va_tensor* k_cache,
@@ -670,6 +699,20 @@ VA_EXPORT va_status verify_attn_opt(const va_tensor* q, const va_tensor* k_cache
                   static_cast<cudaStream_t>(stream));
 }
 
+VA_EXPORT va_status verify_attn_scaled(const va_tensor* q, const va_tensor* k_cache, const va_tensor* v_cache,
+                                       const va_tensor* k_scales, const va_tensor* v_scales,
+                                       const va_tensor* block_table, const va_tensor* cu_seqlens_q,
+                                       const va_tensor* seqused_k, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                       float softmax_scale, va_tensor* out, const va_options* opts, void* workspace,
+                                       size_t workspace_bytes, int32_t num_splits, void* event_after_main,
+                                       void* stream) {
+  if (!k_scales || !v_scales) return VA_ERR_NULL;
+  const PageScales scales{k_scales, v_scales};
+  return run_call(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, max_seqlen_q, max_seqlen_k,
+                  softmax_scale, nullptr, nullptr, out, opts, workspace, workspace_bytes, workspace == nullptr,
+                  num_splits, static_cast<cudaEvent_t>(event_after_main), static_cast<cudaStream_t>(stream), &scales);
+}
+
 // Descriptor checks of verify_attn_block_table_from_indptr (host only).
 static va_status validate_block_table_args(const va_tensor* indptr, const va_tensor* indices,
                                            const va_tensor* bt, const va_tensor* seqused) {
@@ -707,17 +750,21 @@ VA_EXPORT va_status verify_attn_block_table_from_indptr(const va_tensor* kv_indp
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }
 
-VA_EXPORT va_status verify_attn_mla(const va_tensor* q, const va_tensor* kv_cache,
-                                    const va_tensor* block_table, const va_tensor* cu_seqlens_q,
-                                    const va_tensor* seqused_k, int32_t max_seqlen_q,
-                                    int32_t max_seqlen_k, float softmax_scale,
-                                    const va_tensor* k_descale, const va_tensor* v_descale,
-                                    va_tensor* out, void* workspace, size_t workspace_bytes,
-                                    int32_t num_splits, void* event_after_main, void* stream) {
+// Shared body of verify_attn_mla and verify_attn_mla_scaled.
+static va_status run_mla_call(const va_tensor* q, const va_tensor* kv_cache, const va_tensor* block_table,
+                              const va_tensor* cu_seqlens_q, const va_tensor* seqused_k, int32_t max_seqlen_q,
+                              int32_t max_seqlen_k, float softmax_scale, const va_tensor* k_descale,
+                              const va_tensor* v_descale, va_tensor* out, void* workspace, size_t workspace_bytes,
+                              int32_t num_splits, void* event_after_main, void* stream, const PageScales* scales) {
   Shapes sh;
   va_status s = validate_mla(q, kv_cache, block_table, cu_seqlens_q, seqused_k, max_seqlen_q,
                              max_seqlen_k, k_descale, v_descale, out, &sh);
   if (s != VA_OK) return s;
+  if (scales) {
+    if (sh.kv_dtype != VA_FP8_E4M3) return VA_ERR_DTYPE;
+    s = check_page_scales(scales->k, sh.num_blocks, 1);
+    if (s != VA_OK) return s;
+  }
   if (num_splits < 0) return VA_ERR_UNSUPPORTED;
   std::unique_lock<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
@@ -728,6 +775,8 @@ VA_EXPORT va_status verify_attn_mla(const va_tensor* q, const va_tensor* kv_cach
   if (s != VA_OK) return s;
   if (!workspace) {
     if (sh.total_q == 0 || sh.num_seqs == 0) return VA_OK;
+    if (scales) s = refuse_capture(static_cast<cudaStream_t>(stream));
+    if (s != VA_OK) return s;
     s = library_workspace(st, (size_t)plan.workspace_bytes, static_cast<cudaStream_t>(stream));
     if (s != VA_OK) return s;
     workspace = st->ws;
@@ -737,7 +786,31 @@ VA_EXPORT va_status verify_attn_mla(const va_tensor* q, const va_tensor* kv_cach
   }
   return launch_mla(q, kv_cache, block_table, cu_seqlens_q, seqused_k, max_seqlen_q, max_seqlen_k,
                     softmax_scale, k_descale, v_descale, out, sh, plan, workspace, workspace_bytes,
-                    static_cast<cudaEvent_t>(event_after_main), static_cast<cudaStream_t>(stream));
+                    static_cast<cudaEvent_t>(event_after_main), static_cast<cudaStream_t>(stream), scales);
+}
+
+VA_EXPORT va_status verify_attn_mla(const va_tensor* q, const va_tensor* kv_cache,
+                                    const va_tensor* block_table, const va_tensor* cu_seqlens_q,
+                                    const va_tensor* seqused_k, int32_t max_seqlen_q,
+                                    int32_t max_seqlen_k, float softmax_scale,
+                                    const va_tensor* k_descale, const va_tensor* v_descale,
+                                    va_tensor* out, void* workspace, size_t workspace_bytes,
+                                    int32_t num_splits, void* event_after_main, void* stream) {
+  return run_mla_call(q, kv_cache, block_table, cu_seqlens_q, seqused_k, max_seqlen_q, max_seqlen_k, softmax_scale,
+                      k_descale, v_descale, out, workspace, workspace_bytes, num_splits, event_after_main, stream,
+                      nullptr);
+}
+
+VA_EXPORT va_status verify_attn_mla_scaled(const va_tensor* q, const va_tensor* kv_cache, const va_tensor* scales,
+                                           const va_tensor* block_table, const va_tensor* cu_seqlens_q,
+                                           const va_tensor* seqused_k, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                           float softmax_scale, va_tensor* out, void* workspace,
+                                           size_t workspace_bytes, int32_t num_splits, void* event_after_main,
+                                           void* stream) {
+  if (!scales) return VA_ERR_NULL;
+  const PageScales ps{scales, scales};
+  return run_mla_call(q, kv_cache, block_table, cu_seqlens_q, seqused_k, max_seqlen_q, max_seqlen_k, softmax_scale,
+                      nullptr, nullptr, out, workspace, workspace_bytes, num_splits, event_after_main, stream, &ps);
 }
 
 VA_EXPORT size_t verify_attn_mla_workspace_size(int32_t num_seqs, int32_t num_q_heads,

@@ -49,6 +49,12 @@ struct PartialOut {
   va_tensor* lse;
 };
 
+// Scales of a page-scaled e4m3 cache (a latent cache: one tensor for both).
+struct PageScales {
+  const va_tensor* k;
+  const va_tensor* v;
+};
+
 // Launches the main and merge kernels with the given workspace and options
 // (NULL = all off); with `part`, the merge writes the shard's o and lse.
 va_status launch(const va_tensor* q, const va_tensor* k, const va_tensor* v, const va_tensor* bt,
@@ -56,7 +62,7 @@ va_status launch(const va_tensor* q, const va_tensor* k, const va_tensor* v, con
                  float scale, const va_tensor* kd, const va_tensor* vd, va_tensor* out,
                  const Shapes& sh, const va_plan& plan, void* ws, size_t ws_bytes,
                  cudaEvent_t ev_mid, cudaStream_t stream, const va_options* opts = nullptr,
-                 const PartialOut* part = nullptr);
+                 const PartialOut* part = nullptr, const PageScales* scales = nullptr);
 
 // SM count of the current device (initialises the per-device state once).
 va_status current_device_sms(int* sms);

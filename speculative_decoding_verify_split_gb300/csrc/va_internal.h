@@ -68,6 +68,12 @@ struct Params {
   int64_t op_s0, op_s1;
   float* lse_part;           // [total_q, hq]
   int64_t lse_s0, lse_s1;
+  // Page-scaled e4m3 cache (null: none): the value of a code is
+  // code * scale[page, head]. A latent cache has one scale for both (v_scales
+  // = k_scales).
+  const float* k_scales;
+  const float* v_scales;
+  int64_t ks_s0, ks_s1, vs_s0, vs_s1;
 
   // Split-KV decomposition: one stream of key tiles over all work items
   // j = b * hkv + kvh, cut into num_splits equal ranges (one per CTA). Each

@@ -179,6 +179,10 @@ constexpr float kOvershoot = 2.8f;  // move only if the tile max > m_ref + kOver
 
 
 constexpr int kMaxSlots = 5;
+constexpr int kMaxVSlots = 3;
+// Page-scaled caches: per V ring slot the tile's eight pages' (K scale, log2
+// of the V scale), behind the barriers and the scan scratch.
+constexpr int kOffScales = 768;
 // Barrier slots (8 bytes each) after kOffBar.
 enum : int {
   kBarFullK = 0,
@@ -194,9 +198,11 @@ enum : int {
   kBarOFull,
   kBarOFree,
   kBarDrain,
-  kNumBars
+  kBarScales,  // page-scaled caches: a V slot's page scales are written
+  kNumBars = kBarScales + kMaxVSlots
 };
-static_assert(8 * kNumBars + 16 + 34 * 8 + 4 * 2 * kMaxSlots <= 1024, "barrier area");
+static_assert(8 * kNumBars + 16 + 34 * 8 + 4 * 2 * kMaxSlots <= kOffScales, "barrier area");
+static_assert(kOffScales + kMaxVSlots * 8 * 8 <= 1024 && kOffScales % 16 == 0, "page scales");
 
 template <bool FP8>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -208,11 +214,21 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 
 // VAR: compiled with the sliding-window / soft-cap / sink code (the plain path
 // is compiled without it). QTM: the FP8 layout with Q and P in TMEM (Cfg).
-template <bool FP8, bool VAR, bool QTM>
+// SCL: a page-scaled cache (FP8). The V scale vs of a key's page is folded
+// into the key's weight, P = 2^(s + log2 vs - m_ref): the reference max is
+// taken over s + log2 vs, O accumulates P times the codes, and the normaliser
+// l sums P / vs. K's scale multiplies the page's logits. Both are per page,
+// so they cost nothing per key: a thread's 32 keys of a tile are two pages,
+// each with its own factor and offset in the FMA of P's exponent, and its own
+// partial sum of l. The V producers, which walk the page ids anyway, bring
+// the scales to shared memory with the V tile's slot.
+template <bool FP8, bool VAR, bool QTM, bool SCL>
 __global__ void __launch_bounds__(kThreads, 1)
     va_main_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<FP8, VAR, QTM>;
+  static_assert(FP8 || !SCL, "page scales are for e4m3 caches");
+  static_assert(!SCL || C::kVSlots <= kMaxVSlots, "page scales: one place per V slot");
   constexpr int kT = C::kT;
   constexpr int kSBufs = C::kSBufs;
   constexpr int kPBufs = C::kPBufs;
@@ -266,6 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(kBarOFull), 1);
     mbar_init(bar(kBarOFree), kSwWarps);
     mbar_init(bar(kBarDrain), 2);
+    if constexpr (SCL)
+      for (int s = 0; s < C::kVSlots; ++s) mbar_init(bar(kBarScales + s), 1);
     *abort_flag = 0;
     for (int s = 0; s < 2 * kMaxSlots; ++s) slot_tile[s] = -1;
     fence_mbar_init();
@@ -331,13 +349,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int* bt_row = p.block_table + (int64_t)pc.b * p.bt_s0;
       int win = -1;       // first page index cached in the lanes
       int my_page = -1;   // page id of page (win + lane)
+      ScaleWindow sw;
       for (int lt = pc.lt0; lt < pc.lt1 && ok; ++lt, ++it) {
         if (it % nprod != prod) continue;
         const int s = it % nslots;
         // page ids first (a block-table load every 32 pages), so that their
         // latency overlaps the wait for the ring slot
         const int pg0 = lt * kPagesPerTile;
-        if (win < 0 || pg0 + kPagesPerTile > win + 32) {
+        if (SCL && !is_k) {
+          if (win < 0 || pg0 + kPagesPerTile > win + 32) {
+            win = pg0;
+            sw.move(p, bt_row, pc.kvh, win, 32, pg_first, npages);
+            my_page = sw.id;
+          } else {
+            sw.advance(p, pc.kvh);
+          }
+        } else if (win < 0 || pg0 + kPagesPerTile > win + 32) {
           win = pg0;
           const int pg = win + lane;
           my_page = pg < npages ? bt_row[(int64_t)pg * p.bt_s1] : -1;
@@ -376,6 +403,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (id >= 0)
             tma_load_4d_hint(dst + ch * C::kRegion + i * 2048, tmap, ch * (128 / C::kEsize), pc.kvh, 0, id,
                              bar(bar_full + s), kv_policy);
+        }
+        if (SCL && !is_k) {
+          // the tile's page scales, free with the V slot: the softmax of the
+          // slot's previous tile read them before its P V freed it
+          const int i = win + lane - pg0;
+          if (i >= 0 && i < kPagesPerTile)
+            reinterpret_cast<float2*>(sm + C::kOffBar + kOffScales)[s * kPagesPerTile + i] = softmax_scales(sw.ks, sw.vs);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarScales + s));
         }
         __syncwarp();
       }
@@ -704,6 +740,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             rx = rs / xs;
           }
         }
+        // page-scaled: factor and offset of the keys of this thread's two
+        // pages (keys [0, 16) and [16, 32)); the factor stays a positive
+        // normal number, so that a masked key's -inf stays -inf
+        float xs2[2] = {xs, xs}, rx2[2] = {rx, rx}, lv[2] = {0.f, 0.f};
+        if constexpr (SCL) {
+          const int vs = cur % C::kVSlots;
+          if (wait_or_fail(kBarScales + vs, (cur / C::kVSlots) & 1, 8192)) {
+            const float4 sc = reinterpret_cast<const float4*>(sm + C::kOffBar + kOffScales)[vs * (kPagesPerTile / 2) + qtr];
+            lv[0] = sc.y;
+            lv[1] = sc.w;
+            if (VAR && p.softcap_log2 > 0.f) {
+              rx2[0] = rx * sc.x;
+              rx2[1] = rx * sc.z;
+            } else {
+              xs2[0] = fmaxf(xs * sc.x, 1.2e-38f);
+              xs2[1] = fmaxf(xs * sc.z, 1.2e-38f);
+            }
+          }
+        }
         if (wait_or_fail(kBarSFull + b, (cur / kSBufs) & 1, 256)) {
           tc_fence_after();
           if constexpr (FP8) {
@@ -741,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // logit l by at most |l| 2^-11 log2 units (0.5 % of a key's
               // weight at l = 10).
 #pragma unroll
-              for (int i = 0; i < kKpt; ++i) x[i] = tanh_approx(x[i] * rx);
+              for (int i = 0; i < kKpt; ++i) x[i] = tanh_approx(x[i] * (SCL ? rx2[i / 16] : rx));
             }
           }
           const int key0 = lt * kT + kKpt * qtr;
@@ -759,9 +814,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         float tmax = -INFINITY;
+        if constexpr (SCL) {
+          float t2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < kKpt; i += 2) tmax = fmax3(tmax, x[i], x[i + 1]);
-        tmax = exchange(tmax * xs, true);  // log2 units (xs > 0 keeps the order)
+          for (int i = 0; i < kKpt; i += 2) t2[i / 16] = fmax3(t2[i / 16], x[i], x[i + 1]);
+          tmax = exchange(fmaxf(fmaf(t2[0], xs2[0], lv[0]), fmaf(t2[1], xs2[1], lv[1])), true);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kKpt; i += 2) tmax = fmax3(tmax, x[i], x[i + 1]);
+          tmax = exchange(tmax * xs, true);  // log2 units (xs > 0 keeps the order)
+        }
         if (!ok) continue;
 
         // P buffer pb was last read by PV(cur - kPBufs). (A P over S(cur):
@@ -813,12 +875,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned char* pbuf = sm + C::kOffP + pb * C::kPBuf;
         if constexpr (FP8) {
           uint32_t ph[8], pl[8];
+          const float off2[2] = {lv[0] - mref_s, lv[1] - mref_s};
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float a = ex2(fmaf(x[2 * i], xs, -mref_s));
-            const float bb = ex2(fmaf(x[2 * i + 1], xs, -mref_s));
-            ls0 += a;
-            ls1 += bb;
+            const float a = ex2(SCL ? fmaf(x[2 * i], xs2[i / 8], off2[i / 8]) : fmaf(x[2 * i], xs, -mref_s));
+            const float bb = ex2(SCL ? fmaf(x[2 * i + 1], xs2[i / 8], off2[i / 8]) : fmaf(x[2 * i + 1], xs, -mref_s));
+            if (SCL) {
+              // ls0, ls1: the sums of the first and of the second page
+              if (i < 8)
+                ls0 += a + bb;
+              else
+                ls1 += a + bb;
+            } else {
+              ls0 += a;
+              ls1 += bb;
+            }
             uint32_t h2, l2;
             split_p(a, bb, h2, l2);
             if (i & 1) {
@@ -857,7 +928,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(base) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
           *reinterpret_cast<uint4*>(base + 128) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
         }
-        l += ls0 + ls1;
+        if constexpr (SCL)
+          l += ls0 * ex2(-lv[0]) + ls1 * ex2(-lv[1]);  // the weights without vs
+        else
+          l += ls0 + ls1;
         // V rows no row may see and whose pages may hold anything are zeroed,
         // so that 0 * garbage cannot reach O: past S in the item's last tile
         // (partial page, pages never loaded), and in its first tile the pages
@@ -983,9 +1057,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-template <bool FP8, bool VAR, bool QTM>
+template <bool FP8, bool VAR, bool QTM, bool SCL = false>
 cudaError_t set_smem() {
-  return cudaFuncSetAttribute(va_main_tc_kernel<FP8, VAR, QTM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(va_main_tc_kernel<FP8, VAR, QTM, SCL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Cfg<FP8, VAR, QTM>::kSmemBytes);
 }
 
@@ -995,14 +1069,17 @@ cudaError_t prepare_main_tc() {
   if (e == cudaSuccess) e = set_smem<false, false, false>();
   if (e == cudaSuccess) e = set_smem<true, true, false>();
   if (e == cudaSuccess) e = set_smem<false, true, false>();
+  if (e == cudaSuccess) e = set_smem<true, false, true, true>();
+  if (e == cudaSuccess) e = set_smem<true, false, false, true>();
+  if (e == cudaSuccess) e = set_smem<true, true, false, true>();
   return e;
 }
 
-template <bool FP8, bool VAR, bool QTM>
+template <bool FP8, bool VAR, bool QTM, bool SCL = false>
 static cudaError_t launch_one(cudaLaunchConfig_t& cfg, const Params& p, const CUtensorMap& tm_k,
                               const CUtensorMap& tm_v) {
   cfg.dynamicSmemBytes = Cfg<FP8, VAR, QTM>::kSmemBytes;
-  return cudaLaunchKernelEx(&cfg, va_main_tc_kernel<FP8, VAR, QTM>, p, tm_k, tm_v);
+  return cudaLaunchKernelEx(&cfg, va_main_tc_kernel<FP8, VAR, QTM, SCL>, p, tm_k, tm_v);
 }
 
 cudaError_t launch_main_tc(const Params& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
@@ -1019,6 +1096,11 @@ cudaError_t launch_main_tc(const Params& p, const CUtensorMap& tm_k, const CUten
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (p.k_scales) {
+    if (var) return launch_one<true, true, false, true>(cfg, p, tm_k, tm_v);
+    return p.q_in_tmem ? launch_one<true, false, true, true>(cfg, p, tm_k, tm_v)
+                       : launch_one<true, false, false, true>(cfg, p, tm_k, tm_v);
+  }
   if (p.kv_fp8) {
     if (var) return launch_one<true, true, false>(cfg, p, tm_k, tm_v);
     return p.q_in_tmem ? launch_one<true, false, true>(cfg, p, tm_k, tm_v)

@@ -116,15 +116,18 @@ enum : int {
   kBarOFull,
   kBarOFree,
   kBarDrain,
-  kNumBars
+  kBarScales,  // page-scaled caches: a ring slot's page scales are written
+  kNumBars = kBarScales + kSlots
 };
 // barrier area: mbarriers | TMEM address, abort flag | scan scratch (34 x 8) |
 // last tile issued into each ring slot | per-row factors [2 rounds][64] floats
 // at +1024 (2 KB in all); then the batch's lengths (1 KB)
 constexpr int kOffTmemSlot = 8 * kNumBars;
-constexpr int kOffScratch = 256;
+constexpr int kOffScratch = 320;
 constexpr int kOffSlotTile = kOffScratch + 34 * 8;  // last tile issued into each slot
 constexpr int kOffRowVals = 1024;
+constexpr int kOffScales = 1536;  // page-scaled: per ring slot its four pages' (scale, log2 of it)
+static_assert(kOffScales + kSlots * kPagesPerTile * 8 <= 2048, "page scales");
 static_assert(kOffTmemSlot + 8 <= kOffScratch && kOffSlotTile + 4 * kSlots <= kOffRowVals, "barrier area");
 
 // Four bf16 values (two words) times 2^e -> e4m3 hi and lo bytes, in order.
@@ -148,6 +151,12 @@ __device__ __forceinline__ int core_off(int m, int k, int row_bytes) {
   return (m >> 3) * (8 * row_bytes) + (k >> 4) * 128 + (m & 7) * 16 + (k & 15);
 }
 
+// SCL: a page-scaled cache, one scale a page for keys and values; as in the
+// GQA kernel it multiplies the page's logits, and as the value's scale joins
+// the weight, P = 2^(s + log2 scale - m_ref), with l summing P / scale. A
+// thread's 16 keys of a tile are one page. The producers bring the scales
+// with the ring slot.
+template <bool SCL>
 __global__ void __launch_bounds__(kThreads, 1)
     va_mla_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tm_kv,
                      const __grid_constant__ CUtensorMap tm_pe) {
@@ -194,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(kBarOFull), 1);
     mbar_init(bar(kBarOFree), kSwWarps);
     mbar_init(bar(kBarDrain), 2);
+    if constexpr (SCL)
+      for (int s = 0; s < kSlots; ++s) mbar_init(bar(kBarScales + s), 1);
     *abort_flag = 0;
     for (int s = 0; s < kSlots; ++s) slot_tile[s] = -1;
     fence_mbar_init();
@@ -257,11 +268,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int* bt_row = p.block_table + (int64_t)pc.b * p.bt_s0;
       int win = -1;
       int my_page = -1;
+      ScaleWindow sw;
       for (int lt = pc.lt0; lt < pc.lt1 && ok; ++lt, ++it) {
         if (it % kProducers != prod) continue;
         const int s = it % kSlots;
         const int pg0 = lt * kPagesPerTile;
-        if (win < 0 || pg0 + kPagesPerTile > win + 32) {
+        if constexpr (SCL) {
+          // this warp's tiles of a window start 0, 12 and 24 pages into it
+          if (win < 0 || pg0 + kPagesPerTile > win + 32) {
+            win = pg0;
+            sw.move(p, bt_row, 0, win, 36, 0, npages);
+            my_page = sw.id;
+          } else {
+            sw.advance(p, 0);
+          }
+        } else if (win < 0 || pg0 + kPagesPerTile > win + 32) {
           win = pg0;
           const int pg = win + lane;
           my_page = pg < npages ? bt_row[(int64_t)pg * p.bt_s1] : -1;
@@ -304,6 +325,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d_hint(dst + 4 * kRegion + i * 1024, &tm_pe, kMlaNope, 0, 0, id, bar(kBarFull + s),
                                kv_policy);
           }
+        }
+        if constexpr (SCL) {
+          const int i = win + lane - pg0;
+          if (i >= 0 && i < kPagesPerTile)
+            reinterpret_cast<float2*>(sm + kOffBar + kOffScales)[s * kPagesPerTile + i] = softmax_scales(sw.ks, sw.vs);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarScales + s));
         }
         __syncwarp();
       }
@@ -561,6 +589,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         float x[16];  // logits of keys [16 qtr, +16) of this tile, this row
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = -INFINITY;
+        // the factor of the raw dot products (a positive normal number: -inf
+        // stays -inf) and, page-scaled, the offset log2 scale of the page
+        float xs = rs, lv = 0.f;
+        if constexpr (SCL) {
+          const int s = cur % kSlots;
+          if (wait_or_fail(kBarScales + s, (cur / kSlots) & 1, 8192)) {
+            const float2 sc = reinterpret_cast<const float2*>(sm + kOffBar + kOffScales)[s * kPagesPerTile + qtr];
+            xs = fmaxf(rs * sc.x, 1.2e-38f);
+            lv = sc.y;
+          }
+        }
         if (wait_or_fail(kBarSFull + b, (cur / kSBufs) & 1, 256)) {
           tc_fence_after();
           // the hi and lo partials of row r, keys [32 kh + 16 sub, +16): two
@@ -585,7 +624,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float tmax = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 16; i += 2) tmax = fmax3(tmax, x[i], x[i + 1]);
-        tmax *= rs;  // x holds the raw dot products; rs > 0 keeps the order
+        // x holds the raw dot products; xs > 0 keeps the order
+        if constexpr (SCL)
+          tmax = fmaf(tmax, xs, lv);
+        else
+          tmax *= xs;
         // A row's reference moves only when one of its four threads sees a
         // key above m_ref + kOvershoot. One vote over all softmax threads
         // finds out; only then is the row max exchanged (the reference stays
@@ -615,10 +658,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mref_s = m_new != -INFINITY ? m_new - kPShift : INFINITY;
         uint32_t ph[4], pl[4];
         float ls = 0.f;
+        const float off2 = SCL ? lv - mref_s : -mref_s;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float a = ex2(fmaf(x[2 * i], rs, -mref_s));
-          const float bb = ex2(fmaf(x[2 * i + 1], rs, -mref_s));
+          const float a = ex2(fmaf(x[2 * i], xs, off2));
+          const float bb = ex2(fmaf(x[2 * i + 1], xs, off2));
           ls += a + bb;
           uint32_t h2, l2;
           split_p(a, bb, h2, l2);
@@ -653,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
+        if constexpr (SCL) ls *= ex2(-lv);  // the weights without the scale
         l = l * alpha + ls;
         m_ref = m_new;
         // latent rows past S in the item's last tile (a partial page, pages
@@ -724,7 +769,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 cudaError_t prepare_mla_tc() {
-  return cudaFuncSetAttribute(va_mla_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes + 1024);
+  cudaError_t e =
+      cudaFuncSetAttribute(va_mla_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes + 1024);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(va_mla_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes + 1024);
+  return e;
 }
 
 cudaError_t launch_mla_tc(const Params& p, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
@@ -740,7 +789,8 @@ cudaError_t launch_mla_tc(const Params& p, const CUtensorMap& tm_kv, const CUten
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, va_mla_tc_kernel, p, tm_kv, tm_pe);
+  return p.k_scales ? cudaLaunchKernelEx(&cfg, va_mla_tc_kernel<true>, p, tm_kv, tm_pe)
+                    : cudaLaunchKernelEx(&cfg, va_mla_tc_kernel<false>, p, tm_kv, tm_pe);
 }
 
 }  // namespace va

@@ -280,6 +280,57 @@ __device__ __forceinline__ bool next_piece(const Params& p, long long t0, long l
   return false;
 }
 
+// A page's scales as the softmax takes them: K's, and log2 of V's, each
+// clamped to [kMinPageScale, kMaxPageScale] (NaN as the smallest).
+__device__ __forceinline__ float2 softmax_scales(float ks, float vs) {
+  ks = fminf(fmaxf(ks, kMinPageScale), kMaxPageScale);
+  vs = fminf(fmaxf(vs, kMinPageScale), kMaxPageScale);
+  return make_float2(ks, log2f(vs));
+}
+
+// A producer warp's window of 32 page ids with their scales, one page a lane,
+// and the next window's on their way: its ids are loaded a window ahead and
+// its scales once the ids have arrived, so that a window switch waits for
+// neither round trip.
+struct ScaleWindow {
+  int id = -1, next_id = -1, next_win = -1;
+  float ks = 1.f, vs = 1.f, next_ks = 1.f, next_vs = 1.f;
+  bool have_next = false;
+
+  __device__ __forceinline__ void load(const Params& p, int kvh, int page, float& k, float& v) const {
+    k = v = 1.f;
+    if ((unsigned)page < (unsigned)p.num_blocks) {
+      k = p.k_scales[(int64_t)page * p.ks_s0 + (int64_t)kvh * p.ks_s1];
+      v = p.v_scales[(int64_t)page * p.vs_s0 + (int64_t)kvh * p.vs_s1];
+    }
+  }
+  // Moves to the window of pages [win, win + 32); `step`: from one window's
+  // start to the next one's. Pages outside [pg_first, npages) have no entry.
+  __device__ __forceinline__ void move(const Params& p, const int* bt_row, int kvh, int win, int step, int pg_first,
+                                       int npages) {
+    const int lane = threadIdx.x & 31;
+    auto entry = [&](int pg) { return pg >= pg_first && pg < npages ? bt_row[(int64_t)pg * p.bt_s1] : -1; };
+    if (next_win == win) {
+      if (!have_next) load(p, kvh, next_id, next_ks, next_vs);
+      id = next_id;
+      ks = next_ks;
+      vs = next_vs;
+    } else {
+      id = entry(win + lane);
+      load(p, kvh, id, ks, vs);
+    }
+    next_win = win + step;
+    next_id = entry(next_win + lane);
+    have_next = false;
+  }
+  // Called at a later tile of the window: the next window's ids are here.
+  __device__ __forceinline__ void advance(const Params& p, int kvh) {
+    if (have_next) return;
+    load(p, kvh, next_id, next_ks, next_vs);
+    have_next = true;
+  }
+};
+
 __device__ __forceinline__ void fail(const Params& p, volatile int* abort_flag, int code) {
   *abort_flag = 1;
   if (p.ws_status) atomicOr(p.ws_status, code);

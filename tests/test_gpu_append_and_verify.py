@@ -1,0 +1,132 @@
+"""The calls as a decoder makes them: a prompt appended in chunks, then verify
+steps that append drafts, attend, take back what was refused, and go on, over
+every kind of cache."""
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_verify_split_gb300 as va
+from append_util import decode, table
+from oracle.attention_fp64 import softmax_attend
+from oracle.page_scaled_fp64 import page_scaled_oracle
+from parity_gate import check_gates
+
+pytestmark = pytest.mark.gpu
+
+
+class Decoder:
+    """Sequences in one cache, with what each has been fed (fp64) kept beside."""
+
+    def __init__(self, kind, latent, hq, hkv, seed):
+        self.kind, self.latent, self.hq, self.hkv = kind, latent, hq, hkv
+        self.g = torch.Generator().manual_seed(seed)
+        self.B, self.width, self.pages = 3, 24, 80
+        self.dim = 576 if latent else 256
+        dt = torch.bfloat16 if kind == "bf16" else torch.float8_e4m3fn
+        shape = (self.pages, 16, 1 if latent else hkv, self.dim)
+        nan = torch.full(shape, float("nan")).to(dt).cuda()
+        self.cache = [nan, nan.clone()]
+        self.scales = [torch.full(shape[::2][:2], float("nan"), device="cuda") for _ in range(2)] if kind == "scaled" else [None, None]
+        self.descale = [torch.tensor([0.03], device="cuda"), torch.tensor([0.05], device="cuda")] if kind == "e4m3" else [None, None]
+        self.bt = torch.randperm(self.pages, generator=self.g)[:self.B * self.width].reshape(self.B, self.width).int().cuda()
+        self.len = [0] * self.B
+        self.cos_sin = table(400, 64 if latent else 128).cuda()
+        self.scale = self.dim ** -0.5
+        self.fed = [[] for _ in range(self.B)]     # per sequence: rows of (k, v) in fp64, after the rotation
+
+    def rnd(self, *s):
+        return torch.randn(*s, generator=self.g).to(torch.bfloat16).cuda()
+
+    def rot(self, x, pos):
+        """fp64 rotation by halves of x [n, heads, dim] at positions pos."""
+        n = self.cos_sin.shape[1] // 2
+        c, s = self.cos_sin.cpu().double()[pos][:, None, :n], self.cos_sin.cpu().double()[pos][:, None, n:]
+        y = x.cpu().double().clone()
+        o = 512 if self.latent else 0
+        a, b = y[..., o:o + n].clone(), y[..., o + n:o + 2 * n].clone()
+        y[..., o:o + n], y[..., o + n:o + 2 * n] = a * c - b * s, b * c + a * s
+        return y
+
+    def step(self, news, attend):
+        T = sum(news)
+        pos = torch.cat([torch.arange(l, l + n) for l, n in zip(self.len, news)])
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32).cuda()
+        self.len = [l + n for l, n in zip(self.len, news)]
+        used = torch.tensor(self.len, dtype=torch.int32).cuda()
+        q = self.rnd(T, self.hq, self.dim)
+        if self.latent:
+            row = self.rnd(T, 576)
+            k = self.rot(row[:, None], pos)
+            v = k[..., :512]
+            qr = self.rot(q, pos)
+            va.append_mla(row[:, :512], row[:, 512:], self.cache[0], self.bt, cu, used, q_pe=q[..., 512:], q_pe_out=q[..., 512:],
+                          cos_sin=self.cos_sin, descale=self.descale[0], scales=self.scales[0])
+        else:
+            qkv = self.rnd(T, self.hq + 2 * self.hkv, 256)
+            qkv[:, :self.hq] = q
+            q = qkv[:, :self.hq]
+            k, v = qkv[:, self.hq:self.hq + self.hkv], qkv[:, self.hq + self.hkv:]
+            qr = self.rot(q, pos)
+            va.append_kv(k, v, *self.cache, self.bt, cu, used, q=q, q_out=q, cos_sin=self.cos_sin, k_descale=self.descale[0],
+                         v_descale=self.descale[1], k_scales=self.scales[0], v_scales=self.scales[1])
+            k, v = self.rot(k, pos), v.cpu().double()
+        for b in range(self.B):
+            a, z = int(cu[b]), int(cu[b + 1])
+            self.fed[b] += [(k[i].numpy(), v[i].numpy()) for i in range(a, z)]
+        if not attend:
+            return
+        mk = self.width * 16
+        if self.latent and self.kind == "scaled":
+            out = va.verify_attn_mla_scaled(q, self.cache[0], self.scales[0], self.bt, cu, used, max(news), mk, self.scale)
+        elif self.latent:
+            out = va.verify_attn_mla(q, self.cache[0], self.bt, cu, used, max(news), mk, self.scale, self.descale[0], self.descale[0])
+        elif self.kind == "scaled":
+            out = va.verify_attn_scaled(q, *self.cache, *self.scales, self.bt, cu, used, max(news), mk, self.scale)
+        else:
+            out = va.verify_attn(q, *self.cache, self.bt, cu, used, max(news), mk, self.scale, *self.descale)
+        self.check(out, q, qr, cu, used, news)
+
+    def check(self, out, q, qr, cu, used, news):
+        got = out.double().cpu().numpy()
+        # on the bytes of the cache, exactly what the attention promises
+        c = [np.nan_to_num(decode(x.cpu())) for x in self.cache]
+        if self.latent:
+            c[1] = c[0][..., :512]
+        s = [x.cpu().numpy() if x is not None else np.full((self.pages, c[0].shape[2]), 1.0 if d is None else float(d))
+             for x, d in zip(self.scales, self.descale)]
+        if self.latent:
+            s[1] = s[0]
+        ref, tol = page_scaled_oracle(decode(q.cpu()), c[0], c[1], s[0], s[1], self.bt.cpu().numpy(), cu.cpu().numpy(), used.cpu().numpy(), self.scale)
+        assert (np.abs(got - ref) <= tol).all()
+        check_gates(got, ref)
+        # and near the attention of what was fed: bf16 keys and values within
+        # 2^-8, e4m3 ones within 2^-4 of each, so the weighted sums within a
+        # few times that of the rows' own size
+        G = self.hq // self.hkv
+        num = den = 0.0
+        for b in range(self.B):
+            K = np.stack([x[0] for x in self.fed[b]])
+            V = np.stack([x[1] for x in self.fed[b]])
+            a, z = int(cu[b]), int(cu[b + 1])
+            vis = np.arange(z - a) + self.len[b] - (z - a) + 1
+            for h in range(self.hq):
+                want = softmax_attend(qr[a:z, h].numpy(), K[:, h // G], V[:, h // G], vis, self.scale)
+                num += ((got[a:z, h] - want) ** 2).sum()
+                den += (want ** 2).sum()
+        assert np.sqrt(num / den) <= (2.0 ** -6 if self.kind == "bf16" else 2.0 ** -2)
+
+    def take_back(self, counts):
+        for b, n in enumerate(counts):
+            self.len[b] -= n
+            del self.fed[b][len(self.fed[b]) - n:]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "scaled"])
+@pytest.mark.parametrize("latent", [False, True])
+def test_prompt_then_verify_steps(kind, latent):
+    d = Decoder(kind, latent, 8, 1 if latent else 2, 600)
+    d.step([37, 100, 5], False)                    # prompts in two chunks, the second mid-page
+    d.step([20, 1, 60], False)
+    for k in range(6):
+        d.step([4, 2 + k % 3, 1 + k % 4], True)
+        d.take_back([k % 4, (k + 1) % 2, 0])       # refused drafts
