@@ -9,15 +9,15 @@ CPU fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
-import threading
 from typing import Optional
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libverify_attn.so")
+BINDING_PATH = os.path.join(_PKG, "_lib", "va_binding.so")
 
 VA_BF16, VA_FP8_E4M3, VA_INT32, VA_FP32 = 0, 1, 2, 3
 VA_OK = 0
@@ -62,6 +62,11 @@ class VaPlan(ctypes.Structure):
 class VaOptions(ctypes.Structure):
     _fields_ = [("window_left", ctypes.c_int32), ("softcap", ctypes.c_float),
                 ("sinks", ctypes.POINTER(VaTensor))]
+
+
+class VaRope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.POINTER(VaTensor)), ("positions", ctypes.POINTER(VaTensor)),
+                ("interleaved", ctypes.c_int32)]
 
 
 class VerifyAttnError(RuntimeError):
@@ -121,16 +126,17 @@ def _lib():
         lib.verify_attn_last_device_error.restype = ctypes.c_int32
         lib.verify_attn_set_wait_limit.argtypes = [ctypes.c_uint64]
         lib.verify_attn_set_wait_limit.restype = ctypes.c_int32
-        V = ctypes.c_void_p   # descriptors packed by _pack, passed by address
-        lib.verify_attn_append_kv.argtypes = [V] * 15
+        R, V = ctypes.POINTER(VaRope), ctypes.c_void_p
+        lib.verify_attn_append_kv.argtypes = [P] * 6 + [R] + [P] * 7 + [V]
         lib.verify_attn_append_kv.restype = ctypes.c_int32
-        lib.verify_attn_append_mla.argtypes = [V] * 12
+        lib.verify_attn_append_mla.argtypes = [P] * 6 + [R] + [P] * 4 + [V]
         lib.verify_attn_append_mla.restype = ctypes.c_int32
-        lib.verify_attn_scaled.argtypes = [V] * 8 + [ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
-                                                     V, V, V, ctypes.c_size_t, ctypes.c_int32, V, V]
+        lib.verify_attn_scaled.argtypes = [P] * 8 + [ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                                                     P, ctypes.POINTER(VaOptions), V,
+                                                     ctypes.c_size_t, ctypes.c_int32, V, V]
         lib.verify_attn_scaled.restype = ctypes.c_int32
-        lib.verify_attn_mla_scaled.argtypes = [V] * 6 + [ctypes.c_int32, ctypes.c_int32,
-                                                         ctypes.c_float, V, V, ctypes.c_size_t,
+        lib.verify_attn_mla_scaled.argtypes = [P] * 6 + [ctypes.c_int32, ctypes.c_int32,
+                                                         ctypes.c_float, P, V, ctypes.c_size_t,
                                                          ctypes.c_int32, V, V]
         lib.verify_attn_mla_scaled.restype = ctypes.c_int32
         lib.verify_attn_status_string.argtypes = [ctypes.c_int32]
@@ -166,108 +172,27 @@ def _ref(d):
     return None if d is None else ctypes.byref(d)
 
 
-_DESC = struct.Struct("@Pii8q")     # one va_tensor
-_ROPE = struct.Struct("@PPi4x")     # one va_rope
-_OPTIONS = struct.Struct("@ifP")    # one va_options
-_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
-_MAX_DESCS = 16
+_NATIVE = None
 
 
-class _Packed(threading.local):
-    """This thread's descriptors of the call being made: ``_MAX_DESCS``
-    va_tensor and a va_rope behind them. Packing into one buffer costs a
-    fraction of a ctypes structure per tensor, which is what a small call's
-    time goes into."""
-
-    def __init__(self):
-        self.buf = ctypes.create_string_buffer(_DESC.size * _MAX_DESCS + _ROPE.size)
-        self.base = ctypes.addressof(self.buf)
-
-
-_packed = _Packed()
-assert _DESC.size == ctypes.sizeof(VaTensor)
-
-
-def _pack(*tensors):
-    """Addresses of the descriptors of ``tensors`` (None -> NULL), valid until
-    this thread's next call of it."""
-    buf, base, off, out = _packed.buf, _packed.base, 0, []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        code = _DTYPES.get(t.dtype)
-        if code is None:
-            raise TypeError(f"unsupported dtype {t.dtype}")
-        shape = t.shape
-        n = len(shape)
-        if n > 4:
-            raise ValueError("at most 4 dimensions")
-        pad = _PAD[n]
-        _DESC.pack_into(buf, off, t.data_ptr(), code, n, *shape, *pad, *t.stride(), *pad)
-        out.append(base + off)
-        off += _DESC.size
-    return out
+def _native():
+    """The compiled half of the binding (csrc/va_binding.cpp)."""
+    global _NATIVE
+    if _NATIVE is None:
+        _lib()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"native binding not built: {BINDING_PATH} is missing "
+                               "(run `python -c 'import __graft_entry__ as g; g.build()'`)")
+        spec = importlib.util.spec_from_file_location("va_binding", BINDING_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _NATIVE = mod
+    return _NATIVE
 
 
-def _pack_rope(cos_sin, positions, interleaved):
-    """Address of a va_rope over descriptors packed by _pack (None: no rotation)."""
-    if cos_sin is None:
-        if positions is not None:
-            raise ValueError("positions without cos_sin")
-        return None
-    off = _DESC.size * _MAX_DESCS
-    _ROPE.pack_into(_packed.buf, off, cos_sin, positions or 0, int(interleaved))
-    return _packed.base + off
-
-
-def _pack_options(window_left, softcap, sinks):
-    """Address of a va_options over a descriptor packed by _pack (None: all off)."""
-    if window_left == -1 and not softcap and sinks is None:
-        return None
-    off = _DESC.size * _MAX_DESCS
-    _OPTIONS.pack_into(_packed.buf, off, int(window_left), float(softcap), sinks or 0)
-    return _packed.base + off
-
-
-def _call_workspace(workspace, nbytes, device, stream):
-    """(tensor, aligned address, bytes) of a call's workspace. Without one it is
-    allocated with torch for this call alone, on the call's stream, so that
-    calls on different streams, or captured into different graphs, share none."""
-    if workspace is None:
-        if stream is None:
-            workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
-        else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
-    a = workspace.data_ptr()
-    off = (-a) % 256
-    return workspace, a + off, workspace.numel() * workspace.element_size() - off
-
-
-def _on_device(fn, device, *args):
-    """fn(*args) with ``device`` current."""
-    if device.type != "cuda" or torch.cuda.current_device() == device.index:
-        return fn(*args)
-    with torch.cuda.device(device):
-        return fn(*args)
-
-
-def _call(fn, where, device, stream, *args):
-    """fn(*args, stream) with ``device`` current; raises on an error status."""
-    if device.type != "cuda":
-        raise ValueError(f"{where}: tensors must be on a CUDA device, not {device}")
-    s = _on_device(fn, device, *args, _stream_handle(stream, device))
-    if s != VA_OK:
-        raise VerifyAttnError(s, where)
-
-
-def _same_device(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on different devices: {device} and {t.device}")
+def _handle(stream):
+    """A stream argument of the compiled binding (None: the current one)."""
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
 def _stream_handle(stream, device) -> int:
@@ -627,13 +552,11 @@ def append_kv(k, v, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, q=No
     ``q_out`` (created if q is given without it; it may be q itself), or None."""
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _same_device(k.device, v, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, q, q_out,
-                 cos_sin, positions, k_descale, v_descale, k_scales, v_scales)
-    r = _pack(q, k, v, block_table, cu_seqlens_q, seqused_k, k_descale, v_descale, k_scales,
-              v_scales, q_out, k_cache, v_cache, cos_sin, positions)
-    rope = _pack_rope(r[13], r[14], interleaved)
-    _call(_lib().verify_attn_append_kv, "verify_attn_append_kv", k.device, stream, *r[:6], rope,
-          *r[6:13])
+    s = _native().append_kv(q, k, v, block_table, cu_seqlens_q, seqused_k, k_descale, v_descale,
+                            k_scales, v_scales, q_out, k_cache, v_cache, cos_sin, positions,
+                            interleaved, _handle(stream))
+    if s != VA_OK:
+        raise VerifyAttnError(s, "verify_attn_append_kv")
     return q_out
 
 
@@ -647,13 +570,11 @@ def append_mla(latent, k_pe, kv_cache, block_table, cu_seqlens_q, seqused_k, q_p
     ``q_pe_out``, or None."""
     if q_pe is not None and q_pe_out is None:
         q_pe_out = torch.empty(q_pe.shape, dtype=q_pe.dtype, device=q_pe.device)
-    _same_device(latent.device, k_pe, kv_cache, block_table, cu_seqlens_q, seqused_k, q_pe,
-                 q_pe_out, cos_sin, positions, descale, scales)
-    r = _pack(q_pe, latent, k_pe, block_table, cu_seqlens_q, seqused_k, descale, scales, q_pe_out,
-              kv_cache, cos_sin, positions)
-    rope = _pack_rope(r[10], r[11], interleaved)
-    _call(_lib().verify_attn_append_mla, "verify_attn_append_mla", latent.device, stream, *r[:6],
-          rope, *r[6:10])
+    s = _native().append_mla(q_pe, latent, k_pe, block_table, cu_seqlens_q, seqused_k, descale,
+                             scales, q_pe_out, kv_cache, cos_sin, positions, interleaved,
+                             _handle(stream))
+    if s != VA_OK:
+        raise VerifyAttnError(s, "verify_attn_append_mla")
     return q_pe_out
 
 
@@ -669,19 +590,12 @@ def verify_attn_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_
     read) None: one of the call's own, from torch's allocator."""
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _same_device(q.device, k_cache, v_cache, k_scales, v_scales, block_table, cu_seqlens_q,
-                 seqused_k, out, sinks, workspace)
-    n = 0      # where the arguments have no plan, the call says why
-    if workspace is None and q.dim() == 3 and k_cache.dim() == 4 and seqused_k.dim() == 1:
-        n = _on_device(_lib().verify_attn_workspace_size, q.device, seqused_k.shape[0],
-                       k_cache.shape[2], q.shape[1], int(max_seqlen_q), int(max_seqlen_k),
-                       VA_FP8_E4M3, int(num_splits))
-    keep, addr, nbytes = _call_workspace(workspace, n, q.device, stream)
-    r = _pack(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_seqlens_q, seqused_k, out, sinks)
-    _call(_lib().verify_attn_scaled, "verify_attn_scaled", q.device, stream, *r[:8],
-          int(max_seqlen_q), int(max_seqlen_k), float(softmax_scale), r[8],
-          _pack_options(window_left, softcap, r[9]), addr, nbytes, int(num_splits),
-          _event_handle(event_after_main))
+    s = _native().attn_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_seqlens_q,
+                              seqused_k, out, sinks, max_seqlen_q, max_seqlen_k, softmax_scale,
+                              window_left, softcap, workspace, num_splits,
+                              _event_handle(event_after_main), _handle(stream))
+    if s != VA_OK:
+        raise VerifyAttnError(s, "verify_attn_scaled")
     return out
 
 
@@ -694,14 +608,9 @@ def verify_attn_mla_scaled(q, kv_cache, scales, block_table, cu_seqlens_q, sequs
     writes them. ``workspace`` as for ``verify_attn_scaled``."""
     if out is None:
         out = torch.empty(q.shape[0], q.shape[1], MLA_NOPE, dtype=torch.bfloat16, device=q.device)
-    _same_device(q.device, kv_cache, scales, block_table, cu_seqlens_q, seqused_k, out, workspace)
-    n = 0
-    if workspace is None and q.dim() == 3 and seqused_k.dim() == 1:
-        n = _on_device(_lib().verify_attn_mla_workspace_size, q.device, seqused_k.shape[0],
-                       q.shape[1], int(max_seqlen_q), int(max_seqlen_k), int(num_splits))
-    keep, addr, nbytes = _call_workspace(workspace, n, q.device, stream)
-    r = _pack(q, kv_cache, scales, block_table, cu_seqlens_q, seqused_k, out)
-    _call(_lib().verify_attn_mla_scaled, "verify_attn_mla_scaled", q.device, stream, *r[:6],
-          int(max_seqlen_q), int(max_seqlen_k), float(softmax_scale), r[6], addr, nbytes,
-          int(num_splits), _event_handle(event_after_main))
+    s = _native().attn_mla_scaled(q, kv_cache, scales, block_table, cu_seqlens_q, seqused_k, out,
+                                  max_seqlen_q, max_seqlen_k, softmax_scale, workspace, num_splits,
+                                  _event_handle(event_after_main), _handle(stream))
+    if s != VA_OK:
+        raise VerifyAttnError(s, "verify_attn_mla_scaled")
     return out

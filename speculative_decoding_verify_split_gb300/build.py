@@ -1,4 +1,5 @@
-"""Builds the C-ABI library ``_lib/libverify_attn.so`` in-tree with nvcc.
+"""Builds the C-ABI library ``_lib/libverify_attn.so`` in-tree with nvcc, and the
+Python extension ``_lib/va_binding.so`` over it with the host compiler.
 
 Every translation unit is compiled for sm_103a only, in parallel, then linked
 into one shared object with the CUDA runtime linked statically (so the
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libverify_attn.so")
+BINDING = os.path.join(LIBDIR, "va_binding.so")
+BINDING_SOURCE = "va_binding.cpp"
 
 SOURCES = ["va_host.cpp", "va_host_append.cpp", "va_main_tc.cu", "va_mla_tc.cu", "va_mla_bf16_tc.cu", "va_merge.cu",
            "va_noalloc.cu", "va_pagetable.cu", "va_append.cu"]
@@ -52,10 +56,45 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_binding(verbose: bool) -> str:
+    """The extension's object: the torch headers of the running interpreter."""
+    import torch
+
+    tdir = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD, BINDING_SOURCE + ".o")
+    cxx = shutil.which("g++") or "g++"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(tdir, "include"), "-isystem",
+           os.path.join(tdir, "include", "torch", "csrc", "api", "include"), "-isystem", cuda, "-isystem", sysconfig.get_paths()["include"],
+           "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    if verbose and res.stderr:
+        sys.stderr.write(res.stderr)
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    """Links the extension against the library beside it and the torch libraries
+    that the interpreter has loaded."""
+    import torch
+
+    tlib = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-shared", obj, "-o", tmp, "-L", LIBDIR, "-lverify_attn", "-L", tlib, "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(ROOT, "include", "verify_attn.h"))
     deps.append(os.path.abspath(__file__))
@@ -67,14 +106,17 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        binding_obj = binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-Xlinker", "--exclude-libs,ALL", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 

@@ -2,6 +2,8 @@
 comparison, with tolerances from the number formats."""
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import torch
 
@@ -16,6 +18,18 @@ from oracle.attention_fp64 import decode_bf16, decode_e4m3fn
 # 4 * 2^-24 of |x1| + |x2|.
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float8_e4m3fn: 2.0 ** -4}
 FP32 = 4 * 2.0 ** -24
+
+
+def descriptors(*tensors):
+    """Arguments of the C calls: pointers to va_tensor, None for none."""
+    return [None if t is None else ctypes.pointer(va.desc(t)) for t in tensors]
+
+
+def rope_of(cos_sin, positions=None, interleaved=0):
+    if cos_sin is None:
+        return None
+    c, p = descriptors(cos_sin, positions)
+    return ctypes.pointer(va.VaRope(c, p, interleaved))
 
 
 def raw(t):

@@ -9,7 +9,7 @@ import torch
 
 import speculative_decoding_verify_split_gb300 as va
 from oracle.append_fp64 import append_oracle, page_scale, rotated, usable
-from append_util import table
+from append_util import descriptors, rope_of, table
 
 NULL, SHAPE, DTYPE, UNSUPPORTED, LAYOUT = 1, 2, 3, 4, 7
 
@@ -33,10 +33,8 @@ def kv_args(**kw):
 
 def call_kv(**kw):
     a = kv_args(**kw)
-    r = va._pack(a["q"], a["k"], a["v"], a["bt"], a["cu"], a["su"], a["kd"], a["vd"], a["ks"], a["vs"], a["q_out"], a["kc"],
-                 a["vc"], a["cos_sin"], a["positions"])
-    rope = va._pack_rope(r[13], r[14], a["interleaved"])
-    return va.library().verify_attn_append_kv(*r[:6], rope, *r[6:13], None)
+    r = descriptors(a["q"], a["k"], a["v"], a["bt"], a["cu"], a["su"], a["kd"], a["vd"], a["ks"], a["vs"], a["q_out"], a["kc"], a["vc"])
+    return va.library().verify_attn_append_kv(*r[:6], rope_of(a["cos_sin"], a["positions"], a["interleaved"]), *r[6:], None)
 
 
 def call_mla(**kw):
@@ -46,10 +44,8 @@ def call_mla(**kw):
              cos_sin=torch.zeros(64, 64), positions=None, interleaved=0, descale=None, scales=None,
              q_out=torch.zeros(5, 4, 64, dtype=torch.bfloat16), kc=torch.zeros(8, 16, 1, 576, dtype=torch.bfloat16))
     a.update(kw)
-    r = va._pack(a["q"], a["latent"], a["k_pe"], a["bt"], a["cu"], a["su"], a["descale"], a["scales"], a["q_out"], a["kc"],
-                 a["cos_sin"], a["positions"])
-    rope = va._pack_rope(r[10], r[11], a["interleaved"])
-    return va.library().verify_attn_append_mla(*r[:6], rope, *r[6:10], None)
+    r = descriptors(a["q"], a["latent"], a["k_pe"], a["bt"], a["cu"], a["su"], a["descale"], a["scales"], a["q_out"], a["kc"])
+    return va.library().verify_attn_append_mla(*r[:6], rope_of(a["cos_sin"], a["positions"], a["interleaved"]), *r[6:], None)
 
 
 BF, F8 = torch.bfloat16, torch.float8_e4m3fn

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import speculative_decoding_verify_split_gb300 as va
-from append_util import decode
+from append_util import decode, descriptors
 from oracle.page_scaled_fp64 import page_scaled_oracle
 from parity_gate import check_gates
 from speculative_decoding_verify_split_gb300.workloads import make_mla_workload, make_workload
@@ -294,9 +294,9 @@ def test_capture_without_a_workspace_is_refused_by_the_library():
     codes = []
 
     def calls(stream):
-        r = va._pack(w.q, w.k_cache, w.v_cache, ks, vs, w.block_table, w.cu_seqlens_q, w.seqused_k, out)
+        r = descriptors(w.q, w.k_cache, w.v_cache, ks, vs, w.block_table, w.cu_seqlens_q, w.seqused_k, out)
         codes.append(va.library().verify_attn_scaled(*r[:8], 2, w.max_seqlen_k, 0.1, r[8], None, None, 0, 0, None, stream))
-        r = va._pack(m.q, m.kv_cache, ms, m.block_table, m.cu_seqlens_q, m.seqused_k, mout)
+        r = descriptors(m.q, m.kv_cache, ms, m.block_table, m.cu_seqlens_q, m.seqused_k, mout)
         codes.append(va.library().verify_attn_mla_scaled(*r[:6], 2, m.max_seqlen_k, 0.1, r[6], None, 0, 0, None, stream))
 
     calls(torch.cuda.current_stream().cuda_stream)

@@ -1,11 +1,13 @@
 """The page-scaled attention's oracle pinned to the plain ones, and the host
 checks of verify_attn_scaled and verify_attn_mla_scaled (no GPU)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import speculative_decoding_verify_split_gb300 as va
-from append_util import decode
+from append_util import decode, descriptors
 from oracle.attention_fp64 import oracle_from_torch
 from oracle.mla_fp64 import mla_oracle_from_torch
 from oracle.page_scaled_fp64 import page_scaled_oracle, read_scales
@@ -84,9 +86,9 @@ def args(**kw):
 
 def call(**kw):
     a = args(**kw)
-    r = va._pack(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["cu"], a["su"], a["out"], a["sinks"])
-    return va.library().verify_attn_scaled(*r[:8], a["mq"], a["mk"], 0.1, r[8], va._pack_options(a["win"], a["cap"], r[9]), a["ws"], a["n"],
-                                           a["splits"], None, None)
+    r = descriptors(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["cu"], a["su"], a["out"], a["sinks"])
+    opts = ctypes.pointer(va.VaOptions(a["win"], a["cap"], r[9]))
+    return va.library().verify_attn_scaled(*r[:8], a["mq"], a["mk"], 0.1, r[8], opts, a["ws"], a["n"], a["splits"], None, None)
 
 
 BAD = [
@@ -113,7 +115,7 @@ def call_mla(**kw):
              bt=torch.zeros(2, 3, dtype=torch.int32), cu=torch.tensor([0, 2, 5], dtype=torch.int32),
              su=torch.tensor([4, 9], dtype=torch.int32), mq=3, mk=48, out=torch.zeros(5, 4, 512, dtype=BF), splits=0)
     a.update(kw)
-    r = va._pack(a["q"], a["kc"], a["s"], a["bt"], a["cu"], a["su"], a["out"])
+    r = descriptors(a["q"], a["kc"], a["s"], a["bt"], a["cu"], a["su"], a["out"])
     return va.library().verify_attn_mla_scaled(*r[:6], a["mq"], a["mk"], 0.1, r[6], None, 0, a["splits"], None, None)
 
 
