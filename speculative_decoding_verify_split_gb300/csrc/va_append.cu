@@ -151,17 +151,42 @@ __device__ __forceinline__ uint2 to_bf16x4(const float* x) {
   return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
 }
 
-__device__ __forceinline__ uint32_t to_e4m3x4(const float* x, float scale) {
-  const uint32_t lo = pack_fp8x2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale));
-  const uint32_t hi = pack_fp8x2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale));
-  return lo | (hi << 16);
+// x / scale. By a power of two in [2^-64, 2^64] the quotient is the product
+// with the (exact) reciprocal.
+struct Divisor {
+  float scale, inv;
+  bool power;
+  __device__ __forceinline__ explicit Divisor(float s) : scale(s) {
+    const uint32_t b = __float_as_uint(s);
+    power = (b & 0x807FFFFFu) == 0 && b >= (63u << 23) && b <= (191u << 23);
+    inv = __uint_as_float((254u << 23) - b);  // 2^-e of 2^e
+  }
+  __device__ __forceinline__ void divide8(float* x) const {
+    if (power) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], inv);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], scale);
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(const float* x) {
+  return pack_fp8x2(x[0], x[1]) | (pack_fp8x2(x[2], x[3]) << 16);
 }
 
-// Four codes under scale `had` as codes under scale `now`.
-__device__ __forceinline__ uint32_t rescale4(uint32_t w, float had, float now) {
-  const float2 a = unpack_fp8x2(w & 0xFFFFu), b = unpack_fp8x2(w >> 16);
-  const float x[4] = {__fmul_rn(a.x, had), __fmul_rn(a.y, had), __fmul_rn(b.x, had), __fmul_rn(b.y, had)};
-  return to_e4m3x4(x, now);
+// Eight codes under scale `had` as codes under scale `now`.
+__device__ __forceinline__ uint2 rescale8(uint2 w, float had, const Divisor& now) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_fp8x2((i < 2 ? w.x : w.y) >> (16 * (i & 1)) & 0xFFFFu);
+    x[2 * i] = __fmul_rn(f.x, had);
+    x[2 * i + 1] = __fmul_rn(f.y, had);
+  }
+  now.divide8(x);
+  return make_uint2(pack_e4m3x4(x), pack_e4m3x4(x + 4));
 }
 
 // A page scale as it is read: finite and positive.
@@ -201,23 +226,39 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
   if ((int)blockIdx.y >= p.hkv) {  // ---- query heads
     const int h0 = ((int)blockIdx.y - p.hkv) * kHeadsPerCta;
     const int nh = p.hq - h0 < kHeadsPerCta ? p.hq - h0 : kHeadsPerCta;
-    const int rows = (int)(u.hi - u.lo) * nh;
-    for (int r = warp; r < rows; r += kWarps) {
-      const int t = r / nh, h = h0 + r - t * nh;
+    const int quads = (nh + 3) / 4;
+    const int tasks = (int)(u.hi - u.lo) * quads;
+    for (int task = warp; task < tasks; task += kWarps) {  // four heads of a token, all their loads at once
+      const int t = task / quads, hb = h0 + 4 * (task - t * quads);
       const int tok = u.tok0 + t;
-      const uint16_t* src = p.q + (int64_t)tok * p.q_s0 + (int64_t)h * p.q_s1;
-      const uint2 w1 = *reinterpret_cast<const uint2*>(src + col.o1);
-      const uint2 w2 = *reinterpret_cast<const uint2*>(src + col.o2);
-      float x[8];
-      unpack4(w1, x);
-      unpack4(w2, x + 4);
+      const uint16_t* src = p.q + (int64_t)tok * p.q_s0;
+      uint2 w1[4], w2[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint16_t* row = src + (int64_t)(hb + i) * p.q_s1;
+        const bool on = hb + i < p.hq;
+        w1[i] = on ? *reinterpret_cast<const uint2*>(row + col.o1) : make_uint2(0, 0);
+        w2[i] = on ? *reinterpret_cast<const uint2*>(row + col.o2) : make_uint2(0, 0);
+      }
+      float4 c = make_float4(0.f, 0.f, 0.f, 0.f), sn = c;
       if (col.turn) {
         const float* cs = table_row(p, tok, u.lo + t) + 4 * lane;
-        rotate8<INTER>(x, *reinterpret_cast<const float4*>(cs), *reinterpret_cast<const float4*>(cs + p.rot / 2));
+        c = *reinterpret_cast<const float4*>(cs);
+        sn = *reinterpret_cast<const float4*>(cs + p.rot / 2);
       }
-      uint16_t* dst = p.q_out + (int64_t)tok * p.qo_s0 + (int64_t)h * p.qo_s1;
-      *reinterpret_cast<uint2*>(dst + col.o1) = to_bf16x4(x);
-      *reinterpret_cast<uint2*>(dst + col.o2) = to_bf16x4(x + 4);
+      uint16_t* out = p.q_out + (int64_t)tok * p.qo_s0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x[8];
+        unpack4(w1[i], x);
+        unpack4(w2[i], x + 4);
+        if (col.turn) rotate8<INTER>(x, c, sn);
+        if (hb + i < p.hq) {
+          uint16_t* dst = out + (int64_t)(hb + i) * p.qo_s1;
+          *reinterpret_cast<uint2*>(dst + col.o1) = to_bf16x4(x);
+          *reinterpret_cast<uint2*>(dst + col.o2) = to_bf16x4(x + 4);
+        }
+      }
     }
     return;
   }
@@ -236,20 +277,35 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
   const float* descale = is_k ? p.k_descale : p.v_descale;
   const int64_t base = (int64_t)page * c.s0 + (int64_t)h * c.s2;
 
+  // the four slots' loads go out together
+  uint2 w1[4], w2[4];
+  float4 cs[4], sn[4];
+  const bool turn = is_k && col.turn;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int s = w4 + 4 * k;
+    const bool on = s >= s_lo && s < s_hi;
+    const uint16_t* row = src + (int64_t)(u.tok0 + s - s_lo) * src_s0;
+    w1[k] = on ? *reinterpret_cast<const uint2*>(row + col.o1) : make_uint2(0, 0);
+    w2[k] = on ? *reinterpret_cast<const uint2*>(row + col.o2) : make_uint2(0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int s = w4 + 4 * k;
+    cs[k] = sn[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (turn && s >= s_lo && s < s_hi) {
+      const float* row = table_row(p, u.tok0 + s - s_lo, u.pg * kPageSize + s) + 4 * lane;
+      cs[k] = *reinterpret_cast<const float4*>(row);
+      sn[k] = *reinterpret_cast<const float4*>(row + p.rot / 2);
+    }
+  }
   float x[4][8];
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int s = w4 + 4 * k;
-    if (s < s_lo || s >= s_hi) continue;  // warp-uniform
-    const int tok = u.tok0 + s - s_lo;
-    const uint16_t* row = src + (int64_t)tok * src_s0;
-    unpack4(*reinterpret_cast<const uint2*>(row + col.o1), x[k]);
-    unpack4(*reinterpret_cast<const uint2*>(row + col.o2), x[k] + 4);
-    if (is_k && col.turn) {
-      const float* cs = table_row(p, tok, u.pg * kPageSize + s) + 4 * lane;
-      rotate8<INTER>(x[k], *reinterpret_cast<const float4*>(cs), *reinterpret_cast<const float4*>(cs + p.rot / 2));
-    }
+    unpack4(w1[k], x[k]);
+    unpack4(w2[k], x[k] + 4);
+    if (turn) rotate8<INTER>(x[k], cs[k], sn[k]);
     if (KIND == kPageScaled) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[k][i]));  // NaN counts as 0
@@ -277,9 +333,9 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
           if (s >= s_lo) continue;
           uint32_t* d1 = reinterpret_cast<uint32_t*>(dst + (int64_t)s * c.s1 + col.o1);
           uint32_t* d2 = reinterpret_cast<uint32_t*>(dst + (int64_t)s * c.s1 + col.o2);
-          const uint32_t a = *d1, b = *d2;
-          *d1 = rescale4(a, had, scale);
-          *d2 = rescale4(b, had, scale);
+          const uint2 now = rescale8(make_uint2(*d1, *d2), had, Divisor(scale));
+          *d1 = now.x;
+          *d2 = now.y;
         }
       }
     }
@@ -288,22 +344,20 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
     divide = descale != nullptr;
     if (divide) scale = *descale;
   }
+  const Divisor by(scale);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int s = w4 + 4 * k;
     if (s < s_lo || s >= s_hi) continue;
+    if (KIND == kPageScaled || divide) by.divide8(x[k]);
     if (KIND == kBf16) {
-      if (divide) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[k][i] = __fdiv_rn(x[k][i], scale);
-      }
       uint16_t* dst = static_cast<uint16_t*>(c.data) + base + (int64_t)s * c.s1;
       *reinterpret_cast<uint2*>(dst + col.o1) = to_bf16x4(x[k]);
       *reinterpret_cast<uint2*>(dst + col.o2) = to_bf16x4(x[k] + 4);
     } else {
       unsigned char* dst = static_cast<unsigned char*>(c.data) + base + (int64_t)s * c.s1;
-      *reinterpret_cast<uint32_t*>(dst + col.o1) = to_e4m3x4(x[k], scale);
-      *reinterpret_cast<uint32_t*>(dst + col.o2) = to_e4m3x4(x[k] + 4, scale);
+      *reinterpret_cast<uint32_t*>(dst + col.o1) = pack_e4m3x4(x[k]);
+      *reinterpret_cast<uint32_t*>(dst + col.o2) = pack_e4m3x4(x[k] + 4);
     }
   }
 }
@@ -355,26 +409,36 @@ __global__ void __launch_bounds__(kThreads) va_append_mla_kernel(const AppendPar
   const int n1 = 8 * lane, n2 = 256 + 8 * lane;
   const int r1 = INTER ? 2 * lane : lane, r2 = INTER ? r1 + 1 : lane + 32;
 
-  float x[2][16], y[2][2];
+  // both slots' loads go out together
+  uint4 wa[2], wb[2];
+  float x[2][16], y[2][2], cs[2], sn[2];
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int s = warp + kWarps * k;
-    if (s < s_lo || s >= s_hi) continue;  // warp-uniform
+    const bool on = s >= s_lo && s < s_hi;
     const int tok = u.tok0 + s - s_lo;
     const uint16_t* lat = p.k + (int64_t)tok * p.k_s0;
     const uint16_t* pe = p.v + (int64_t)tok * p.v_s0;
-    const uint4 a = *reinterpret_cast<const uint4*>(lat + n1), b = *reinterpret_cast<const uint4*>(lat + n2);
-    unpack4(make_uint2(a.x, a.y), x[k]);
-    unpack4(make_uint2(a.z, a.w), x[k] + 4);
-    unpack4(make_uint2(b.x, b.y), x[k] + 8);
-    unpack4(make_uint2(b.z, b.w), x[k] + 12);
-    y[k][0] = bf16_bits_to_float(pe[r1]);
-    y[k][1] = bf16_bits_to_float(pe[r2]);
-    if (p.cos_sin) {
-      const float* cs = table_row(p, tok, u.pg * kPageSize + s) + lane;
-      rotate(y[k][0], y[k][1], cs[0], cs[kMlaPe / 2]);
+    wa[k] = on ? *reinterpret_cast<const uint4*>(lat + n1) : make_uint4(0, 0, 0, 0);
+    wb[k] = on ? *reinterpret_cast<const uint4*>(lat + n2) : make_uint4(0, 0, 0, 0);
+    y[k][0] = on ? bf16_bits_to_float(pe[r1]) : 0.f;
+    y[k][1] = on ? bf16_bits_to_float(pe[r2]) : 0.f;
+    cs[k] = 1.f;
+    sn[k] = 0.f;
+    if (on && p.cos_sin) {
+      const float* row = table_row(p, tok, u.pg * kPageSize + s) + lane;
+      cs[k] = row[0];
+      sn[k] = row[kMlaPe / 2];
     }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    unpack4(make_uint2(wa[k].x, wa[k].y), x[k]);
+    unpack4(make_uint2(wa[k].z, wa[k].w), x[k] + 4);
+    unpack4(make_uint2(wb[k].x, wb[k].y), x[k] + 8);
+    unpack4(make_uint2(wb[k].z, wb[k].w), x[k] + 12);
+    if (p.cos_sin) rotate(y[k][0], y[k][1], cs[k], sn[k]);
     if (KIND == kPageScaled) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[k][i]));  // NaN counts as 0
@@ -402,13 +466,13 @@ __global__ void __launch_bounds__(kThreads) va_append_mla_kernel(const AppendPar
           const int s = warp + kWarps * k;
           if (s >= s_lo) continue;
           unsigned char* row = dst + (int64_t)s * c.s1;
-          uint2 a = *reinterpret_cast<uint2*>(row + n1), b = *reinterpret_cast<uint2*>(row + n2);
+          const Divisor now(scale);
           const uint32_t e = (uint32_t)row[kMlaNope + r1] | ((uint32_t)row[kMlaNope + r2] << 8);
-          a = make_uint2(rescale4(a.x, had, scale), rescale4(a.y, had, scale));
-          b = make_uint2(rescale4(b.x, had, scale), rescale4(b.y, had, scale));
+          const uint2 a = rescale8(*reinterpret_cast<uint2*>(row + n1), had, now);
+          const uint2 b = rescale8(*reinterpret_cast<uint2*>(row + n2), had, now);
+          const uint32_t f = rescale8(make_uint2(e, 0), had, now).x;
           *reinterpret_cast<uint2*>(row + n1) = a;
           *reinterpret_cast<uint2*>(row + n2) = b;
-          const uint32_t f = rescale4(e, had, scale);
           row[kMlaNope + r1] = (unsigned char)f;
           row[kMlaNope + r2] = (unsigned char)(f >> 8);
         }
@@ -419,17 +483,18 @@ __global__ void __launch_bounds__(kThreads) va_append_mla_kernel(const AppendPar
     divide = p.k_descale != nullptr;
     if (divide) scale = *p.k_descale;
   }
+  const Divisor by(scale);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int s = warp + kWarps * k;
     if (s < s_lo || s >= s_hi) continue;
+    if (KIND == kPageScaled || divide) {
+      by.divide8(x[k]);
+      by.divide8(x[k] + 8);
+      y[k][0] = __fdiv_rn(y[k][0], scale);
+      y[k][1] = __fdiv_rn(y[k][1], scale);
+    }
     if (KIND == kBf16) {
-      if (divide) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[k][i] = __fdiv_rn(x[k][i], scale);
-        y[k][0] = __fdiv_rn(y[k][0], scale);
-        y[k][1] = __fdiv_rn(y[k][1], scale);
-      }
       uint16_t* dst = static_cast<uint16_t*>(c.data) + base + (int64_t)s * c.s1;
       const uint2 a = to_bf16x4(x[k]), b = to_bf16x4(x[k] + 4), d = to_bf16x4(x[k] + 8), e = to_bf16x4(x[k] + 12);
       *reinterpret_cast<uint4*>(dst + n1) = make_uint4(a.x, a.y, b.x, b.y);
@@ -438,9 +503,9 @@ __global__ void __launch_bounds__(kThreads) va_append_mla_kernel(const AppendPar
       dst[kMlaNope + r2] = float_to_bf16_bits(y[k][1]);
     } else {
       unsigned char* dst = static_cast<unsigned char*>(c.data) + base + (int64_t)s * c.s1;
-      *reinterpret_cast<uint2*>(dst + n1) = make_uint2(to_e4m3x4(x[k], scale), to_e4m3x4(x[k] + 4, scale));
-      *reinterpret_cast<uint2*>(dst + n2) = make_uint2(to_e4m3x4(x[k] + 8, scale), to_e4m3x4(x[k] + 12, scale));
-      const uint32_t f = pack_fp8x2(__fdiv_rn(y[k][0], scale), __fdiv_rn(y[k][1], scale));
+      *reinterpret_cast<uint2*>(dst + n1) = make_uint2(pack_e4m3x4(x[k]), pack_e4m3x4(x[k] + 4));
+      *reinterpret_cast<uint2*>(dst + n2) = make_uint2(pack_e4m3x4(x[k] + 8), pack_e4m3x4(x[k] + 12));
+      const uint32_t f = pack_fp8x2(y[k][0], y[k][1]);
       dst[kMlaNope + r1] = (unsigned char)f;
       dst[kMlaNope + r2] = (unsigned char)(f >> 8);
     }
