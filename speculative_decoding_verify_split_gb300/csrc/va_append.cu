@@ -380,21 +380,35 @@ __global__ void __launch_bounds__(kThreads) va_append_mla_kernel(const AppendPar
   if (blockIdx.y > 0) {  // ---- query heads
     const int h0 = ((int)blockIdx.y - 1) * kPeHeadsPerCta;
     const int nh = p.hq - h0 < kPeHeadsPerCta ? p.hq - h0 : kPeHeadsPerCta;
-    const int rows = (int)(u.hi - u.lo) * nh;
-    const int l8 = lane & 7;
+    const int l8 = lane & 7, g = lane >> 3;
     const int o1 = INTER ? 8 * l8 : 4 * l8, o2 = INTER ? o1 + 4 : 32 + o1;
-    for (int r = warp * 4 + (lane >> 3); r < rows; r += kWarps * 4) {
-      const int t = r / nh, h = h0 + r - t * nh;
+    for (int t = warp; t < (int)(u.hi - u.lo); t += kWarps) {  // a token's heads g, g + 4, .., all loads at once
       const int tok = u.tok0 + t;
-      const uint16_t* src = p.q + (int64_t)tok * p.q_s0 + (int64_t)h * p.q_s1;
-      float x[8];
-      unpack4(*reinterpret_cast<const uint2*>(src + o1), x);
-      unpack4(*reinterpret_cast<const uint2*>(src + o2), x + 4);
+      const uint16_t* src = p.q + (int64_t)tok * p.q_s0;
+      uint2 w1[kPeHeadsPerCta / 4], w2[kPeHeadsPerCta / 4];
+#pragma unroll
+      for (int i = 0; i < kPeHeadsPerCta / 4; ++i) {
+        const bool on = g + 4 * i < nh;
+        const uint16_t* row = src + (int64_t)(h0 + g + 4 * i) * p.q_s1;
+        w1[i] = on ? *reinterpret_cast<const uint2*>(row + o1) : make_uint2(0, 0);
+        w2[i] = on ? *reinterpret_cast<const uint2*>(row + o2) : make_uint2(0, 0);
+      }
       const float* cs = table_row(p, tok, u.lo + t) + 4 * l8;
-      rotate8<INTER>(x, *reinterpret_cast<const float4*>(cs), *reinterpret_cast<const float4*>(cs + kMlaPe / 2));
-      uint16_t* dst = p.q_out + (int64_t)tok * p.qo_s0 + (int64_t)h * p.qo_s1;
-      *reinterpret_cast<uint2*>(dst + o1) = to_bf16x4(x);
-      *reinterpret_cast<uint2*>(dst + o2) = to_bf16x4(x + 4);
+      const float4 c = *reinterpret_cast<const float4*>(cs);
+      const float4 sn = *reinterpret_cast<const float4*>(cs + kMlaPe / 2);
+      uint16_t* out = p.q_out + (int64_t)tok * p.qo_s0;
+#pragma unroll
+      for (int i = 0; i < kPeHeadsPerCta / 4; ++i) {
+        float x[8];
+        unpack4(w1[i], x);
+        unpack4(w2[i], x + 4);
+        rotate8<INTER>(x, c, sn);
+        if (g + 4 * i < nh) {
+          uint16_t* dst = out + (int64_t)(h0 + g + 4 * i) * p.qo_s1;
+          *reinterpret_cast<uint2*>(dst + o1) = to_bf16x4(x);
+          *reinterpret_cast<uint2*>(dst + o2) = to_bf16x4(x + 4);
+        }
+      }
     }
     return;
   }
