@@ -29,9 +29,9 @@
 namespace va {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kHeadsPerCta = 4;      // query heads of a page's tokens per CTA
+constexpr int kKvThreads = 128;      // GQA caches: K or V rows of a page and KV head, or query heads
+constexpr int kMlaThreads = 256;     // latent caches
+constexpr int kHeadsPerCta = 8;      // query heads of a page's tokens per CTA
 constexpr int kPeHeadsPerCta = 16;   // latent path: 64-wide query parts
 
 // How a cache holds its values.
@@ -49,13 +49,14 @@ struct UnitShared {
 };
 
 // The unit of this CTA, or false if there is none. Contains barriers.
+template <int NT>
 __device__ __forceinline__ bool find_unit(const AppendParams& p, UnitShared* sh, Unit* out) {
   if (threadIdx.x == 0) sh->b = -1;
   __syncthreads();
   // the previous kernel in the stream may write anything read below
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t u = blockIdx.x;
-  for (int b = threadIdx.x; b < p.num_seqs; b += kThreads) {
+  for (int b = threadIdx.x; b < p.num_seqs; b += NT) {
     const int a = p.cu_q[b], e = p.cu_q[b + 1], s = p.seqused_k[b];
     const int64_t g0 = (int64_t)(a / kPageSize) + 2 * (int64_t)b;
     const int64_t g1 = (int64_t)(e / kPageSize) + 2 * ((int64_t)b + 1);
@@ -202,6 +203,13 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+// The largest |value| of eight bf16 ones, in pairs; NaN loses against a number.
+__device__ __forceinline__ float amax8(uint4 w) {
+  auto pair = [](uint32_t v) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v)); };
+  const __nv_bfloat162 m = __hmax2(__hmax2(pair(w.x), pair(w.y)), __hmax2(pair(w.z), pair(w.w)));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -210,21 +218,22 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // ---- keys, values and queries of a GQA cache -----------------------------------
 //
-// blockIdx.y < hkv: the page's K rows (warps 0-3) and V rows (warps 4-7) of
-// one KV head, four slots of the page per warp. Above: the same tokens' rows
-// of kHeadsPerCta query heads, spread over the eight warps.
+// blockIdx.y < 2 hkv: the page's K rows (even) or V rows (odd) of one KV head,
+// four slots of the page per warp. Above: the same tokens' rows of
+// kHeadsPerCta query heads, four at a time, spread over the four warps.
 template <int KIND, bool INTER>
-__global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kKvThreads) va_append_kernel(const AppendParams p) {
+  constexpr int kWarps = kKvThreads / 32;
   __shared__ UnitShared sh;
   __shared__ float s_amax[kWarps];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Unit u;
-  if (!find_unit(p, &sh, &u)) return;  // CTA-uniform
+  if (!find_unit<kKvThreads>(p, &sh, &u)) return;  // CTA-uniform
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Lane col = lane_columns<INTER>(lane, p.rot);
 
-  if ((int)blockIdx.y >= p.hkv) {  // ---- query heads
-    const int h0 = ((int)blockIdx.y - p.hkv) * kHeadsPerCta;
+  if ((int)blockIdx.y >= 2 * p.hkv) {  // ---- query heads
+    const int h0 = ((int)blockIdx.y - 2 * p.hkv) * kHeadsPerCta;
     const int nh = p.hq - h0 < kHeadsPerCta ? p.hq - h0 : kHeadsPerCta;
     const int quads = (nh + 3) / 4;
     const int tasks = (int)(u.hi - u.lo) * quads;
@@ -263,13 +272,12 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
     return;
   }
 
-  // ---- one KV head of the page
-  const int h = (int)blockIdx.y;
+  // ---- K or V of one KV head of the page
+  const int h = (int)blockIdx.y >> 1;
   if (u.pg >= p.bt_width) return;
   const int page = p.block_table[(int64_t)u.b * p.bt_s0 + u.pg * p.bt_s1];
   if ((unsigned)page >= (unsigned)p.num_blocks) return;
-  const bool is_k = warp < kWarps / 2;
-  const int w4 = warp & 3;
+  const bool is_k = (blockIdx.y & 1) == 0;
   const int s_lo = (int)(u.lo - u.pg * kPageSize), s_hi = (int)(u.hi - u.pg * kPageSize);
   const uint16_t* src = (is_k ? p.k + (int64_t)h * p.k_s1 : p.v + (int64_t)h * p.v_s1);
   const int64_t src_s0 = is_k ? p.k_s0 : p.v_s0;
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
   const bool turn = is_k && col.turn;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int s = w4 + 4 * k;
+    const int s = warp + kWarps * k;
     const bool on = s >= s_lo && s < s_hi;
     const uint16_t* row = src + (int64_t)(u.tok0 + s - s_lo) * src_s0;
     w1[k] = on ? *reinterpret_cast<const uint2*>(row + col.o1) : make_uint2(0, 0);
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int s = w4 + 4 * k;
+    const int s = warp + kWarps * k;
     cs[k] = sn[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (turn && s >= s_lo && s < s_hi) {
       const float* row = table_row(p, u.tok0 + s - s_lo, u.pg * kPageSize + s) + 4 * lane;
@@ -317,8 +325,7 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
     amax = warp_max(amax);
     if (lane == 0) s_amax[warp] = amax;
     __syncthreads();
-    const int w0 = is_k ? 0 : 4;
-    amax = fmaxf(fmaxf(s_amax[w0], s_amax[w0 + 1]), fmaxf(s_amax[w0 + 2], s_amax[w0 + 3]));
+    amax = fmaxf(fmaxf(s_amax[0], s_amax[1]), fmaxf(s_amax[2], s_amax[3]));
     float* sp = c.scales + (int64_t)page * c.sc_s0 + (int64_t)h * c.sc_s1;
     scale = scale_for(amax);
     if (s_lo > 0) {  // the page's older tokens keep their scale, or are rounded to the larger one
@@ -329,7 +336,7 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
         unsigned char* dst = static_cast<unsigned char*>(c.data) + base;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int s = w4 + 4 * k;
+          const int s = warp + kWarps * k;
           if (s >= s_lo) continue;
           uint32_t* d1 = reinterpret_cast<uint32_t*>(dst + (int64_t)s * c.s1 + col.o1);
           uint32_t* d2 = reinterpret_cast<uint32_t*>(dst + (int64_t)s * c.s1 + col.o2);
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
         }
       }
     }
-    if (w4 == 0 && lane == 0) *sp = scale;
+    if (threadIdx.x == 0) *sp = scale;
   } else {
     divide = descale != nullptr;
     if (divide) scale = *descale;
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
   const Divisor by(scale);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int s = w4 + 4 * k;
+    const int s = warp + kWarps * k;
     if (s < s_lo || s >= s_hi) continue;
     if (KIND == kPageScaled || divide) by.divide8(x[k]);
     if (KIND == kBf16) {
@@ -369,12 +376,13 @@ __global__ void __launch_bounds__(kThreads) va_append_kernel(const AppendParams 
 // Above: the tokens' 64-wide rope parts of kPeHeadsPerCta query heads, eight
 // lanes a row.
 template <int KIND, bool INTER>
-__global__ void __launch_bounds__(kThreads) va_append_mla_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kMlaThreads, 4) va_append_mla_kernel(const AppendParams p) {
+  constexpr int kWarps = kMlaThreads / 32;
   __shared__ UnitShared sh;
   __shared__ float s_amax[kWarps];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Unit u;
-  if (!find_unit(p, &sh, &u)) return;  // CTA-uniform
+  if (!find_unit<kMlaThreads>(p, &sh, &u)) return;  // CTA-uniform
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (blockIdx.y > 0) {  // ---- query heads
@@ -425,7 +433,7 @@ __global__ void __launch_bounds__(kThreads) va_append_mla_kernel(const AppendPar
 
   // both slots' loads go out together
   uint4 wa[2], wb[2];
-  float x[2][16], y[2][2], cs[2], sn[2];
+  float y[2][2], cs[2], sn[2];
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -448,16 +456,9 @@ __global__ void __launch_bounds__(kThreads) va_append_mla_kernel(const AppendPar
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    unpack4(make_uint2(wa[k].x, wa[k].y), x[k]);
-    unpack4(make_uint2(wa[k].z, wa[k].w), x[k] + 4);
-    unpack4(make_uint2(wb[k].x, wb[k].y), x[k] + 8);
-    unpack4(make_uint2(wb[k].z, wb[k].w), x[k] + 12);
     if (p.cos_sin) rotate(y[k][0], y[k][1], cs[k], sn[k]);
-    if (KIND == kPageScaled) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[k][i]));  // NaN counts as 0
-      amax = fmaxf(amax, fmaxf(fabsf(y[k][0]), fabsf(y[k][1])));
-    }
+    if (KIND == kPageScaled)  // NaN counts as 0
+      amax = fmaxf(fmaxf(amax, fmaxf(amax8(wa[k]), amax8(wb[k]))), fmaxf(fabsf(y[k][0]), fabsf(y[k][1])));
   }
   float scale = 1.f;
   bool divide = false;
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kThreads) va_append_mla_kernel(const AppendPar
         }
       }
     }
-    if (warp == 0 && lane == 0) *sp = scale;
+    if (threadIdx.x == 0) *sp = scale;
   } else {
     divide = p.k_descale != nullptr;
     if (divide) scale = *p.k_descale;
@@ -502,23 +503,28 @@ __global__ void __launch_bounds__(kThreads) va_append_mla_kernel(const AppendPar
   for (int k = 0; k < 2; ++k) {
     const int s = warp + kWarps * k;
     if (s < s_lo || s >= s_hi) continue;
+    float x[16];
+    unpack4(make_uint2(wa[k].x, wa[k].y), x);
+    unpack4(make_uint2(wa[k].z, wa[k].w), x + 4);
+    unpack4(make_uint2(wb[k].x, wb[k].y), x + 8);
+    unpack4(make_uint2(wb[k].z, wb[k].w), x + 12);
     if (KIND == kPageScaled || divide) {
-      by.divide8(x[k]);
-      by.divide8(x[k] + 8);
-      y[k][0] = __fdiv_rn(y[k][0], scale);
-      y[k][1] = __fdiv_rn(y[k][1], scale);
+      by.divide8(x);
+      by.divide8(x + 8);
+      y[k][0] = by.power ? __fmul_rn(y[k][0], by.inv) : __fdiv_rn(y[k][0], scale);
+      y[k][1] = by.power ? __fmul_rn(y[k][1], by.inv) : __fdiv_rn(y[k][1], scale);
     }
     if (KIND == kBf16) {
       uint16_t* dst = static_cast<uint16_t*>(c.data) + base + (int64_t)s * c.s1;
-      const uint2 a = to_bf16x4(x[k]), b = to_bf16x4(x[k] + 4), d = to_bf16x4(x[k] + 8), e = to_bf16x4(x[k] + 12);
+      const uint2 a = to_bf16x4(x), b = to_bf16x4(x + 4), d = to_bf16x4(x + 8), e = to_bf16x4(x + 12);
       *reinterpret_cast<uint4*>(dst + n1) = make_uint4(a.x, a.y, b.x, b.y);
       *reinterpret_cast<uint4*>(dst + n2) = make_uint4(d.x, d.y, e.x, e.y);
       dst[kMlaNope + r1] = float_to_bf16_bits(y[k][0]);
       dst[kMlaNope + r2] = float_to_bf16_bits(y[k][1]);
     } else {
       unsigned char* dst = static_cast<unsigned char*>(c.data) + base + (int64_t)s * c.s1;
-      *reinterpret_cast<uint2*>(dst + n1) = make_uint2(pack_e4m3x4(x[k]), pack_e4m3x4(x[k] + 4));
-      *reinterpret_cast<uint2*>(dst + n2) = make_uint2(pack_e4m3x4(x[k] + 8), pack_e4m3x4(x[k] + 12));
+      *reinterpret_cast<uint2*>(dst + n1) = make_uint2(pack_e4m3x4(x), pack_e4m3x4(x + 4));
+      *reinterpret_cast<uint2*>(dst + n2) = make_uint2(pack_e4m3x4(x + 8), pack_e4m3x4(x + 12));
       const uint32_t f = pack_fp8x2(y[k][0], y[k][1]);
       dst[kMlaNope + r1] = (unsigned char)f;
       dst[kMlaNope + r2] = (unsigned char)(f >> 8);
@@ -538,7 +544,7 @@ KernelFn pick(bool mla, bool inter) {
 
 int append_roles(bool mla, int64_t hkv, int64_t hq, int64_t* roles) {
   const int64_t per = mla ? kPeHeadsPerCta : kHeadsPerCta;
-  *roles = (mla ? 1 : hkv) + (hq + per - 1) / per;
+  *roles = (mla ? 1 : 2 * hkv) + (hq + per - 1) / per;
   return *roles <= 65535;
 }
 
@@ -553,7 +559,7 @@ cudaError_t launch_append(const AppendParams& p, bool mla, cudaStream_t stream) 
   // attention kernels are: it touches memory only after that kernel
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)units, (unsigned)roles);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(mla ? kMlaThreads : kKvThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
