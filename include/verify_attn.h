@@ -490,7 +490,7 @@ typedef struct va_rope {
  * v_scales, without the other, or q without rope), VA_ERR_SHAPE, VA_ERR_DTYPE (also page scales
  * over a BF16 cache), VA_ERR_LAYOUT, VA_ERR_UNSUPPORTED (head_dim other than
  * 256, pages other than 16, rot out of range, descales beside page scales,
- * more heads than a grid holds: 2 Hkv + Hq / 8 > 65535); VA_ERR_CUDA for a failed
+ * more heads than a grid holds: 2 Hkv + Hq / 4 > 65535); VA_ERR_CUDA for a failed
  * launch.
  */
 va_status verify_attn_append_kv(const va_tensor* q, const va_tensor* k, const va_tensor* v,

@@ -45,8 +45,8 @@ struct AppendParams {
   int32_t num_seqs, total_q, hq, hkv, num_blocks;
 };
 
-// CTAs per page (grid.y); false when there are more than a grid can hold.
-int append_roles(bool mla, int64_t hkv, int64_t hq, int64_t* roles);
+// CTAs per page (grid.y).
+int64_t append_roles(bool mla, const AppendParams& p);
 cudaError_t launch_append(const AppendParams& p, bool mla, cudaStream_t stream);
 
 }  // namespace va

@@ -116,8 +116,7 @@ va_status check_queries(const va_tensor* q, const va_tensor* q_out, int64_t tota
 
 va_status run_append(const AppendParams& p, bool mla, void* stream) {
   const int64_t units = p.total_q / kPageSize + 2 * (int64_t)p.num_seqs;
-  int64_t roles = 0;
-  if (units > INT32_MAX || !append_roles(mla, p.hkv, p.hq, &roles)) return VA_ERR_UNSUPPORTED;
+  if (units > INT32_MAX || append_roles(mla, p) > 65535) return VA_ERR_UNSUPPORTED;
   if (p.total_q == 0 || p.num_seqs == 0) return VA_OK;  // no token
   return launch_append(p, mla, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }
