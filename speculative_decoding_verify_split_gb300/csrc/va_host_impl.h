@@ -13,6 +13,7 @@ namespace va_host_impl {
 struct Shapes {
   int64_t total_q, hq, hkv, num_blocks, num_seqs, width;
   int32_t kv_dtype;
+  int32_t share = 1;  // work items per KV head (row_share)
 };
 
 // Elementary checks of a descriptor (pure host code): its element count, a

@@ -74,6 +74,10 @@ struct Params {
   const float* k_scales;
   const float* v_scales;
   int64_t ks_s0, ks_s1, vs_s0, vs_s1;
+  // Work items that share a cache head (page-scaled calls of small batches):
+  // hkv counts kv_share items per cache head, each with group = its part of
+  // the head's query heads. 1 otherwise.
+  int32_t kv_share;
 
   // Split-KV decomposition: one stream of key tiles over all work items
   // j = b * hkv + kvh, cut into num_splits equal ranges (one per CTA). Each
@@ -113,7 +117,11 @@ inline WorkspaceLayout workspace_layout(int64_t num_work, int64_t num_splits, in
   const int64_t pieces = num_work + num_splits;
   w.status_off = 0;
   w.meta_off = 256;
-  w.ml_off = w.meta_off + align_up(sizeof(int32_t) * (size_t)(num_work + 1), 256);
+  // (at least 1 KB: room for the items of a small batch whose rows are shared
+  // out, at most one per SM)
+  size_t meta = align_up(sizeof(int32_t) * (size_t)(num_work + 1), 256);
+  if (meta < 1024) meta = 1024;
+  w.ml_off = w.meta_off + meta;
   w.acc_off = w.ml_off + align_up(sizeof(float) * 2 * (size_t)(pieces * max_rows), 256);
   w.total = w.acc_off + align_up(sizeof(float) * (size_t)dv * (size_t)(pieces * max_rows), 256);
   return w;

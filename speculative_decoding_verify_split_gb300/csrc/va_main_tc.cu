@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // page table need not map them); the softmax zeroes their V rows
       const int pg_first = VAR ? first_key(p, pc.S, pc.L) / kPageSize : 0;
       const int* bt_row = p.block_table + (int64_t)pc.b * p.bt_s0;
+      const int cache_head = SCL ? pc.kvh / p.kv_share : pc.kvh;
       int win = -1;       // first page index cached in the lanes
       int my_page = -1;   // page id of page (win + lane)
       ScaleWindow sw;
@@ -359,10 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (SCL && !is_k) {
           if (win < 0 || pg0 + kPagesPerTile > win + 32) {
             win = pg0;
-            sw.move(p, bt_row, pc.kvh, win, 32, pg_first, npages);
+            sw.move(p, bt_row, cache_head, win, 32, pg_first, npages);
             my_page = sw.id;
           } else {
-            sw.advance(p, pc.kvh);
+            sw.advance(p, cache_head);
           }
         } else if (win < 0 || pg0 + kPagesPerTile > win + 32) {
           win = pg0;
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 1; u < kPagesPerTile; ++u)
             if (i == u) id = ids[u];
           if (id >= 0)
-            tma_load_4d_hint(dst + ch * C::kRegion + i * 2048, tmap, ch * (128 / C::kEsize), pc.kvh, 0, id,
+            tma_load_4d_hint(dst + ch * C::kRegion + i * 2048, tmap, ch * (128 / C::kEsize), cache_head, 0, id,
                              bar(bar_full + s), kv_policy);
         }
         if (SCL && !is_k) {

@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (next_piece(p, t0, t1, jq, tq, pq, seqs)) {
       const int r = 16 * (warp & 3) + (lane & 15), qtr = 2 * ((warp - 4) >> 2) + (lane >> 4);
       if (r < pq.R) {
-        const uint16_t* src = p.q + (int64_t)(pq.q0 + r / p.group) * p.q_s0 + (int64_t)(r % p.group) * p.q_s1;
+        const uint16_t* src =
+            p.q + (int64_t)(pq.q0 + r / p.group) * p.q_s0 + (int64_t)(pq.kvh * p.group + r % p.group) * p.q_s1;
         asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 128 * qtr));
         asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 128 * qtr + 64));
         asm volatile("prefetch.global.L2 [%0];" ::"l"(src + kMlaNope + 16 * qtr));
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = r < pq.R;
       const int tq = row_ok ? r / G : 0;
       const int gq = row_ok ? r - tq * G : 0;
-      const uint16_t* src = p.q + (int64_t)(pq.q0 + tq) * p.q_s0 + (int64_t)gq * p.q_s1;
+      const uint16_t* src = p.q + (int64_t)(pq.q0 + tq) * p.q_s0 + (int64_t)(pq.kvh * G + gq) * p.q_s1;
       // the row's largest |value| first (over its four threads), then the
       // conversion, re-reading the 288 bytes (cache hits)
       const bool ld = ok && row_ok;
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto prefetch_q = [&](const Piece& pq) {
       if (r < pq.R) {
         const int tq = r / G, gq = r - tq * G;
-        const uint16_t* src = p.q + (int64_t)(pq.q0 + tq) * p.q_s0 + (int64_t)gq * p.q_s1;
+        const uint16_t* src = p.q + (int64_t)(pq.q0 + tq) * p.q_s0 + (int64_t)(pq.kvh * G + gq) * p.q_s1;
         asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 128 * qtr));
         asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 128 * qtr + 64));
         asm volatile("prefetch.global.L2 [%0];" ::"l"(src + kMlaNope + 16 * qtr));

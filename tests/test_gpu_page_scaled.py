@@ -185,14 +185,16 @@ def test_interleaved_scales_and_strided_tensors():
 
 
 def test_equal_scales_give_the_descaled_call():
-    """One power of two everywhere: the bits of verify_attn with that descale."""
+    """One power of two everywhere: the bits of verify_attn with that descale,
+    for the same split of the keys (which alone decides the order of sums)."""
     w = make_workload([4, 2], [1024, 769], 16, 1, "fp8_e4m3", seed=555, k_descale=0.5, v_descale=1.0).to("cuda")
     n = w.k_cache.shape[0]
-    got = run(w, torch.full((n, 1), 0.5), torch.ones(n, 1))
-    ref = va.run_workload(w)
-    assert torch.equal(got, ref)
     m = make_mla_workload([4, 2], [1024, 769], 16, "fp8_e4m3", seed=556).to("cuda")
-    assert torch.equal(run_mla(m, torch.ones(m.kv_cache.shape[0], 1)), va.run_mla_workload(m))
+    for splits in (1, 7, 16):
+        got = run(w, torch.full((n, 1), 0.5), torch.ones(n, 1), num_splits=splits)
+        assert torch.equal(got, va.run_workload_ex(w, num_splits=splits))
+        got = run_mla(m, torch.ones(m.kv_cache.shape[0], 1), num_splits=splits)
+        assert torch.equal(got, va.run_mla_workload(m, num_splits=splits))
 
 
 def test_empty_batches():
@@ -331,6 +333,25 @@ def test_waits_that_run_out(mla):
     for splits in (0, 1):
         compare(call(num_splits=splits), *(oracle_mla(w, ks) if mla else oracle(w, ks, vs)))
     assert va.last_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("hq,q,kv", [(16, [4, 2], [1024, 769]), (16, [1, 1], [500, 40]), (8, [3], [100]), (12, [1, 4, 2], [30, 17, 700]),
+                                     (64, [1], [2000])])
+def test_small_batches_in_the_promised_workspace(hq, q, kv):
+    """Small batches hand a KV head's query heads to several CTAs: in exactly the
+    workspace that the size call names, with garbage in it."""
+    w = make_workload(q, kv, hq, 1, "fp8_e4m3", seed=595).to("cuda")
+    ks, vs = scales_for(w, 8)
+    n = va.workspace_size(w.q, w.k_cache, w.seqused_k, w.max_seqlen_q, w.max_seqlen_k)
+    ws = torch.full((n + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = ws[(-ws.data_ptr()) % 256:][:n]
+    compare(run(w, ks, vs, workspace=ws), *oracle(w, ks, vs))
+    m = make_mla_workload(q, kv, hq, "fp8_e4m3", seed=596).to("cuda")
+    s, _ = scales_for(m, 9, spread=4.0)
+    n = va.mla_workspace_size(m.q, m.seqused_k, m.max_seqlen_q, m.max_seqlen_k)
+    ws = torch.full((n + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = ws[(-ws.data_ptr()) % 256:][:n]
+    compare(run_mla(m, s, workspace=ws), *oracle_mla(m, s))
 
 
 def test_workspace_errors():
