@@ -141,9 +141,9 @@ static int64_t tiles_upper_bound(int64_t B, int64_t hkv, int32_t max_q, int32_t 
 // than SMs leaves SMs idle while the others stage, softmax and store up to 64
 // rows; handing a head's query heads out to several CTAs (each reads the
 // keys again, from L2) shortens all three. The most, in powers of two, that
-// still gives every tile an SM of its own: two sequences of 1,024 and 769
-// keys, 16 heads, from a graph
-// of calls: latent cache 23.3 -> 19.2 us a call, GQA cache 12.7 -> 12.3.
+// still gives every tile an SM of its own. Two sequences of 769 to 1,024 keys,
+// 16 heads, graphs of calls: latent cache 23.3 -> 19.2 us a call, GQA cache
+// 12.7 -> 12.3.
 static int32_t row_share(int64_t tiles, int64_t group, int32_t num_sms) {
   int32_t s = 1;
   while (tiles > 0 && group % (2 * s) == 0 && tiles * 2 * s <= num_sms) s *= 2;
