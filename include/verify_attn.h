@@ -543,6 +543,11 @@ va_status verify_attn_append_mla(const va_tensor* q_pe, const va_tensor* latent,
  *               VA_FP8_E4M3), or NULL to use the library's own per-device workspace,
  *               whose calls must be ordered on one stream; during stream
  *               capture NULL is refused (VA_ERR_WORKSPACE).
+ *  num_splits   0: the library's choice, which for small batches is one cluster of
+ *               up to 8 CTAs per (sequence, KV head) that joins its partial results
+ *               on chip, without a merge kernel; > 0 forces the split over that many
+ *               CTAs.
+ *  event_after_main  as verify_attn_ex; with clusters, behind the only kernel.
  * Accuracy: weights keep fp32 precision while the V scales of the pages a row
  * sees lie within a factor of 2^96 of each other.
  * Errors as verify_attn_opt; VA_ERR_NULL without scales, VA_ERR_DTYPE for a

@@ -137,33 +137,46 @@ static int64_t tiles_upper_bound(int64_t B, int64_t hkv, int32_t max_q, int32_t 
   return B * hkv * item_tiles;
 }
 
-// Work items per KV head of a page-scaled call. A batch with fewer key tiles
-// than SMs leaves SMs idle while the others stage, softmax and store up to 64
-// rows; handing a head's query heads out to several CTAs (each reads the
-// keys again, from L2) shortens all three. The most, in powers of two, that
-// still gives every tile an SM of its own. Two sequences of 769 to 1,024 keys,
-// 16 heads, graphs of calls: latent cache 23.3 -> 19.2 us a call, GQA cache
-// 12.7 -> 12.3.
-static int32_t row_share(int64_t tiles, int64_t group, int32_t num_sms) {
+// Whether a page-scaled call runs as one cluster of CTAs per item (CLU of the
+// main kernels), and then the CTAs per cluster and the items per KV head
+// (`share`: a head's query heads handed out to several clusters, which read
+// the keys again, from L2). J (sequence, KV head) pairs of at most T tiles;
+// caps[i]: clusters of 2^i CTAs that the device holds at once.
+//  * The most CTAs per item, up to 8 and as many as tiles, with one cluster per
+//    pair resident.
+//  * Then as many items per head as leave at least eight rows each (64 rows
+//    cost 3 us more than 8 in staging, softmax and stores) and fit.
+//  * A cluster's CTAs take an equal share of their own item only, so the
+//    largest item sets the time, where the split over all CTAs evens the batch
+//    out. Clusters as long as that costs at most four tiles (about 1 us each),
+//    what the work scan and the merge kernel cost, and a quarter tile for each
+//    segment past eight (24 tiles at most) that the merge would have to fold
+//    per item; for items that are as large as their bound on average with a
+//    window (`even`), and half as large without.
+// Measured, us per call in graphs of calls, split over all CTAs against
+// clusters (16 query heads per KV head unless noted):
+//   2 x 1,024 keys, 4 tokens 12.5 / 9.8; 8 x 2,000, 3 tokens 21.5 / 12.8;
+//   16 x 1,000, 1 token 16.2 / 10.8; 32 x 2,000, 1 token 17.6 / 14.2;
+//   64 x 1,000, 4 tokens 25.5 / 18.5; 1 x 8,000, 4 tokens, 8 heads 20.4 / 18.0;
+//   1 x 20,000, 1 token 48.0 / 33.9; 1 x 40,000 50.3 / 58.9 (split);
+//   16 pairs of 513 to 4,096 18.6 / 19.5 (split); 32 x 2 heads, window of 1,023
+//   24.0 / 19.3. Latent cache: 2 x 1,024, 4 tokens 23.3 / 14.3; 2 x 3,000 at
+//   most 27.9 / 20.0; 150 x 300 29.1 / 19.5.
+static bool cluster_plan(int64_t J, int64_t T, int64_t group, int32_t max_q, const int32_t* caps, int32_t num_sms,
+                         bool even, int32_t* cluster, int32_t* share) {
+  if (J < 1 || T < 1) return false;
+  int i = kMaxClusterLog2;
+  while (i > 0 && (J > caps[i] || (1 << (i - 1)) >= T)) --i;
+  if (J > caps[i]) return false;
+  const int64_t per = (T + (1 << i) - 1) >> i;
+  const int64_t segments = T < num_sms / J ? T : num_sms / J;
+  const int64_t quarters = 16 + (segments > 104 ? 96 : segments > 8 ? segments - 8 : 0);
+  if ((4 * per - quarters) * num_sms > (even ? 4 : 2) * J * T) return false;
   int32_t s = 1;
-  while (tiles > 0 && group % (2 * s) == 0 && tiles * 2 * s <= num_sms) s *= 2;
-  return s;
-}
-
-// CTAs of a page-scaled call with a window, whose items (J) have about the same
-// number of tiles (T, the window's bound): a whole number of CTAs per item,
-// so that no CTA starts a second one, unless that makes a CTA's share longer by
-// more than 1.5 tiles than an equal share over all SMs does. Windows of 1,024
-// keys (T = 9), single tokens, 152 CTAs against the whole number, from graphs
-// of calls: J = 64 22.5 -> 19.9 us, J = 70 23.4 -> 20.5, J = 50 21.7 -> 19.2;
-// T = 33: J = 32 26.1 -> 26.1, and J = 90, where the share would grow by 13
-// tiles, 46.7 against 59.3 with one CTA per item. Returns 0 for the plan's own.
-static int32_t aligned_splits(int64_t J, int64_t T, int32_t num_sms) {
-  if (J < 1 || J > num_sms) return 0;
-  const int64_t k = num_sms / J < T ? num_sms / J : T;
-  if (k < 1) return 0;
-  const double longer = (double)T / (double)k - (double)(J * T) / num_sms;
-  return longer <= 1.5 ? (int32_t)(k * J) : 0;
+  while (group % (2 * s) == 0 && group / s * max_q > 8 && 2 * J * s <= caps[i]) s *= 2;
+  *cluster = 1 << i;
+  *share = s;
+  return true;
 }
 
 // The split cost of starting an item (see kPieceCostTiles) for a plan: the
@@ -268,6 +281,9 @@ uint64_t wait_limit_ns() {
 struct DeviceState {
   bool ready = false;
   int sms = 0;
+  // clusters of 2^i CTAs that run at once (main kernel, latent main kernel)
+  int32_t clusters[kMaxClusterLog2 + 1] = {};
+  int32_t mla_clusters[kMaxClusterLog2 + 1] = {};
   void* ws = nullptr;
   size_t ws_bytes = 0;
 };
@@ -288,6 +304,8 @@ static va_status device_state(DeviceState** out) {
     if (prepare_main_tc() != cudaSuccess || prepare_mla_tc() != cudaSuccess ||
         prepare_mla_bf16_tc() != cudaSuccess)
       return VA_ERR_CUDA;
+    if (main_tc_clusters(st.clusters) != cudaSuccess || mla_tc_clusters(st.mla_clusters) != cudaSuccess)
+      return VA_ERR_CUDA;
     st.ready = true;
   }
   *out = &st;
@@ -306,6 +324,15 @@ va_status validate_options(const va_options* opts, const Shapes& sh) {
     if (!t->data) return VA_ERR_NULL;
   }
   return VA_OK;
+}
+
+// Turns the plan of a split over all CTAs into one of clusters: the same tiles
+// and (unused but for its status word) workspace.
+static void use_clusters(va_plan* plan, const Shapes& sh) {
+  plan->num_work *= sh.share;
+  plan->max_rows /= sh.share;
+  plan->num_splits = plan->num_work * sh.cluster;
+  plan->kernel = kKernelTc;
 }
 
 static void set_page_scales(Params* p, const PageScales* s) {
@@ -358,6 +385,7 @@ va_status launch(const va_tensor* q, const va_tensor* k, const va_tensor* v, con
   p.hkv = (int32_t)sh.hkv * sh.share;
   p.group = (int32_t)(sh.hq / p.hkv);
   p.kv_share = sh.share;
+  p.cluster = sh.cluster;
   p.num_blocks = (int32_t)sh.num_blocks;
   p.total_q = (int32_t)sh.total_q;
   p.max_seqlen_q = max_q;
@@ -402,7 +430,7 @@ va_status launch(const va_tensor* q, const va_tensor* k, const va_tensor* v, con
   }
   if (launch_main_tc(p, tm_k, tm_v, stream) != cudaSuccess) return VA_ERR_CUDA;
   if (ev_mid && cudaEventRecord(ev_mid, stream) != cudaSuccess) return VA_ERR_CUDA;
-  if (launch_merge(p, stream) != cudaSuccess) return VA_ERR_CUDA;
+  if (p.cluster == 0 && launch_merge(p, stream) != cudaSuccess) return VA_ERR_CUDA;
   return VA_OK;
 }
 
@@ -461,15 +489,13 @@ va_status validate_mla(const va_tensor* q, const va_tensor* kv, const va_tensor*
 // The split heuristic of make_plan on latent tiles (64 keys for an FP8 cache,
 // 32 for BF16), value width 512.
 va_status make_mla_plan(int64_t B, int64_t hq, int32_t max_q, int32_t max_k, int32_t num_sms,
-                        int32_t force, va_plan* plan, int32_t kv_dtype, int32_t share = 1) {
+                        int32_t force, va_plan* plan, int32_t kv_dtype) {
   if (!plan) return VA_ERR_NULL;
   if (B < 0 || hq < 1 || max_q < 1 || max_k < 0 || num_sms < 1) return VA_ERR_UNSUPPORTED;
   if (kv_dtype != VA_FP8_E4M3 && kv_dtype != VA_BF16) return VA_ERR_UNSUPPORTED;
   if (hq * max_q > kMaxRows) return VA_ERR_UNSUPPORTED;
   const int tile = kv_dtype == VA_FP8_E4M3 ? kMlaTileKeys : kMlaTileKeysBf16;
   const int cost = kv_dtype == VA_FP8_E4M3 ? kMlaPieceCostTiles : kMlaPieceCostTilesBf16;
-  B *= share;
-  hq /= share;
   const int64_t item_tiles = ((int64_t)max_k + tile - 1) / tile;
   const int64_t tiles_bound = B * item_tiles;
   if (tiles_bound + B * cost > INT32_MAX / 2) return VA_ERR_UNSUPPORTED;
@@ -544,6 +570,7 @@ va_status launch_mla(const va_tensor* q, const va_tensor* kv, const va_tensor* b
   p.hkv = sh.share;
   p.group = (int32_t)sh.hq / sh.share;
   p.kv_share = sh.share;
+  p.cluster = sh.cluster;
   p.num_blocks = (int32_t)sh.num_blocks;
   p.total_q = (int32_t)sh.total_q;
   p.max_seqlen_q = max_q;
@@ -574,7 +601,7 @@ va_status launch_mla(const va_tensor* q, const va_tensor* kv, const va_tensor* b
   if ((p.kv_fp8 ? launch_mla_tc(p, tm, tm_pe, stream) : launch_mla_bf16_tc(p, tm, stream)) != cudaSuccess)
     return VA_ERR_CUDA;
   if (ev_mid && cudaEventRecord(ev_mid, stream) != cudaSuccess) return VA_ERR_CUDA;
-  if (launch_merge(p, stream) != cudaSuccess) return VA_ERR_CUDA;
+  if (p.cluster == 0 && launch_merge(p, stream) != cudaSuccess) return VA_ERR_CUDA;
   return VA_OK;
 }
 
@@ -680,26 +707,10 @@ static va_status run_call(const va_tensor* q, const va_tensor* k_cache, const va
   s = make_plan(sh.num_seqs, sh.hkv, sh.hq, max_seqlen_q, max_seqlen_k, sh.kv_dtype, st->sms, num_splits, &plan,
                 window);
   if (s != VA_OK) return s;
-  if (scales && num_splits == 0) {
-    const int64_t bytes = plan.workspace_bytes;
-    sh.share = row_share(tiles_upper_bound(sh.num_seqs, sh.hkv, max_seqlen_q, max_seqlen_k, plan.tile_keys, window),
-                         sh.hq / sh.hkv, st->sms);
-    for (; sh.share > 1; sh.share /= 2) {  // in the workspace that verify_attn_workspace_size promises
-      s = make_plan(sh.num_seqs, sh.hkv * sh.share, sh.hq, max_seqlen_q, max_seqlen_k, sh.kv_dtype, st->sms, 0, &plan,
-                    window);
-      if (s != VA_OK) return s;
-      if (plan.workspace_bytes <= bytes) break;
-    }
-    if (sh.share == 1) {
-      const int64_t J = sh.num_seqs * sh.hkv;
-      const int32_t whole =
-          window >= 0 && J > 0
-              ? aligned_splits(J, tiles_upper_bound(1, 1, max_seqlen_q, max_seqlen_k, plan.tile_keys, window), st->sms)
-              : 0;
-      s = make_plan(sh.num_seqs, sh.hkv, sh.hq, max_seqlen_q, max_seqlen_k, sh.kv_dtype, st->sms, whole, &plan, window);
-    }
-    if (s != VA_OK) return s;
-  }
+  if (scales && num_splits == 0 &&
+      cluster_plan(sh.num_seqs * sh.hkv, tiles_upper_bound(1, 1, max_seqlen_q, max_seqlen_k, plan.tile_keys, window),
+                   sh.hq / sh.hkv, max_seqlen_q, st->clusters, st->sms, window >= 0, &sh.cluster, &sh.share))
+    use_clusters(&plan, sh);
   if (own_ws) {
     if (sh.total_q == 0 || sh.num_seqs == 0) return VA_OK;
     if (scales) s = refuse_capture(stream);
@@ -827,18 +838,10 @@ static va_status run_mla_call(const va_tensor* q, const va_tensor* kv_cache, con
   va_plan plan;
   s = make_mla_plan(sh.num_seqs, sh.hq, max_seqlen_q, max_seqlen_k, st->sms, num_splits, &plan, sh.kv_dtype);
   if (s != VA_OK) return s;
-  if (scales && num_splits == 0) {
-    const int64_t bytes = plan.workspace_bytes;
-    sh.share = row_share(sh.num_seqs * (((int64_t)max_seqlen_k + plan.tile_keys - 1) / plan.tile_keys), sh.hq, st->sms);
-    for (; sh.share > 1; sh.share /= 2) {  // partial rows are padded to four: fewer may need more
-      s = make_mla_plan(sh.num_seqs, sh.hq, max_seqlen_q, max_seqlen_k, st->sms, 0, &plan, sh.kv_dtype, sh.share);
-      if (s != VA_OK) return s;
-      if (plan.workspace_bytes <= bytes) break;
-    }
-    if (sh.share == 1)
-      s = make_mla_plan(sh.num_seqs, sh.hq, max_seqlen_q, max_seqlen_k, st->sms, 0, &plan, sh.kv_dtype);
-    if (s != VA_OK) return s;
-  }
+  if (scales && num_splits == 0 &&
+      cluster_plan(sh.num_seqs, ((int64_t)max_seqlen_k + plan.tile_keys - 1) / plan.tile_keys, sh.hq, max_seqlen_q,
+                   st->mla_clusters, st->sms, false, &sh.cluster, &sh.share))
+    use_clusters(&plan, sh);
   if (!workspace) {
     if (sh.total_q == 0 || sh.num_seqs == 0) return VA_OK;
     if (scales) s = refuse_capture(static_cast<cudaStream_t>(stream));

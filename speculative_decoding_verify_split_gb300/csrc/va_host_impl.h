@@ -13,7 +13,9 @@ namespace va_host_impl {
 struct Shapes {
   int64_t total_q, hq, hkv, num_blocks, num_seqs, width;
   int32_t kv_dtype;
-  int32_t share = 1;  // work items per KV head (row_share)
+  // page-scaled calls (cluster_plan): CTAs of an item's cluster, 0 for the split
+  // over all CTAs; work items per KV head
+  int32_t cluster = 0, share = 1;
 };
 
 // Elementary checks of a descriptor (pure host code): its element count, a

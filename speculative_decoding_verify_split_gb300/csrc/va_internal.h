@@ -78,6 +78,11 @@ struct Params {
   // hkv counts kv_share items per cache head, each with group = its part of
   // the head's query heads. 1 otherwise.
   int32_t kv_share;
+  // > 0: CTAs per item, one cluster each, which join their partials through
+  // distributed shared memory and write the output (page-scaled calls of small
+  // batches; no merge kernel, num_splits = num_work * cluster). 0: the split
+  // over all CTAs.
+  int32_t cluster;
 
   // Split-KV decomposition: one stream of key tiles over all work items
   // j = b * hkv + kvh, cut into num_splits equal ranges (one per CTA). Each
@@ -117,11 +122,7 @@ inline WorkspaceLayout workspace_layout(int64_t num_work, int64_t num_splits, in
   const int64_t pieces = num_work + num_splits;
   w.status_off = 0;
   w.meta_off = 256;
-  // (at least 1 KB: room for the items of a small batch whose rows are shared
-  // out, at most one per SM)
-  size_t meta = align_up(sizeof(int32_t) * (size_t)(num_work + 1), 256);
-  if (meta < 1024) meta = 1024;
-  w.ml_off = w.meta_off + meta;
+  w.ml_off = w.meta_off + align_up(sizeof(int32_t) * (size_t)(num_work + 1), 256);
   w.acc_off = w.ml_off + align_up(sizeof(float) * 2 * (size_t)(pieces * max_rows), 256);
   w.total = w.acc_off + align_up(sizeof(float) * (size_t)dv * (size_t)(pieces * max_rows), 256);
   return w;
@@ -147,6 +148,12 @@ constexpr int kTcTileKeysBf16 = 64;  // keys per tile, BF16 KV
 constexpr int kPieceCostTiles = 4;
 constexpr int kPieceCostTilesSmall = 1;
 constexpr int64_t kSmallSplitTiles = 16;
+constexpr int kMaxClusterLog2 = 3;
+constexpr int kMaxCluster = 1 << kMaxClusterLog2;  // CTAs of a cluster (the portable limit)
+// Clusters of 2^i CTAs, i = 0..kMaxClusterLog2, of the page-scaled kernels that
+// the current device holds at once.
+cudaError_t main_tc_clusters(int32_t* caps);
+cudaError_t mla_tc_clusters(int32_t* caps);
 
 cudaError_t launch_merge(const Params& p, cudaStream_t stream);
 
@@ -192,5 +199,27 @@ cudaError_t prepare_mla_bf16_tc();
 cudaError_t launch_mla_bf16_tc(const Params& p, const CUtensorMap& tm_kv, cudaStream_t stream);
 cudaError_t launch_main_tc(const Params& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                            cudaStream_t stream);
+
+// Clusters of 2^i CTAs of `fn` that run at once; 0 where the device gives none.
+template <class F>
+inline cudaError_t cluster_caps(F fn, int threads, size_t smem, int32_t* caps) {
+  for (int i = 0; i <= kMaxClusterLog2; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1u << i);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << i;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+    if (e != cudaSuccess) return e;
+    caps[i] = n;
+  }
+  return cudaSuccess;
+}
 
 }  // namespace va

@@ -222,13 +222,18 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 // each with its own factor and offset in the FMA of P's exponent, and its own
 // partial sum of l. The V producers, which walk the page ids anyway, bring
 // the scales to shared memory with the V tile's slot.
-template <bool FP8, bool VAR, bool QTM, bool SCL>
+// CLU: one cluster of CTAs per item (small batches); each CTA leaves its
+// partial in shared memory (in the drained rings) and the cluster joins them
+// there: no work scan, no partials in global memory, no merge kernel. A CTA
+// without a tile skips the roles and meets the others at the join.
+template <bool FP8, bool VAR, bool QTM, bool SCL, bool CLU>
 __global__ void __launch_bounds__(kThreads, 1)
     va_main_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<FP8, VAR, QTM>;
   static_assert(FP8 || !SCL, "page scales are for e4m3 caches");
   static_assert(!SCL || C::kVSlots <= kMaxVSlots, "page scales: one place per V slot");
+  static_assert(!CLU || SCL, "the cluster join takes no v_descale");
   constexpr int kT = C::kT;
   constexpr int kSBufs = C::kSBufs;
   constexpr int kPBufs = C::kPBufs;
@@ -311,15 +316,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long t0, t1, ts_first = 0;
   int j_first = 0;
   bool seqs_cached = false;
-  locate_work<kThreads>(p, c, scratch, s_j, s_ts, &t0, &t1, &j_first, &ts_first,
-                        reinterpret_cast<SeqMeta*>(sm + C::kOffSeqs), &seqs_cached);
+  SeqMeta meta{};  // CLU: the item's lengths
+  if constexpr (CLU) {
+    meta = locate_cluster_work(p, c, p.cluster, &t0, &t1, &j_first, reinterpret_cast<SeqMeta*>(sm + C::kOffSeqs));
+    seqs_cached = p.num_seqs <= kSeqCache;
+  } else {
+    locate_work<kThreads>(p, c, scratch, s_j, s_ts, &t0, &t1, &j_first, &ts_first,
+                          reinterpret_cast<SeqMeta*>(sm + C::kOffSeqs), &seqs_cached);
+  }
   const SeqMeta* seqs = seqs_cached ? reinterpret_cast<const SeqMeta*>(sm + C::kOffSeqs) : nullptr;
-  if (t0 >= t1) {  // CTA-uniform
+  if (!CLU && t0 >= t1) {  // CTA-uniform
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
     return;
   }
+  // CLU: the partial's rows, padded against bank conflicts, then (m, l)
+  constexpr int kPartStride = kHeadDim + 4;
+  constexpr int kOffMl = kMaxRows * kPartStride * 4;
+  static_assert(!CLU || kOffMl + kMaxRows * 8 <= C::kRingBytes, "the partial fits in the rings");
+  float* part = reinterpret_cast<float*>(sm);
+  float* part_ml = reinterpret_cast<float*>(sm + kOffMl);
 
-  if (warp == 0 || warp == 2 || warp == 3) {
+  if (CLU && t0 >= t1) {
+    if (tid < kMaxRows) {
+      part_ml[2 * tid] = -INFINITY;
+      part_ml[2 * tid + 1] = 0.f;
+    }
+  } else if (warp == 0 || warp == 2 || warp == 3) {
     // ======================= TMA producers ======================================
     // Warp 0 streams the K tiles, warps 2 and 3 the V tiles of even and odd
     // tiles: one warp alone cannot issue the 2 KB page boxes fast enough to
@@ -982,8 +1004,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) continue;
       // an attention sink joins the normaliser once per row: here for rows
       // written directly, in the merge for split ones
+      const bool direct = !CLU && pc.direct;
       if constexpr (VAR) {
-        if (p.sinks && pc.direct && row_ok && m_ref != -INFINITY)
+        if (p.sinks && direct && row_ok && m_ref != -INFINITY)
           lrow += exp2f(p.sinks[pc.kvh * G + gq] * kLog2e - (m_ref - kPShift));
       }
       const float inv = lrow > 0.f ? vd / lrow : 0.f;
@@ -992,7 +1015,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto emit = [&](const uint32_t* o, int col, auto n_c) {
         constexpr int n = decltype(n_c)::value;
         if (!row_ok) return;
-        if (pc.direct) {
+        if constexpr (CLU) {
+          float* dst = part + r * kPartStride + col;
+#pragma unroll
+          for (int v4 = 0; v4 < n / 4; ++v4)
+            reinterpret_cast<uint4*>(dst)[v4] = make_uint4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
+        } else if (direct) {
           uint16_t* dst = p.out + (int64_t)(pc.q0 + tq) * p.o_s0 + (int64_t)(pc.kvh * G + gq) * p.o_s1 + col;
           uint32_t w[n / 2];
 #pragma unroll
@@ -1040,7 +1068,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           emit(o, 128 * kh + 64 * sub + 32 * k, std::integral_constant<int, 32>{});
         }
       }
-      if (row_ok && !pc.direct && kh == 0 && sub == 0) {
+      if (CLU) {
+        if (row_ok && kh == 0 && sub == 0) {
+          part_ml[2 * r] = (m_ref == -INFINITY) ? -INFINITY : m_ref - kPShift;
+          part_ml[2 * r + 1] = lrow;
+        }
+      } else if (row_ok && !direct && kh == 0 && sub == 0) {
         p.ws_ml[(piece * p.max_rows + r) * 2 + 0] = (m_ref == -INFINITY) ? -INFINITY : m_ref - kPShift;
         p.ws_ml[(piece * p.max_rows + r) * 2 + 1] = lrow;
       }
@@ -1054,14 +1087,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if constexpr (CLU) {
+    __syncwarp();
+    cluster_sync();  // every CTA's partial is written
+    join_cluster<kThreads, kHeadDim>(p, c / p.cluster, meta, c % p.cluster, smem_addr(part), kPartStride,
+                                     smem_addr(part_ml));
+    cluster_sync();  // no CTA ends while another still reads it
+  }
 }
 
 }  // namespace
 
-template <bool FP8, bool VAR, bool QTM, bool SCL = false>
+template <bool FP8, bool VAR, bool QTM, bool SCL = false, bool CLU = false>
 cudaError_t set_smem() {
-  return cudaFuncSetAttribute(va_main_tc_kernel<FP8, VAR, QTM, SCL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(va_main_tc_kernel<FP8, VAR, QTM, SCL, CLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Cfg<FP8, VAR, QTM>::kSmemBytes);
+}
+
+cudaError_t main_tc_clusters(int32_t* caps) {
+  return cluster_caps(va_main_tc_kernel<true, true, false, true, true>, kThreads, Cfg<true, true, false>::kSmemBytes, caps);
 }
 
 cudaError_t prepare_main_tc() {
@@ -1073,14 +1117,16 @@ cudaError_t prepare_main_tc() {
   if (e == cudaSuccess) e = set_smem<true, false, true, true>();
   if (e == cudaSuccess) e = set_smem<true, false, false, true>();
   if (e == cudaSuccess) e = set_smem<true, true, false, true>();
+  if (e == cudaSuccess) e = set_smem<true, false, false, true, true>();
+  if (e == cudaSuccess) e = set_smem<true, true, false, true, true>();
   return e;
 }
 
-template <bool FP8, bool VAR, bool QTM, bool SCL = false>
+template <bool FP8, bool VAR, bool QTM, bool SCL = false, bool CLU = false>
 static cudaError_t launch_one(cudaLaunchConfig_t& cfg, const Params& p, const CUtensorMap& tm_k,
                               const CUtensorMap& tm_v) {
   cfg.dynamicSmemBytes = Cfg<FP8, VAR, QTM>::kSmemBytes;
-  return cudaLaunchKernelEx(&cfg, va_main_tc_kernel<FP8, VAR, QTM, SCL>, p, tm_k, tm_v);
+  return cudaLaunchKernelEx(&cfg, va_main_tc_kernel<FP8, VAR, QTM, SCL, CLU>, p, tm_k, tm_v);
 }
 
 cudaError_t launch_main_tc(const Params& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
@@ -1092,11 +1138,19 @@ cudaError_t launch_main_tc(const Params& p, const CUtensorMap& tm_k, const CUten
   cfg.gridDim = dim3(p.num_splits);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (p.cluster > 0) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    return var ? launch_one<true, true, false, true, true>(cfg, p, tm_k, tm_v)
+               : launch_one<true, false, false, true, true>(cfg, p, tm_k, tm_v);
+  }
   if (p.k_scales) {
     if (var) return launch_one<true, true, false, true>(cfg, p, tm_k, tm_v);
     return p.q_in_tmem ? launch_one<true, false, true, true>(cfg, p, tm_k, tm_v)

@@ -160,20 +160,18 @@ __global__ void __launch_bounds__(kMlaNope, 2) va_merge_mla_kernel(const Params 
   __shared__ float s_sc[kRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int j = blockIdx.x;  // item j: sequence b's query heads [kvh G, +G)
-  const int b = j / p.hkv;
-  const int kvh = j - b * p.hkv;
+  const int j = blockIdx.x;  // one KV head: item j is sequence j
   const int r0 = blockIdx.y * kRows;
   const int d = threadIdx.x;
-  const int L = seq_q_len(p, b);
+  const int L = seq_q_len(p, j);
   const int G = p.group;
   const int R = G * L;
   if (r0 >= R) return;  // CTA-uniform
   const int nrow = R - r0 < kRows ? R - r0 : kRows;
-  const int q0 = p.cu_q[b];
+  const int q0 = p.cu_q[j];
   auto dst = [&](int rr) {
     const int t = (r0 + rr) / G, g = (r0 + rr) - t * G;
-    return p.out + (int64_t)(q0 + t) * p.o_s0 + (int64_t)(kvh * G + g) * p.o_s1 + d;
+    return p.out + (int64_t)(q0 + t) * p.o_s0 + (int64_t)g * p.o_s1 + d;
   };
   const int nt = work_tiles(p, j);
   if (nt == 0) {

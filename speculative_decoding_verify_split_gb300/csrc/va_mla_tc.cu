@@ -155,8 +155,8 @@ __device__ __forceinline__ int core_off(int m, int k, int row_bytes) {
 // GQA kernel it multiplies the page's logits, and as the value's scale joins
 // the weight, P = 2^(s + log2 scale - m_ref), with l summing P / scale. A
 // thread's 16 keys of a tile are one page. The producers bring the scales
-// with the ring slot.
-template <bool SCL>
+// with the ring slot. CLU: one cluster of CTAs per item, as in the GQA kernel.
+template <bool SCL, bool CLU>
 __global__ void __launch_bounds__(kThreads, 1)
     va_mla_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tm_kv,
                      const __grid_constant__ CUtensorMap tm_pe) {
@@ -230,13 +230,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long t0, t1, ts_first = 0;
   int j_first = 0;
   bool seqs_cached = false;
-  locate_work<kThreads>(p, c, scratch, s_j, s_ts, &t0, &t1, &j_first, &ts_first,
-                        reinterpret_cast<SeqMeta*>(sm + kOffSeqs), &seqs_cached);
+  SeqMeta meta{};  // CLU: the item's lengths
+  if constexpr (CLU) {
+    meta = locate_cluster_work(p, c, p.cluster, &t0, &t1, &j_first, reinterpret_cast<SeqMeta*>(sm + kOffSeqs));
+    seqs_cached = p.num_seqs <= kSeqCache;
+  } else {
+    locate_work<kThreads>(p, c, scratch, s_j, s_ts, &t0, &t1, &j_first, &ts_first,
+                          reinterpret_cast<SeqMeta*>(sm + kOffSeqs), &seqs_cached);
+  }
   const SeqMeta* seqs = seqs_cached ? reinterpret_cast<const SeqMeta*>(sm + kOffSeqs) : nullptr;
-  if (t0 >= t1) {  // CTA-uniform
+  if (!CLU && t0 >= t1) {  // CTA-uniform
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
     return;
   }
+  // CLU: the partial's rows in the drained ring, then (m, l)
+  constexpr int kOffMl = kMaxRows * kMlaNope * 4;
+  static_assert(!CLU || kOffMl + kMaxRows * 8 <= kOffQpe, "the partial fits in the ring");
+  float* part = reinterpret_cast<float*>(sm);
+  float* part_ml = reinterpret_cast<float*>(sm + kOffMl);
   if (warp >= 4 && warp < 12) {
     // the first item's Q rows into L2 before the ring's first loads flood HBM
     int jq = j_first;
@@ -255,7 +266,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
 
-  if (warp == 0 || warp == 2 || warp == 3) {
+  if (CLU && t0 >= t1) {
+    if (tid < kMaxRows) {
+      part_ml[2 * tid] = -INFINITY;
+      part_ml[2 * tid + 1] = 0.f;
+    }
+  } else if (warp == 0 || warp == 2 || warp == 3) {
     // ======================= TMA producers ======================================
     const int prod = warp == 0 ? 0 : warp - 1;
     const uint64_t kv_policy = l2_evict_first_policy();  // the cache rows are read once
@@ -744,6 +760,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         const int col = 128 * a + 32 * q + lane;
         const int nrow = ldr - r0 < 32 ? ldr - r0 : 32;
+        if constexpr (CLU) {
+#pragma unroll
+          for (int w = 0; w < 32; ++w)
+            if (r0 + w < pc.R) part[(r0 + w) * kMlaNope + col] = __uint_as_float(o[w]);
+          continue;
+        }
 #pragma unroll
         for (int w = 0; w < 8; ++w)
           if (4 * w < nrow)
@@ -751,7 +773,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_float4(__uint_as_float(o[4 * w]), __uint_as_float(o[4 * w + 1]),
                             __uint_as_float(o[4 * w + 2]), __uint_as_float(o[4 * w + 3]));
       }
-      if (row_ok && kh == 0 && sub == 0) {
+      if (CLU) {
+        if (row_ok && kh == 0 && sub == 0) {
+          part_ml[2 * r] = (m_ref == -INFINITY) ? -INFINITY : m_ref - kPShift;
+          part_ml[2 * r + 1] = lrow;
+        }
+      } else if (row_ok && kh == 0 && sub == 0) {
         p.ws_ml[(piece * p.max_rows + r) * 2 + 0] = (m_ref == -INFINITY) ? -INFINITY : m_ref - kPShift;
         p.ws_ml[(piece * p.max_rows + r) * 2 + 1] = lrow;
       }
@@ -765,16 +792,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if constexpr (CLU) {
+    __syncwarp();
+    cluster_sync();  // every CTA's partial is written
+    join_cluster<kThreads, kMlaNope>(p, c / p.cluster, meta, c % p.cluster, smem_addr(part), kMlaNope, smem_addr(part_ml));
+    cluster_sync();  // no CTA ends while another still reads it
+  }
 }
 
 }  // namespace
 
+cudaError_t mla_tc_clusters(int32_t* caps) {
+  return cluster_caps(va_mla_tc_kernel<true, true>, kThreads, kSmemBytes + 1024, caps);
+}
+
 cudaError_t prepare_mla_tc() {
-  cudaError_t e =
-      cudaFuncSetAttribute(va_mla_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes + 1024);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(va_mla_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes + 1024);
-  return e;
+  for (auto fn : {va_mla_tc_kernel<false, false>, va_mla_tc_kernel<true, false>, va_mla_tc_kernel<true, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes + 1024);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_mla_tc(const Params& p, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
@@ -785,13 +822,20 @@ cudaError_t launch_mla_tc(const Params& p, const CUtensorMap& tm_kv, const CUten
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes + 1024;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.k_scales ? cudaLaunchKernelEx(&cfg, va_mla_tc_kernel<true>, p, tm_kv, tm_pe)
-                    : cudaLaunchKernelEx(&cfg, va_mla_tc_kernel<false>, p, tm_kv, tm_pe);
+  if (p.cluster > 0) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, va_mla_tc_kernel<true, true>, p, tm_kv, tm_pe);
+  }
+  return p.k_scales ? cudaLaunchKernelEx(&cfg, va_mla_tc_kernel<true, false>, p, tm_kv, tm_pe)
+                    : cudaLaunchKernelEx(&cfg, va_mla_tc_kernel<false, false>, p, tm_kv, tm_pe);
 }
 
 }  // namespace va

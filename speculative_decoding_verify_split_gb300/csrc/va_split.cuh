@@ -7,8 +7,17 @@
 #include <cuda_bf16.h>
 
 #include "va_internal.h"
+#include "va_ptx.cuh"
 
 namespace va {
+
+__device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {
+  return __uint_as_float(((uint32_t)b) << 16);
+}
+
+__device__ __forceinline__ uint16_t float_to_bf16_bits(float f) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(f));
+}
 
 // Draft tokens of sequence b, clamped to [0, max_seqlen_q] and to the rows of q.
 __device__ __forceinline__ int seq_q_len(const Params& p, int b) {
@@ -239,6 +248,78 @@ __device__ long long locate_work(const Params& p, int c, long long* scratch, int
   return N;
 }
 
+// The same for a launch of one cluster per item: CTA `rank` of C takes an equal
+// share of the item's tiles (none, if there are fewer tiles than CTAs). The
+// item's first tile is unit 0. Fills the item's entry of the cache, if the
+// batch has room there; contains a barrier.
+__device__ __forceinline__ SeqMeta locate_cluster_work(const Params& p, int c, int C, long long* t0, long long* t1,
+                                                       int* out_j, SeqMeta* cache) {
+  const int j = c / C, rank = c - j * C;
+  const int b = j / p.hkv;
+  const SeqMeta m = seq_meta(p, nullptr, b);
+  const int nt = meta_tiles(p, m);
+  *t0 = (long long)nt * rank / C;
+  *t1 = (long long)nt * (rank + 1) / C;
+  *out_j = j;
+  if (threadIdx.x == 0) {
+    if (p.num_seqs <= kSeqCache) cache[b] = m;
+    if (*t0 < *t1) prefetch_first_pages(p, j, *t0);
+  }
+  __syncthreads();
+  return m;
+}
+
+// A cluster's join of its item's partials (O, m, l of each CTA, in shared
+// memory at `part`: R rows of `stride` floats, and `ml`: (m, l) per row): this
+// CTA sums its part of the R x DV outputs over the CTAs, in rank order, with
+// the weights 2^(m_k - max m), and writes it as bf16. Rows without a visible
+// key are 0. NT threads of the CTA; between two cluster barriers.
+template <int NT, int DV>
+__device__ __forceinline__ void join_cluster(const Params& p, int j, const SeqMeta& m, int rank, uint32_t part, int stride,
+                                             uint32_t ml) {
+  const int C = p.cluster;
+  const int b = j / p.hkv, kvh = j - b * p.hkv;
+  const int G = p.group, R = G * m.L;
+  const int units = R * (DV / 4), per = (units + C - 1) / C;
+  const int end = (rank + 1) * per < units ? (rank + 1) * per : units;
+  for (int u = rank * per + (int)threadIdx.x; u < end; u += NT) {
+    const int r = u / (DV / 4), c4 = u - r * (DV / 4);
+    float2 x[kMaxCluster];
+    float4 o[kMaxCluster];
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) {
+      x[k] = make_float2(-INFINITY, 0.f);
+      o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < C) {
+        x[k] = ptx::ld_cluster_f2(ptx::cluster_addr(ml + 8 * r, k));
+        o[k] = ptx::ld_cluster_f4(ptx::cluster_addr(part + 4 * (r * stride + 4 * c4), k));
+      }
+    }
+    float M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, x[k].x);
+    float den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) {
+      if (x[k].x == -INFINITY) continue;  // no visible key (or no tile): its partial holds nothing
+      const float w = exp2f(x[k].x - M);
+      den = fmaf(w, x[k].y, den);
+      acc.x = fmaf(w, o[k].x, acc.x);
+      acc.y = fmaf(w, o[k].y, acc.y);
+      acc.z = fmaf(w, o[k].z, acc.z);
+      acc.w = fmaf(w, o[k].w, acc.w);
+    }
+    const int t = r / G, g = r - t * G;
+    if (p.sinks && M != -INFINITY) den += exp2f(p.sinks[kvh * G + g] * 1.4426950408889634f - M);
+    const float inv = M != -INFINITY && den > 0.f ? 1.f / den : 0.f;
+    uint16_t* dst = p.out + (int64_t)(m.q0 + t) * p.o_s0 + (int64_t)(kvh * G + g) * p.o_s1 + 4 * c4;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(
+        (uint32_t)float_to_bf16_bits(acc.x * inv) | ((uint32_t)float_to_bf16_bits(acc.y * inv) << 16),
+        (uint32_t)float_to_bf16_bits(acc.z * inv) | ((uint32_t)float_to_bf16_bits(acc.w * inv) << 16));
+  }
+}
+
 // One (sequence, KV head) item's share of this CTA. Tile indices are absolute
 // within the sequence: the item's tiles are [tb, nt), this CTA's [lt0, lt1).
 struct Piece {
@@ -334,14 +415,6 @@ struct ScaleWindow {
 __device__ __forceinline__ void fail(const Params& p, volatile int* abort_flag, int code) {
   *abort_flag = 1;
   if (p.ws_status) atomicOr(p.ws_status, code);
-}
-
-__device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {
-  return __uint_as_float(((uint32_t)b) << 16);
-}
-
-__device__ __forceinline__ uint16_t float_to_bf16_bits(float f) {
-  return __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
 }  // namespace va

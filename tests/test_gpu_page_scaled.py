@@ -338,8 +338,8 @@ def test_waits_that_run_out(mla):
 @pytest.mark.parametrize("hq,q,kv", [(16, [4, 2], [1024, 769]), (16, [1, 1], [500, 40]), (8, [3], [100]), (12, [1, 4, 2], [30, 17, 700]),
                                      (64, [1], [2000])])
 def test_small_batches_in_the_promised_workspace(hq, q, kv):
-    """Small batches hand a KV head's query heads to several CTAs: in exactly the
-    workspace that the size call names, with garbage in it."""
+    """Small batches run as clusters: in exactly the workspace that the size call
+    names, with garbage in it."""
     w = make_workload(q, kv, hq, 1, "fp8_e4m3", seed=595).to("cuda")
     ks, vs = scales_for(w, 8)
     n = va.workspace_size(w.q, w.k_cache, w.seqused_k, w.max_seqlen_q, w.max_seqlen_k)
@@ -352,6 +352,66 @@ def test_small_batches_in_the_promised_workspace(hq, q, kv):
     ws = torch.full((n + 256,), 0xFF, dtype=torch.uint8, device="cuda")
     ws = ws[(-ws.data_ptr()) % 256:][:n]
     compare(run_mla(m, s, workspace=ws), *oracle_mla(m, s))
+
+
+# (sequences, KV heads, query heads, tokens, keys): clusters of 8, 4, 2 and 1
+# CTAs, with a KV head's query heads in one to sixteen of them, more sequences
+# than the kernels cache, and batches just past the clusters' reach
+CLUSTERS = [(1, 1, 16, [1], [900]), (1, 1, 64, [1], [130]), (2, 2, 32, [4], [700, 40]), (5, 1, 16, [4, 1], [1000, 300, 17]),
+            (7, 2, 6, [3], [500, 1]), (16, 1, 16, [2], [600, 513, 128]), (20, 1, 8, [4], [400, 129]), (33, 1, 5, [1, 0, 2], [300, 0, 64]),
+            (38, 2, 8, [2], [200, 127]), (70, 1, 4, [1], [150, 90, 1]), (76, 2, 4, [3], [100, 33]), (80, 2, 8, [1], [260, 16]),
+            (153, 1, 16, [1], [100, 20]), (600, 1, 2, [1, 2, 0], [40, 5, 17])]
+
+
+@pytest.mark.parametrize("ci", range(len(CLUSTERS)))
+@pytest.mark.parametrize("kw", [{}, dict(window_left=50, softcap=10.0, sinks=True)])
+def test_batches_of_every_size(ci, kw):
+    B, hkv, hq, q, kv = CLUSTERS[ci]
+    q, kv = [q[i % len(q)] for i in range(B)], [kv[i % len(kv)] for i in range(B)]
+    w = make_workload(q, kv, hq, hkv, "fp8_e4m3", seed=620 + ci).to("cuda")
+    ks, vs = scales_for(w, 60 + ci)
+    kw, okw = dict(kw), dict(kw)
+    if kw.get("sinks"):
+        kw["sinks"] = torch.linspace(-3, 3, hq, device="cuda")
+        okw["sinks"] = kw["sinks"].cpu().numpy().astype(np.float64)
+    compare(run(w, ks, vs, **kw), *oracle(w, ks, vs, **okw))
+    if hkv == 1 and not kw:
+        m = make_mla_workload(q, kv, hq, "fp8_e4m3", seed=640 + ci).to("cuda")
+        s, _ = scales_for(m, 80 + ci, spread=4.0)
+        compare(run_mla(m, s), *oracle_mla(m, s))
+
+
+@pytest.mark.parametrize("scale", [-0.0625, 0.0, 0.2])
+def test_sign_of_the_softmax_scale(scale):
+    w = make_workload([4, 2], [300, 130], 16, 1, "fp8_e4m3", seed=660).to("cuda")
+    m = make_mla_workload([4, 2], [300, 130], 16, "fp8_e4m3", seed=661).to("cuda")
+    w.softmax_scale, m.softmax_scale = scale, scale / 3
+    ks, vs = scales_for(w, 9)
+    s, _ = scales_for(m, 10, spread=4.0)
+    for splits in (0, 1, 3):
+        compare(run(w, ks, vs, num_splits=splits), *oracle(w, ks, vs))
+        compare(run_mla(m, s, num_splits=splits), *oracle_mla(m, s))
+
+
+def test_back_to_back_calls_on_changing_inputs():
+    """Unsynchronised calls whose inputs kernels rewrite right before each: the
+    results of the calls made alone (clusters, and the split over all CTAs)."""
+    for splits in (0, 5):
+        ws = [make_workload([4, 2, 3], [500, 129, 64], 16, 1, "fp8_e4m3", seed=670 + i).to("cuda") for i in range(2)]
+        sc = [[x.cuda() for x in scales_for(w, i)] for i, w in enumerate(ws)]
+        ref = [run(w, *s, num_splits=splits) for w, s in zip(ws, sc)]
+        cur, cs = ws[0], [x.clone() for x in sc[0]]
+        bufs = [cur.q.clone(), cur.k_cache.clone(), cur.v_cache.clone(), cur.block_table.clone()]
+        outs = []
+        for k in range(12):
+            w, s = ws[k % 2], sc[k % 2]
+            for dst, src in zip(bufs + cs, [w.q, w.k_cache, w.v_cache, w.block_table] + s):
+                (dst.view(torch.uint8) if dst.dtype == torch.float8_e4m3fn else dst).copy_(
+                    src.view(torch.uint8) if src.dtype == torch.float8_e4m3fn else src)
+            outs.append(va.verify_attn_scaled(*bufs[:3], *cs, bufs[3], w.cu_seqlens_q, w.seqused_k, w.max_seqlen_q, w.max_seqlen_k,
+                                              w.softmax_scale, num_splits=splits))
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, ref[k % 2]) for k, o in enumerate(outs))
 
 
 def test_workspace_errors():
