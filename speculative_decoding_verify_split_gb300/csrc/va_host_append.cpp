@@ -161,12 +161,15 @@ VA_EXPORT va_status verify_attn_append_kv(const va_tensor* q, const va_tensor* k
     if (s == VA_OK) s = check_rows(t);
   if (s != VA_OK) return s;
   if (!rows_distinct(k_cache) || !rows_distinct(v_cache)) return VA_ERR_LAYOUT;
+  // K and V in one place (views that interleave have different addresses)
+  if (k_cache->data && k_cache->data == v_cache->data) return VA_ERR_LAYOUT;
   if ((k_scales != nullptr) != (v_scales != nullptr)) return VA_ERR_NULL;
   if (k_scales) {
     if (k_cache->dtype != VA_FP8_E4M3) return VA_ERR_DTYPE;
     if (k_descale || v_descale) return VA_ERR_UNSUPPORTED;  // a page's scale is its descale
     s = check_page_scales(k_scales, k_cache->shape[0], hkv);
     if (s == VA_OK) s = check_page_scales(v_scales, k_cache->shape[0], hkv);
+    if (s == VA_OK && k_scales->data && k_scales->data == v_scales->data) s = VA_ERR_LAYOUT;
   } else {
     s = check_descale(k_descale);
     if (s == VA_OK) s = check_descale(v_descale);

@@ -51,6 +51,7 @@ def call_mla(**kw):
 BF, F8 = torch.bfloat16, torch.float8_e4m3fn
 E4 = dict(kc=torch.zeros(8, 16, 2, 256, dtype=torch.uint8).view(F8), vc=torch.zeros(8, 16, 2, 256, dtype=torch.uint8).view(F8))
 S82 = torch.ones(8, 2)
+ONE = torch.zeros(8, 16, 2, 256, dtype=BF)
 
 KV_BAD = [
     (dict(k=None), NULL), (dict(v=None), NULL), (dict(bt=None), NULL), (dict(cu=None), NULL), (dict(su=None), NULL),
@@ -82,6 +83,7 @@ KV_BAD = [
     (dict(E4, ks=torch.ones(1, 2).expand(8, 2), vs=S82), LAYOUT), (dict(E4, ks=S82, vs=torch.ones(8, 1).expand(8, 2)), LAYOUT),
     (dict(cos_sin=torch.zeros(64, 130)[:, :128]), LAYOUT), (dict(positions=torch.zeros(10, dtype=torch.int32)[::2]), LAYOUT),
     (dict(su=torch.zeros(4, dtype=torch.int32)[::2]), LAYOUT),
+    (dict(kc=ONE, vc=ONE), LAYOUT), (dict(E4, ks=S82, vs=S82), LAYOUT),                 # K and V in one place
 ]
 
 
