@@ -381,8 +381,9 @@ struct ScaleWindow {
   __device__ __forceinline__ void load(const Params& p, int kvh, int page, float& k, float& v) const {
     k = v = 1.f;
     if ((unsigned)page < (unsigned)p.num_blocks) {
-      k = p.k_scales[(int64_t)page * p.ks_s0 + (int64_t)kvh * p.ks_s1];
-      v = p.v_scales[(int64_t)page * p.vs_s0 + (int64_t)kvh * p.vs_s1];
+      // through L2: a CTA reads a scale once
+      k = __ldcg(p.k_scales + (int64_t)page * p.ks_s0 + (int64_t)kvh * p.ks_s1);
+      v = __ldcg(p.v_scales + (int64_t)page * p.vs_s0 + (int64_t)kvh * p.vs_s1);
     }
   }
   // Moves to the window of pages [win, win + 32); `step`: from one window's

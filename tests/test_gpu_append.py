@@ -133,6 +133,13 @@ def test_strided_tensors(kind):
 
 
 @pytest.mark.parametrize("mla", [False, True])
+def test_bf16_caches_take_descales(mla):
+    b = Batch([4, 3], [40, 35], 4, 1, "bf16", 64, 31, dim=576 if mla else 256)
+    b.descales = [torch.tensor([0.3]), torch.tensor([4.0])]
+    (check_mla if mla else check_kv)(b)
+
+
+@pytest.mark.parametrize("mla", [False, True])
 def test_empty_batches(mla):
     run = run_mla if mla else run_kv
     b = Batch([], [], 2, 1, "bf16", 64, 19, dim=576 if mla else 256)

@@ -130,3 +130,54 @@ def test_prompt_then_verify_steps(kind, latent):
     for k in range(6):
         d.step([4, 2 + k % 3, 1 + k % 4], True)
         d.take_back([k % 4, (k + 1) % 2, 0])       # refused drafts
+
+
+@pytest.mark.parametrize("latent", [False, True])
+@pytest.mark.parametrize("B", [1, 3, 40])
+def test_decoding_without_a_pause(latent, B):
+    """Steps of one token each, append and attention queued back to back with no
+    synchronisation (each kernel may start while the one before it ends): the
+    bits of the same steps with a pause after every call."""
+    g = torch.Generator().manual_seed(7)
+    steps, dim, width = 50, 576 if latent else 256, 8
+    size = torch.exp2(4 * torch.rand(steps, 1, 1, 1, generator=g) - 2)       # so that page scales grow on the way
+    kv = (size * torch.randn(steps, 2, B, dim, generator=g)).to(torch.bfloat16).cuda()
+    q0 = torch.randn(steps, B, 16, dim, generator=g).to(torch.bfloat16).cuda()
+    bt = torch.randperm(B * width, generator=g).int().reshape(B, width).cuda()
+    cu = torch.arange(B + 1, dtype=torch.int32).cuda()
+    used = [torch.full((B,), 30 + i, dtype=torch.int32).cuda() for i in range(steps)]
+    cos_sin = table(128, 64 if latent else 256).cuda()
+    big = torch.zeros(1 << 28, device="cuda")
+
+    def run(pause):
+        cache = [torch.zeros(B * width, 16, 1, dim, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.full((B * width, 1), 2.0 ** -12, device="cuda") for _ in range(2)]
+        outs = [torch.zeros(B, 16, 512 if latent else 256, dtype=torch.bfloat16, device="cuda") for _ in range(steps)]
+        q = q0.clone()
+        torch.cuda.synchronize()
+        if not pause:
+            for _ in range(8):
+                big.add_(1)                       # the launches queue up behind it
+        for i in range(steps):
+            if latent:
+                va.append_mla(kv[i, 0][:, :512], kv[i, 0][:, 512:], cache[0], bt, cu, used[i], q_pe=q[i][..., 512:],
+                              q_pe_out=q[i][..., 512:], cos_sin=cos_sin, scales=scales[0])
+            else:
+                va.append_kv(kv[i, 0][:, None], kv[i, 1][:, None], *cache, bt, cu, used[i], q=q[i], q_out=q[i], cos_sin=cos_sin,
+                             k_scales=scales[0], v_scales=scales[1])
+            if pause:
+                torch.cuda.synchronize()
+            if latent:
+                va.verify_attn_mla_scaled(q[i], cache[0], scales[0], bt, cu, used[i], 1, width * 16, dim ** -0.5, out=outs[i])
+            else:
+                va.verify_attn_scaled(q[i], *cache, *scales, bt, cu, used[i], 1, width * 16, dim ** -0.5, out=outs[i])
+            if pause:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs, cache, scales
+
+    a, b = run(True), run(False)
+    assert all(torch.equal(x, y) for x, y in zip(a[0], b[0]))
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a[1], b[1]))
+    assert all(torch.equal(x, y) for x, y in zip(a[2], b[2]))
+    assert not torch.equal(a[0][0], a[0][-1]) and a[0][-1].any()
