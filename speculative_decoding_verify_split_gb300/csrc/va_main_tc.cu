@@ -584,6 +584,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return ok;
     };
+    // S of tile cur and, page-scaled, its pages' scales, with one vote
+    auto wait_tile = [&](int cur) {
+      if (!ok) return false;
+      bool got = true;
+      if constexpr (SCL) got = mbar_wait(bar(kBarScales + cur % C::kVSlots), (cur / C::kVSlots) & 1, abort_flag, p.wait_limit_ns);
+      got = __all_sync(0xffffffffu, got && mbar_wait(bar(kBarSFull + (cur & (kSBufs - 1))), (cur / kSBufs) & 1, abort_flag,
+                                                     p.wait_limit_ns));
+      if (!got) {
+        if (lane == 0) fail(p, abort_flag, 256);
+        ok = false;
+      }
+      return ok;
+    };
     // Row-wide combine of a per-thread value: lanes t and t^16 share a row in
     // this warp, the partner warp of the quadrant holds the other half. Values
     // go through shared memory (double-buffered by round parity) around the
@@ -767,10 +780,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // pages (keys [0, 16) and [16, 32)); the factor stays a positive
         // normal number, so that a masked key's -inf stays -inf
         float xs2[2] = {xs, xs}, rx2[2] = {rx, rx}, lv[2] = {0.f, 0.f};
+        const bool here = wait_tile(cur);
         if constexpr (SCL) {
-          const int vs = cur % C::kVSlots;
-          if (wait_or_fail(kBarScales + vs, (cur / C::kVSlots) & 1, 8192)) {
-            const float4 sc = reinterpret_cast<const float4*>(sm + C::kOffBar + kOffScales)[vs * (kPagesPerTile / 2) + qtr];
+          if (here) {
+            const float4 sc = reinterpret_cast<const float4*>(sm + C::kOffBar + kOffScales)[(cur % C::kVSlots) * (kPagesPerTile / 2) + qtr];
             lv[0] = sc.y;
             lv[1] = sc.w;
             if (VAR && p.softcap_log2 > 0.f) {
@@ -782,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (wait_or_fail(kBarSFull + b, (cur / kSBufs) & 1, 256)) {
+        if (here) {
           tc_fence_after();
           if constexpr (FP8) {
             // the hi and lo partials of row 16q + rl, keys [64 kh + 32 sub,

@@ -79,7 +79,7 @@ static_assert(kSmemBytes + 1024 <= 232448, "shared memory (with the 1 KB alignme
 static_assert(kTileBytes % 1024 == 0 && kOffQpe % 1024 == 0, "swizzle atoms");
 static_assert((kPBufs & (kPBufs - 1)) == 0, "P buffers: a power of two");
 
-constexpr int kThreads = 416;  // 13 warps
+constexpr int kThreads = 512;  // 16 warps
 constexpr int kSoftmaxThreads = 256;
 constexpr int kBarAllSoftmax = 5;  // named barriers: 1-4 per quadrant, 5 all softmax warps
 
@@ -101,6 +101,11 @@ constexpr uint32_t kIdPV = instr_desc(0, 0, false, 64, 128, true);   // A = V^T 
 // flushed to zero below m_ref - 16 carry no more mass than with 1.
 constexpr float kPShift = 6.f;
 constexpr float kHeadroom = 1.f;
+// Page scales spread the logits further (both the keys and the weights take
+// them), so the reference moves ten times as often; 3 instead of 1 saves a
+// sixth of the moves (latent mid context 179.9 -> 178.6 us) and costs no
+// accuracy beside kHeadroomFirst, which leaves as many keys below the floor.
+constexpr float kHeadroomScaled = 3.f;
 constexpr float kHeadroomFirst = 4.f;
 constexpr float kOvershoot = 2.8f;
 
@@ -266,14 +271,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
 
+  const bool alt = p.max_rows <= 48;
+  const int prod = alt ? (warp < 3 ? warp : -1) : (warp == 0 ? 0 : (warp == 2 || warp == 3) ? warp - 1 : -1);
+  const bool qk_warp = warp == (alt ? 3 : 1), pv_warp = warp == (alt ? 15 : 12);
   if (CLU && t0 >= t1) {
     if (tid < kMaxRows) {
       part_ml[2 * tid] = -INFINITY;
       part_ml[2 * tid + 1] = 0.f;
     }
-  } else if (warp == 0 || warp == 2 || warp == 3) {
+  } else if (prod >= 0) {
     // ======================= TMA producers ======================================
-    const int prod = warp == 0 ? 0 : warp - 1;
     const uint64_t kv_policy = l2_evict_first_policy();  // the cache rows are read once
     int it = 0;
     int j = j_first;
@@ -362,10 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1 || warp == 12) {
+  } else if (qk_warp || pv_warp) {
     // ======================= MMA issuers ==========================================
     if (lane == 0) {
-      const bool is_qk = warp == 1;
+      const bool is_qk = qk_warp;
       const uint32_t qpe = sbase + kOffQpe;
       int it = 0, piece_idx = 0;
       int j = j_first;
@@ -475,6 +482,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool got = __all_sync(0xffffffffu, mbar_wait(bar(b), par, abort_flag, p.wait_limit_ns));
       if (!got) {
         if (lane == 0) fail(p, abort_flag, code);
+        ok = false;
+      }
+      return ok;
+    };
+    // S of tile cur, page-scaled its pages' scales, and the P buffer that P V of
+    // tile cur - kPBufs read, with one vote
+    auto wait_tile = [&](int cur) {
+      if (!ok) return false;
+      bool got = true;
+      if constexpr (SCL) got = mbar_wait(bar(kBarScales + cur % kSlots), (cur / kSlots) & 1, abort_flag, p.wait_limit_ns);
+      got = got && mbar_wait(bar(kBarSFull + (cur & (kSBufs - 1))), (cur / kSBufs) & 1, abort_flag, p.wait_limit_ns);
+      if (cur >= kPBufs)
+        got = got && mbar_wait(bar(kBarPFree + (cur & (kPBufs - 1))), ((cur - kPBufs) / kPBufs) & 1, abort_flag,
+                               p.wait_limit_ns);
+      got = __all_sync(0xffffffffu, got);
+      if (!got) {
+        if (lane == 0) fail(p, abort_flag, 256);
         ok = false;
       }
       return ok;
@@ -591,6 +615,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = r < pc.R;
       const int tq = row_ok ? r / G : 0;
 
+      // a quadrant none of whose 16 rows is in use has no S to read and no P to
+      // write (its P rows reach only output columns that are never read); it
+      // takes part in the votes, the rescales, the epilogue
+      const bool idle = 16 * q >= pc.R;
       float m_ref = -INFINITY;
       float l = 0.f;
       const int vis_end = pc.S - pc.L + tq;  // last visible key of this row
@@ -609,15 +637,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the factor of the raw dot products (a positive normal number: -inf
         // stays -inf) and, page-scaled, the offset log2 scale of the page
         float xs = rs, lv = 0.f;
-        if constexpr (SCL) {
-          const int s = cur % kSlots;
-          if (wait_or_fail(kBarScales + s, (cur / kSlots) & 1, 8192)) {
-            const float2 sc = reinterpret_cast<const float2*>(sm + kOffBar + kOffScales)[s * kPagesPerTile + qtr];
-            xs = fmaxf(rs * sc.x, 1.2e-38f);
-            lv = sc.y;
-          }
+        const bool here = wait_tile(cur);
+        if (SCL && here) {
+          const float2 sc = reinterpret_cast<const float2*>(sm + kOffBar + kOffScales)[(cur % kSlots) * kPagesPerTile + qtr];
+          xs = fmaxf(rs * sc.x, 1.2e-38f);
+          lv = sc.y;
         }
-        if (wait_or_fail(kBarSFull + b, (cur / kSBufs) & 1, 256)) {
+        if (idle) {
+          if (here && lane == 0) mbar_arrive(bar(kBarSFree + b));
+        } else if (here) {
           tc_fence_after();
           // the hi and lo partials of row r, keys [32 kh + 16 sub, +16): two
           // 16-lane loads (hi rows in lanes 32q.., lo rows in lanes
@@ -658,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (named_bar_or(kBarAllSoftmax, kSoftmaxThreads, ok && tmax > m_ref + kOvershoot)) {
           tmax = exchange(tmax, true);
           const bool need = ok && tmax > m_ref + kOvershoot;
-          m_new = need ? tmax + (m_ref == -INFINITY ? kHeadroomFirst : kHeadroom) : m_ref;
+          m_new = need ? tmax + (m_ref == -INFINITY ? kHeadroomFirst : SCL ? kHeadroomScaled : kHeadroom) : m_ref;
           const bool rescale = need && (m_ref != -INFINITY) && (cur > first);
           alpha = rescale ? ex2(m_ref - m_new) : 1.f;
           // O^T keeps a row in a column across all 128 lanes: every softmax
@@ -669,48 +697,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) continue;
 
-        // P buffer pb was last read by P V(cur - kPBufs)
-        if (cur >= kPBufs && !wait_or_fail(kBarPFree + pb, ((cur - kPBufs) / kPBufs) & 1, 512)) continue;
         // a row with no visible key yet (m_new = -inf) gets P = ex2(-inf) = 0
         const float mref_s = m_new != -INFINITY ? m_new - kPShift : INFINITY;
-        uint32_t ph[4], pl[4];
         float ls = 0.f;
-        const float off2 = SCL ? lv - mref_s : -mref_s;
+        if (!idle) {
+          uint32_t ph[4], pl[4];
+          const float off2 = SCL ? lv - mref_s : -mref_s;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = ex2(fmaf(x[2 * i], xs, off2));
-          const float bb = ex2(fmaf(x[2 * i + 1], xs, off2));
-          ls += a + bb;
-          uint32_t h2, l2;
-          split_p(a, bb, h2, l2);
-          if (i & 1) {
-            ph[i >> 1] |= h2 << 16;
-            pl[i >> 1] |= l2 << 16;
-          } else {
-            ph[i >> 1] = h2;
-            pl[i >> 1] = l2;
+          for (int i = 0; i < 8; ++i) {
+            const float a = ex2(fmaf(x[2 * i], xs, off2));
+            const float bb = ex2(fmaf(x[2 * i + 1], xs, off2));
+            ls += a + bb;
+            uint32_t h2, l2;
+            split_p(a, bb, h2, l2);
+            if (i & 1) {
+              ph[i >> 1] |= h2 << 16;
+              pl[i >> 1] |= l2 << 16;
+            } else {
+              ph[i >> 1] = h2;
+              pl[i >> 1] = l2;
+            }
           }
+          // P^T operand: row r, keys [16 qtr, +16) = one core-matrix row
+          unsigned char* pbuf = sm + kOffP + pb * kPBuf;
+          const int off = core_off(r, 16 * qtr, kT);
+          *reinterpret_cast<uint4*>(pbuf + off) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+          *reinterpret_cast<uint4*>(pbuf + kPHalf + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
         }
-        // P^T operand: row r, keys [16 qtr, +16) = one core-matrix row
-        unsigned char* pbuf = sm + kOffP + pb * kPBuf;
-        const int off = core_off(r, 16 * qtr, kT);
-        *reinterpret_cast<uint4*>(pbuf + off) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-        *reinterpret_cast<uint4*>(pbuf + kPHalf + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
         // then the rows that moved (P V(cur - 1) has to be in O^T first; the
         // wait overlaps the work above)
         if (any) {
           const int xp = cur - 1;
           if (!wait_or_fail(kBarPFree + (xp & (kPBufs - 1)), (xp / kPBufs) & 1, 1024)) continue;
           tc_fence_after();
+          // the factors of rows [0, 32) and [32, 64), four to a load; a half in
+          // which no row moved stays as it is
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t o[32];
-            const uint32_t ta = tmem + lane_base + kColO + 64 * (2 * kh + (k >> 1)) + 32 * (k & 1);
-            tmem_ld_32x32b_x32(ta, o);
-            tmem_wait_ld();
+          for (int half = 0; half < 2; ++half) {
+            if (!__any_sync(0xffffffffu, al[32 * half + lane] != 1.f)) continue;
+            const float4* af = reinterpret_cast<const float4*>(al + 32 * half);
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+              uint32_t o[32];
+              const uint32_t ta = tmem + lane_base + kColO + 64 * (2 * kh + k) + 32 * half;
+              tmem_ld_32x32b_x32(ta, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al[32 * (k & 1) + i]);
-            tmem_st_32x32b_x32(ta, o);
+              for (int i = 0; i < 8; ++i) {
+                const float4 f = af[i];
+                o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * f.x);
+                o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * f.y);
+                o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * f.z);
+                o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * f.w);
+              }
+              tmem_st_32x32b_x32(ta, o);
+            }
           }
           tmem_wait_st();
         }
