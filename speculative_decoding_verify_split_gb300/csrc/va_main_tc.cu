@@ -741,6 +741,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tq = row_ok ? r / G : 0;
       const int gq = row_ok ? r - tq * G : 0;
 
+      // a quadrant none of whose 16 rows is in use reads no S and writes no P (its
+      // P lanes reach only lanes of O that are never read)
+      const bool idle = 16 * q >= pc.R;
       // -- key tiles
       float m_ref = -INFINITY;
       float l = 0.f;
@@ -795,179 +798,187 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (here) {
-          tc_fence_after();
-          if constexpr (FP8) {
-            // the hi and lo partials of row 16q + rl, keys [64 kh + 32 sub,
-            // +32): two 16-lane loads (hi rows in lanes 32q.., lo rows in
-            // lanes 32q + 16..) whose second halves go to threads 16-31, so
-            // every thread gets both terms of its own keys. S buffer b is then
-            // free for Q K^T of a later tile, or is overwritten by P(cur) and
-            // freed by P V's commit.
-            uint32_t vh[32], vl[32];
-            tmem_ld_16x32bx2_x32<32>(tmem + lane_base + kColS + b * kT + 64 * kh, vh);
-            tmem_ld_16x32bx2_x32<32>(tmem + lane_base + (16u << 16) + kColS + b * kT + 64 * kh, vl);
-            tmem_wait_ld();
-            tc_fence_before();
-            if constexpr (!C::kPOverS) {
+        if (idle) {
+          if constexpr (!C::kPOverS) {
+            if (here && lane == 0) mbar_arrive(bar(kBarSFree + b));
+            if (cur >= kPBufs) wait_or_fail(kBarPFree + pb, ((cur - kPBufs) / kPBufs) & 1, 512);
+          }
+          if (!ok) continue;
+        } else {
+          if (here) {
+            tc_fence_after();
+            if constexpr (FP8) {
+              // the hi and lo partials of row 16q + rl, keys [64 kh + 32 sub,
+              // +32): two 16-lane loads (hi rows in lanes 32q.., lo rows in
+              // lanes 32q + 16..) whose second halves go to threads 16-31, so
+              // every thread gets both terms of its own keys. S buffer b is then
+              // free for Q K^T of a later tile, or is overwritten by P(cur) and
+              // freed by P V's commit.
+              uint32_t vh[32], vl[32];
+              tmem_ld_16x32bx2_x32<32>(tmem + lane_base + kColS + b * kT + 64 * kh, vh);
+              tmem_ld_16x32bx2_x32<32>(tmem + lane_base + (16u << 16) + kColS + b * kT + 64 * kh, vl);
+              tmem_wait_ld();
+              tc_fence_before();
+              if constexpr (!C::kPOverS) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarSFree + b));
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(vh[i]) + __uint_as_float(vl[i]);
+            } else {
+              uint32_t v[16];
+              tmem_ld_16x32bx2_x16<16>(tmem + lane_base + kColS + b * kT + 32 * kh, v);
+              tmem_wait_ld();
+              tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(kBarSFree + b));
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
             }
+            if constexpr (VAR) {
+              if (p.softcap_log2 > 0.f) {
+                // soft cap c tanh(logit / c), before masking, kept as the tanh
+                // (see xs). tanh.approx's relative error of ~2^-11 moves a
+                // logit l by at most |l| 2^-11 log2 units (0.5 % of a key's
+                // weight at l = 10).
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(vh[i]) + __uint_as_float(vl[i]);
-          } else {
-            uint32_t v[16];
-            tmem_ld_16x32bx2_x16<16>(tmem + lane_base + kColS + b * kT + 32 * kh, v);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarSFree + b));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
-          }
-          if constexpr (VAR) {
-            if (p.softcap_log2 > 0.f) {
-              // soft cap c tanh(logit / c), before masking, kept as the tanh
-              // (see xs). tanh.approx's relative error of ~2^-11 moves a
-              // logit l by at most |l| 2^-11 log2 units (0.5 % of a key's
-              // weight at l = 10).
-#pragma unroll
-              for (int i = 0; i < kKpt; ++i) x[i] = tanh_approx(x[i] * (SCL ? rx2[i / 16] : rx));
+                for (int i = 0; i < kKpt; ++i) x[i] = tanh_approx(x[i] * (SCL ? rx2[i / 16] : rx));
+              }
             }
-          }
-          const int key0 = lt * kT + kKpt * qtr;
-          if (lt * kT + kT - 1 > mask_from) {  // tail tile: causal mask
-#pragma unroll
-            for (int i = 0; i < kKpt; ++i)
-              if (key0 + i > vis_end) x[i] = -INFINITY;
-          }
-          if constexpr (VAR) {
-            if (lt * kT < vis_lo_max) {  // a window's first tiles: keys before the row's window
+            const int key0 = lt * kT + kKpt * qtr;
+            if (lt * kT + kT - 1 > mask_from) {  // tail tile: causal mask
 #pragma unroll
               for (int i = 0; i < kKpt; ++i)
-                if (key0 + i < vis_lo) x[i] = -INFINITY;
+                if (key0 + i > vis_end) x[i] = -INFINITY;
+            }
+            if constexpr (VAR) {
+              if (lt * kT < vis_lo_max) {  // a window's first tiles: keys before the row's window
+#pragma unroll
+                for (int i = 0; i < kKpt; ++i)
+                  if (key0 + i < vis_lo) x[i] = -INFINITY;
+              }
             }
           }
-        }
-        float tmax = -INFINITY;
-        if constexpr (SCL) {
-          float t2[2] = {-INFINITY, -INFINITY};
+          float tmax = -INFINITY;
+          if constexpr (SCL) {
+            float t2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < kKpt; i += 2) t2[i / 16] = fmax3(t2[i / 16], x[i], x[i + 1]);
-          tmax = exchange(fmaxf(fmaf(t2[0], xs2[0], lv[0]), fmaf(t2[1], xs2[1], lv[1])), true);
-        } else {
+            for (int i = 0; i < kKpt; i += 2) t2[i / 16] = fmax3(t2[i / 16], x[i], x[i + 1]);
+            tmax = exchange(fmaxf(fmaf(t2[0], xs2[0], lv[0]), fmaf(t2[1], xs2[1], lv[1])), true);
+          } else {
 #pragma unroll
-          for (int i = 0; i < kKpt; i += 2) tmax = fmax3(tmax, x[i], x[i + 1]);
-          tmax = exchange(tmax * xs, true);  // log2 units (xs > 0 keeps the order)
-        }
-        if (!ok) continue;
+            for (int i = 0; i < kKpt; i += 2) tmax = fmax3(tmax, x[i], x[i + 1]);
+            tmax = exchange(tmax * xs, true);  // log2 units (xs > 0 keeps the order)
+          }
+          if (!ok) continue;
 
-        // P buffer pb was last read by PV(cur - kPBufs). (A P over S(cur):
-        // Q K^T(cur) already waited for that.)
-        if (!C::kPOverS && cur >= kPBufs &&
-            !wait_or_fail(kBarPFree + pb, ((cur - kPBufs) / kPBufs) & 1, 512))
-          continue;
+          // P buffer pb was last read by PV(cur - kPBufs). (A P over S(cur):
+          // Q K^T(cur) already waited for that.)
+          if (!C::kPOverS && cur >= kPBufs &&
+              !wait_or_fail(kBarPFree + pb, ((cur - kPBufs) / kPBufs) & 1, 512))
+            continue;
 
-        const bool need = tmax > m_ref + kOvershoot;
-        // A row's first reference takes more headroom: its running max keeps
-        // growing over the next tiles (by ~sd * (sqrt(2 ln n) - sqrt(2 ln T))),
-        // and every later move waits for P V of the previous tile.
-        const float m_new = need ? tmax + (m_ref == -INFINITY ? kHeadroomFirst : kHeadroom) : m_ref;
-        const bool rescale = need && (m_ref != -INFINITY) && (cur > first);
-        const float alpha = rescale ? ex2(m_ref - m_new) : 1.f;
-        if (__any_sync(0xffffffffu, rescale)) {
-          // O holds earlier tiles of this piece: wait for PV(cur - 1), then
-          // scale this thread's part of the row in TMEM
-          const int xp = cur - 1;
-          if (!wait_or_fail(kBarPFree + (xp & (kPBufs - 1)), (xp / kPBufs) & 1, 1024)) continue;
-          tc_fence_after();
+          const bool need = tmax > m_ref + kOvershoot;
+          // A row's first reference takes more headroom: its running max keeps
+          // growing over the next tiles (by ~sd * (sqrt(2 ln n) - sqrt(2 ln T))),
+          // and every later move waits for P V of the previous tile.
+          const float m_new = need ? tmax + (m_ref == -INFINITY ? kHeadroomFirst : kHeadroom) : m_ref;
+          const bool rescale = need && (m_ref != -INFINITY) && (cur > first);
+          const float alpha = rescale ? ex2(m_ref - m_new) : 1.f;
+          if (__any_sync(0xffffffffu, rescale)) {
+            // O holds earlier tiles of this piece: wait for PV(cur - 1), then
+            // scale this thread's part of the row in TMEM
+            const int xp = cur - 1;
+            if (!wait_or_fail(kBarPFree + (xp & (kPBufs - 1)), (xp / kPBufs) & 1, 1024)) continue;
+            tc_fence_after();
 #pragma unroll 1
-          for (int k = 0; k < (FP8 ? 4 : 2); ++k) {
-            uint32_t o[32];
-            const uint32_t ta = tmem + lane_base + kColO + 128 * kh + 32 * k;
-            if constexpr (FP8) {
-              tmem_ld_32x32b_x32(ta, o);
-              tmem_wait_ld();
+            for (int k = 0; k < (FP8 ? 4 : 2); ++k) {
+              uint32_t o[32];
+              const uint32_t ta = tmem + lane_base + kColO + 128 * kh + 32 * k;
+              if constexpr (FP8) {
+                tmem_ld_32x32b_x32(ta, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st_32x32b_x32(ta, o);
-            } else {
-              tmem_ld_16x32bx2_x32<64>(ta, o);
-              tmem_wait_ld();
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st_32x32b_x32(ta, o);
+              } else {
+                tmem_ld_16x32bx2_x32<64>(ta, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st_16x32bx2_x32<64>(ta, o);
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st_16x32bx2_x32<64>(ta, o);
+              }
             }
+            tmem_wait_st();
           }
-          tmem_wait_st();
-        }
-        l *= alpha;
-        m_ref = m_new;
+          l *= alpha;
+          m_ref = m_new;
 
-        // P = 2^(x - m_ref + kPShift) into the K-major no-swizzle A operand
-        // a row with no visible key yet (m_ref = -inf) gets P = ex2(-inf) = 0
-        const float mref_s = m_ref != -INFINITY ? m_ref - kPShift : INFINITY;
-        float ls0 = 0.f, ls1 = 0.f;
-        unsigned char* pbuf = sm + C::kOffP + pb * C::kPBuf;
-        if constexpr (FP8) {
-          uint32_t ph[8], pl[8];
-          const float off2[2] = {lv[0] - mref_s, lv[1] - mref_s};
+          // P = 2^(x - m_ref + kPShift) into the K-major no-swizzle A operand
+          // a row with no visible key yet (m_ref = -inf) gets P = ex2(-inf) = 0
+          const float mref_s = m_ref != -INFINITY ? m_ref - kPShift : INFINITY;
+          float ls0 = 0.f, ls1 = 0.f;
+          unsigned char* pbuf = sm + C::kOffP + pb * C::kPBuf;
+          if constexpr (FP8) {
+            uint32_t ph[8], pl[8];
+            const float off2[2] = {lv[0] - mref_s, lv[1] - mref_s};
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float a = ex2(SCL ? fmaf(x[2 * i], xs2[i / 8], off2[i / 8]) : fmaf(x[2 * i], xs, -mref_s));
-            const float bb = ex2(SCL ? fmaf(x[2 * i + 1], xs2[i / 8], off2[i / 8]) : fmaf(x[2 * i + 1], xs, -mref_s));
-            if (SCL) {
-              // ls0, ls1: the sums of the first and of the second page
-              if (i < 8)
-                ls0 += a + bb;
-              else
-                ls1 += a + bb;
-            } else {
+            for (int i = 0; i < 16; ++i) {
+              const float a = ex2(SCL ? fmaf(x[2 * i], xs2[i / 8], off2[i / 8]) : fmaf(x[2 * i], xs, -mref_s));
+              const float bb = ex2(SCL ? fmaf(x[2 * i + 1], xs2[i / 8], off2[i / 8]) : fmaf(x[2 * i + 1], xs, -mref_s));
+              if (SCL) {
+                // ls0, ls1: the sums of the first and of the second page
+                if (i < 8)
+                  ls0 += a + bb;
+                else
+                  ls1 += a + bb;
+              } else {
+                ls0 += a;
+                ls1 += bb;
+              }
+              uint32_t h2, l2;
+              split_p(a, bb, h2, l2);
+              if (i & 1) {
+                ph[i >> 1] |= h2 << 16;
+                pl[i >> 1] |= l2 << 16;
+              } else {
+                ph[i >> 1] = h2;
+                pl[i >> 1] = l2;
+              }
+            }
+            // A operand of P V in TMEM, P tile pb or over S(cur) (pb == b
+            // then): lane 32q + rl (hi row) and
+            // lane 32q + 16 + rl (lo row) take the e4m3 bytes of keys
+            // [64 kh, +64) at columns [16 kh, +16). This thread holds keys
+            // [32 qtr, +32) of both: two 16-lane stores, its hi bytes into the
+            // hi row and its lo bytes into the lo row, threads 16-31 at +8.
+            // Over S, the quadrant's other warp read its S columns before the
+            // exchange.
+            const uint32_t pcol = C::kPOverS ? kColS + pb * kT : kColP + pb * (kT / 4);
+            tc_fence_after();
+            tmem_st_16x32bx2_x8<8>(tmem + lane_base + pcol + 16 * kh, ph);
+            tmem_st_16x32bx2_x8<8>(tmem + lane_base + (16u << 16) + pcol + 16 * kh, pl);
+            tmem_wait_st();
+          } else {
+            uint32_t pw[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float a = ex2(fmaf(x[2 * i], xs, -mref_s));
+              const float bb = ex2(fmaf(x[2 * i + 1], xs, -mref_s));
               ls0 += a;
               ls1 += bb;
+              pw[i] = pack_bf16x2(a, bb);
             }
-            uint32_t h2, l2;
-            split_p(a, bb, h2, l2);
-            if (i & 1) {
-              ph[i >> 1] |= h2 << 16;
-              pl[i >> 1] |= l2 << 16;
-            } else {
-              ph[i >> 1] = h2;
-              pl[i >> 1] = l2;
-            }
+            // keys [16 qtr, +16) = 32 bytes = core-matrix columns 2 qtr, 2 qtr + 1 of row r
+            unsigned char* base = pbuf + (r >> 3) * C::kPSbo + (2 * qtr) * 128 + (r & 7) * 16;
+            *reinterpret_cast<uint4*>(base) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+            *reinterpret_cast<uint4*>(base + 128) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
           }
-          // A operand of P V in TMEM, P tile pb or over S(cur) (pb == b
-          // then): lane 32q + rl (hi row) and
-          // lane 32q + 16 + rl (lo row) take the e4m3 bytes of keys
-          // [64 kh, +64) at columns [16 kh, +16). This thread holds keys
-          // [32 qtr, +32) of both: two 16-lane stores, its hi bytes into the
-          // hi row and its lo bytes into the lo row, threads 16-31 at +8.
-          // Over S, the quadrant's other warp read its S columns before the
-          // exchange.
-          const uint32_t pcol = C::kPOverS ? kColS + pb * kT : kColP + pb * (kT / 4);
-          tc_fence_after();
-          tmem_st_16x32bx2_x8<8>(tmem + lane_base + pcol + 16 * kh, ph);
-          tmem_st_16x32bx2_x8<8>(tmem + lane_base + (16u << 16) + pcol + 16 * kh, pl);
-          tmem_wait_st();
-        } else {
-          uint32_t pw[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float a = ex2(fmaf(x[2 * i], xs, -mref_s));
-            const float bb = ex2(fmaf(x[2 * i + 1], xs, -mref_s));
-            ls0 += a;
-            ls1 += bb;
-            pw[i] = pack_bf16x2(a, bb);
-          }
-          // keys [16 qtr, +16) = 32 bytes = core-matrix columns 2 qtr, 2 qtr + 1 of row r
-          unsigned char* base = pbuf + (r >> 3) * C::kPSbo + (2 * qtr) * 128 + (r & 7) * 16;
-          *reinterpret_cast<uint4*>(base) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
-          *reinterpret_cast<uint4*>(base + 128) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
+          if constexpr (SCL)
+            l += ls0 * ex2(-lv[0]) + ls1 * ex2(-lv[1]);  // the weights without vs
+          else
+            l += ls0 + ls1;
         }
-        if constexpr (SCL)
-          l += ls0 * ex2(-lv[0]) + ls1 * ex2(-lv[1]);  // the weights without vs
-        else
-          l += ls0 + ls1;
         // V rows no row may see and whose pages may hold anything are zeroed,
         // so that 0 * garbage cannot reach O: past S in the item's last tile
         // (partial page, pages never loaded), and in its first tile the pages
