@@ -52,7 +52,7 @@ constexpr int kRegion = kT * 128;              // 8 KB: 64 rows x 128 bytes, 128
 constexpr int kPeRegion = kT * kMlaPe;         // 4 KB: 64 rows x 64 bytes, 64-byte swizzle
 constexpr int kTileBytes = 4 * kRegion + kPeRegion;  // 36 KB
 constexpr int kSlots = 5;
-constexpr int kProducers = 3;                  // warps 0, 2, 3 take every third tile
+constexpr int kProducers = 3;                  // producer warps: each takes every third tile
 // A producer's wait for a slot relies on its own previous wait (kProducers
 // tiles back) to keep that slot's empty barrier within one phase.
 static_assert(kProducers <= kSlots, "producers exceed the ring");
@@ -160,7 +160,11 @@ __device__ __forceinline__ int core_off(int m, int k, int row_bytes) {
 // GQA kernel it multiplies the page's logits, and as the value's scale joins
 // the weight, P = 2^(s + log2 scale - m_ref), with l summing P / scale. A
 // thread's 16 keys of a tile are one page. The producers bring the scales
-// with the ring slot. CLU: one cluster of CTAs per item, as in the GQA kernel.
+// with the ring slot. 64 sequences of 8K to 32K keys, 3 draft tokens (733 MB):
+// 175 us (the bound is the MMA instruction rate and the piece boundaries, as
+// without scales). CLU: one cluster of CTAs per item, as in the GQA kernel: two
+// sequences of 1,024 and 769 keys 14.2 us a call (23.3 split over all CTAs),
+// 4.0 of them staging Q's 576 columns.
 template <bool SCL, bool CLU>
 __global__ void __launch_bounds__(kThreads, 1)
     va_mla_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tm_kv,
@@ -271,6 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
 
+  // With at most 48 packed rows the softmax warps of quadrant 3 are idle; the
+  // two MMA issuers then sit on that quadrant's scheduler, where no ALU work
+  // competes with them (latent mid context, 48 rows: 190.6 -> 184.0 us).
   const bool alt = p.max_rows <= 48;
   const int prod = alt ? (warp < 3 ? warp : -1) : (warp == 0 ? 0 : (warp == 2 || warp == 3) ? warp - 1 : -1);
   const bool qk_warp = warp == (alt ? 3 : 1), pv_warp = warp == (alt ? 15 : 12);
@@ -353,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (SCL) {
           const int i = win + lane - pg0;
           if (i >= 0 && i < kPagesPerTile)
-            reinterpret_cast<float2*>(sm + kOffBar + kOffScales)[s * kPagesPerTile + i] = softmax_scales(sw.ks, sw.vs);
+            reinterpret_cast<float2*>(sm + kOffBar + kOffScales)[s * kPagesPerTile + i] =
+                softmax_scales(sw.ks, sw.vs);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarScales + s));
         }
@@ -491,7 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_tile = [&](int cur) {
       if (!ok) return false;
       bool got = true;
-      if constexpr (SCL) got = mbar_wait(bar(kBarScales + cur % kSlots), (cur / kSlots) & 1, abort_flag, p.wait_limit_ns);
+      if constexpr (SCL)
+        got = mbar_wait(bar(kBarScales + cur % kSlots), (cur / kSlots) & 1, abort_flag, p.wait_limit_ns);
       got = got && mbar_wait(bar(kBarSFull + (cur & (kSBufs - 1))), (cur / kSBufs) & 1, abort_flag, p.wait_limit_ns);
       if (cur >= kPBufs)
         got = got && mbar_wait(bar(kBarPFree + (cur & (kPBufs - 1))), ((cur - kPBufs) / kPBufs) & 1, abort_flag,
@@ -639,7 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float xs = rs, lv = 0.f;
         const bool here = wait_tile(cur);
         if (SCL && here) {
-          const float2 sc = reinterpret_cast<const float2*>(sm + kOffBar + kOffScales)[(cur % kSlots) * kPagesPerTile + qtr];
+          const float2 sc =
+              reinterpret_cast<const float2*>(sm + kOffBar + kOffScales)[(cur % kSlots) * kPagesPerTile + qtr];
           xs = fmaxf(rs * sc.x, 1.2e-38f);
           lv = sc.y;
         }
@@ -836,7 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (CLU) {
     __syncwarp();
     cluster_sync();  // every CTA's partial is written
-    join_cluster<kThreads, kMlaNope>(p, c / p.cluster, meta, c % p.cluster, smem_addr(part), kMlaNope, smem_addr(part_ml));
+    join_cluster<kThreads, kMlaNope>(p, c / p.cluster, meta, c % p.cluster, smem_addr(part), kMlaNope,
+                                     smem_addr(part_ml));
     cluster_sync();  // no CTA ends while another still reads it
   }
 }
