@@ -190,6 +190,17 @@ def _native():
     return _NATIVE
 
 
+def _empty(shape, like, stream):
+    """An output that the call creates: from the allocator's pool of the stream
+    that writes it, so that memory freed by its owner is not reused under it."""
+    if stream is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+
+
 def _handle(stream):
     """A stream argument of the compiled binding (None: the current one)."""
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
@@ -551,7 +562,7 @@ def append_kv(k, v, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, q=No
     ``verify_attn_scaled``. Caches and scales are written in place. Returns
     ``q_out`` (created if q is given without it; it may be q itself), or None."""
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _empty(q.shape, q, stream)
     s = _native().append_kv(q, k, v, block_table, cu_seqlens_q, seqused_k, k_descale, v_descale,
                             k_scales, v_scales, q_out, k_cache, v_cache, cos_sin, positions,
                             interleaved, _handle(stream))
@@ -569,7 +580,7 @@ def append_mla(latent, k_pe, kv_cache, block_table, cu_seqlens_q, seqused_k, q_p
     ``verify_attn_mla_scaled``). q_pe_out is usually ``q[..., 512:]``. Returns
     ``q_pe_out``, or None."""
     if q_pe is not None and q_pe_out is None:
-        q_pe_out = torch.empty(q_pe.shape, dtype=q_pe.dtype, device=q_pe.device)
+        q_pe_out = _empty(q_pe.shape, q_pe, stream)
     s = _native().append_mla(q_pe, latent, k_pe, block_table, cu_seqlens_q, seqused_k, descale,
                              scales, q_pe_out, kv_cache, cos_sin, positions, interleaved,
                              _handle(stream))
@@ -589,7 +600,7 @@ def verify_attn_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_
     device tensor, zeroed before its first use if its status word is to be
     read) None: one of the call's own, from torch's allocator."""
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _empty(q.shape, q, stream)
     s = _native().attn_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_seqlens_q,
                               seqused_k, out, sinks, max_seqlen_q, max_seqlen_k, softmax_scale,
                               window_left, softcap, workspace, num_splits,
@@ -607,7 +618,7 @@ def verify_attn_mla_scaled(q, kv_cache, scales, block_table, cu_seqlens_q, sequs
     include/verify_attn.h): scales [num_blocks, 1] fp32, as ``append_mla``
     writes them. ``workspace`` as for ``verify_attn_scaled``."""
     if out is None:
-        out = torch.empty(q.shape[0], q.shape[1], MLA_NOPE, dtype=torch.bfloat16, device=q.device)
+        out = _empty((*q.shape[:2], MLA_NOPE), q, stream)
     s = _native().attn_mla_scaled(q, kv_cache, scales, block_table, cu_seqlens_q, seqused_k, out,
                                   max_seqlen_q, max_seqlen_k, softmax_scale, workspace, num_splits,
                                   _event_handle(event_after_main), _handle(stream))

@@ -90,7 +90,9 @@ __device__ __forceinline__ bool find_unit(const AppendParams& p, UnitShared* sh,
   __syncthreads();
   const int b = sh->b;
   if (b < 0) return false;
-  const int a = sh->a, L = sh->L;
+  // (prefix sums that decrease may name a unit twice: whatever was left here,
+  // the rows stay inside the tensors)
+  const int a = sh->a, L = sh->L < p.total_q - a ? sh->L : p.total_q - a;
   const int64_t S = sh->S;
   if (L <= 0) return false;
   const int64_t pos0 = S - L;
@@ -337,7 +339,8 @@ __global__ void __launch_bounds__(kKvThreads, 8) va_append_kernel(const AppendPa
       const unsigned char* row = static_cast<unsigned char*>(c.data) + base + (int64_t)s * c.s1;
       old[k] = make_uint2(0, 0);
       if (s < s_lo)
-        old[k] = make_uint2(*reinterpret_cast<const uint32_t*>(row + col.o1), *reinterpret_cast<const uint32_t*>(row + col.o2));
+        old[k] = make_uint2(*reinterpret_cast<const uint32_t*>(row + col.o1),
+                            *reinterpret_cast<const uint32_t*>(row + col.o2));
     }
   }
   float x[4][8];

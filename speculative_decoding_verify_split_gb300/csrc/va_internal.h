@@ -152,8 +152,8 @@ constexpr int kMaxClusterLog2 = 3;
 constexpr int kMaxCluster = 1 << kMaxClusterLog2;  // CTAs of a cluster (the portable limit)
 // Clusters of 2^i CTAs, i = 0..kMaxClusterLog2, of the page-scaled kernels that
 // the current device holds at once.
-cudaError_t main_tc_clusters(int32_t* caps);
-cudaError_t mla_tc_clusters(int32_t* caps);
+void main_tc_clusters(int32_t* caps);
+void mla_tc_clusters(int32_t* caps);
 
 cudaError_t launch_merge(const Params& p, cudaStream_t stream);
 
@@ -200,9 +200,10 @@ cudaError_t launch_mla_bf16_tc(const Params& p, const CUtensorMap& tm_kv, cudaSt
 cudaError_t launch_main_tc(const Params& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                            cudaStream_t stream);
 
-// Clusters of 2^i CTAs of `fn` that run at once; 0 where the device gives none.
+// Clusters of 2^i CTAs of `fn` that run at once; 0 where the device has none or
+// does not say.
 template <class F>
-inline cudaError_t cluster_caps(F fn, int threads, size_t smem, int32_t* caps) {
+inline void cluster_caps(F fn, int threads, size_t smem, int32_t* caps) {
   for (int i = 0; i <= kMaxClusterLog2; ++i) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1u << i);
@@ -215,11 +216,12 @@ inline cudaError_t cluster_caps(F fn, int threads, size_t smem, int32_t* caps) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
-    if (e != cudaSuccess) return e;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
     caps[i] = n;
   }
-  return cudaSuccess;
 }
 
 }  // namespace va

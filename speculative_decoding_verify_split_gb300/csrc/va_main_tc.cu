@@ -1138,9 +1138,8 @@ cudaError_t set_smem() {
                               Cfg<FP8, VAR, QTM>::kSmemBytes);
 }
 
-cudaError_t main_tc_clusters(int32_t* caps) {
-  return cluster_caps(va_main_tc_kernel<true, true, false, true, true>, kThreads,
-                      Cfg<true, true, false>::kSmemBytes, caps);
+void main_tc_clusters(int32_t* caps) {
+  cluster_caps(va_main_tc_kernel<true, true, false, true, true>, kThreads, Cfg<true, true, false>::kSmemBytes, caps);
 }
 
 cudaError_t prepare_main_tc() {

@@ -854,8 +854,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t mla_tc_clusters(int32_t* caps) {
-  return cluster_caps(va_mla_tc_kernel<true, true>, kThreads, kSmemBytes + 1024, caps);
+void mla_tc_clusters(int32_t* caps) {
+  cluster_caps(va_mla_tc_kernel<true, true>, kThreads, kSmemBytes + 1024, caps);
 }
 
 cudaError_t prepare_mla_tc() {

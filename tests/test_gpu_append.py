@@ -86,6 +86,34 @@ def test_infinities_and_nan_in_new_tokens(kind, mla):
     (check_mla if mla else check_kv)(b)
 
 
+@pytest.mark.parametrize("mla", [False, True])
+@pytest.mark.parametrize("cu,used", [([0, 30, 10, 40, 24], [40, 30, 35, 20]), ([0, -5, 300, 24, 24], [40, 30, 35, 20]),
+                                     ([0, 8, 8, 20, 2000000000], [-3, 2000000000, 0, 17])])
+def test_broken_prefix_sums_stay_inside(mla, cu, used):
+    """Prefix sums that decrease, are negative or pass the rows, and lengths that
+    make no sense: unspecified rows, but nothing outside the tensors."""
+    b = Batch([6, 6, 6, 6], [40, 30, 35, 20], 4, 1, "scaled", 64, 33, dim=576 if mla else 256)
+    b.cu, b.used = torch.tensor(cu, dtype=torch.int32), torch.tensor(used, dtype=torch.int32)
+    T, guard = b.q.shape[0], 4096
+    wide = torch.full((T * 4 * 576 + 2 * guard,), 7.0, dtype=torch.bfloat16, device="cuda")
+    cache = [torch.full((b.pages * 16 * 576 + 2 * guard,), 0x11, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    inner = [c[guard:guard + b.pages * 16 * b.dim].view(torch.float8_e4m3fn).view(b.pages, 16, 1, b.dim) for c in cache]
+    scales = [torch.ones(b.pages, 1, device="cuda") for _ in range(2)]
+    w = b.q.shape[2]
+    q_out = wide[guard:guard + T * 4 * w].view(T, 4, w)
+    if mla:
+        row = gpu(b.k)[:, 0]
+        va.append_mla(row[:, :512], row[:, 512:], inner[0], gpu(b.block_table), gpu(b.cu), gpu(b.used), q_pe=gpu(b.q), q_pe_out=q_out,
+                      cos_sin=gpu(b.cos_sin), scales=scales[0])
+    else:
+        va.append_kv(gpu(b.k), gpu(b.v), *inner, gpu(b.block_table), gpu(b.cu), gpu(b.used), q=gpu(b.q), q_out=q_out,
+                     cos_sin=gpu(b.cos_sin), k_scales=scales[0], v_scales=scales[1])
+    torch.cuda.synchronize()
+    assert (wide[:guard] == 7.0).all() and (wide[guard + T * 4 * w:] == 7.0).all()
+    for c in cache:
+        assert (c[:guard] == 0x11).all() and (c[guard + b.pages * 16 * b.dim:] == 0x11).all()
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("mla", [False, True])
 def test_pages_that_do_not_exist(kind, mla):

@@ -181,3 +181,48 @@ def test_decoding_without_a_pause(latent, B):
     assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a[1], b[1]))
     assert all(torch.equal(x, y) for x, y in zip(a[2], b[2]))
     assert not torch.equal(a[0][0], a[0][-1]) and a[0][-1].any()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("latent", [False, True])
+def test_outputs_made_for_another_stream(latent, handle):
+    """Outputs that the calls create on a given stream, dropped at once while the
+    current stream allocates and fills memory of the same size: no result of a
+    kept call changes."""
+    d = Decoder("scaled", latent, 8, 1 if latent else 2, 700)
+    d.step([37, 100, 5], False)
+    used = torch.tensor(d.len, dtype=torch.int32).cuda()
+    cu = torch.tensor([0, 1, 2, 3], dtype=torch.int32).cuda()
+    q = d.rnd(3, 8, d.dim)
+    s = torch.cuda.Stream()
+    arg = s.cuda_stream if handle else s
+    torch.cuda.synchronize()
+
+    def call(stream):
+        if latent:
+            return va.verify_attn_mla_scaled(q, d.cache[0], d.scales[0], d.bt, cu, used, 1, d.width * 16, d.scale, stream=stream)
+        return va.verify_attn_scaled(q, *d.cache, *d.scales, d.bt, cu, used, 1, d.width * 16, d.scale, stream=stream)
+
+    ref = call(None).clone()
+    kept = []
+    for i in range(40):
+        out = call(arg)
+        if i % 2:
+            kept.append(out)
+        del out
+        torch.empty_like(ref).fill_(float("nan"))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in kept)
+    row = d.rnd(3, 1, 576)
+    kv = [d.rnd(3, 2, 256) for _ in range(2)]
+    for st in (None, arg):
+        cache, scales = [c.clone() for c in d.cache], [x.clone() for x in d.scales]
+        torch.cuda.synchronize()
+        if latent:
+            r = va.append_mla(row[:, 0, :512], row[:, 0, 512:], cache[0], d.bt, cu, used, q_pe=q[..., 512:], cos_sin=d.cos_sin,
+                              scales=scales[0], stream=st)
+        else:
+            r = va.append_kv(*kv, *cache, d.bt, cu, used, q=q, cos_sin=d.cos_sin, k_scales=scales[0], v_scales=scales[1], stream=st)
+        torch.cuda.synchronize()
+        first = r.clone() if st is None else first
+        assert torch.equal(r, first)
