@@ -22,13 +22,13 @@
 //
 // Every byte is read and written once, so the bound is memory: the prompts of
 // 8 sequences (14,274 tokens, 32 query and 2 KV heads, page scales, 526 MB)
-// take 83.7 us, 93 % of the measured copy bandwidth; latent prompts of 39,119
-// tokens (16 query parts, 238 MB) 43.5 us, 81 %: there half the warps' time
+// take 83.4 us, 93 % of the measured copy bandwidth; latent prompts of 39,119
+// tokens (16 query parts, 238 MB) 42.5 us, 82 %: there half the warps' time
 // is instruction issue (ncu: 55 % of the issue slots), and the 128-byte query
 // parts are stored 1,152 bytes apart. A verify step is latency: the launch and
 // two dependent round trips (lengths; page id, rows and table), one more where
 // an older token's scale is read: 2.1 us for two sequences, 3.4 us for 64,
-// 5.0 us for 256 (1.8 waves of CTAs, half of them without tokens), back to
+// 4.8 us for 256 (1.8 waves of CTAs, half of them without tokens), back to
 // back; the call costs the host 3.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -62,38 +62,65 @@ struct UnitShared {
   int b, a, L, S;
 };
 
-// The unit of this CTA, or false if there is none. Contains barriers.
+// The unit of this CTA, or false if there is none. Waits for the stream's
+// previous kernel, which may write anything read from there on.
 template <int NT>
 __device__ __forceinline__ bool find_unit(const AppendParams& p, UnitShared* sh, Unit* out) {
-  if (threadIdx.x == 0) sh->b = -1;
-  __syncthreads();
-  // the previous kernel in the stream may write anything read below
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t u = blockIdx.x;
   // cu[b] lies in [0, total_q], so only these sequences can hold unit u: few
   // of a batch of short ones
   const int64_t slack = p.total_q / kPageSize;
   const int b0 = u > slack ? (int)((u - slack - 1) / 2) : 0;
   const int b1 = u / 2 + 1 < p.num_seqs ? (int)(u / 2 + 1) : p.num_seqs;
-  for (int b = b0 + threadIdx.x; b < b1; b += NT) {
-    const int a = p.cu_q[b], e = p.cu_q[b + 1], s = p.seqused_k[b];
+  auto holds = [&](int b, int a, int e) {
     const int64_t g0 = (int64_t)(a / kPageSize) + 2 * (int64_t)b;
     const int64_t g1 = (int64_t)(e / kPageSize) + 2 * ((int64_t)b + 1);
-    if (a >= 0 && g0 <= u && u < g1) {
-      const int end = e < p.total_q ? e : p.total_q;
-      sh->b = b;
-      sh->a = a;
-      sh->L = end - a;
-      sh->S = s;
+    return a >= 0 && g0 <= u && u < g1;
+  };
+  int b, a, L;
+  int64_t S;
+  if (b1 - b0 <= 32) {
+    // one sequence a lane: every warp finds the unit for itself
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    b = b0 + lane;
+    int e = 0, s = 0;
+    a = -1;
+    if (b < b1) {
+      a = p.cu_q[b];
+      e = p.cu_q[b + 1];
+      s = p.seqused_k[b];
     }
+    const unsigned who = __ballot_sync(0xffffffffu, b < b1 && holds(b, a, e));
+    if (who == 0) return false;
+    const int src = __ffs((int)who) - 1;
+    b = b0 + src;
+    a = __shfl_sync(0xffffffffu, a, src);
+    L = __shfl_sync(0xffffffffu, e, src) - a;
+    S = __shfl_sync(0xffffffffu, s, src);
+  } else {
+    if (threadIdx.x == 0) sh->b = -1;
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int j = b0 + threadIdx.x; j < b1; j += NT) {
+      const int ja = p.cu_q[j], je = p.cu_q[j + 1], js = p.seqused_k[j];
+      if (holds(j, ja, je)) {
+        sh->b = j;
+        sh->a = ja;
+        sh->L = je - ja;
+        sh->S = js;
+      }
+    }
+    __syncthreads();
+    b = sh->b;
+    if (b < 0) return false;
+    a = sh->a;
+    L = sh->L;
+    S = sh->S;
   }
-  __syncthreads();
-  const int b = sh->b;
-  if (b < 0) return false;
-  // (prefix sums that decrease may name a unit twice: whatever was left here,
-  // the rows stay inside the tensors)
-  const int a = sh->a, L = sh->L < p.total_q - a ? sh->L : p.total_q - a;
-  const int64_t S = sh->S;
+  // (prefix sums that decrease may name a unit twice: whatever was found, the
+  // rows stay inside the tensors)
+  L = L < p.total_q - a ? L : p.total_q - a;
   if (L <= 0) return false;
   const int64_t pos0 = S - L;
   const int64_t first = pos0 > 0 ? pos0 : 0;  // tokens before position 0 have no place
