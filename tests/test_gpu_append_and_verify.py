@@ -226,3 +226,84 @@ def test_outputs_made_for_another_stream(latent, handle):
         torch.cuda.synchronize()
         first = r.clone() if st is None else first
         assert torch.equal(r, first)
+
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_a_captured_decoding_step(latent):
+    """Append and attention captured once, replayed token after token with the
+    lengths advanced on the device: the eager steps' bits."""
+    g = torch.Generator().manual_seed(8)
+    B, steps, dim, width = 5, 40, 576 if latent else 256, 6
+    kv = torch.randn(steps, 2, B, dim, generator=g).to(torch.bfloat16).cuda()
+    q0 = torch.randn(steps, B, 16, dim, generator=g).to(torch.bfloat16).cuda()
+    bt = torch.randperm(B * width, generator=g).int().reshape(B, width).cuda()
+    cu = torch.arange(B + 1, dtype=torch.int32).cuda()
+    start = torch.tensor([1, 15, 16, 17, 33], dtype=torch.int32).cuda()
+    cos_sin = table(128, 64 if latent else 256).cuda()
+
+    def state():
+        return dict(cache=[torch.zeros(B * width, 16, 1, dim, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)],
+                    scales=[torch.ones(B * width, 1, device="cuda") for _ in range(2)], used=start.clone(), q=q0[0].clone(),
+                    kv=kv[0].clone(), out=torch.zeros(B, 16, 512 if latent else 256, dtype=torch.bfloat16, device="cuda"))
+
+    def step(t):
+        if latent:
+            va.append_mla(t["kv"][0, :, :512], t["kv"][0, :, 512:], t["cache"][0], bt, cu, t["used"], q_pe=t["q"][..., 512:],
+                          q_pe_out=t["q"][..., 512:], cos_sin=cos_sin, scales=t["scales"][0])
+            va.verify_attn_mla_scaled(t["q"], t["cache"][0], t["scales"][0], bt, cu, t["used"], 1, width * 16, dim ** -0.5, out=t["out"])
+        else:
+            va.append_kv(t["kv"][0][:, None], t["kv"][1][:, None], *t["cache"], bt, cu, t["used"], q=t["q"], q_out=t["q"],
+                         cos_sin=cos_sin, k_scales=t["scales"][0], v_scales=t["scales"][1])
+            va.verify_attn_scaled(t["q"], *t["cache"], *t["scales"], bt, cu, t["used"], 1, width * 16, dim ** -0.5, out=t["out"])
+        t["used"] += 1
+
+    e, r = state(), state()
+    want = []
+    for i in range(steps):
+        e["q"].copy_(q0[i])
+        e["kv"].copy_(kv[i])
+        step(e)
+        want.append(e["out"].clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(r)
+    r["used"].copy_(start)
+    for i in range(steps):
+        r["q"].copy_(q0[i])
+        r["kv"].copy_(kv[i])
+        graph.replay()
+        assert torch.equal(r["out"], want[i]), i
+    for x, y in zip(e["cache"] + e["scales"], r["cache"] + r["scales"]):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_calls_from_several_threads():
+    """Four threads with a stream each decode their own sequences at the same time."""
+    from concurrent.futures import ThreadPoolExecutor
+    base = Decoder("scaled", False, 8, 2, 710)
+    base.step([37, 100, 5], False)
+    torch.cuda.synchronize()
+    cu = torch.tensor([0, 2, 4, 6], dtype=torch.int32).cuda()
+    g = torch.Generator().manual_seed(9)
+    new = torch.randn(4, 20, 6, 12, 256, generator=g).to(torch.bfloat16).cuda()
+
+    def decode(i):
+        cache, scales = [c.clone() for c in base.cache], [x.clone() for x in base.scales]
+        used = [torch.tensor([n + 2 * (k + 1) for n in base.len], dtype=torch.int32).cuda() for k in range(20)]
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        outs = []
+        with torch.cuda.stream(s):
+            for k in range(20):
+                x = new[i, k]
+                q = va.append_kv(x[:, 8:10], x[:, 10:], *cache, base.bt, cu, used[k], q=x[:, :8], cos_sin=base.cos_sin,
+                                 k_scales=scales[0], v_scales=scales[1])
+                outs.append(va.verify_attn_scaled(q, *cache, *scales, base.bt, cu, used[k], 2, base.width * 16, base.scale))
+            s.synchronize()
+        return torch.stack(outs)
+
+    want = [decode(i) for i in range(4)]
+    with ThreadPoolExecutor(4) as ex:
+        for _ in range(3):
+            got = list(ex.map(decode, range(4)))
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
