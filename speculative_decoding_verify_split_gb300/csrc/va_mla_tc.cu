@@ -839,16 +839,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if constexpr (CLU) {
+    __syncwarp();
+    cluster_arrive();  // behind this thread's part of the partial
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
   if constexpr (CLU) {
     __syncwarp();
-    cluster_sync();  // every CTA's partial is written
     join_cluster<kThreads, kMlaNope>(p, c / p.cluster, meta, c % p.cluster, smem_addr(part), kMlaNope,
                                      smem_addr(part_ml));
-    cluster_sync();  // no CTA ends while another still reads it
   }
 }
 

@@ -338,9 +338,11 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Named barrier over `count` threads (a multiple of 32).
-// All threads of all CTAs of the cluster; orders shared memory between them.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// Barrier of all threads of all CTAs of the cluster, in two halves; orders
+// shared memory between them. Threads arrive one by one and wait by warp.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Address, in the cluster's shared window, of CTA `rank`'s counterpart of this

@@ -273,7 +273,10 @@ __device__ __forceinline__ SeqMeta locate_cluster_work(const Params& p, int c, i
 // memory at `part`: R rows of `stride` floats, and `ml`: (m, l) per row): this
 // CTA sums its part of the R x DV outputs over the CTAs, in rank order, with
 // the weights 2^(m_k - max m), and writes it as bf16. Rows without a visible
-// key are 0. NT threads of the CTA; between two cluster barriers.
+// key are 0. NT threads of the CTA, each of which has arrived at the cluster's
+// barrier behind its part of the partial. A thread arrives a second time when
+// it has read what it needs of the others, and no CTA ends before all have:
+// that second barrier passes while the sums are made and written.
 template <int NT, int DV>
 __device__ __forceinline__ void join_cluster(const Params& p, int j, const SeqMeta& m, int rank, uint32_t part, int stride,
                                              uint32_t ml) {
@@ -282,8 +285,12 @@ __device__ __forceinline__ void join_cluster(const Params& p, int j, const SeqMe
   const int G = p.group, R = G * m.L;
   const int units = R * (DV / 4), per = (units + C - 1) / C;
   const int end = (rank + 1) * per < units ? (rank + 1) * per : units;
-  for (int u = rank * per + (int)threadIdx.x; u < end; u += NT) {
+  int u = rank * per + (int)threadIdx.x;
+  const bool any = u < end;
+  ptx::cluster_wait();  // every CTA's partial is written
+  for (; u < end; u += NT) {
     const int r = u / (DV / 4), c4 = u - r * (DV / 4);
+    const int t = r / G, g = r - t * G;
     float2 x[kMaxCluster];
     float4 o[kMaxCluster];
 #pragma unroll
@@ -298,6 +305,7 @@ __device__ __forceinline__ void join_cluster(const Params& p, int j, const SeqMe
     float M = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, x[k].x);
+    if (u + NT >= end) ptx::cluster_arrive();  // this thread's last reads
     float den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -310,7 +318,6 @@ __device__ __forceinline__ void join_cluster(const Params& p, int j, const SeqMe
       acc.z = fmaf(w, o[k].z, acc.z);
       acc.w = fmaf(w, o[k].w, acc.w);
     }
-    const int t = r / G, g = r - t * G;
     if (p.sinks && M != -INFINITY) den += exp2f(p.sinks[kvh * G + g] * 1.4426950408889634f - M);
     const float inv = M != -INFINITY && den > 0.f ? 1.f / den : 0.f;
     uint16_t* dst = p.out + (int64_t)(m.q0 + t) * p.o_s0 + (int64_t)(kvh * G + g) * p.o_s1 + 4 * c4;
@@ -318,6 +325,9 @@ __device__ __forceinline__ void join_cluster(const Params& p, int j, const SeqMe
         (uint32_t)float_to_bf16_bits(acc.x * inv) | ((uint32_t)float_to_bf16_bits(acc.y * inv) << 16),
         (uint32_t)float_to_bf16_bits(acc.z * inv) | ((uint32_t)float_to_bf16_bits(acc.w * inv) << 16));
   }
+  if (!any) ptx::cluster_arrive();
+  __syncwarp();
+  ptx::cluster_wait();
 }
 
 // One (sequence, KV head) item's share of this CTA. Tile indices are absolute
