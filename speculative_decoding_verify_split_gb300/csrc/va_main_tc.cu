@@ -1127,7 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
   if constexpr (CLU) {
     __syncwarp();
-    join_cluster<kThreads, kHeadDim>(p, c / p.cluster, meta, c % p.cluster, smem_addr(part), kPartStride,
+    join_cluster<kThreads, kHeadDim>(p, j_first, meta, c & (p.cluster - 1), smem_addr(part), kPartStride,
                                      smem_addr(part_ml));
   }
 }

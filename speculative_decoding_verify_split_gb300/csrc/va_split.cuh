@@ -254,17 +254,15 @@ __device__ long long locate_work(const Params& p, int c, long long* scratch, int
 // batch has room there; contains a barrier.
 __device__ __forceinline__ SeqMeta locate_cluster_work(const Params& p, int c, int C, long long* t0, long long* t1,
                                                        int* out_j, SeqMeta* cache) {
-  const int j = c / C, rank = c - j * C;
+  const int log2c = 31 - __clz(C);  // C is a power of two
+  const int j = c >> log2c, rank = c & (C - 1);
   const int b = j / p.hkv;
   const SeqMeta m = seq_meta(p, nullptr, b);
-  const int nt = meta_tiles(p, m);
-  *t0 = (long long)nt * rank / C;
-  *t1 = (long long)nt * (rank + 1) / C;
+  const int nt = meta_tiles(p, m);  // below 2^27 (the table's tokens fit an int32)
+  *t0 = (nt * rank) >> log2c;
+  *t1 = (nt * (rank + 1)) >> log2c;
   *out_j = j;
-  if (threadIdx.x == 0) {
-    if (p.num_seqs <= kSeqCache) cache[b] = m;
-    if (*t0 < *t1) prefetch_first_pages(p, j, *t0);
-  }
+  if (threadIdx.x == 32 && p.num_seqs <= kSeqCache) cache[b] = m;
   __syncthreads();
   return m;
 }
@@ -283,7 +281,7 @@ __device__ __forceinline__ void join_cluster(const Params& p, int j, const SeqMe
   const int C = p.cluster;
   const int b = j / p.hkv, kvh = j - b * p.hkv;
   const int G = p.group, R = G * m.L;
-  const int units = R * (DV / 4), per = (units + C - 1) / C;
+  const int units = R * (DV / 4), per = (units + C - 1) >> (31 - __clz(C));
   const int end = (rank + 1) * per < units ? (rank + 1) * per : units;
   int u = rank * per + (int)threadIdx.x;
   const bool any = u < end;
