@@ -79,6 +79,8 @@ static_assert(kSmemBytes + 1024 <= 232448, "shared memory (with the 1 KB alignme
 static_assert(kTileBytes % 1024 == 0 && kOffQpe % 1024 == 0, "swizzle atoms");
 static_assert((kPBufs & (kPBufs - 1)) == 0, "P buffers: a power of two");
 
+constexpr int kNarRows = 32;  // NAR: packed rows at most
+
 constexpr int kThreads = 512;  // 16 warps
 constexpr int kSoftmaxThreads = 256;
 constexpr int kBarAllSoftmax = 5;  // named barriers: 1-4 per quadrant, 5 all softmax warps
@@ -165,7 +167,7 @@ __device__ __forceinline__ int core_off(int m, int k, int row_bytes) {
 // without scales). CLU: one cluster of CTAs per item, as in the GQA kernel: two
 // sequences of 1,024 and 769 keys 14.2 us a call (23.3 split over all CTAs),
 // 4.0 of them staging Q's 576 columns.
-template <bool SCL, bool CLU>
+template <bool SCL, bool CLU, bool NAR>
 __global__ void __launch_bounds__(kThreads, 1)
     va_mla_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tm_kv,
                      const __grid_constant__ CUtensorMap tm_pe) {
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t adesc = smem_desc(kst + a * kRegion + kk * 4096, kRegion, 1024, kLayoutSw128);
                 const uint32_t d = tmem + kColO + 64 * a;
                 mma_f8f6f4(d, adesc, bhi, kIdPV, (i == 0 && kk == 0) ? 0u : 1u);
-                mma_f8f6f4(d, adesc, blo, kIdPV, 1u);
+                if constexpr (!NAR) mma_f8f6f4(d, adesc, blo, kIdPV, 1u);
               }
             }
             mma_commit(bar(kBarPFree + pb));
@@ -702,7 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // O^T keeps a row in a column across all 128 lanes: every softmax
           // warp scales its lanes' part of the rows that moved, so the
           // decision is taken by all of them at once
-          if (kh == 0 && sub == 0) al[r] = alpha;
+          if (kh == 0 && sub == 0 && (!NAR || r < kNarRows)) {
+            al[r] = alpha;
+            if constexpr (NAR) al[kNarRows + r] = alpha;
+          }
           any = named_bar_or(kBarAllSoftmax, kSoftmaxThreads, rescale);
         }
         if (!ok) continue;
@@ -732,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned char* pbuf = sm + kOffP + pb * kPBuf;
           const int off = core_off(r, 16 * qtr, kT);
           *reinterpret_cast<uint4*>(pbuf + off) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-          *reinterpret_cast<uint4*>(pbuf + kPHalf + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+          *reinterpret_cast<uint4*>(pbuf + (NAR ? core_off(kNarRows, 0, kT) : kPHalf) + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
         }
         // then the rows that moved (P V(cur - 1) has to be in O^T first; the
         // wait overlaps the work above)
@@ -802,13 +807,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t piece = (int64_t)pc.j + c;
       const int ldr = mla_row_stride(p.max_rows);
 #pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        const int a = 2 * kh + (k >> 1);
-        const int r0 = 32 * (k & 1);
+      for (int k = 0; k < (NAR ? 2 : 4); ++k) {
+        const int a = 2 * kh + (NAR ? k : k >> 1);
+        const int r0 = NAR ? 0 : 32 * (k & 1);
         if (r0 >= pc.R) continue;  // warp-uniform
         uint32_t o[32];
         tmem_ld_32x32b_x32(tmem + lane_base + kColO + 64 * a + r0, o);
-        tmem_wait_ld();
+        if constexpr (NAR) {
+          uint32_t lo[32];
+          tmem_ld_32x32b_x32(tmem + lane_base + kColO + 64 * a + kNarRows, lo);
+          tmem_wait_ld();
+#pragma unroll
+          for (int w = 0; w < 32; ++w) o[w] = __float_as_uint(__uint_as_float(o[w]) + __uint_as_float(lo[w]));
+        } else {
+          tmem_wait_ld();
+        }
         const int col = 128 * a + 32 * q + lane;
         const int nrow = ldr - r0 < 32 ? ldr - r0 : 32;
         if constexpr (CLU) {
@@ -854,14 +867,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+using Kernel = void (*)(const Params, const CUtensorMap, const CUtensorMap);
+Kernel pick(const Params& p) {
+  const bool nar = p.max_rows <= kNarRows;
+  if (p.cluster > 0) return nar ? va_mla_tc_kernel<true, true, true> : va_mla_tc_kernel<true, true, false>;
+  if (p.k_scales) return nar ? va_mla_tc_kernel<true, false, true> : va_mla_tc_kernel<true, false, false>;
+  return va_mla_tc_kernel<false, false, false>;
+}
+
 }  // namespace
 
 void mla_tc_clusters(int32_t* caps) {
-  cluster_caps(va_mla_tc_kernel<true, true>, kThreads, kSmemBytes + 1024, caps);
+  // one CTA an SM in either form
+  cluster_caps(va_mla_tc_kernel<true, true, false>, kThreads, kSmemBytes + 1024, caps);
 }
 
 cudaError_t prepare_mla_tc() {
-  for (auto fn : {va_mla_tc_kernel<false, false>, va_mla_tc_kernel<true, false>, va_mla_tc_kernel<true, true>}) {
+  for (auto fn : {va_mla_tc_kernel<false, false, false>, va_mla_tc_kernel<true, false, false>,
+                  va_mla_tc_kernel<true, false, true>, va_mla_tc_kernel<true, true, false>,
+                  va_mla_tc_kernel<true, true, true>}) {
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes + 1024);
     if (e != cudaSuccess) return e;
   }
@@ -886,10 +910,8 @@ cudaError_t launch_mla_tc(const Params& p, const CUtensorMap& tm_kv, const CUten
     attr[1].val.clusterDim.x = (unsigned)p.cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, va_mla_tc_kernel<true, true>, p, tm_kv, tm_pe);
   }
-  return p.k_scales ? cudaLaunchKernelEx(&cfg, va_mla_tc_kernel<true, false>, p, tm_kv, tm_pe)
-                    : cudaLaunchKernelEx(&cfg, va_mla_tc_kernel<false, false>, p, tm_kv, tm_pe);
+  return cudaLaunchKernelEx(&cfg, pick(p), p, tm_kv, tm_pe);
 }
 
 }  // namespace va
