@@ -464,40 +464,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Warp 1 issues Q K^T into the S buffers, warp 12 issues P V into O: the
     // two write different TMEM columns, and splitting them halves the
     // per-tile issue work of one thread (waits, descriptors, commits).
-    if (lane == 0) {
-      const bool is_qk = warp == 1;
-      const uint32_t qbase = sbase + C::kOffQ;
-      int it = 0, piece_idx = 0;
-      int j = j_first;
-      long long ts = ts_first;
-      Piece pc;
-      bool ok = true;
-      auto wait_or_fail = [&](int b, uint32_t par, int code) {
-        if (!ok) return false;
-        if (!mbar_wait(bar(b), par, abort_flag, p.wait_limit_ns)) {
-          fail(p, abort_flag, code);
-          ok = false;
-        }
-        return ok;
-      };
-      while (ok && next_piece(p, t0, t1, j, ts, pc, seqs)) {
-        const int first = it;
-        const int ntile = pc.lt1 - pc.lt0;
-        if (is_qk) {
-          if (!wait_or_fail(kBarQFull, piece_idx & 1, 2)) break;
+    // The whole warp walks the tiles and waits, and one elected thread issues:
+    // the operands are then the warp's and not one lane's of a diverged warp
+    // (see va_mla_tc.cu).
+    const bool is_qk = warp == 1;
+    const uint32_t qbase = sbase + C::kOffQ;
+    int it = 0, piece_idx = 0;
+    int j = j_first;
+    long long ts = ts_first;
+    Piece pc;
+    bool ok = true;
+    auto arrived = [&](int b, uint32_t par) { return mbar_wait(bar(b), par, abort_flag, p.wait_limit_ns); };
+    auto all_or_fail = [&](bool got, int code) {
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) fail(p, abort_flag, code);
+        ok = false;
+      }
+      return ok;
+    };
+    while (ok && next_piece(p, t0, t1, j, ts, pc, seqs)) {
+      const int first = __shfl_sync(0xffffffffu, it, 0);
+      const int ntile = __shfl_sync(0xffffffffu, pc.lt1 - pc.lt0, 0);
+      if (is_qk) {
+        if (!all_or_fail(arrived(kBarQFull, piece_idx & 1), 2)) break;
+        tc_fence_after();
+        for (int i = 0; i < ntile && ok; ++i) {
+          const int cur = first + i;
+          const int s = cur % C::kKSlots;
+          const int b = cur & (kSBufs - 1);
+          bool got = arrived(kBarFullK + s, (cur / C::kKSlots) & 1);
+          // S buffer b is free once the softmax has read S(cur - kSBufs) or,
+          // with P written over it, once P V(cur - kSBufs) has read that P
+          if (cur >= kSBufs)
+            got = got && arrived(C::kPOverS ? kBarPFree + b : kBarSFree + b, ((cur - kSBufs) / kSBufs) & 1);
+          if (!all_or_fail(got, 32)) break;
           tc_fence_after();
-          for (int i = 0; i < ntile && ok; ++i) {
-            const int cur = first + i;
-            const int s = cur % C::kKSlots;
-            const int b = cur & (kSBufs - 1);
-            if (!wait_or_fail(kBarFullK + s, (cur / C::kKSlots) & 1, 32)) break;
-            // S buffer b is free once the softmax has read S(cur - kSBufs) or,
-            // with P written over it, once P V(cur - kSBufs) has read that P
-            if (cur >= kSBufs &&
-                !wait_or_fail(C::kPOverS ? kBarPFree + b : kBarSFree + b, ((cur - kSBufs) / kSBufs) & 1, 64))
-              break;
-            tc_fence_after();
-            const uint32_t kst = sbase + s * C::kTensorBytes;
+          const uint32_t kst = sbase + s * C::kTensorBytes;
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < C::kQkSteps; ++k) {
               const uint32_t koff = (uint32_t)((k >> 2) * C::kRegion + (k & 3) * 32);
@@ -515,17 +518,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(bar(kBarEmptyK + s));
             if (i == ntile - 1) mma_commit(bar(kBarQFree));
           }
-        } else {
-          for (int i = 0; i < ntile && ok; ++i) {
-            const int x = first + i;
-            const int pb = x & (kPBufs - 1);
-            const int s = x % C::kVSlots;
-            if (!wait_or_fail(kBarPFull + pb, (x / kPBufs) & 1, 4)) break;
-            if (!wait_or_fail(kBarFullV + s, (x / C::kVSlots) & 1, 8)) break;
-            if (i == 0 && piece_idx > 0 && !wait_or_fail(kBarOFree, (piece_idx - 1) & 1, 16)) break;
-            tc_fence_after();
-            const uint32_t vst = sbase + (C::kKSlots + s) * C::kTensorBytes;
-            const uint32_t pbuf = sbase + C::kOffP + pb * C::kPBuf;
+          __syncwarp();
+        }
+      } else {
+        for (int i = 0; i < ntile && ok; ++i) {
+          const int x = first + i;
+          const int pb = x & (kPBufs - 1);
+          const int s = x % C::kVSlots;
+          bool got = arrived(kBarPFull + pb, (x / kPBufs) & 1) && arrived(kBarFullV + s, (x / C::kVSlots) & 1);
+          if (i == 0 && piece_idx > 0) got = got && arrived(kBarOFree, (piece_idx - 1) & 1);
+          if (!all_or_fail(got, 4)) break;
+          tc_fence_after();
+          const uint32_t vst = sbase + (C::kKSlots + s) * C::kTensorBytes;
+          const uint32_t pbuf = sbase + C::kOffP + pb * C::kPBuf;
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < C::kPvSteps; ++kk) {
               const uint64_t bdesc = smem_desc(vst + kk * (C::kKeysPerPvStep / 8) * 1024, C::kRegion,
@@ -544,11 +550,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(bar(kBarEmptyV + s));
             if (i == ntile - 1) mma_commit(bar(kBarOFull));
           }
+          __syncwarp();
         }
-        it = first + ntile;
-        ++piece_idx;
       }
-      // every tensor-core operation of both issuers has finished before TMEM is freed
+      it = first + ntile;
+      ++piece_idx;
+    }
+    // every tensor-core operation of both issuers has finished before TMEM is freed
+    if (elect_one()) {
       mma_commit(bar(kBarDrain));
       mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
     }

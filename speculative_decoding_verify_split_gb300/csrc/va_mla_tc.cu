@@ -381,37 +381,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (qk_warp || pv_warp) {
     // ======================= MMA issuers ==========================================
-    if (lane == 0) {
-      const bool is_qk = qk_warp;
-      const uint32_t qpe = sbase + kOffQpe;
-      int it = 0, piece_idx = 0;
-      int j = j_first;
-      long long ts = ts_first;
-      Piece pc;
-      bool ok = true;
-      auto wait_or_fail = [&](int b, uint32_t par, int code) {
-        if (!ok) return false;
-        if (!mbar_wait(bar(b), par, abort_flag, p.wait_limit_ns)) {
-          fail(p, abort_flag, code);
-          ok = false;
-        }
-        return ok;
-      };
-      while (ok && next_piece(p, t0, t1, j, ts, pc, seqs)) {
-        const int first = it;
-        const int ntile = pc.lt1 - pc.lt0;
-        if (is_qk) {
-          if (!wait_or_fail(kBarQFull, piece_idx & 1, 2)) break;
+    const bool is_qk = qk_warp;
+    const uint32_t qpe = sbase + kOffQpe;
+    int it = 0, piece_idx = 0;
+    int j = j_first;
+    long long ts = ts_first;
+    Piece pc;
+    bool ok = true;
+    // The whole warp walks the tiles and waits, with one vote a tile, and one
+    // elected thread issues. In a branch that only one lane enters, every
+    // operand of every tcgen05.mma is a lane's value that has to be moved to
+    // the warp's registers first, and an MMA of N = 64 costs its issuer about
+    // 50 cycles; so the issue, and not the tensor cores, was the bound (latent
+    // mid context, page-scaled, 48 rows 175.4 -> 159.1 us, 16 rows 162.2 ->
+    // 135; with one descale 180.1 -> 157.4).
+    auto arrived = [&](int b, uint32_t par) { return mbar_wait(bar(b), par, abort_flag, p.wait_limit_ns); };
+    auto all_or_fail = [&](bool got, int code) {
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) fail(p, abort_flag, code);
+        ok = false;
+      }
+      return ok;
+    };
+    while (ok && next_piece(p, t0, t1, j, ts, pc, seqs)) {
+      const int first = __shfl_sync(0xffffffffu, it, 0);
+      const int ntile = __shfl_sync(0xffffffffu, pc.lt1 - pc.lt0, 0);
+      if (is_qk) {
+        if (!all_or_fail(arrived(kBarQFull, piece_idx & 1), 2)) break;
+        tc_fence_after();
+        for (int i = 0; i < ntile && ok; ++i) {
+          const int cur = first + i;
+          const int s = cur % kSlots;
+          const int b = cur & (kSBufs - 1);
+          bool got = arrived(kBarFull + s, (cur / kSlots) & 1);
+          if (cur >= kSBufs) got = got && arrived(kBarSFree + b, ((cur - kSBufs) / kSBufs) & 1);
+          if (!all_or_fail(got, 32)) break;
           tc_fence_after();
-          for (int i = 0; i < ntile && ok; ++i) {
-            const int cur = first + i;
-            const int s = cur % kSlots;
-            const int b = cur & (kSBufs - 1);
-            if (!wait_or_fail(kBarFull + s, (cur / kSlots) & 1, 32)) break;
-            if (cur >= kSBufs && !wait_or_fail(kBarSFree + b, ((cur - kSBufs) / kSBufs) & 1, 64)) break;
-            tc_fence_after();
-            const uint32_t kst = sbase + s * kTileBytes;
-            const uint32_t d = tmem + kColS + b * kT;
+          const uint32_t kst = sbase + s * kTileBytes;
+          const uint32_t d = tmem + kColS + b * kT;
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kQkSteps; ++k) {
               const uint64_t bdesc = smem_desc(kst + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024, kLayoutSw128);
@@ -426,17 +434,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(bar(kBarSFull + b));
             if (i == ntile - 1) mma_commit(bar(kBarQFree));
           }
-        } else {
-          for (int i = 0; i < ntile && ok; ++i) {
-            const int x = first + i;
-            const int pb = x & (kPBufs - 1);
-            const int s = x % kSlots;
-            if (!wait_or_fail(kBarPFull + pb, (x / kPBufs) & 1, 4)) break;
-            if (!wait_or_fail(kBarFull + s, (x / kSlots) & 1, 8)) break;
-            if (i == 0 && piece_idx > 0 && !wait_or_fail(kBarOFree, (piece_idx - 1) & 1, 16)) break;
-            tc_fence_after();
-            const uint32_t kst = sbase + s * kTileBytes;
-            const uint32_t pbuf = sbase + kOffP + pb * kPBuf;
+          __syncwarp();
+        }
+      } else {
+        for (int i = 0; i < ntile && ok; ++i) {
+          const int x = first + i;
+          const int pb = x & (kPBufs - 1);
+          const int s = x % kSlots;
+          bool got = arrived(kBarPFull + pb, (x / kPBufs) & 1) && arrived(kBarFull + s, (x / kSlots) & 1);
+          if (i == 0 && piece_idx > 0) got = got && arrived(kBarOFree, (piece_idx - 1) & 1);
+          if (!all_or_fail(got, 4)) break;
+          tc_fence_after();
+          const uint32_t kst = sbase + s * kTileBytes;
+          const uint32_t pbuf = sbase + kOffP + pb * kPBuf;
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kPvSteps; ++kk) {
               const uint64_t bhi = smem_desc(pbuf + kk * 256, 128, 8 * kT, kLayoutNone);
@@ -454,10 +465,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(bar(kBarEmpty + s));
             if (i == ntile - 1) mma_commit(bar(kBarOFull));
           }
+          __syncwarp();
         }
-        it = first + ntile;
-        ++piece_idx;
       }
+      it = first + ntile;
+      ++piece_idx;
+    }
+    if (elect_one()) {
       mma_commit(bar(kBarDrain));
       mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
     }
