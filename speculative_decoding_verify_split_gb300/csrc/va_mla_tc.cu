@@ -91,7 +91,8 @@ constexpr uint32_t kColQ = 384;
 constexpr uint32_t kTmemCols = 512;
 
 constexpr uint32_t kIdQK = instr_desc(0, 0, false, kT, 128);         // e4m3 x e4m3, N = 64 keys
-constexpr uint32_t kIdPV = instr_desc(0, 0, false, 64, 128, true);   // A = V^T MN-major, N = 64 rows
+// A = V^T MN-major, N = the packed rows in use (a multiple of 16)
+__device__ __forceinline__ uint32_t id_pv(int n) { return instr_desc(0, 0, false, n, 128, true); }
 
 // P = 2^(s - m_ref + kPShift) as in the GQA kernel. The reference max moves
 // only when a tile's max passes m_ref + kOvershoot (2.8: P stays <= 2^8.8,
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // With at most 48 packed rows the softmax warps of quadrant 3 are idle; the
   // two MMA issuers then sit on that quadrant's scheduler, where no ALU work
   // competes with them (latent mid context, 48 rows: 190.6 -> 184.0 us).
+  const int nar = p.max_rows <= 16 ? 16 : 32;  // NAR: P's low terms are rows nar ... of P^T
   const bool alt = p.max_rows <= 48;
   const int prod = alt ? (warp < 3 ? warp : -1) : (warp == 0 ? 0 : (warp == 2 || warp == 3) ? warp - 1 : -1);
   const bool qk_warp = warp == (alt ? 3 : 1), pv_warp = warp == (alt ? 15 : 12);
@@ -383,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ======================= MMA issuers ==========================================
     const bool is_qk = qk_warp;
     const uint32_t qpe = sbase + kOffQpe;
+    const uint32_t idpv = id_pv(NAR ? 2 * nar : (p.max_rows + 15) & ~15);
     int it = 0, piece_idx = 0;
     int j = j_first;
     long long ts = ts_first;
@@ -457,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // V^T chunk a: latent columns [128 a, +128) of keys [32 kk, +32)
                 const uint64_t adesc = smem_desc(kst + a * kRegion + kk * 4096, kRegion, 1024, kLayoutSw128);
                 const uint32_t d = tmem + kColO + 64 * a;
-                mma_f8f6f4(d, adesc, bhi, kIdPV, (i == 0 && kk == 0) ? 0u : 1u);
-                if constexpr (!NAR) mma_f8f6f4(d, adesc, blo, kIdPV, 1u);
+                mma_f8f6f4(d, adesc, bhi, idpv, (i == 0 && kk == 0) ? 0u : 1u);
+                if constexpr (!NAR) mma_f8f6f4(d, adesc, blo, idpv, 1u);
               }
             }
             mma_commit(bar(kBarPFree + pb));
@@ -718,9 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // O^T keeps a row in a column across all 128 lanes: every softmax
           // warp scales its lanes' part of the rows that moved, so the
           // decision is taken by all of them at once
-          if (kh == 0 && sub == 0 && (!NAR || r < kNarRows)) {
+          if (kh == 0 && sub == 0 && (!NAR || r < nar)) {
             al[r] = alpha;
-            if constexpr (NAR) al[kNarRows + r] = alpha;
+            if constexpr (NAR) al[nar + r] = alpha;
           }
           any = named_bar_or(kBarAllSoftmax, kSoftmaxThreads, rescale);
         }
@@ -751,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned char* pbuf = sm + kOffP + pb * kPBuf;
           const int off = core_off(r, 16 * qtr, kT);
           *reinterpret_cast<uint4*>(pbuf + off) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-          *reinterpret_cast<uint4*>(pbuf + (NAR ? core_off(kNarRows, 0, kT) : kPHalf) + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+          *reinterpret_cast<uint4*>(pbuf + (NAR ? core_off(nar, 0, kT) : kPHalf) + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
         }
         // then the rows that moved (P V(cur - 1) has to be in O^T first; the
         // wait overlaps the work above)
@@ -762,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the factors of rows [0, 32) and [32, 64), four to a load; a half in
           // which no row moved stays as it is
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
+          for (int half = 0; half < (NAR ? nar >> 4 : 2); ++half) {
             if (!__any_sync(0xffffffffu, al[32 * half + lane] != 1.f)) continue;
             const float4* af = reinterpret_cast<const float4*>(al + 32 * half);
 #pragma unroll 1
@@ -829,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_32x32b_x32(tmem + lane_base + kColO + 64 * a + r0, o);
         if constexpr (NAR) {
           uint32_t lo[32];
-          tmem_ld_32x32b_x32(tmem + lane_base + kColO + 64 * a + kNarRows, lo);
+          tmem_ld_32x32b_x32(tmem + lane_base + kColO + 64 * a + nar, lo);
           tmem_wait_ld();
 #pragma unroll
           for (int w = 0; w < 32; ++w) o[w] = __float_as_uint(__uint_as_float(o[w]) + __uint_as_float(lo[w]));
