@@ -714,7 +714,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++round;
         if (named_bar_or(kBarAllSoftmax, kSoftmaxThreads, ok && tmax > m_ref + kOvershoot)) {
           tmax = exchange(tmax, true);
-          const bool need = ok && tmax > m_ref + kOvershoot;
+          // page-scaled, a large page moves many rows: those that are above
+          // their reference at all move along, and spare a later move
+          const bool need = ok && tmax > m_ref + (SCL ? 0.f : kOvershoot);
           m_new = need ? tmax + (m_ref == -INFINITY ? kHeadroomFirst : SCL ? kHeadroomScaled : kHeadroom) : m_ref;
           const bool rescale = need && (m_ref != -INFINITY) && (cur > first);
           alpha = rescale ? ex2(m_ref - m_new) : 1.f;
