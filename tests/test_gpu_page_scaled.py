@@ -123,6 +123,21 @@ def test_latent(hq, splits):
     compare(run_mla(w, s, num_splits=splits), *oracle_mla(w, s))
 
 
+@pytest.mark.parametrize("hq,q", [(1, 1), (15, 1), (16, 1), (17, 1), (16, 2), (8, 4), (11, 3), (16, 3), (49, 1), (16, 4)])
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_latent_rows_and_rising_scales(hq, q, splits):
+    """Packed rows around 16, 32 and 48 (the sizes at which the latent kernel
+    lays P and its accumulator out differently), over pages whose scales rise
+    along the sequence, so that the reference of a row moves again and again."""
+    w = make_mla_workload([q, q, max(1, q - 1)], [2500, 700, 70], hq, "fp8_e4m3", seed=560 + hq + q).to("cuda")
+    s = torch.ones(w.kv_cache.shape[0], 1)
+    table = w.block_table.cpu()
+    for b, n in enumerate(w.seqused_k.tolist()):
+        pages = -(-n // 16)
+        s[table[b, :pages].long(), 0] = torch.exp2((torch.arange(pages) * 10 // pages - 9).float() / 2)
+    compare(run_mla(w, s, num_splits=splits), *oracle_mla(w, s))
+
+
 @pytest.mark.parametrize("mla", [False, True])
 def test_scales_far_apart(mla):
     """V's scales from 2^-40 to 2^40 over the pages, and K's so that the keys
