@@ -148,29 +148,32 @@ static int64_t tiles_upper_bound(int64_t B, int64_t hkv, int32_t max_q, int32_t 
 //    cost 3 us more than 8 in staging, softmax and stores) and fit.
 //  * A cluster's CTAs take an equal share of their own item only, so the
 //    largest item sets the time, where the split over all CTAs evens the batch
-//    out. Clusters as long as that costs at most four tiles (about 1 us each),
-//    what the work scan and the merge kernel cost, and a quarter tile for each
-//    segment past eight (24 tiles at most) that the merge would have to fold
-//    per item; for items that are as large as their bound on average with a
-//    window (`even`), and half as large without.
+//    out. Clusters as long as that costs at most 1,280 keys, what the work scan
+//    and the merge kernel cost, and a quarter tile for each segment past eight
+//    (24 tiles at most) that the merge would have to fold per item; for items
+//    that are as large as their bound on average with a window (`even`), and
+//    half as large without. Over 216 shapes of each kind (1 to 152 items of 8 to
+//    512 tiles, of one size, from half of it and from an eighth of it) the
+//    choice loses 0.6 % to the better of the two on average, and clusters alone
+//    or the split alone 12 and 19 % (GQA), 5 and 29 % (latent).
 // Measured, us per call in graphs of calls, split over all CTAs against
 // clusters (16 query heads per KV head unless noted):
-//   2 x 1,024 keys, 4 tokens 12.5 / 9.8; 8 x 2,000, 3 tokens 21.5 / 12.8;
-//   16 x 1,000, 1 token 16.2 / 10.8; 32 x 2,000, 1 token 17.6 / 14.2;
-//   64 x 1,000, 4 tokens 25.5 / 18.5; 1 x 8,000, 4 tokens, 8 heads 20.4 / 18.0;
-//   1 x 20,000, 1 token 48.0 / 33.9; 1 x 40,000 50.3 / 58.9 (split);
-//   16 pairs of 513 to 4,096 18.6 / 19.5 (split); 32 x 2 heads, window of 1,023
-//   24.0 / 19.3. Latent cache: 2 x 1,024, 4 tokens 23.3 / 14.3; 2 x 3,000 at
-//   most 27.9 / 20.0; 150 x 300 29.1 / 19.5.
-static bool cluster_plan(int64_t J, int64_t T, int64_t group, int32_t max_q, const int32_t* caps, int32_t num_sms,
-                         bool even, int32_t* cluster, int32_t* share) {
+//   2 x 1,024 keys, 4 tokens 12.5 / 8.3; 32 x 2,000, 1 token 17.8 / 12.9;
+//   64 x 1,000, 2 tokens, 8 heads 19.1 / 13.7; 1 x 8,000, 4 tokens 21.3 / 16.4;
+//   1 x 20,000, 1 token 47.2 / 30.8; 16 x 3,000, 2 tokens 17.5 / 15.3;
+//   1 x 40,000 49.7 / 54.4 (split); 32 x 2 heads, window of 1,023 24.0 / 17.9.
+//   Latent cache: 2 x 1,024, 4 tokens 23.3 / 12.3; 32 x 2,000, 1 token
+//   25.9 / 18.6; 76 x 1,500, 4 tokens 52.8 / 36.9; 100 x 600, 1 token
+//   27.6 / 21.3; 8 x 16,384 at most, 2 tokens 33.8 / 42.8 (split).
+static bool cluster_plan(int64_t J, int64_t T, int32_t tile_keys, int64_t group, int32_t max_q,
+                         const int32_t* caps, int32_t num_sms, bool even, int32_t* cluster, int32_t* share) {
   if (J < 1 || T < 1) return false;
   int i = kMaxClusterLog2;
   while (i > 0 && (J > caps[i] || (1 << (i - 1)) >= T)) --i;
   if (J > caps[i]) return false;
   const int64_t per = (T + (1 << i) - 1) >> i;
   const int64_t segments = T < num_sms / J ? T : num_sms / J;
-  const int64_t quarters = 16 + (segments > 104 ? 96 : segments > 8 ? segments - 8 : 0);
+  const int64_t quarters = 4 * 1280 / tile_keys + (segments > 104 ? 96 : segments > 8 ? segments - 8 : 0);
   if ((4 * per - quarters) * num_sms > (even ? 4 : 2) * J * T) return false;
   int32_t s = 1;
   while (group % (2 * s) == 0 && group / s * max_q > 8 && 2 * J * s <= caps[i]) s *= 2;
@@ -709,7 +712,8 @@ static va_status run_call(const va_tensor* q, const va_tensor* k_cache, const va
   if (s != VA_OK) return s;
   if (scales && num_splits == 0 &&
       cluster_plan(sh.num_seqs * sh.hkv, tiles_upper_bound(1, 1, max_seqlen_q, max_seqlen_k, plan.tile_keys, window),
-                   sh.hq / sh.hkv, max_seqlen_q, st->clusters, st->sms, window >= 0, &sh.cluster, &sh.share))
+                   plan.tile_keys, sh.hq / sh.hkv, max_seqlen_q, st->clusters, st->sms, window >= 0,
+                   &sh.cluster, &sh.share))
     use_clusters(&plan, sh);
   if (own_ws) {
     if (sh.total_q == 0 || sh.num_seqs == 0) return VA_OK;
@@ -839,8 +843,8 @@ static va_status run_mla_call(const va_tensor* q, const va_tensor* kv_cache, con
   s = make_mla_plan(sh.num_seqs, sh.hq, max_seqlen_q, max_seqlen_k, st->sms, num_splits, &plan, sh.kv_dtype);
   if (s != VA_OK) return s;
   if (scales && num_splits == 0 &&
-      cluster_plan(sh.num_seqs, ((int64_t)max_seqlen_k + plan.tile_keys - 1) / plan.tile_keys, sh.hq, max_seqlen_q,
-                   st->mla_clusters, st->sms, false, &sh.cluster, &sh.share))
+      cluster_plan(sh.num_seqs, ((int64_t)max_seqlen_k + plan.tile_keys - 1) / plan.tile_keys, plan.tile_keys, sh.hq,
+                   max_seqlen_q, st->mla_clusters, st->sms, false, &sh.cluster, &sh.share))
     use_clusters(&plan, sh);
   if (!workspace) {
     if (sh.total_q == 0 || sh.num_seqs == 0) return VA_OK;
