@@ -222,17 +222,17 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 // each with its own factor and offset in the FMA of P's exponent, and its own
 // partial sum of l. The V producers, which walk the page ids anyway, bring
 // the scales to shared memory with the V tile's slot. It stays HBM-bound:
-// 16 sequences of 64K to 128K keys (888 MB) 142.9 us, 64 of 8K to 32K (674 MB)
-// 110.5 us, 92 and 90 % of the measured copy bandwidth, what the same cache
-// with one descale takes.
+// 16 sequences of 64K to 128K keys (888 MB) 139 to 141 us, 64 of 8K to 32K
+// (674 MB) 108 to 110 us by the box, 93 and 91 % of the measured copy
+// bandwidth, what the same cache with one descale takes.
 // CLU: one cluster of CTAs per item (small batches); each CTA leaves its
 // partial in shared memory (in the drained rings) and the cluster joins them
 // there: no work scan, no partials in global memory, no merge kernel. A CTA
 // without a tile skips the roles and meets the others at the join. Latency
-// is the bound; two sequences of 1,024 and 769 keys take 9.6 us a call (12.7
-// split over all CTAs), of which (stamps) the lengths are 1.2, the block table
-// 1.4, the first tile 0.9, QK, softmax and PV 1.9, the epilogue 0.5, the
-// barrier 0.9, the join 1.3 and the last barrier 0.7.
+// is the bound: two sequences of 1,024 and 769 keys take 8.2 us a call (12.5
+// split over all CTAs), a chain of the launch, the lengths, the block table and
+// the first tile (a round trip each), one tile's QK, softmax and PV, the
+// epilogue, and the join between two cluster barriers.
 template <bool FP8, bool VAR, bool QTM, bool SCL, bool CLU>
 __global__ void __launch_bounds__(kThreads, 1)
     va_main_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,

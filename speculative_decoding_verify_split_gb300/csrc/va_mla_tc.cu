@@ -163,11 +163,16 @@ __device__ __forceinline__ int core_off(int m, int k, int row_bytes) {
 // GQA kernel it multiplies the page's logits, and as the value's scale joins
 // the weight, P = 2^(s + log2 scale - m_ref), with l summing P / scale. A
 // thread's 16 keys of a tile are one page. The producers bring the scales
-// with the ring slot. 64 sequences of 8K to 32K keys, 3 draft tokens (733 MB):
-// 175 us (the bound is the MMA instruction rate and the piece boundaries, as
-// without scales). CLU: one cluster of CTAs per item, as in the GQA kernel: two
-// sequences of 1,024 and 769 keys 14.2 us a call (23.3 split over all CTAs),
-// 4.0 of them staging Q's 576 columns.
+// with the ring slot. 64 sequences of 8K to 32K keys (733 MB), 16 heads: 154 us
+// with 3 draft tokens, 132 with one, 70 and 84 % of the measured copy bandwidth;
+// of the 154 the merge kernel is 12 and the rescales of O^T 10.
+// CLU: one cluster of CTAs per item, as in the GQA kernel: two sequences of
+// 1,024 and 769 keys 12.1 us a call (23.3 split over all CTAs), 4 of them
+// staging Q's 576 columns.
+// NAR: at most 32 packed rows. P's two terms are then stacked in the N of P V
+// (rows r and nar + r of P^T, columns r and nar + r of O^T, added up in the
+// epilogue): half its instructions, and N = 32 for 16 rows (64 sequences of 8K
+// to 32K, one token: N = 64 135.9 us, N = 32 132.5).
 template <bool SCL, bool CLU, bool NAR>
 __global__ void __launch_bounds__(kThreads, 1)
     va_mla_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tm_kv,
@@ -280,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // With at most 48 packed rows the softmax warps of quadrant 3 are idle; the
   // two MMA issuers then sit on that quadrant's scheduler, where no ALU work
-  // competes with them (latent mid context, 48 rows: 190.6 -> 184.0 us).
+  // competes with them (latent mid context, 48 rows: 158.4 -> 156.7 us, 16
+  // rows 134.3 -> 131.9).
   const int nar = p.max_rows <= 16 ? 16 : 32;  // NAR: P's low terms are rows nar ... of P^T
   const bool alt = p.max_rows <= 48;
   const int prod = alt ? (warp < 3 ? warp : -1) : (warp == 0 ? 0 : (warp == 2 || warp == 3) ? warp - 1 : -1);
