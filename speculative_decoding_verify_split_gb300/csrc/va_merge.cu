@@ -45,8 +45,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) va_merge_kernel(const Params
   const int kvh = j - b * p.hkv;
   // the split metadata (written for every item) is read with the lengths,
   // not after them: one round trip instead of two before the partials
-  const long long N = p.ws_meta[p.num_work];
-  const long long ts = p.ws_meta[j];
+  const int N = p.ws_meta[p.num_work];
+  const int ts = p.ws_meta[j];
   const int L = seq_q_len(p, b);
   const int G = p.group;
   if (r >= G * L) return;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) va_merge_kernel(const Params
   const int ns = c1 - c0 + 1;
   // A CTA range can only be empty when there are fewer split units than CTAs;
   // otherwise skip the two 64-bit divisions per segment.
-  const bool may_be_empty = N < (long long)p.num_splits;
+  const bool may_be_empty = N < p.num_splits;
 
   float M = -INFINITY, den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -156,8 +156,8 @@ template <int GROUPS, int SEGS>
 __global__ void __launch_bounds__(kMlaNope, 2) va_merge_mla_kernel(const Params p) {
   constexpr int kRows = 4 * GROUPS;  // rows per CTA
   static_assert(SEGS * kRows == 32, "warp 0: one lane per (segment, row)");
-  __shared__ float s_w[SEGS][kRows];
-  __shared__ float s_sc[kRows];
+  __shared__ __align__(16) float s_w[SEGS][kRows];
+  __shared__ __align__(16) float s_sc[kRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int j = blockIdx.x;  // one KV head: item j is sequence j
@@ -169,21 +169,29 @@ __global__ void __launch_bounds__(kMlaNope, 2) va_merge_mla_kernel(const Params 
   if (r0 >= R) return;  // CTA-uniform
   const int nrow = R - r0 < kRows ? R - r0 : kRows;
   const int q0 = p.cu_q[j];
-  auto dst = [&](int rr) {
-    const int t = (r0 + rr) / G, g = (r0 + rr) - t * G;
-    return p.out + (int64_t)(q0 + t) * p.o_s0 + (int64_t)g * p.o_s1 + d;
+  // writes the CTA's rows in order: one division, for the first
+  auto put_rows = [&](auto value) {
+    int g = r0 % G;
+    uint16_t* dst = p.out + (int64_t)(q0 + r0 / G) * p.o_s0 + (int64_t)g * p.o_s1 + d;
+    const int64_t next = p.o_s0 - (int64_t)(G - 1) * p.o_s1;  // the next token's first head
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      if (i < nrow) *dst = value(i);
+      dst += ++g == G ? next : p.o_s1;
+      if (g == G) g = 0;
+    }
   };
   const int nt = work_tiles(p, j);
   if (nt == 0) {
-    for (int rr = 0; rr < nrow; ++rr) *dst(rr) = 0;
+    put_rows([](int) { return (uint16_t)0; });
     return;
   }
-  const long long N = p.ws_meta[p.num_work];
-  const long long ts = p.ws_meta[j];
+  const int N = p.ws_meta[p.num_work];
+  const int ts = p.ws_meta[j];
   const int c0 = split_of(ts, N, p.num_splits);
   const int c1 = split_of(ts + nt - 1, N, p.num_splits);
   const int ns = c1 - c0 + 1;
-  const bool may_be_empty = N < (long long)p.num_splits;
+  const bool may_be_empty = N < p.num_splits;
   const int ldr = mla_row_stride(p.max_rows);
   // a CTA range can be empty only with fewer split units than CTAs; such a
   // segment wrote nothing and is never read
@@ -230,24 +238,28 @@ __global__ void __launch_bounds__(kMlaNope, 2) va_merge_mla_kernel(const Params 
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      float x = acc[i] * s_sc[i];
+    for (int gg = 0; gg < GROUPS; ++gg) {
+      const float4 sc = *reinterpret_cast<const float4*>(&s_sc[4 * gg]);
+      float x = acc[4 * gg] * sc.x, y = acc[4 * gg + 1] * sc.y, z = acc[4 * gg + 2] * sc.z, u = acc[4 * gg + 3] * sc.w;
 #pragma unroll
       for (int k = 0; k < SEGS; ++k) {
-        const float4 v = a[k][i / 4];
-        const int e = i % 4;
-        x = fmaf(s_w[k][i], e == 0 ? v.x : (e == 1 ? v.y : (e == 2 ? v.z : v.w)), x);
+        const float4 w = *reinterpret_cast<const float4*>(&s_w[k][4 * gg]), v = a[k][gg];
+        x = fmaf(w.x, v.x, x);
+        y = fmaf(w.y, v.y, y);
+        z = fmaf(w.z, v.z, z);
+        u = fmaf(w.w, v.w, u);
       }
-      acc[i] = x;
+      acc[4 * gg] = x;
+      acc[4 * gg + 1] = y;
+      acc[4 * gg + 2] = z;
+      acc[4 * gg + 3] = u;
     }
     __syncthreads();  // s_w and s_sc are rewritten by the next group
   }
   const float vd = p.v_descale ? *p.v_descale : 1.0f;
   if (d < kRows) s_sc[d] = (M == -INFINITY || !(den > 0.f)) ? 0.f : vd / den;  // lanes 0..kRows-1
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    if (i < nrow) *dst(i) = float_to_bf16_bits(acc[i] * s_sc[i]);
+  put_rows([&](int i) { return (uint16_t)float_to_bf16_bits(acc[i] * s_sc[i]); });
 }
 
 // Log-sum-exp merge of shard results (verify_attn_merge_partials):

@@ -113,6 +113,14 @@ __device__ __forceinline__ int split_of(long long x, long long N, int G) {
   return (int)(((x + 1) * (long long)G - 1) / N);
 }
 
+// The same where every thread of a grid asks for it (the merges): N is what the
+// split left in 32 bits, and while the product fits too the division is a
+// 32-bit one, a tenth of the instructions.
+__device__ __forceinline__ int split_of(int x, int N, int G) {
+  if ((uint32_t)N <= 0xFFFFFFFFu / (uint32_t)G) return (int)((((uint32_t)x + 1) * (uint32_t)G - 1) / (uint32_t)N);
+  return split_of((long long)x, (long long)N, G);
+}
+
 // Block-wide exclusive scan of one value per thread (NT threads, NT % 32 == 0).
 // Returns the exclusive prefix; *total receives the block sum. Uses 32 slots
 // of shared scratch; contains __syncthreads.
