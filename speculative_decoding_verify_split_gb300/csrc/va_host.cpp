@@ -162,7 +162,7 @@ static int64_t tiles_upper_bound(int64_t B, int64_t hkv, int32_t max_q, int32_t 
 //   64 x 1,000, 2 tokens, 8 heads 19.1 / 13.7; 1 x 8,000, 4 tokens 21.3 / 16.4;
 //   1 x 20,000, 1 token 47.2 / 30.8; 16 x 3,000, 2 tokens 17.5 / 15.3;
 //   1 x 40,000 49.7 / 54.4 (split); 32 x 2 heads, window of 1,023 24.0 / 17.9.
-//   Latent cache: 2 x 1,024, 4 tokens 23.3 / 12.3; 32 x 2,000, 1 token
+//   Latent cache: 2 x 1,024, 4 tokens 23.3 / 10.6; 32 x 2,000, 1 token
 //   25.9 / 18.6; 76 x 1,500, 4 tokens 52.8 / 36.9; 100 x 600, 1 token
 //   27.6 / 21.3; 8 x 16,384 at most, 2 tokens 33.8 / 42.8 (split).
 static bool cluster_plan(int64_t J, int64_t T, int32_t tile_keys, int64_t group, int32_t max_q,

@@ -80,6 +80,12 @@ static_assert(kTileBytes % 1024 == 0 && kOffQpe % 1024 == 0, "swizzle atoms");
 static_assert((kPBufs & (kPBufs - 1)) == 0, "P buffers: a power of two");
 
 constexpr int kNarRows = 32;  // NAR: packed rows at most
+constexpr int kNarPBuf = 2 * kNarRows * kT;  // both terms of P
+// NAR in clusters, at most 16 rows: the latent part of Q on its way to tensor memory, in
+// the P buffers' unused half: 16 rows of hi bytes, then of lo, a row's 16-byte
+// groups g at g ^ (row % 8)
+constexpr int kOffQStage = kOffP + kPBufs * kNarPBuf;
+static_assert(kOffQStage + 2 * 16 * kMlaNope <= kOffX, "the staged Q fits behind the P buffers");
 
 constexpr int kThreads = 512;  // 16 warps
 constexpr int kSoftmaxThreads = 256;
@@ -152,6 +158,13 @@ __device__ __forceinline__ float bf16_amax2(uint32_t w) {
   return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xFFFF0000u)));
 }
 
+// The power of two that takes a row of largest |value| amax into [2^7, 2^8).
+__device__ __forceinline__ int q_exponent(float amax) {
+  if (!(amax > 0.f && amax < INFINITY)) return 0;
+  const int e = 7 - ((int)((__float_as_uint(amax) >> 23) & 0xFF) - 127);
+  return e < -120 ? -120 : (e > 120 ? 120 : e);
+}
+
 // Byte offset of element (row m, column k) in a no-swizzle K-major operand
 // whose rows are `row_bytes` long: 8-row x 16-byte core matrices, K-adjacent
 // ones 128 bytes apart, 8-row groups 8 * row_bytes apart.
@@ -163,12 +176,11 @@ __device__ __forceinline__ int core_off(int m, int k, int row_bytes) {
 // GQA kernel it multiplies the page's logits, and as the value's scale joins
 // the weight, P = 2^(s + log2 scale - m_ref), with l summing P / scale. A
 // thread's 16 keys of a tile are one page. The producers bring the scales
-// with the ring slot. 64 sequences of 8K to 32K keys (733 MB), 16 heads: 154 us
-// with 3 draft tokens, 132 with one, 70 and 84 % of the measured copy bandwidth;
-// of the 154 the merge kernel is 12 and the rescales of O^T 10.
+// with the ring slot. 64 sequences of 8K to 32K keys (733 MB), 16 heads: 152 us
+// with 3 draft tokens, 131 with one, 71 and 84 % of the measured copy bandwidth;
+// of the 152 the merge kernel is 11 and the rescales of O^T 10.
 // CLU: one cluster of CTAs per item, as in the GQA kernel: two sequences of
-// 1,024 and 769 keys 12.1 us a call (23.3 split over all CTAs), 4 of them
-// staging Q's 576 columns.
+// 1,024 and 769 keys 10.6 us a call (23.3 split over all CTAs).
 // NAR: at most 32 packed rows. P's two terms are then stacked in the N of P V
 // (rows r and nar + r of P^T, columns r and nar + r of O^T, added up in the
 // epilogue): half its instructions, and N = 32 for 16 rows (64 sequences of 8K
@@ -455,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!all_or_fail(got, 4)) break;
           tc_fence_after();
           const uint32_t kst = sbase + s * kTileBytes;
-          const uint32_t pbuf = sbase + kOffP + pb * kPBuf;
+          const uint32_t pbuf = sbase + kOffP + pb * (NAR ? kNarPBuf : kPBuf);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kPvSteps; ++kk) {
@@ -575,12 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       amax = exchange(amax, true);
-      int e = 0;
-      if (amax > 0.f && amax < INFINITY) {
-        const int E = (int)((__float_as_uint(amax) >> 23) & 0xFF) - 127;
-        e = 7 - E;
-        e = e < -120 ? -120 : (e > 120 ? 120 : e);
-      }
+      const int e = q_exponent(amax);
       const float up = __uint_as_float((uint32_t)(e + 127) << 23) * (q_neg ? -1.f : 1.f);
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
       if (ok) {
@@ -624,6 +631,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return cscale * down;  // rows past R stage zeros: their logits are 0
     };
+    // The same in a cluster whose rows are one quadrant's (there it is the start
+    // that counts): the quadrant's two warps alone would convert 144 columns a
+    // thread. Here sixteen threads share a row, each
+    // with its loads in flight at once and the row's max by shuffles; the
+    // converted latent part goes through shared memory to the quadrant's
+    // warps, which move it to the TMEM operand; the rows' factors through
+    // row_vals[48, 64), which no rescale of 16 rows uses (two sequences of 1,024 and 769
+    // keys 11.9 -> 10.6 us; in the split over all CTAs its
+    // registers cost the tile loop 1 to 4 %).
+    auto stage_q16 = [&](const Piece& pq, int qidx) -> float {
+      const int row = (tid - 128) >> 4, cc = tid & 15;
+      const bool ld = ok && row < pq.R;
+      uint4 x[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) x[i] = make_uint4(0, 0, 0, 0);
+      if (ld) {
+        const int tq = row / G, gq = row - tq * G;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(pq.q0 + tq) * p.q_s0 +
+                                                          (int64_t)(pq.kvh * G + gq) * p.q_s1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = src[16 * i + cc];
+        if (cc < 8) x[4] = src[64 + cc];
+      }
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 5; ++i)
+        amax = fmaxf(amax, fmaxf(fmaxf(bf16_amax2(x[i].x), bf16_amax2(x[i].y)),
+                                 fmaxf(bf16_amax2(x[i].z), bf16_amax2(x[i].w))));
+#pragma unroll
+      for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const int e = q_exponent(amax);
+      const float up = __uint_as_float((uint32_t)(e + 127) << 23) * (q_neg ? -1.f : 1.f);
+      unsigned char* stage = sm + kOffQStage + row * kMlaNope;
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        split_q4(x[i].x, x[i].y, up, hi[0], lo[0]);
+        split_q4(x[i].z, x[i].w, up, hi[1], lo[1]);
+        const int c8 = 16 * i + cc;  // eight columns
+        const int off = (((c8 >> 1) ^ (row & 7)) << 4) + ((c8 & 1) << 3);
+        *reinterpret_cast<uint2*>(stage + off) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(stage + 16 * kMlaNope + off) = make_uint2(lo[0], lo[1]);
+      }
+      if (cc == 0) row_vals[48 + row] = __uint_as_float((uint32_t)(127 - e) << 23);
+      if (qidx > 0) wait_or_fail(kBarQFree, (qidx - 1) & 1, 128);
+      if (ok && cc < 8) {
+        split_q4(x[4].x, x[4].y, up, hi[0], lo[0]);
+        split_q4(x[4].z, x[4].w, up, hi[1], lo[1]);
+        *reinterpret_cast<uint2*>(qpe_s + core_off(row, 8 * cc, kMlaPe)) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(qpe_s + core_off(16 + row, 8 * cc, kMlaPe)) = make_uint2(lo[0], lo[1]);
+      }
+      named_bar(kBarAllSoftmax, kSoftmaxThreads);
+      const float down = row_vals[48 + rl];
+      if (ok) {
+        if (q == 0) {
+          // this lane's TMEM row: hi of row rl, or lo; columns [256 kh, +256)
+          const unsigned char* src = sm + kOffQStage + sub * (16 * kMlaNope) + rl * kMlaNope;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t d[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 v = *reinterpret_cast<const uint4*>(src + (((16 * kh + 4 * h + i) ^ (rl & 7)) << 4));
+              d[4 * i] = v.x;
+              d[4 * i + 1] = v.y;
+              d[4 * i + 2] = v.z;
+              d[4 * i + 3] = v.w;
+            }
+            tmem_st_32x32b_x16(tmem + lane_base + kColQ + 64 * kh + 16 * h, d);
+          }
+          tmem_wait_st();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarQFull));
+      }
+      return cscale * down;
+    };
+    auto stage = [&](const Piece& pq, int qidx) -> float {
+      if constexpr (NAR && CLU)
+        if (nar == 16) return stage_q16(pq, qidx);
+      return stage_q(pq, qidx);
+    };
     // The next piece's Q segments of this thread (three 128-byte lines) into
     // L2, a piece ahead: under full HBM load a round trip to DRAM takes
     // several microseconds, and staging Q sits on the softmax's path.
@@ -643,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int jn = j;
       long long tsn = ts;
       const bool has_next = next_piece(p, t0, t1, jn, tsn, pn, seqs);
-      const float rs = staged_next ? rs_next : stage_q(pc, piece_idx);
+      const float rs = staged_next ? rs_next : stage(pc, piece_idx);
       staged_next = false;
       if (has_next) prefetch_q(pn);
       const bool row_ok = r < pc.R;
@@ -662,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b = cur & (kSBufs - 1);
         const int pb = cur & (kPBufs - 1);
         if (lt == pc.lt1 - 1 && has_next) {
-          rs_next = stage_q(pn, piece_idx + 1);
+          rs_next = stage(pn, piece_idx + 1);
           staged_next = true;
         }
         float x[16];  // logits of keys [16 qtr, +16) of this tile, this row
@@ -759,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           // P^T operand: row r, keys [16 qtr, +16) = one core-matrix row
-          unsigned char* pbuf = sm + kOffP + pb * kPBuf;
+          unsigned char* pbuf = sm + kOffP + pb * (NAR ? kNarPBuf : kPBuf);
           const int off = core_off(r, 16 * qtr, kT);
           *reinterpret_cast<uint4*>(pbuf + off) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
           *reinterpret_cast<uint4*>(pbuf + (NAR ? core_off(nar, 0, kT) : kPHalf) + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);

@@ -435,3 +435,19 @@ def test_workspace_errors():
     with pytest.raises(va.VerifyAttnError) as e:
         run(w, ks, vs, workspace=torch.zeros(512, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 5
+
+
+@pytest.mark.parametrize("scale", [-0.0625, 0.0, 0.2])
+@pytest.mark.parametrize("hq,q", [(8, 1), (16, 1), (16, 4)])
+def test_latent_sign_of_the_softmax_scale_and_size_of_q(scale, hq, q):
+    """Both ways of staging Q (one row group and more), with heads from 2^-20
+    times their size up (to 2^20 where the softmax scale is 0) and an all-zero
+    row: each row has its own power of two."""
+    w = make_mla_workload([q, q], [900, 200], hq, "fp8_e4m3", seed=570 + hq + q).to("cuda")
+    s, _ = scales_for(w, hq, spread=2.0)
+    e = torch.linspace(-20, 20 if scale == 0.0 else 0, hq, device="cuda").round()
+    w.q.copy_((w.q.float() * torch.exp2(e)[None, :, None]).to(torch.bfloat16))
+    w.q[0, 0] = 0
+    w.softmax_scale = scale
+    for splits in (0, 1):
+        compare(run_mla(w, s, num_splits=splits), *oracle_mla(w, s), gates=False)
