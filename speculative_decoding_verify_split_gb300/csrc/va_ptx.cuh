@@ -234,8 +234,6 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b,
       : "memory");
 }
 
-// Arrives on `bar` once every tcgen05 operation issued so far by this thread
-// has completed.
 // One thread of a converged warp, the same one at every call.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -243,6 +241,8 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// Arrives on `bar` once every tcgen05 operation issued so far by this thread
+// has completed.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
@@ -344,7 +344,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Named barrier over `count` threads (a multiple of 32).
 // Barrier of all threads of all CTAs of the cluster, in two halves; orders
 // shared memory between them. Threads arrive one by one and wait by warp.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
@@ -375,6 +374,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+// Named barrier over `count` threads (a multiple of 32).
 __device__ __forceinline__ void named_bar(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
