@@ -21,14 +21,18 @@
 // back-to-back calls overlap a merge with the next call's launch and setup.
 //  * FP8 E4M3 cache, kind::f8f6f4. Q (bf16) is scaled per row by an exact
 //    power of two 2^e and split into two e4m3 terms, Qh = e4m3(Q 2^e) and
-//    Ql = e4m3(Q 2^e - Qh); P is split the same way. The two terms are
+//    Ql = e4m3(Q 2^e - Qh). P V is kind::mxf8f6f4: P is split too, per block of
+//    32 keys of a row with a power of two of the block's own, which the MMA
+//    takes as the block's scale (va_fp8.cuh), so that weights keep their 8 bits
+//    whatever larger weights the row holds elsewhere. The two terms are
 //    stacked in one M=128 MMA: packed row 16q + i uses A rows 32q + i (hi)
 //    and 32q + 16 + i (lo), so the hi and lo results land in lanes i and
 //    16 + i of the same TMEM lane quadrant; two 16-lane TMEM loads hand each
 //    softmax thread both terms of its own keys, which it adds.
 //    Q K^T and P V take their A operands (Q, P) from TMEM: Q is staged there
 //    by the softmax warps, P written there beside the one S tile, which is
-//    free again once the softmax has loaded it. The shared memory this
+//    free again once the softmax has loaded it; P's block scales (512 bytes a
+//    tile) go through shared memory. The shared memory this
 //    leaves to the rings holds 4 K + 3 V slots. The variant kernel, whose
 //    soft cap can make the softmax the bottleneck, keeps Q in shared memory
 //    and two S tiles, each P written over its S (3 K + 3 V). K and V are
@@ -53,12 +57,14 @@
 //              maxima and sums through shared memory around a per-quadrant
 //              named barrier. They also stage Q (the next item's during the
 //              current item's last tile) and write the epilogue.
-// Online softmax in log2 units keeps a per-row reference m_ref and computes
-// P = 2^(s - m_ref + 6) <= 2^8.8; m_ref moves (and O, l are rescaled in
-// TMEM) only when a tile's max exceeds it by more than 2.8, and a row's first
-// m_ref sits 4 above its first tile's max, so rescales are rare. The tile
-// max is taken over the raw dot products and the (positive) row scale
-// applied inside the FMA of P's exponent. The VAR instantiation adds the
+// Online softmax in log2 units keeps a per-row reference m_ref. FP8: P =
+// 2^(s - e) with the block's exponent e, which does not depend on m_ref, and
+// block scale 2^(e - m_ref); m_ref is the first tile's max, rounded down, and
+// moves (O and l are rescaled in TMEM) only when a tile's max exceeds it by more
+// than 32. BF16: P = 2^(s - m_ref + 6); m_ref moves when a tile's max exceeds it
+// by more than 2.8, and a row's first m_ref sits 4 above its first tile's max, so
+// rescales are rare. The max is taken over the raw dot products and the
+// (positive) row scale applied inside the FMA of P's exponent. The VAR instantiation adds the
 // generic attention's variants (sliding
 // window, logit soft cap, sinks). Waits are bounded in time and warp-uniform:
 // on a timeout the kernel sets the workspace status word, stops issuing
@@ -100,7 +106,7 @@ struct Cfg {
   static constexpr bool kQInTmem = QTM;
   static constexpr bool kPOverS = FP8 && !QTM;
   static constexpr int kSBufs = FP8 ? (kQInTmem ? 1 : 2) : 4;  // S tiles in TMEM
-  static constexpr int kPBufs = FP8 ? 2 : 4;               // P buffers: TMEM (fp8) / smem (bf16)
+  static constexpr int kPBufs = FP8 ? (kQInTmem ? 1 : 2) : 4;  // P buffers: TMEM (fp8) / smem (bf16)
   static constexpr int kEsize = FP8 ? 1 : 2;               // bytes per KV element
   static constexpr int kChunks = kHeadDim * kEsize / 128;  // 128-byte d chunks (2 or 4)
   static constexpr int kRegion = kT * 128;                 // one d chunk of a K or V tile
@@ -136,13 +142,14 @@ struct Cfg {
   static constexpr int kKeysPerPvStep = 32 / kEsize;
   static constexpr uint32_t kFmt = FP8 ? 0u : 1u;          // e4m3 / bf16
   static constexpr uint32_t kIdQK = instr_desc(kFmt, kFmt, false, kT, kM);
-  static constexpr uint32_t kIdPV = instr_desc(kFmt, kFmt, true, kHeadDim, kM);
+  static constexpr uint32_t kIdPV = FP8 ? instr_desc_mx(true, kHeadDim, kM) : instr_desc(kFmt, kFmt, true, kHeadDim, kM);
   static_assert(kTensorBytes == 32768, "ring slot size");
   // shared memory: rings | Q (smem Q only) | P buffers (smem P only) | row
   // exchange | barriers
   static constexpr int kOffQ = kRingBytes;
   static constexpr int kOffP = kOffQ + (kQInTmem ? 0 : 32768);
-  static constexpr int kOffX = kOffP + (kPInTmem ? 0 : 32768);  // [2 parity][2 kh][64 rows] floats
+  static constexpr int kOffX = kOffP + (kPInTmem ? 0 : 32768);  // [2 parity (BF16)][2 kh][64 rows] floats
+  [[maybe_unused]] static constexpr int kOffSf = kOffX + 512;  // FP8: P's block scales, [32 lanes][4 quadrants][4 blocks] bytes
   static constexpr int kOffBar = kOffX + 1024;
   static constexpr int kOffSeqs = kOffBar + 1024;  // the batch's lengths (SeqMeta, kSeqCache)
   static constexpr int kSmemBytes = kOffSeqs + 16 * kSeqCache;
@@ -161,21 +168,30 @@ constexpr int kThreads = 416;  // 13 warps
 constexpr int kSoftmaxThreads = 256;
 
 // TMEM columns. O [0, 256), then BF16: four 64-column S tiles; FP8 with Q
-// in shared memory: two 128-column S tiles, each P (32 columns) written over
-// its S; FP8 with Q in TMEM: one 128-column S tile, two P tiles of 32 columns
-// (128 keys of e4m3, hi row in lane 32q + i, lo row in lane 32q + 16 + i, as
-// S) and the Q A operand (64 columns: 256 e4m3 bytes of each hi and lo row).
+// in shared memory: two 128-column S tiles, each P written over its S; FP8
+// with Q in TMEM: one 128-column S tile, one P tile and the Q A operand (64
+// columns: 256 e4m3 bytes of each hi and lo row). A P tile is 32 columns (128
+// keys of e4m3, hi row in lane 32q + i, lo row in lane 32q + 16 + i, as S), then
+// the block scales of its 128 rows (4 columns), then V's (8 columns, all 1).
 constexpr uint32_t kColO = 0;    // 256 fp32 columns
 constexpr uint32_t kColS = 256;
 constexpr uint32_t kColP = 384;  // FP8, Q in TMEM
+constexpr uint32_t kColSfA = 32;  // behind P's first column
+constexpr uint32_t kColSfB = 40;
 constexpr uint32_t kColQ = 448;  // FP8, Q in TMEM
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kScaleOnes = 0x7F7F7F7Fu;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPShift = 6.f;      // P = 2^(s - m_ref + kPShift)
+// FP8: a row's reference moves only when a tile's max passes m_ref + kFar, to
+// that max rounded down. P's block scales keep the weights in range, so this
+// only bounds the fp32 sums (l <= 2 n 2^kFar / vs, vs >= 2^-64).
+constexpr float kFar = 32.f;
+// BF16: P = 2^(s - m_ref + kPShift), no block scales.
+constexpr float kPShift = 6.f;
 constexpr float kHeadroom = 1.f;    // m_ref = tile max + kHeadroom when it moves
 constexpr float kHeadroomFirst = 4.f;  // ... and + kHeadroomFirst for a row's first reference
-constexpr float kOvershoot = 2.8f;  // move only if the tile max > m_ref + kOvershoot (P <= 2^8.8 < 448)
+constexpr float kOvershoot = 2.8f;  // move only if the tile max > m_ref + kOvershoot (P <= 2^8.8)
 
 
 constexpr int kMaxSlots = 5;
@@ -215,9 +231,9 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 // VAR: compiled with the sliding-window / soft-cap / sink code (the plain path
 // is compiled without it). QTM: the FP8 layout with Q and P in TMEM (Cfg).
 // SCL: a page-scaled cache (FP8). The V scale vs of a key's page is folded
-// into the key's weight, P = 2^(s + log2 vs - m_ref): the reference max is
-// taken over s + log2 vs, O accumulates P times the codes, and the normaliser
-// l sums P / vs. K's scale multiplies the page's logits. Both are per page,
+// into the key's weight, P = 2^(s + log2 vs - e): references and block exponents
+// are taken over s + log2 vs, O accumulates P times the codes, and the
+// normaliser l sums P / vs. K's scale multiplies the page's logits. Both are per page,
 // so they cost nothing per key: a thread's 32 keys of a tile are two pages,
 // each with its own factor and offset in the FMA of P's exponent, and its own
 // partial sum of l. The V producers, which walk the page ids anyway, bring
@@ -244,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kT = C::kT;
   constexpr int kSBufs = C::kSBufs;
   constexpr int kPBufs = C::kPBufs;
+  constexpr float kShift = FP8 ? 0.f : kPShift;  // O and l are sums of 2^(s - m_ref + kShift)
   constexpr int kPagesPerTile = C::kPagesPerTile;
   constexpr int kKpt = C::kKpt;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -532,15 +549,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t vst = sbase + (C::kKSlots + s) * C::kTensorBytes;
           const uint32_t pbuf = sbase + C::kOffP + pb * C::kPBuf;
           if (elect_one()) {
+            // P(x) sits in the P tile (or over S buffer pb), 8 columns per K-step
+            const uint32_t pt = tmem + (C::kPOverS ? kColS + pb * kT : kColP);
+            if constexpr (FP8)
+              tmem_cp_scales(pt + kColSfA, smem_desc(sbase + C::kOffSf, 0, 128, kLayoutNone));
 #pragma unroll
             for (int kk = 0; kk < C::kPvSteps; ++kk) {
               const uint64_t bdesc = smem_desc(vst + kk * (C::kKeysPerPvStep / 8) * 1024, C::kRegion,
                                                1024, kLayoutSw128);
               const uint32_t acc = (i == 0 && kk == 0) ? 0u : 1u;
-              if constexpr (C::kPInTmem) {
-                // P(x) sits in P tile pb (or over S buffer pb), 8 columns per K-step
-                const uint32_t pcol = C::kPOverS ? kColS + pb * kT : kColP + pb * (kT / 4);
-                mma_f8f6f4_ta(tmem + kColO, tmem + pcol + 8 * kk, bdesc, C::kIdPV, acc);
+              if constexpr (FP8) {
+                mma_mxf8_ta(tmem + kColO, pt + 8 * kk, bdesc, C::kIdPV | ((uint32_t)kk << 29), pt + kColSfA,
+                            pt + kColSfB, acc);
               } else {
                 const uint64_t a = smem_desc(pbuf + kk * 256, 128, C::kPSbo, kLayoutNone);
                 mma<FP8>(tmem + kColO, a, bdesc, C::kIdPV, acc);
@@ -617,19 +637,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // Row-wide combine of a per-thread value: lanes t and t^16 share a row in
     // this warp, the partner warp of the quadrant holds the other half. Values
-    // go through shared memory (double-buffered by round parity) around the
-    // quadrant's named barrier (ids 1..4, 64 threads). Both warps call this the
-    // same number of times, failed or not, so the barrier never strands one.
+    // go through shared memory around the quadrant's named barrier (ids 1..4, 64
+    // threads), double-buffered by round parity (BF16) or followed by a second
+    // barrier (FP8: it combines a few times per item only). Both warps call this
+    // the same number of times, failed or not, so the barrier never strands one.
     int xround = 0;
     auto exchange = [&](float v, bool is_max) {
       v = is_max ? fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16)) : v + __shfl_xor_sync(0xffffffffu, v, 16);
-      const int par = xround & 1;
+      const int par = FP8 ? 0 : xround & 1;
       ++xround;
       if (sub == 0) xch[(par * 2 + kh) * 64 + r] = v;
       named_bar(1 + q, 64);
       const float other = xch[(par * 2 + (kh ^ 1)) * 64 + r];
+      if constexpr (FP8) named_bar(1 + q, 64);
       return is_max ? fmaxf(v, other) : v + other;
     };
+    // FP8: V's block scales are 1. With a P tile of its own they stay.
+    if constexpr (FP8 && !C::kPOverS) {
+      if (kh == 0) {
+        tmem_fill_32x32b_x8(tmem + lane_base + kColP + kColSfB, kScaleOnes);
+        tmem_wait_st();
+      }
+    }
     // Q tile of piece pq (the qidx-th piece of this CTA) into the swizzled
     // K-major A operand, after Q K^T of the previous piece has read the old
     // one; this thread: d [64 qtr, +64). Returns the row's logit scale.
@@ -817,6 +846,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        // over S, V's block scales are written with every P, in all quadrants
+        if constexpr (C::kPOverS) {
+          if (here && kh == 0 && idle) {
+            tc_fence_after();
+            tmem_fill_32x32b_x8(tmem + lane_base + kColS + b * kT + kColSfB, kScaleOnes);
+            tmem_wait_st();
+          }
+        }
         if (idle) {
           if constexpr (!C::kPOverS) {
             if (here && lane == 0) mbar_arrive(bar(kBarSFree + b));
@@ -878,85 +915,86 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
+          // this thread's max over its keys: FP8 32 of them, a block of P, in log2
+          // units (xs > 0 keeps the order)
           float tmax = -INFINITY;
-          if constexpr (SCL) {
-            float t2[2] = {-INFINITY, -INFINITY};
+          float t2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < kKpt; i += 2) t2[i / 16] = fmax3(t2[i / 16], x[i], x[i + 1]);
-            tmax = exchange(fmaxf(fmaf(t2[0], xs2[0], lv[0]), fmaf(t2[1], xs2[1], lv[1])), true);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kKpt; i += 2) tmax = fmax3(tmax, x[i], x[i + 1]);
-            tmax = exchange(tmax * xs, true);  // log2 units (xs > 0 keeps the order)
+          for (int i = 0; i < kKpt; i += 2) t2[i / 16] = fmax3(t2[i / 16], x[i], x[i + 1]);
+          bool move = true;  // some row's reference may move
+          if constexpr (FP8) {
+            tmax = fmaxf(fmaf(t2[0], xs2[0], lv[0]), fmaf(t2[1], xs2[1], lv[1]));
+            // (an item's first tile sets them: no vote)
+            move = cur == first || named_bar_or(1 + q, 64, ok && tmax > m_ref + kFar);
           }
+          float rmax = -INFINITY;
+          if (move) rmax = exchange(FP8 ? tmax : t2[0] * xs, true);
           if (!ok) continue;
 
-          // P buffer pb was last read by PV(cur - kPBufs). (A P over S(cur):
-          // Q K^T(cur) already waited for that.)
-          if (!C::kPOverS && cur >= kPBufs &&
-              !wait_or_fail(kBarPFree + pb, ((cur - kPBufs) / kPBufs) & 1, 512))
-            continue;
+          // P buffer pb was last read by PV(cur - kPBufs)
+          if (!FP8 && cur >= kPBufs && !wait_or_fail(kBarPFree + pb, ((cur - kPBufs) / kPBufs) & 1, 512)) continue;
 
-          const bool need = tmax > m_ref + kOvershoot;
-          // A row's first reference takes more headroom: its running max keeps
-          // growing over the next tiles (by ~sd * (sqrt(2 ln n) - sqrt(2 ln T))),
-          // and every later move waits for P V of the previous tile.
-          const float m_new = need ? tmax + (m_ref == -INFINITY ? kHeadroomFirst : kHeadroom) : m_ref;
-          const bool rescale = need && (m_ref != -INFINITY) && (cur > first);
-          const float alpha = rescale ? ex2(m_ref - m_new) : 1.f;
-          if (__any_sync(0xffffffffu, rescale)) {
-            // O holds earlier tiles of this piece: wait for PV(cur - 1), then
-            // scale this thread's part of the row in TMEM
-            const int xp = cur - 1;
-            if (!wait_or_fail(kBarPFree + (xp & (kPBufs - 1)), (xp / kPBufs) & 1, 1024)) continue;
-            tc_fence_after();
+          if (move) {
+            const bool need = rmax > m_ref + (FP8 ? kFar : kOvershoot);
+            // BF16: a row's first reference takes more headroom: its running max
+            // keeps growing over the next tiles (by ~sd * (sqrt(2 ln n) -
+            // sqrt(2 ln T))), and every later move waits for P V of the previous
+            // tile.
+            const float top = FP8 ? floorf(rmax) : rmax + (m_ref == -INFINITY ? kHeadroomFirst : kHeadroom);
+            const float m_new = need ? top : m_ref;
+            const bool rescale = need && (m_ref != -INFINITY) && (cur > first);
+            const float alpha = rescale ? ex2(m_ref - m_new) : 1.f;
+            if (__any_sync(0xffffffffu, rescale)) {
+              // O holds earlier tiles of this piece: wait for PV(cur - 1), then
+              // scale this thread's part of the row in TMEM
+              const int xp = cur - 1;
+              if (!wait_or_fail(kBarPFree + (xp & (kPBufs - 1)), (xp / kPBufs) & 1, 1024)) continue;
+              tc_fence_after();
 #pragma unroll 1
-            for (int k = 0; k < (FP8 ? 4 : 2); ++k) {
-              uint32_t o[32];
-              const uint32_t ta = tmem + lane_base + kColO + 128 * kh + 32 * k;
-              if constexpr (FP8) {
-                tmem_ld_32x32b_x32(ta, o);
-                tmem_wait_ld();
+              for (int k = 0; k < (FP8 ? 8 : 2); ++k) {
+                if constexpr (FP8) {
+                  uint32_t o[16];
+                  const uint32_t ta = tmem + lane_base + kColO + 128 * kh + 16 * k;
+                  tmem_ld_32x32b_x16(ta, o);
+                  tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tmem_st_32x32b_x32(ta, o);
-              } else {
-                tmem_ld_16x32bx2_x32<64>(ta, o);
-                tmem_wait_ld();
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                  tmem_st_32x32b_x16(ta, o);
+                } else {
+                  uint32_t o[32];
+                  const uint32_t ta = tmem + lane_base + kColO + 128 * kh + 32 * k;
+                  tmem_ld_16x32bx2_x32<64>(ta, o);
+                  tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tmem_st_16x32bx2_x32<64>(ta, o);
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                  tmem_st_16x32bx2_x32<64>(ta, o);
+                }
               }
+              tmem_wait_st();
             }
-            tmem_wait_st();
+            l *= alpha;
+            m_ref = m_new;
           }
-          l *= alpha;
-          m_ref = m_new;
 
-          // P = 2^(x - m_ref + kPShift) into the K-major no-swizzle A operand
-          // a row with no visible key yet (m_ref = -inf) gets P = ex2(-inf) = 0
-          const float mref_s = m_ref != -INFINITY ? m_ref - kPShift : INFINITY;
+          // a row with no visible key yet (m_ref = -inf) gets P = 0
           float ls0 = 0.f, ls1 = 0.f;
-          unsigned char* pbuf = sm + C::kOffP + pb * C::kPBuf;
           if constexpr (FP8) {
+            // P = 2^(x - e), e the block's exponent (va_fp8.cuh); ls0 and ls1: the
+            // sums of the first and of the second page
+            const float e = block_exponent(tmax);
+            const float es = block_scale(e, m_ref);
+            const float off2[2] = {lv[0] - e, lv[1] - e};
             uint32_t ph[8], pl[8];
-            const float off2[2] = {lv[0] - mref_s, lv[1] - mref_s};
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float a = ex2(SCL ? fmaf(x[2 * i], xs2[i / 8], off2[i / 8]) : fmaf(x[2 * i], xs, -mref_s));
-              const float bb = ex2(SCL ? fmaf(x[2 * i + 1], xs2[i / 8], off2[i / 8]) : fmaf(x[2 * i + 1], xs, -mref_s));
-              if (SCL) {
-                // ls0, ls1: the sums of the first and of the second page
-                if (i < 8)
-                  ls0 += a + bb;
-                else
-                  ls1 += a + bb;
-              } else {
-                ls0 += a;
-                ls1 += bb;
-              }
+              const float a = ex2(fmaf(x[2 * i], xs2[i / 8], off2[i / 8]));
+              const float bb = ex2(fmaf(x[2 * i + 1], xs2[i / 8], off2[i / 8]));
+              if (i < 8)
+                ls0 += a + bb;
+              else
+                ls1 += a + bb;
               uint32_t h2, l2;
-              split_p(a, bb, h2, l2);
+              split_weights(a, bb, h2, l2);
               if (i & 1) {
                 ph[i >> 1] |= h2 << 16;
                 pl[i >> 1] |= l2 << 16;
@@ -965,20 +1003,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pl[i >> 1] = l2;
               }
             }
-            // A operand of P V in TMEM, P tile pb or over S(cur) (pb == b
+            if constexpr (SCL)
+              l += (ls0 * ex2(-lv[0]) + ls1 * ex2(-lv[1])) * exp2_int(es);  // the weights without vs
+            else
+              l += (ls0 + ls1) * exp2_int(es);
+            // PV(cur - 1) has read the scales' shared memory (and the P tile)
+            if (cur > 0 && !wait_or_fail(kBarPFree + ((cur - 1) & (kPBufs - 1)), ((cur - 1) / kPBufs) & 1, 512)) continue;
+            const uint32_t sf = sbase + C::kOffSf + 16 * rl + 4 * q + qtr;
+            st_shared_u8(sf, scale_byte(es));
+            st_shared_u8(sf + 256, scale_byte(es) - kLoShift);
+            // A operand of P V in TMEM, in the P tile or over S(cur) (pb == b
             // then): lane 32q + rl (hi row) and
             // lane 32q + 16 + rl (lo row) take the e4m3 bytes of keys
             // [64 kh, +64) at columns [16 kh, +16). This thread holds keys
             // [32 qtr, +32) of both: two 16-lane stores, its hi bytes into the
             // hi row and its lo bytes into the lo row, threads 16-31 at +8.
             // Over S, the quadrant's other warp read its S columns before the
-            // exchange.
-            const uint32_t pcol = C::kPOverS ? kColS + pb * kT : kColP + pb * (kT / 4);
+            // vote.
+            const uint32_t pcol = C::kPOverS ? kColS + pb * kT : kColP;
             tc_fence_after();
             tmem_st_16x32bx2_x8<8>(tmem + lane_base + pcol + 16 * kh, ph);
             tmem_st_16x32bx2_x8<8>(tmem + lane_base + (16u << 16) + pcol + 16 * kh, pl);
+            if (C::kPOverS && kh == 0) tmem_fill_32x32b_x8(tmem + lane_base + pcol + kColSfB, kScaleOnes);
             tmem_wait_st();
           } else {
+            // P = 2^(x - m_ref + kPShift) into the K-major no-swizzle A operand
+            const float mref_s = m_ref != -INFINITY ? m_ref - kPShift : INFINITY;
+            unsigned char* pbuf = sm + C::kOffP + pb * C::kPBuf;
             uint32_t pw[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -992,11 +1043,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned char* base = pbuf + (r >> 3) * C::kPSbo + (2 * qtr) * 128 + (r & 7) * 16;
             *reinterpret_cast<uint4*>(base) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
             *reinterpret_cast<uint4*>(base + 128) = make_uint4(pw[4], pw[5], pw[6], pw[7]);
-          }
-          if constexpr (SCL)
-            l += ls0 * ex2(-lv[0]) + ls1 * ex2(-lv[1]);  // the weights without vs
-          else
             l += ls0 + ls1;
+          }
         }
         // V rows no row may see and whose pages may hold anything are zeroed,
         // so that 0 * garbage cannot reach O: past S in the item's last tile
@@ -1050,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool direct = !CLU && pc.direct;
       if constexpr (VAR) {
         if (p.sinks && direct && row_ok && m_ref != -INFINITY)
-          lrow += exp2f(p.sinks[pc.kvh * G + gq] * kLog2e - (m_ref - kPShift));
+          lrow += exp2f(p.sinks[pc.kvh * G + gq] * kLog2e - (m_ref - kShift));
       }
       const float inv = lrow > 0.f ? vd / lrow : 0.f;
       const int64_t piece = (int64_t)pc.j + c;
@@ -1113,11 +1161,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (CLU) {
         if (row_ok && kh == 0 && sub == 0) {
-          part_ml[2 * r] = (m_ref == -INFINITY) ? -INFINITY : m_ref - kPShift;
+          part_ml[2 * r] = (m_ref == -INFINITY) ? -INFINITY : m_ref - kShift;
           part_ml[2 * r + 1] = lrow;
         }
       } else if (row_ok && !direct && kh == 0 && sub == 0) {
-        p.ws_ml[(piece * p.max_rows + r) * 2 + 0] = (m_ref == -INFINITY) ? -INFINITY : m_ref - kPShift;
+        p.ws_ml[(piece * p.max_rows + r) * 2 + 0] = (m_ref == -INFINITY) ? -INFINITY : m_ref - kShift;
         p.ws_ml[(piece * p.max_rows + r) * 2 + 1] = lrow;
       }
       tc_fence_before();
