@@ -7,28 +7,33 @@
 // the latent c as the value. All Hq heads x L draft tokens (<= 64 rows) of a
 // sequence share every cache row, so each row is read from HBM once.
 //
-// The work split, the per-row online softmax in log2 units with a lazy
-// reference max, the e4m3 hi/lo split of Q and P and the bounded waits are
-// those of the GQA kernel (va_main_tc.cu). What differs is the tensor-memory
-// plan, which a 512-wide value forces. With Q and P split into two e4m3 terms
-// stacked in the MMA's M (hi rows and lo rows), O would need 128 lanes x 512
-// fp32 columns, all of TMEM. So:
+// The work split, the per-row online softmax in log2 units, the e4m3 hi/lo
+// split of Q and, with block scales, of P and the bounded waits are those of the
+// GQA kernel (va_main_tc.cu). What differs is the tensor-memory plan, which a
+// 512-wide value forces. With Q and P split into two e4m3 terms stacked in the
+// MMA's M (hi rows and lo rows), O would need 128 lanes x 512 fp32 columns, all
+// of TMEM. So:
 //  * S = Q K^T as before: M = 128 stacked rows (hi and lo of packed row
 //    16q + i in lanes 32q + i and 32q + 16 + i), N = 64 keys, K = 576. The
-//    latent part of Q is the A operand in TMEM (128 columns), the rope part a
-//    no-swizzle A operand in smem (8 KB); K is the cache tile.
+//    latent part of Q is the A operand in TMEM (112 columns), its last 64
+//    columns and the rope part a no-swizzle A operand in smem (16 KB); K is the
+//    cache tile.
 //  * O is kept transposed, O^T = V^T P^T: M = 128 latent columns per chunk,
-//    N = 64 packed rows, K = keys. The two e4m3 terms of P are two MMAs into
-//    the same accumulator (stacked in K, not M), so O^T takes 4 chunks x 64
-//    columns = 256 TMEM columns. V^T is the cache tile's latent part read as
-//    an MN-major A operand; P^T is a K-major B operand in smem.
-//  TMEM: O^T 0-255, two 64-column S tiles 256-383, Q latent 384-511.
+//    N = the packed rows in use (a multiple of 16), K = keys. V^T is the cache
+//    tile's latent part read as an MN-major A operand; P^T is a K-major B operand
+//    in smem. Above 32 rows the two e4m3 terms of P are two MMAs into the same
+//    accumulator (stacked in K), each with the block scales of its term; up to 32
+//    rows a page-scaled call stacks them in N. O^T takes 4 chunks x 64 columns =
+//    256 TMEM columns.
+//  TMEM: O^T 0-255, two 64-column S tiles 256-383, Q latent 384-495, block
+//  scales 496-511 (V's, all 1; P's, one set per P buffer).
 // A cache tile is 64 keys = 4 pages; a page is 5 TMA boxes of 16 rows: four
 // 128-byte latent chunks (128-byte swizzle) and the 64-byte rope part (64-byte
 // swizzle, its own tensor map), so a tile fills four 8 KB regions and one of
-// 4 KB; five ring slots (180 KB) are in flight, beside four P^T buffers (the
-// tensor pipe runs Q K^T up to two tiles ahead of P V, so the softmax's wait
-// for the P buffer of tile t - 4 never blocks). A slot is freed after P V,
+// 4 KB; five ring slots (180 KB) are in flight, beside three P^T buffers (the
+// tensor pipe runs Q K^T up to two tiles ahead of P V; four buffers, for which
+// Q's second smem part leaves no room, would save 1 % of a 64-row call). A slot
+// is freed after P V,
 // since the same bytes are K and V. The cache loads carry an L2 evict_first
 // policy, and the kernel is launched as a programmatic dependent of the
 // stream's previous kernel (setup before griddepcontrol.wait), as in the GQA
@@ -60,32 +65,36 @@ constexpr int kBoxes = kPagesPerTile * kRegions;  // 20 boxes per tile (16 of 2 
 constexpr uint32_t kPageBytes = 4 * 2048 + 1024;   // one page's boxes
 static_assert(kBoxes <= 32, "one box per lane");
 constexpr int kSBufs = 2;
-constexpr int kPBufs = 4;                      // P^T buffers: the wait for P V(t - 4) never blocks
+constexpr int kPBufs = 3;                      // P^T buffers, and their block scales
 constexpr int kPHalf = 64 * kT;                // one e4m3 term of P: 64 rows x 64 keys
 constexpr int kPBuf = 2 * kPHalf;              // hi then lo
-constexpr int kQpeBytes = 128 * kMlaPe;        // 128 stacked rows x 64 bytes
-constexpr int kQkSteps = kMlaNope / 32;        // 16 K-steps from the TMEM A operand
-constexpr int kQkPeSteps = kMlaPe / 32;        // 2 from the smem A operand
+constexpr int kQkSteps = kMlaNope / 32;        // 16 K-steps over the latent part
+constexpr int kQkTmemSteps = kQkSteps - 2;     // all but the last two from the TMEM A operand
+constexpr int kQkPeSteps = kMlaPe / 32;        // 2 over the rope part
+// the smem A operand: 128 stacked rows of the rope part and the last latent steps
+constexpr int kQpeRow = kMlaPe + 32 * (kQkSteps - kQkTmemSteps);
+constexpr int kQpeBytes = 128 * kQpeRow;
 constexpr int kPvSteps = kT / 32;              // 2 K-steps of 32 keys
 constexpr int kChunks = kMlaNope / 128;        // 4 O^T chunks of 128 latent columns
 
 constexpr int kOffQpe = kSlots * kTileBytes;
 constexpr int kOffP = kOffQpe + kQpeBytes;
 constexpr int kOffX = kOffP + kPBufs * kPBuf;  // [2 parity][2 kh][64 rows] floats
-constexpr int kOffBar = kOffX + 1024;
+constexpr int kOffSf = kOffX + 1024;           // per P buffer its block scales: [32 rows][4 row groups][4] bytes
+constexpr int kOffBar = kOffSf + 512 * kPBufs;
 constexpr int kOffSeqs = kOffBar + 2048;  // the batch's lengths (SeqMeta, kSeqCache)
 constexpr int kSmemBytes = kOffSeqs + 16 * kSeqCache;
 static_assert(kSmemBytes + 1024 <= 232448, "shared memory (with the 1 KB alignment slack)");
 static_assert(kTileBytes % 1024 == 0 && kOffQpe % 1024 == 0, "swizzle atoms");
-static_assert((kPBufs & (kPBufs - 1)) == 0, "P buffers: a power of two");
 
 constexpr int kNarRows = 32;  // NAR: packed rows at most
-constexpr int kNarPBuf = 2 * kNarRows * kT;  // both terms of P
+__host__ __device__ constexpr int nar_p_buf(int rows) { return 2 * rows * kT; }  // both terms of P
 // NAR in clusters, at most 16 rows: the latent part of Q on its way to tensor memory, in
-// the P buffers' unused half: 16 rows of hi bytes, then of lo, a row's 16-byte
+// the P buffers' unused part: 16 rows of hi bytes, then of lo, a row's 16-byte
 // groups g at g ^ (row % 8)
-constexpr int kOffQStage = kOffP + kPBufs * kNarPBuf;
+constexpr int kOffQStage = kOffP + kPBufs * nar_p_buf(16);
 static_assert(kOffQStage + 2 * 16 * kMlaNope <= kOffX, "the staged Q fits behind the P buffers");
+static_assert(nar_p_buf(kNarRows) <= kPBuf, "P buffers");
 
 constexpr int kThreads = 512;  // 16 warps
 constexpr int kSoftmaxThreads = 256;
@@ -94,29 +103,18 @@ constexpr int kBarAllSoftmax = 5;  // named barriers: 1-4 per quadrant, 5 all so
 constexpr uint32_t kColO = 0;
 constexpr uint32_t kColS = 256;
 constexpr uint32_t kColQ = 384;
+constexpr uint32_t kColSf = 496;  // block scales: V's (four columns, all 1), then P's (four per buffer)
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kScaleOnes = 0x7F7F7F7Fu;
+static_assert(kColQ + 8 * kQkTmemSteps <= kColSf && kColSf + 4 + 4 * kPBufs <= kTmemCols, "tensor memory");
 
 constexpr uint32_t kIdQK = instr_desc(0, 0, false, kT, 128);         // e4m3 x e4m3, N = 64 keys
 // A = V^T MN-major, N = the packed rows in use (a multiple of 16)
-__device__ __forceinline__ uint32_t id_pv(int n) { return instr_desc(0, 0, false, n, 128, true); }
+__device__ __forceinline__ uint32_t id_pv(int n) { return instr_desc_mx(false, n, 128, true); }
 
-// P = 2^(s - m_ref + kPShift) as in the GQA kernel. The reference max moves
-// only when a tile's max passes m_ref + kOvershoot (2.8: P stays <= 2^8.8,
-// under e4m3's 448), to that max + kHeadroom. A row's first reference takes
-// kHeadroomFirst instead: MLA logits are wide (sd ~2.5 log2 units on random
-// data), so the running max keeps growing for many tiles after the first,
-// and every move here costs a CTA-wide pass over O^T; with 4 the moves all
-// but vanish, and m_ref still ends near the row's max, so that the keys
-// flushed to zero below m_ref - 16 carry no more mass than with 1.
-constexpr float kPShift = 6.f;
-constexpr float kHeadroom = 1.f;
-// Page scales spread the logits further (both the keys and the weights take
-// them), so the reference moves ten times as often; 3 instead of 1 saves a
-// sixth of the moves (latent mid context 179.9 -> 178.6 us) and costs no
-// accuracy beside kHeadroomFirst, which leaves as many keys below the floor.
-constexpr float kHeadroomScaled = 3.f;
-constexpr float kHeadroomFirst = 4.f;
-constexpr float kOvershoot = 2.8f;
+// A row's reference moves only when a tile's max passes m_ref + kFar, as in the
+// GQA kernel; a move costs a CTA-wide pass over O^T.
+constexpr float kFar = 32.f;
 
 enum : int {
   kBarFull = 0,
@@ -174,11 +172,11 @@ __device__ __forceinline__ int core_off(int m, int k, int row_bytes) {
 
 // SCL: a page-scaled cache, one scale a page for keys and values; as in the
 // GQA kernel it multiplies the page's logits, and as the value's scale joins
-// the weight, P = 2^(s + log2 scale - m_ref), with l summing P / scale. A
+// the weight, P = 2^(s + log2 scale - e), with l summing P / scale. A
 // thread's 16 keys of a tile are one page. The producers bring the scales
-// with the ring slot. 64 sequences of 8K to 32K keys (733 MB), 16 heads: 152 us
-// with 3 draft tokens, 131 with one, 71 and 84 % of the measured copy bandwidth;
-// of the 152 the merge kernel is 11 and the rescales of O^T 10.
+// with the ring slot. 64 sequences of 8K to 32K keys (733 MB), 16 heads: 154 us
+// with 3 draft tokens, 137 with one, 70 and 81 % of the measured copy bandwidth;
+// of the 154 the merge kernel is 11.
 // CLU: one cluster of CTAs per item, as in the GQA kernel: two sequences of
 // 1,024 and 769 keys 10.6 us a call (23.3 split over all CTAs).
 // NAR: at most 32 packed rows. P's two terms are then stacked in the N of P V
@@ -444,11 +442,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < kQkSteps; ++k) {
               const uint64_t bdesc = smem_desc(kst + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024, kLayoutSw128);
-              mma_f8f6f4_ta(d, tmem + kColQ + 8 * k, bdesc, kIdQK, k ? 1u : 0u);
+              if (k < kQkTmemSteps)
+                mma_f8f6f4_ta(d, tmem + kColQ + 8 * k, bdesc, kIdQK, k ? 1u : 0u);
+              else
+                mma_f8f6f4(d, smem_desc(qpe + (kQkPeSteps + k - kQkTmemSteps) * 256, 128, 8 * kQpeRow, kLayoutNone), bdesc,
+                           kIdQK, 1u);
             }
 #pragma unroll
             for (int k = 0; k < kQkPeSteps; ++k) {
-              const uint64_t adesc = smem_desc(qpe + k * 256, 128, 8 * kMlaPe, kLayoutNone);
+              const uint64_t adesc = smem_desc(qpe + k * 256, 128, 8 * kQpeRow, kLayoutNone);
               const uint64_t bdesc = smem_desc(kst + 4 * kRegion + k * 32, 16, 512, kLayoutSw64);
               mma_f8f6f4(d, adesc, bdesc, kIdQK, 1u);
             }
@@ -460,15 +462,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         for (int i = 0; i < ntile && ok; ++i) {
           const int x = first + i;
-          const int pb = x & (kPBufs - 1);
+          const int pb = x % kPBufs;
           const int s = x % kSlots;
           bool got = arrived(kBarPFull + pb, (x / kPBufs) & 1) && arrived(kBarFull + s, (x / kSlots) & 1);
           if (i == 0 && piece_idx > 0) got = got && arrived(kBarOFree, (piece_idx - 1) & 1);
           if (!all_or_fail(got, 4)) break;
           tc_fence_after();
           const uint32_t kst = sbase + s * kTileBytes;
-          const uint32_t pbuf = sbase + kOffP + pb * (NAR ? kNarPBuf : kPBuf);
+          const uint32_t pbuf = sbase + kOffP + pb * (NAR ? nar_p_buf(nar) : kPBuf);
           if (elect_one()) {
+            const uint32_t sf = tmem + kColSf + 4 + 4 * pb;
+            tmem_cp_scales(sf, smem_desc(sbase + kOffSf + 512 * pb, 0, 128, kLayoutNone));
 #pragma unroll
             for (int kk = 0; kk < kPvSteps; ++kk) {
               const uint64_t bhi = smem_desc(pbuf + kk * 256, 128, 8 * kT, kLayoutNone);
@@ -478,8 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // V^T chunk a: latent columns [128 a, +128) of keys [32 kk, +32)
                 const uint64_t adesc = smem_desc(kst + a * kRegion + kk * 4096, kRegion, 1024, kLayoutSw128);
                 const uint32_t d = tmem + kColO + 64 * a;
-                mma_f8f6f4(d, adesc, bhi, idpv, (i == 0 && kk == 0) ? 0u : 1u);
-                if constexpr (!NAR) mma_f8f6f4(d, adesc, blo, idpv, 1u);
+                mma_mxf8(d, adesc, bhi, idpv | ((uint32_t)kk << 4), tmem + kColSf, sf,
+                         (i == 0 && kk == 0) ? 0u : 1u);
+                if constexpr (!NAR)
+                  mma_mxf8(d, adesc, blo, idpv | ((uint32_t)(kPvSteps + kk) << 4), tmem + kColSf, sf, 1u);
               }
             }
             mma_commit(bar(kBarPFree + pb));
@@ -540,8 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         got = mbar_wait(bar(kBarScales + cur % kSlots), (cur / kSlots) & 1, abort_flag, p.wait_limit_ns);
       got = got && mbar_wait(bar(kBarSFull + (cur & (kSBufs - 1))), (cur / kSBufs) & 1, abort_flag, p.wait_limit_ns);
       if (cur >= kPBufs)
-        got = got && mbar_wait(bar(kBarPFree + (cur & (kPBufs - 1))), ((cur - kPBufs) / kPBufs) & 1, abort_flag,
-                               p.wait_limit_ns);
+        got = got && mbar_wait(bar(kBarPFree + cur % kPBufs), ((cur - kPBufs) / kPBufs) & 1, abort_flag, p.wait_limit_ns);
       got = __all_sync(0xffffffffu, got);
       if (!got) {
         if (lane == 0) fail(p, abort_flag, 256);
@@ -561,11 +566,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float other = xch[(par * 2 + (kh ^ 1)) * 64 + r];
       return is_max ? fmaxf(v, other) : v + other;
     };
+    // This lane's last 16 words of Q's latent part (columns 448 on) go to the smem
+    // A operand, behind the rope part: their place in tensor memory holds the block
+    // scales.
+    auto store_tail = [&](const uint32_t (&d)[16]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(qpe_s + core_off(32 * q + lane, kMlaPe + 16 * i, kQpeRow)) =
+            make_uint4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+    };
+    // V's block scales are 1 (P's, in the columns behind, come with every tile)
+    if (kh == 0) {
+      tmem_fill_32x32b_x8(tmem + lane_base + kColSf, kScaleOnes);
+      tmem_wait_st();
+    }
     // Q of piece pq: latent columns [128 qtr, +128) and rope columns
     // [16 qtr, +16) of row r, scaled by 2^e and split into e4m3 hi and lo.
     // The latent part goes to the TMEM A operand (hi row in lane 32q + rl, lo
-    // row in lane 32q + 16 + rl, four columns a word), the rope part to the
-    // smem A operand. Returns the row's logit scale.
+    // row in lane 32q + 16 + rl, four columns a word), its last 64 columns and
+    // the rope part to the smem A operand. Returns the row's logit scale.
     auto stage_q = [&](const Piece& pq, int qidx) -> float {
       if (qidx > 0) wait_or_fail(kBarQFree, (qidx - 1) & 1, 128);
       const bool row_ok = r < pq.R;
@@ -611,7 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             d2[w] = sub ? lw[w] : recv;   // columns of sub 1's span
           }
           tmem_st_32x32b_x16(tmem + lane_base + kColQ + 64 * kh + 16 * hf, d1);
-          tmem_st_32x32b_x16(tmem + lane_base + kColQ + 64 * kh + 32 + 16 * hf, d2);
+          if (kh == 1 && hf == 1)
+            store_tail(d2);
+          else
+            tmem_st_32x32b_x16(tmem + lane_base + kColQ + 64 * kh + 32 + 16 * hf, d2);
         }
         uint32_t ph[4], pl[4];
 #pragma unroll
@@ -621,8 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           split_q4(a.z, a.w, up, ph[w + 1], pl[w + 1]);
         }
         const int mh = 32 * q + rl, ml = mh + 16;
-        *reinterpret_cast<uint4*>(qpe_s + core_off(mh, 16 * qtr, kMlaPe)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-        *reinterpret_cast<uint4*>(qpe_s + core_off(ml, 16 * qtr, kMlaPe)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+        *reinterpret_cast<uint4*>(qpe_s + core_off(mh, 16 * qtr, kQpeRow)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+        *reinterpret_cast<uint4*>(qpe_s + core_off(ml, 16 * qtr, kQpeRow)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
         tmem_wait_st();
         fence_proxy_async_smem();
         tc_fence_before();
@@ -679,8 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && cc < 8) {
         split_q4(x[4].x, x[4].y, up, hi[0], lo[0]);
         split_q4(x[4].z, x[4].w, up, hi[1], lo[1]);
-        *reinterpret_cast<uint2*>(qpe_s + core_off(row, 8 * cc, kMlaPe)) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(qpe_s + core_off(16 + row, 8 * cc, kMlaPe)) = make_uint2(lo[0], lo[1]);
+        *reinterpret_cast<uint2*>(qpe_s + core_off(row, 8 * cc, kQpeRow)) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(qpe_s + core_off(16 + row, 8 * cc, kQpeRow)) = make_uint2(lo[0], lo[1]);
       }
       named_bar(kBarAllSoftmax, kSoftmaxThreads);
       const float down = row_vals[48 + rl];
@@ -699,7 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               d[4 * i + 2] = v.z;
               d[4 * i + 3] = v.w;
             }
-            tmem_st_32x32b_x16(tmem + lane_base + kColQ + 64 * kh + 16 * h, d);
+            if (kh == 1 && h == 3)
+              store_tail(d);
+            else
+              tmem_st_32x32b_x16(tmem + lane_base + kColQ + 64 * kh + 16 * h, d);
           }
           tmem_wait_st();
         }
@@ -751,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int lt = pc.lt0; lt < pc.lt1; ++lt, ++it) {
         const int cur = it;
         const int b = cur & (kSBufs - 1);
-        const int pb = cur & (kPBufs - 1);
+        const int pb = cur % kPBufs;
         if (lt == pc.lt1 - 1 && has_next) {
           rs_next = stage(pn, piece_idx + 1);
           staged_next = true;
@@ -792,55 +817,51 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (key0 + i > vis_end) x[i] = -INFINITY;
           }
         }
-        float tmax = -INFINITY;
+        float top = -INFINITY;  // of this thread's raw dot products; xs > 0 keeps the order
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) tmax = fmax3(tmax, x[i], x[i + 1]);
-        // x holds the raw dot products; xs > 0 keeps the order
-        if constexpr (SCL)
-          tmax = fmaf(tmax, xs, lv);
-        else
-          tmax *= xs;
-        // A row's reference moves only when one of its four threads sees a
-        // key above m_ref + kOvershoot. One vote over all softmax threads
-        // finds out; only then is the row max exchanged (the reference stays
-        // put on most tiles, and the exchange costs a barrier of its own).
-        // The decisions are those of an exchange on every tile.
+        for (int i = 0; i < 16; i += 2) top = fmax3(top, x[i], x[i + 1]);
+        const float tmax = SCL ? fmaf(top, xs, lv) : top * xs;
+        // the block exponent of the row's 32 keys of this warp (va_fp8.cuh)
+        const float e = block_exponent(fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 16)));
+        // A row's reference moves only when one of its four threads sees a key
+        // above m_ref + kFar. One vote over all softmax threads finds out (an
+        // item's first tile sets the references: no vote); only then is the row
+        // max exchanged.
         float m_new = m_ref, alpha = 1.f;
         bool any = false;
         float* al = row_vals + (round & 1) * 64;
         ++round;
-        if (named_bar_or(kBarAllSoftmax, kSoftmaxThreads, ok && tmax > m_ref + kOvershoot)) {
-          tmax = exchange(tmax, true);
-          // page-scaled, a large page moves many rows: those that are above
-          // their reference at all move along, and spare a later move
-          const bool need = ok && tmax > m_ref + (SCL ? 0.f : kOvershoot);
-          m_new = need ? tmax + (m_ref == -INFINITY ? kHeadroomFirst : SCL ? kHeadroomScaled : kHeadroom) : m_ref;
-          const bool rescale = need && (m_ref != -INFINITY) && (cur > first);
-          alpha = rescale ? ex2(m_ref - m_new) : 1.f;
-          // O^T keeps a row in a column across all 128 lanes: every softmax
-          // warp scales its lanes' part of the rows that moved, so the
-          // decision is taken by all of them at once
-          if (kh == 0 && sub == 0 && (!NAR || r < nar)) {
-            al[r] = alpha;
-            if constexpr (NAR) al[nar + r] = alpha;
+        if (cur == first || named_bar_or(kBarAllSoftmax, kSoftmaxThreads, ok && tmax > m_ref + kFar)) {
+          const float rmax = exchange(tmax, true);
+          const bool need = ok && rmax > m_ref + kFar;
+          m_new = need ? floorf(rmax) : m_ref;
+          if (cur != first) {
+            const bool rescale = need && (m_ref != -INFINITY);
+            alpha = rescale ? ex2(m_ref - m_new) : 1.f;
+            // O^T keeps a row in a column across all 128 lanes: every softmax
+            // warp scales its lanes' part of the rows that moved, so the
+            // decision is taken by all of them at once
+            if (kh == 0 && sub == 0 && (!NAR || r < nar)) {
+              al[r] = alpha;
+              if constexpr (NAR) al[nar + r] = alpha;
+            }
+            any = named_bar_or(kBarAllSoftmax, kSoftmaxThreads, rescale);
           }
-          any = named_bar_or(kBarAllSoftmax, kSoftmaxThreads, rescale);
         }
         if (!ok) continue;
 
-        // a row with no visible key yet (m_new = -inf) gets P = ex2(-inf) = 0
-        const float mref_s = m_new != -INFINITY ? m_new - kPShift : INFINITY;
         float ls = 0.f;
         if (!idle) {
+          // P = 2^(s - e); all -inf, and so 0, without a visible key
           uint32_t ph[4], pl[4];
-          const float off2 = SCL ? lv - mref_s : -mref_s;
+          const float off2 = lv - e;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float a = ex2(fmaf(x[2 * i], xs, off2));
             const float bb = ex2(fmaf(x[2 * i + 1], xs, off2));
             ls += a + bb;
             uint32_t h2, l2;
-            split_p(a, bb, h2, l2);
+            split_weights(a, bb, h2, l2);
             if (i & 1) {
               ph[i >> 1] |= h2 << 16;
               pl[i >> 1] |= l2 << 16;
@@ -849,17 +870,25 @@ __global__ void __launch_bounds__(kThreads, 1)
               pl[i >> 1] = l2;
             }
           }
+          const float es = block_scale(e, m_new);
+          if constexpr (SCL) ls *= ex2(-lv);  // the weights without the scale
+          ls *= exp2_int(es);
           // P^T operand: row r, keys [16 qtr, +16) = one core-matrix row
-          unsigned char* pbuf = sm + kOffP + pb * (NAR ? kNarPBuf : kPBuf);
+          unsigned char* pbuf = sm + kOffP + pb * (NAR ? nar_p_buf(nar) : kPBuf);
           const int off = core_off(r, 16 * qtr, kT);
           *reinterpret_cast<uint4*>(pbuf + off) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
           *reinterpret_cast<uint4*>(pbuf + (NAR ? core_off(nar, 0, kT) : kPHalf) + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+          // its block's scale: sub 0 that of the high terms, sub 1 that of the low
+          // ones: the row's bytes [hi 0, hi 1, lo 0, lo 1], or NAR two rows' [0, 1]
+          const int n = NAR ? r + sub * nar : r;
+          st_shared_u8(sbase + kOffSf + 512 * pb + 16 * (n & 31) + 4 * (n >> 5) + (NAR ? 0 : 2 * sub) + kh,
+                       scale_byte(es) - sub * kLoShift);
         }
         // then the rows that moved (P V(cur - 1) has to be in O^T first; the
         // wait overlaps the work above)
         if (any) {
           const int xp = cur - 1;
-          if (!wait_or_fail(kBarPFree + (xp & (kPBufs - 1)), (xp / kPBufs) & 1, 1024)) continue;
+          if (!wait_or_fail(kBarPFree + xp % kPBufs, (xp / kPBufs) & 1, 1024)) continue;
           tc_fence_after();
           // the factors of rows [0, 32) and [32, 64), four to a load; a half in
           // which no row moved stays as it is
@@ -886,7 +915,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        if constexpr (SCL) ls *= ex2(-lv);  // the weights without the scale
         l = l * alpha + ls;
         m_ref = m_new;
         // latent rows past S in the item's last tile (a partial page, pages
@@ -955,11 +983,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (CLU) {
         if (row_ok && kh == 0 && sub == 0) {
-          part_ml[2 * r] = (m_ref == -INFINITY) ? -INFINITY : m_ref - kPShift;
+          part_ml[2 * r] = m_ref;
           part_ml[2 * r + 1] = lrow;
         }
       } else if (row_ok && kh == 0 && sub == 0) {
-        p.ws_ml[(piece * p.max_rows + r) * 2 + 0] = (m_ref == -INFINITY) ? -INFINITY : m_ref - kPShift;
+        p.ws_ml[(piece * p.max_rows + r) * 2 + 0] = m_ref;
         p.ws_ml[(piece * p.max_rows + r) * 2 + 1] = lrow;
       }
       tc_fence_before();

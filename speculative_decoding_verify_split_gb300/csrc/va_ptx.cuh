@@ -252,6 +252,17 @@ __device__ __forceinline__ void mma_mxf8_ta(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
+// The same with A in shared memory.
+__device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa_tmem,
+                                         uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::
+          "r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
 // 32 rows x 16 bytes of shared memory (8-row groups of 128 bytes, descriptor
 // with that stride and no swizzle) into four columns, to all four lane
 // quadrants: the scale words of 128 rows. Ordered before later MMAs of the

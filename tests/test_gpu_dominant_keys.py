@@ -122,14 +122,14 @@ class Case:
 
 
 @pytest.mark.parametrize("paged", [True, False])
-@pytest.mark.parametrize("latent", [False])
+@pytest.mark.parametrize("latent", [False, True])
 @pytest.mark.parametrize("S", [1025, 8192, 65531])
 @pytest.mark.parametrize("splits", [0, 1, 10])
 def test_a_sink(paged, latent, S, splits):
     Case(latent, S, 16, seed=S).check(paged, splits)
 
 
-@pytest.mark.parametrize("latent", [False])
+@pytest.mark.parametrize("latent", [False, True])
 @pytest.mark.parametrize("hq,L", [(4, 1), (16, 2), (16, 3), (16, 4)])
 @pytest.mark.parametrize("at", [0, 700, 4090])
 def test_where_the_sink_lies_and_rows(latent, hq, L, at):
@@ -139,7 +139,7 @@ def test_where_the_sink_lies_and_rows(latent, hq, L, at):
         c.check(True, splits)
 
 
-@pytest.mark.parametrize("latent", [False])
+@pytest.mark.parametrize("latent", [False, True])
 @pytest.mark.parametrize("every", [33, 128, 1000])
 def test_many_dominant_keys(latent, every):
     """One key in `every`: each tile holds some, beside keys that count."""
@@ -148,7 +148,7 @@ def test_many_dominant_keys(latent, every):
         c.check(True, splits)
 
 
-@pytest.mark.parametrize("latent", [False])
+@pytest.mark.parametrize("latent", [False, True])
 @pytest.mark.parametrize("scale", [2.0 ** -6, 32.0])
 def test_a_sink_in_a_page_of_another_scale(latent, scale):
     """Its page's V scale is a sixty-fourth, or 32 times, of the others'."""
@@ -197,7 +197,7 @@ def test_a_sink_over_shards():
     assert err.max() <= ROW
 
 
-@pytest.mark.parametrize("latent", [False])
+@pytest.mark.parametrize("latent", [False, True])
 @pytest.mark.parametrize("hq,L", [(8, 1), (16, 2), (16, 4)])
 @pytest.mark.parametrize("levels", [(0, 1, 2, 3, 4, 5), (5, 4, 3, 2, 1, 0), (2, 0, 4, 1, 5, 3), (0, 0, 6, 6, 0, 0)])
 def test_levels_far_apart(latent, hq, L, levels):
