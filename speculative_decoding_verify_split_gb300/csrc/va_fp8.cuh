@@ -33,13 +33,19 @@ constexpr int kBlockTop = 7;  // floor(log2) of a block's largest p
 constexpr int kLoShift = 5;   // the low terms' scale is 2^-kLoShift of the high terms'
 
 // The exponent e of a block whose largest weight is 2^d, a whole number (finite
-// for d = -inf or NaN, a block without weights).
-__device__ __forceinline__ float block_exponent(float d) { return fmaxf(floorf(d), -1e30f) - (float)kBlockTop; }
-// log2 of a block's scale, in the range of its type and of exp2_int. Weights
-// below 2^-113 of 2^m_ref fade out.
-__device__ __forceinline__ float block_scale(float e, float m_ref) { return fminf(fmaxf(e - m_ref, -120.f), 100.f); }
+// for d = -inf or NaN, a block without weights), not below kMinScale of the
+// reference: below that p falls under 2^7, down to 0 in O for weights under
+// 2^-137 of 2^m_ref.
+constexpr float kMinScale = -122.f;
+__device__ __forceinline__ float block_exponent(float d, float m_ref) {
+  return fmaxf(fmaxf(floorf(d), -1e30f) - (float)kBlockTop, m_ref + kMinScale);
+}
+// log2 of the block's scale: in [kMinScale, 100], so that the low terms' byte is
+// at least 0 (m_ref = -inf: no visible key, p = 0).
+__device__ __forceinline__ float block_scale(float e, float m_ref) { return fminf(e - m_ref, 100.f); }
 __device__ __forceinline__ uint32_t scale_byte(float x) { return (uint32_t)((int)x + 127); }
 __device__ __forceinline__ float exp2_int(float x) { return __uint_as_float(scale_byte(x) << 23); }
+static_assert(kMinScale + 127 - kLoShift >= 0, "scale bytes");
 
 // p (two fp32 values, a first) -> e4m3 hi and scaled lo bytes, via f16x2.
 __device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {

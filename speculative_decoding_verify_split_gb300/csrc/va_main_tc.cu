@@ -981,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (FP8) {
             // P = 2^(x - e), e the block's exponent (va_fp8.cuh); ls0 and ls1: the
             // sums of the first and of the second page
-            const float e = block_exponent(tmax);
+            const float e = block_exponent(tmax, m_ref);
             const float es = block_scale(e, m_ref);
             const float off2[2] = {lv[0] - e, lv[1] - e};
             uint32_t ph[8], pl[8];

@@ -821,8 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; i += 2) top = fmax3(top, x[i], x[i + 1]);
         const float tmax = SCL ? fmaf(top, xs, lv) : top * xs;
-        // the block exponent of the row's 32 keys of this warp (va_fp8.cuh)
-        const float e = block_exponent(fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 16)));
+        const float bmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 16));  // of a block of P
         // A row's reference moves only when one of its four threads sees a key
         // above m_ref + kFar. One vote over all softmax threads finds out (an
         // item's first tile sets the references: no vote); only then is the row
@@ -852,8 +851,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         float ls = 0.f;
         if (!idle) {
-          // P = 2^(s - e); all -inf, and so 0, without a visible key
+          // P = 2^(s - e), e the block's exponent (va_fp8.cuh); 0 without a visible key
           uint32_t ph[4], pl[4];
+          const float e = block_exponent(bmax, m_new);
           const float off2 = lv - e;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {

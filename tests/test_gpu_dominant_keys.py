@@ -223,3 +223,27 @@ def test_levels_far_apart(latent, hq, L, levels):
     for paged in (True, False):
         for splits in (0, 1, 3):
             c.check(paged, splits)
+
+
+@pytest.mark.parametrize("latent", [False, True])
+@pytest.mark.parametrize("gap", [40, 72, 110])
+def test_value_scales_at_both_ends_of_their_range(latent, gap):
+    """One key in a page of scale 2^64, `gap` log2 units above the others, whose
+    pages' scale is 2^-64: weight times scale of the others falls to 2^-238 of the
+    row's largest, and they must not count for more than they are."""
+    c = Case(latent, 1000, 16, seed=12)
+    dim = 576 if latent else 256
+    c.scales.fill_(2.0 ** -64)
+    c.scales[int(c.table[0, 0])] = 2.0 ** 64
+    c.q[..., dim - 1] = gap / math.log2(math.e) * (2.0 ** -64 if latent else 1.0)
+    for t in (c.cache,) if latent else (c.k, c.v):        # a value of the size of the others', nothing else on its page
+        x = t.float()
+        pg = int(c.table[0, 0])
+        if t is not (None if latent else c.k):
+            x[pg] = 0.0
+            x[pg, 0, 0, :256] = 3.0
+        if latent:
+            x[pg, 0, 0, dim - 1] = 1.0
+        t.copy_(x.to(F8))
+    for splits in (0, 1, 3):
+        c.check(True, splits)
