@@ -550,8 +550,18 @@ va_status verify_attn_append_mla(const va_tensor* q_pe, const va_tensor* latent,
  *               on chip, without a merge kernel; > 0 forces the split over that many
  *               CTAs.
  *  event_after_main  as verify_attn_ex; with clusters, behind the only kernel.
- * Accuracy: weights keep fp32 precision while the V scales of the pages a row
- * sees lie within a factor of 2^96 of each other.
+ * Accuracy, with w a key's softmax weight times its page's V scale:
+ *  - The keys of a sequence are taken in blocks of 32 from its start on. w enters
+ *    the product with V to 8 bits while it is within 2^-14 of its block's largest,
+ *    and in steps of at most 2^-21 of that one below. Blocks do not limit each other while
+ *    their largest w lie within 2^-115 of the row's.
+ *  - The normaliser is a sum in fp32; it counts a key while its w is within
+ *    2^-126 of the row's largest.
+ *  - Q enters the logits as two e4m3 terms, scaled by the row's largest |q|: 8
+ *    bits, in steps of at most 2^-16 of that one.
+ *  - Logits below 2^20 in magnitude (fp32 holds them to 2^-4 there).
+ * verify_attn, its variants and verify_attn_mla over e4m3 caches are the same, with
+ * one V scale for all pages.
  * Errors as verify_attn_opt; VA_ERR_NULL without scales, VA_ERR_DTYPE for a
  * BF16 cache or scales that are not fp32, VA_ERR_SHAPE for scales of another
  * shape, VA_ERR_LAYOUT for a zero stride or an address off 4 bytes.
