@@ -525,6 +525,9 @@ va_status verify_attn_append_mla(const va_tensor* q_pe, const va_tensor* latent,
                                  const va_tensor* descale, va_tensor* scales, va_tensor* q_pe_out,
                                  va_tensor* kv_cache, void* stream);
 
+/* num_splits of the page-scaled calls: see verify_attn_scaled. */
+#define VA_LIBRARY_STATUS (1 << 30)
+
 /*
  * verify_attn_scaled - verify attention over a page-scaled e4m3 cache: a key's
  * stored codes stand for code * k_scales[page, head], a value's for
@@ -548,7 +551,10 @@ va_status verify_attn_append_mla(const va_tensor* q_pe, const va_tensor* latent,
  *  num_splits   0: the library's choice, which for small batches is one cluster of
  *               up to 8 CTAs per (sequence, KV head) that joins its partial results
  *               on chip, without a merge kernel; > 0 forces the split over that many
- *               CTAs.
+ *               CTAs. With VA_LIBRARY_STATUS added a wait that runs out is reported
+ *               by verify_attn_last_device_error(NULL, ...) instead of the
+ *               workspace's status word: for a workspace that is given back behind
+ *               the call.
  *  event_after_main  as verify_attn_ex; with clusters, behind the only kernel.
  * Accuracy, with w a key's softmax weight times its page's V scale:
  *  - The keys of a sequence are taken in blocks of 32 from its start on. w enters
@@ -603,11 +609,12 @@ va_status verify_attn_mla_scaled(const va_tensor* q, const va_tensor* kv_cache, 
  * kernels only ever set bits in it.
  *
  *  workspace  the 256-byte-aligned workspace pointer that was passed to
- *             verify_attn_ex, verify_attn_opt, verify_attn_mla or
- *             verify_attn_partial; or NULL for the library's own scratch on
+ *             verify_attn_ex, verify_attn_opt, verify_attn_mla,
+ *             verify_attn_partial or a page-scaled call; or NULL for the library's own scratch on
  *             the current device: the workspace of calls made without one
  *             (verify_attn, and the others with a NULL workspace) and the
- *             built-in array of verify_attn_noalloc. The library's workspace
+ *             built-in array of verify_attn_noalloc, whose word page-scaled calls
+ *             with VA_LIBRARY_STATUS use too. The library's workspace
  *             is replaced when it grows; its word then starts at 0 again.
  *  bits       host int32, written: the OR of the words read (0 = no bounded
  *             wait ran out since the last read and clear). Nonzero bits name

@@ -304,7 +304,8 @@ def last_device_error(workspace: Optional[torch.Tensor] = None, stream=None, dev
     """Reads and clears the status word of bounded waits that ran out (0 =
     none): of ``workspace`` as the wrappers passed it, or with None, of the
     library's own scratch on the device (its workspace and the no-alloc
-    array). Synchronises ``stream`` (see include/verify_attn.h)."""
+    array) and of page-scaled calls without a workspace. Synchronises
+    ``stream`` (see include/verify_attn.h)."""
     if workspace is not None:
         dev = workspace.device
     else:
@@ -598,7 +599,8 @@ def verify_attn_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_
     scales [num_blocks, Hkv] fp32 for K and for V, as ``append_kv`` writes
     them, with the variants of ``verify_attn_opt``. ``workspace`` (a uint8
     device tensor, zeroed before its first use if its status word is to be
-    read) None: one of the call's own, from torch's allocator."""
+    read) None: one of the call's own, from torch's allocator; a bounded wait
+    that ran out is then reported by ``last_device_error()``."""
     if out is None:
         out = _empty(q.shape, q, stream)
     s = _native().attn_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_seqlens_q,

@@ -222,12 +222,16 @@ class CallWorkspace {
 };
 
 // The attention calls' tail: workspace (a tensor or None), num_splits, event, stream.
+// Without a workspace the call's own is given back behind it, so its waits report
+// to the library's status word.
 struct Tail {
   void* ws = nullptr;
   size_t bytes = 0;
   int32_t splits = 0;
   void* event = nullptr;
   cudaStream_t stream = nullptr;
+
+  int32_t splits_arg() const { return ws || splits < 0 ? splits : splits | VA_LIBRARY_STATUS; }
 
   bool read(PyObject* workspace, PyObject* num_splits, PyObject* ev, PyObject* st, c10::Device device) {
     if (!read_int(num_splits, &splits) || !read_stream(st, device, &stream)) return false;
@@ -284,7 +288,7 @@ PyObject* attn_scaled(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* ws = tail.ws ? tail.ws : own.get();
     return status_of(args.device, [&] {
       return verify_attn_scaled(t[0], t[1], t[2], t[3], t[4], t[5], t[6], t[7], max_q, max_k, scale, t[8], &opt, ws,
-                                tail.ws ? tail.bytes : need, tail.splits, tail.event, tail.stream);
+                                tail.ws ? tail.bytes : need, tail.splits_arg(), tail.event, tail.stream);
     });
   });
 }
@@ -313,7 +317,7 @@ PyObject* attn_mla_scaled(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* ws = tail.ws ? tail.ws : own.get();
     return status_of(args.device, [&] {
       return verify_attn_mla_scaled(t[0], t[1], t[2], t[3], t[4], t[5], max_q, max_k, scale, t[6], ws,
-                                    tail.ws ? tail.bytes : need, tail.splits, tail.event, tail.stream);
+                                    tail.ws ? tail.bytes : need, tail.splits_arg(), tail.event, tail.stream);
     });
   });
 }

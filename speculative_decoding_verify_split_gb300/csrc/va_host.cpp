@@ -338,14 +338,25 @@ static void use_clusters(va_plan* plan, const Shapes& sh) {
   plan->kernel = kKernelTc;
 }
 
-static void set_page_scales(Params* p, const PageScales* s) {
-  if (!s) return;
+static va_status set_page_scales(Params* p, const PageScales* s) {
+  if (!s) return VA_OK;
   p->k_scales = static_cast<const float*>(s->k->data);
   p->ks_s0 = s->k->stride[0];
   p->ks_s1 = s->k->stride[1];
   p->v_scales = static_cast<const float*>(s->v->data);
   p->vs_s0 = s->v->stride[0];
   p->vs_s1 = s->v->stride[1];
+  if (!s->library_status) return VA_OK;
+  void* word = nullptr;
+  const va_status e = noalloc_scratch(&word, true);  // the array's first word
+  p->ws_status = static_cast<int32_t*>(word);
+  return e;
+}
+
+// The call's num_splits without VA_LIBRARY_STATUS; *library: whether it was set.
+static int32_t take_library_status(int32_t num_splits, bool* library) {
+  *library = num_splits > 0 && (num_splits & VA_LIBRARY_STATUS) != 0;
+  return *library ? num_splits & ~VA_LIBRARY_STATUS : num_splits;
 }
 
 va_status launch(const va_tensor* q, const va_tensor* k, const va_tensor* v, const va_tensor* bt,
@@ -417,13 +428,14 @@ va_status launch(const va_tensor* q, const va_tensor* k, const va_tensor* v, con
     p.lse_s0 = part->lse->stride[0];
     p.lse_s1 = part->lse->stride[1];
   }
-  set_page_scales(&p, scales);
   const WorkspaceLayout lay = workspace_layout(plan.num_work, plan.num_splits, plan.max_rows);
   char* base = static_cast<char*>(ws);
   p.ws_meta = reinterpret_cast<int32_t*>(base + lay.meta_off);
   p.ws_ml = reinterpret_cast<float*>(base + lay.ml_off);
   p.ws_acc = reinterpret_cast<float*>(base + lay.acc_off);
   p.ws_status = reinterpret_cast<int32_t*>(base + lay.status_off);
+  const va_status scaled = set_page_scales(&p, scales);
+  if (scaled != VA_OK) return scaled;
   CUtensorMap tm_k, tm_v;
   std::memset(&tm_k, 0, sizeof(tm_k));
   std::memset(&tm_v, 0, sizeof(tm_v));
@@ -588,11 +600,12 @@ va_status launch_mla(const va_tensor* q, const va_tensor* kv, const va_tensor* b
   p.piece_cost = p.kv_fp8 ? kMlaPieceCostTiles : kMlaPieceCostTilesBf16;
   p.dv = kMlaNope;
   p.wait_limit_ns = wait_limit_ns();
-  set_page_scales(&p, scales);
   const WorkspaceLayout lay =
       workspace_layout(plan.num_work, plan.num_splits, mla_row_stride(plan.max_rows), kMlaNope);
   char* base = static_cast<char*>(ws);
   p.ws_status = reinterpret_cast<int32_t*>(base + lay.status_off);
+  const va_status scaled = set_page_scales(&p, scales);
+  if (scaled != VA_OK) return scaled;
   p.ws_meta = reinterpret_cast<int32_t*>(base + lay.meta_off);
   p.ws_ml = reinterpret_cast<float*>(base + lay.ml_off);
   p.ws_acc = reinterpret_cast<float*>(base + lay.acc_off);
@@ -776,7 +789,8 @@ VA_EXPORT va_status verify_attn_scaled(const va_tensor* q, const va_tensor* k_ca
                                        size_t workspace_bytes, int32_t num_splits, void* event_after_main,
                                        void* stream) {
   if (!k_scales || !v_scales) return VA_ERR_NULL;
-  const PageScales scales{k_scales, v_scales};
+  PageScales scales{k_scales, v_scales, false};
+  num_splits = take_library_status(num_splits, &scales.library_status);
   return run_call(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, max_seqlen_q, max_seqlen_k,
                   softmax_scale, nullptr, nullptr, out, opts, workspace, workspace_bytes, workspace == nullptr,
                   num_splits, static_cast<cudaEvent_t>(event_after_main), static_cast<cudaStream_t>(stream), &scales);
@@ -881,7 +895,8 @@ VA_EXPORT va_status verify_attn_mla_scaled(const va_tensor* q, const va_tensor* 
                                            size_t workspace_bytes, int32_t num_splits, void* event_after_main,
                                            void* stream) {
   if (!scales) return VA_ERR_NULL;
-  const PageScales ps{scales, scales};
+  PageScales ps{scales, scales, false};
+  num_splits = take_library_status(num_splits, &ps.library_status);
   return run_mla_call(q, kv_cache, block_table, cu_seqlens_q, seqused_k, max_seqlen_q, max_seqlen_k, softmax_scale,
                       nullptr, nullptr, out, workspace, workspace_bytes, num_splits, event_after_main, stream, &ps);
 }

@@ -52,10 +52,13 @@ struct PartialOut {
   va_tensor* lse;
 };
 
-// Scales of a page-scaled e4m3 cache (a latent cache: one tensor for both).
+// Scales of a page-scaled e4m3 cache (a latent cache: one tensor for both), and
+// whether waits that run out are reported by the library's status word instead
+// of the workspace's (VA_LIBRARY_STATUS).
 struct PageScales {
   const va_tensor* k;
   const va_tensor* v;
+  bool library_status;
 };
 
 // Launches the main and merge kernels with the given workspace and options
