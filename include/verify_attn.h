@@ -480,8 +480,11 @@ typedef struct va_rope {
  *               below e4m3's normal range). Slots behind the new tokens are
  *               left as they are.
  *
- * k_cache and v_cache (k_scales and v_scales) may be interleaved views of one
- * tensor, not the same view (VA_ERR_LAYOUT).
+ * What is written (q_out, the caches, the scales) has a place of its own for
+ * every element: in some order of the dimensions each stride is at least what the
+ * inner ones span (else VA_ERR_LAYOUT). k_cache and v_cache (k_scales and
+ * v_scales) may be interleaved views of one tensor, not the same view
+ * (VA_ERR_LAYOUT), and share no element.
  * Tokens at negative positions (L > S) are neither stored nor rotated. Rows of
  * q_out behind the last sequence are left as they were. Block-table entries
  * outside [0, num_blocks) and positions past the table's width store nothing.

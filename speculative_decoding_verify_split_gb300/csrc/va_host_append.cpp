@@ -31,11 +31,32 @@ va_status check_rows(const va_tensor* t) {
   return VA_OK;
 }
 
-// Rows written by the call: distinct tokens (and heads) at distinct places.
-bool rows_distinct(const va_tensor* t) {
-  for (int i = 0; i < t->ndim - 1; ++i)
-    if (t->shape[i] > 1 && t->stride[i] < t->shape[t->ndim - 1]) return false;
+// Whether the elements of a tensor that is written have places of their own:
+// runs of `width` elements over its first `dims` dimensions, whose strides are
+// nested in some order (each at least what the ones inside it span).
+bool places_distinct(const va_tensor* t, int dims, int64_t width) {
+  int order[4], n = 0;
+  for (int i = 0; i < dims; ++i) {
+    if (t->shape[i] <= 1) continue;
+    int j = n++;
+    for (; j > 0 && t->stride[order[j - 1]] > t->stride[i]; --j) order[j] = order[j - 1];
+    order[j] = i;
+  }
+  int64_t span = width;
+  for (int j = 0; j < n; ++j) {
+    const int64_t stride = t->stride[order[j]], steps = t->shape[order[j]] - 1;
+    if (stride < span || stride > (INT64_MAX - span) / steps) return false;
+    span += stride * steps;
+  }
   return true;
+}
+
+bool rows_distinct(const va_tensor* t) { return places_distinct(t, t->ndim - 1, t->shape[t->ndim - 1]); }
+
+// The scales of a page-scaled cache that the call writes.
+va_status check_written_scales(const va_tensor* t, int64_t num_blocks, int64_t hkv) {
+  const va_status s = check_page_scales(t, num_blocks, hkv);
+  return s == VA_OK && !places_distinct(t, 2, 1) ? VA_ERR_LAYOUT : s;
 }
 
 va_status check_rope(const va_rope* r, int64_t total_q, int64_t max_rot, AppendParams* p) {
@@ -167,8 +188,8 @@ VA_EXPORT va_status verify_attn_append_kv(const va_tensor* q, const va_tensor* k
   if (k_scales) {
     if (k_cache->dtype != VA_FP8_E4M3) return VA_ERR_DTYPE;
     if (k_descale || v_descale) return VA_ERR_UNSUPPORTED;  // a page's scale is its descale
-    s = check_page_scales(k_scales, k_cache->shape[0], hkv);
-    if (s == VA_OK) s = check_page_scales(v_scales, k_cache->shape[0], hkv);
+    s = check_written_scales(k_scales, k_cache->shape[0], hkv);
+    if (s == VA_OK) s = check_written_scales(v_scales, k_cache->shape[0], hkv);
     if (s == VA_OK && k_scales->data && k_scales->data == v_scales->data) s = VA_ERR_LAYOUT;
   } else {
     s = check_descale(k_descale);
@@ -220,7 +241,7 @@ VA_EXPORT va_status verify_attn_append_mla(const va_tensor* q_pe, const va_tenso
   if (scales) {
     if (kv_cache->dtype != VA_FP8_E4M3) return VA_ERR_DTYPE;
     if (descale) return VA_ERR_UNSUPPORTED;
-    s = check_page_scales(scales, kv_cache->shape[0], 1);
+    s = check_written_scales(scales, kv_cache->shape[0], 1);
   } else {
     s = check_descale(descale);
   }
