@@ -25,6 +25,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libverify_attn.so")
 BINDING = os.path.join(LIBDIR, "va_binding.so")
 BINDING_SOURCE = "va_binding.cpp"
+BINDING_STAMP = os.path.join(LIBDIR, "va_binding.abi")  # the torch and Python that BINDING was built for
 
 SOURCES = ["va_host.cpp", "va_host_append.cpp", "va_main_tc.cu", "va_mla_tc.cu", "va_mla_bf16_tc.cu", "va_merge.cu",
            "va_noalloc.cu", "va_pagetable.cu", "va_append.cu"]
@@ -91,32 +92,55 @@ def _link_binding(obj: str) -> None:
     os.replace(tmp, BINDING)
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def binding_abi() -> str:
+    """What the extension is built against: another torch or interpreter reads its
+    tensors with another layout."""
+    import torch
+
+    return f"torch {torch.__version__} cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} python {sysconfig.get_config_var('SOABI')}"
+
+
+def _older(target: str, deps) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(d) > os.path.getmtime(target) for d in deps if os.path.exists(d))
+
+
+_COMMON_DEPS = [os.path.join(ROOT, "include", "verify_attn.h"), os.path.abspath(__file__)]
+
+
+def library_stale() -> bool:
+    return _older(LIB, _COMMON_DEPS + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != BINDING_SOURCE])
+
+
+def binding_stale() -> bool:
+    if _older(BINDING, _COMMON_DEPS + [os.path.join(CSRC, BINDING_SOURCE)]) or not os.path.exists(BINDING_STAMP):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(ROOT, "include", "verify_attn.h"))
-    deps.append(os.path.abspath(__file__))
-    return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
+    try:
+        with open(BINDING_STAMP) as f:
+            return f.read() != binding_abi()
+    except ImportError:  # no torch here: building the extension says so, behind the library
+        return True
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    lib, binding = force or library_stale(), force or binding_stale()
+    if not lib and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding, verbose)
-        objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        binding_obj = binding.result()
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-Xlinker", "--exclude-libs,ALL", *objs, "-o", tmp]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+        binding_obj = ex.submit(_compile_binding, verbose) if binding else None
+        if lib:
+            objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+            tmp = LIB + ".tmp"
+            cmd = [nvcc(), *ARCH, "-shared", "-Xlinker", "--exclude-libs,ALL", *objs, "-o", tmp]
+            res = subprocess.run(cmd, capture_output=True, text=True)
+            if res.returncode != 0:
+                raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+            os.replace(tmp, LIB)  # whether or not the extension compiles
+        if binding:
+            _link_binding(binding_obj.result())
+            with open(BINDING_STAMP, "w") as f:
+                f.write(binding_abi())
     return LIB
 
 
