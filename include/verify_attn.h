@@ -615,9 +615,9 @@ va_status verify_attn_mla_scaled(const va_tensor* q, const va_tensor* kv_cache, 
  *             verify_attn_ex, verify_attn_opt, verify_attn_mla,
  *             verify_attn_partial or a page-scaled call; or NULL for the library's own scratch on
  *             the current device: the workspace of calls made without one
- *             (verify_attn, and the others with a NULL workspace) and the
- *             built-in array of verify_attn_noalloc, whose word page-scaled calls
- *             with VA_LIBRARY_STATUS use too. The library's workspace
+ *             (verify_attn, and the others with a NULL workspace), the
+ *             built-in array of verify_attn_noalloc, and the word of page-scaled
+ *             calls with VA_LIBRARY_STATUS. The library's workspace
  *             is replaced when it grows; its word then starts at 0 again.
  *  bits       host int32, written: the OR of the words read (0 = no bounded
  *             wait ran out since the last read and clear). Nonzero bits name

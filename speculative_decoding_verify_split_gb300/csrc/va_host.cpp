@@ -289,7 +289,11 @@ struct DeviceState {
   int32_t mla_clusters[kMaxClusterLog2 + 1] = {};
   void* ws = nullptr;
   size_t ws_bytes = 0;
+  int32_t* status = nullptr;  // g_status on this device
 };
+
+// The status word of page-scaled calls with VA_LIBRARY_STATUS.
+static __device__ int32_t g_status;
 
 static std::mutex g_mu;
 static DeviceState g_dev[kMaxDevices];
@@ -309,6 +313,9 @@ static va_status device_state(DeviceState** out) {
       return VA_ERR_CUDA;
     main_tc_clusters(st.clusters);
     mla_tc_clusters(st.mla_clusters);
+    void* word = nullptr;
+    if (cudaGetSymbolAddress(&word, g_status) != cudaSuccess) return VA_ERR_CUDA;
+    st.status = static_cast<int32_t*>(word);
     st.ready = true;
   }
   *out = &st;
@@ -338,19 +345,15 @@ static void use_clusters(va_plan* plan, const Shapes& sh) {
   plan->kernel = kKernelTc;
 }
 
-static va_status set_page_scales(Params* p, const PageScales* s) {
-  if (!s) return VA_OK;
+static void set_page_scales(Params* p, const PageScales* s) {
+  if (!s) return;
   p->k_scales = static_cast<const float*>(s->k->data);
   p->ks_s0 = s->k->stride[0];
   p->ks_s1 = s->k->stride[1];
   p->v_scales = static_cast<const float*>(s->v->data);
   p->vs_s0 = s->v->stride[0];
   p->vs_s1 = s->v->stride[1];
-  if (!s->library_status) return VA_OK;
-  void* word = nullptr;
-  const va_status e = noalloc_scratch(&word, true);  // the array's first word
-  p->ws_status = static_cast<int32_t*>(word);
-  return e;
+  if (s->status) p->ws_status = s->status;
 }
 
 // The call's num_splits without VA_LIBRARY_STATUS; *library: whether it was set.
@@ -434,8 +437,7 @@ va_status launch(const va_tensor* q, const va_tensor* k, const va_tensor* v, con
   p.ws_ml = reinterpret_cast<float*>(base + lay.ml_off);
   p.ws_acc = reinterpret_cast<float*>(base + lay.acc_off);
   p.ws_status = reinterpret_cast<int32_t*>(base + lay.status_off);
-  const va_status scaled = set_page_scales(&p, scales);
-  if (scaled != VA_OK) return scaled;
+  set_page_scales(&p, scales);
   CUtensorMap tm_k, tm_v;
   std::memset(&tm_k, 0, sizeof(tm_k));
   std::memset(&tm_v, 0, sizeof(tm_v));
@@ -604,8 +606,7 @@ va_status launch_mla(const va_tensor* q, const va_tensor* kv, const va_tensor* b
       workspace_layout(plan.num_work, plan.num_splits, mla_row_stride(plan.max_rows), kMlaNope);
   char* base = static_cast<char*>(ws);
   p.ws_status = reinterpret_cast<int32_t*>(base + lay.status_off);
-  const va_status scaled = set_page_scales(&p, scales);
-  if (scaled != VA_OK) return scaled;
+  set_page_scales(&p, scales);
   p.ws_meta = reinterpret_cast<int32_t*>(base + lay.meta_off);
   p.ws_ml = reinterpret_cast<float*>(base + lay.ml_off);
   p.ws_acc = reinterpret_cast<float*>(base + lay.acc_off);
@@ -718,6 +719,12 @@ static va_status run_call(const va_tensor* q, const va_tensor* k_cache, const va
   DeviceState* st = nullptr;
   s = device_state(&st);
   if (s != VA_OK) return s;
+  PageScales ps;
+  if (scales && scales->library_status) {
+    ps = *scales;
+    ps.status = st->status;
+    scales = &ps;
+  }
   va_plan plan;
   const int32_t window = opts ? opts->window_left : -1;
   s = make_plan(sh.num_seqs, sh.hkv, sh.hq, max_seqlen_q, max_seqlen_k, sh.kv_dtype, st->sms, num_splits, &plan,
@@ -789,7 +796,7 @@ VA_EXPORT va_status verify_attn_scaled(const va_tensor* q, const va_tensor* k_ca
                                        size_t workspace_bytes, int32_t num_splits, void* event_after_main,
                                        void* stream) {
   if (!k_scales || !v_scales) return VA_ERR_NULL;
-  PageScales scales{k_scales, v_scales, false};
+  PageScales scales{k_scales, v_scales};
   num_splits = take_library_status(num_splits, &scales.library_status);
   return run_call(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, max_seqlen_q, max_seqlen_k,
                   softmax_scale, nullptr, nullptr, out, opts, workspace, workspace_bytes, workspace == nullptr,
@@ -853,6 +860,12 @@ static va_status run_mla_call(const va_tensor* q, const va_tensor* kv_cache, con
   DeviceState* st = nullptr;
   s = device_state(&st);
   if (s != VA_OK) return s;
+  PageScales ps;
+  if (scales && scales->library_status) {
+    ps = *scales;
+    ps.status = st->status;
+    scales = &ps;
+  }
   va_plan plan;
   s = make_mla_plan(sh.num_seqs, sh.hq, max_seqlen_q, max_seqlen_k, st->sms, num_splits, &plan, sh.kv_dtype);
   if (s != VA_OK) return s;
@@ -895,7 +908,7 @@ VA_EXPORT va_status verify_attn_mla_scaled(const va_tensor* q, const va_tensor* 
                                            size_t workspace_bytes, int32_t num_splits, void* event_after_main,
                                            void* stream) {
   if (!scales) return VA_ERR_NULL;
-  PageScales ps{scales, scales, false};
+  PageScales ps{scales, scales};
   num_splits = take_library_status(num_splits, &ps.library_status);
   return run_mla_call(q, kv_cache, block_table, cu_seqlens_q, seqused_k, max_seqlen_q, max_seqlen_k, softmax_scale,
                       nullptr, nullptr, out, workspace, workspace_bytes, num_splits, event_after_main, stream, &ps);
@@ -1048,19 +1061,20 @@ VA_EXPORT va_status verify_attn_last_device_error(const void* workspace, int32_t
     return take_status(const_cast<void*>(workspace), bits, st_);
   }
   void* lib_ws = nullptr;
+  int32_t* word = nullptr;
   {
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceState* st = nullptr;
     const va_status s = device_state(&st);
     if (s != VA_OK) return s;
     lib_ws = st->ws;
+    word = st->status;
   }
-  if (lib_ws) {
-    const va_status s = take_status(lib_ws, bits, st_);
-    if (s != VA_OK) return s;
-  }
+  va_status s = take_status(word, bits, st_);
+  if (s == VA_OK && lib_ws) s = take_status(lib_ws, bits, st_);
+  if (s != VA_OK) return s;
   void* scratch = nullptr;
-  va_status s = noalloc_scratch(&scratch, false);
+  s = noalloc_scratch(&scratch, false);
   if (s != VA_OK) return s;
   if (scratch) s = take_status(scratch, bits, st_);
   return s;

@@ -52,13 +52,14 @@ struct PartialOut {
   va_tensor* lse;
 };
 
-// Scales of a page-scaled e4m3 cache (a latent cache: one tensor for both), and
-// whether waits that run out are reported by the library's status word instead
-// of the workspace's (VA_LIBRARY_STATUS).
+// Scales of a page-scaled e4m3 cache (a latent cache: one tensor for both);
+// library_status (VA_LIBRARY_STATUS): waits that run out are reported in `status`,
+// the library's word, instead of the workspace's.
 struct PageScales {
   const va_tensor* k;
   const va_tensor* v;
-  bool library_status;
+  bool library_status = false;
+  int32_t* status = nullptr;
 };
 
 // Launches the main and merge kernels with the given workspace and options
