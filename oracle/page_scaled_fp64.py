@@ -14,6 +14,7 @@ import numpy as np
 from .attention_fp64 import PAGE_SIZE, first_visible_key, softcapped, visible_keys
 
 MIN_SCALE, MAX_SCALE = 2.0 ** -64, 2.0 ** 64
+BLOCK = 32  # keys that share a block scale of P
 
 
 def read_scales(scales: np.ndarray) -> np.ndarray:
@@ -30,8 +31,10 @@ def page_scaled_oracle(q, k, v, k_scales, v_scales, block_table, cu_seqlens_q, s
     * Q is two e4m3 terms, within 2^-8 of each column, so a logit moves by at
       most d = 2^-8 |scale| sum|q_c k_c| (and by tanh.approx's 2^-11 of the
       logit with a soft cap), a weight by e^{2 d} - 1 of itself;
-    * P is two e4m3 terms, within 2^-8 of a weight, and flushed below 2^-10 of
-      a code: at most 2^-12 of the row's largest weight times value scale;
+    * P is two e4m3 terms, within 2^-8 of a weight, and rounded in steps that are
+      at most 2^-21 of the largest weight times value scale among the 32 keys
+      (counted from the sequence's start) that share a block scale: half a step
+      a key. Blocks under 2^-115 of the row's largest fade out;
     * fp32 accumulation over n keys, n 2^-24, and the output's half step 2^-8."""
     T, Hq = q.shape[:2]
     Hkv = k.shape[2]
@@ -70,7 +73,9 @@ def page_scaled_oracle(q, k, v, k_scales, v_scales, block_table, cu_seqlens_q, s
                 o = (w * vs) @ C
                 dmax = d.max(axis=1, keepdims=True)
                 part = (w * vs) @ np.abs(C)
-                floor = 2.0 ** -12 * (w * vs).max(axis=1, keepdims=True) * np.abs(C).sum(axis=0)
+                block = np.flatnonzero(np.diff(keys // BLOCK, prepend=-1))
+                top, size = np.maximum.reduceat(w * vs, block, axis=1), np.add.reduceat(np.abs(C), block, axis=0)
+                floor = 2.0 ** -22 * top @ size + 2.0 ** -115 * top.max(axis=1, keepdims=True) * size.sum(axis=0)
                 with np.errstate(over="ignore"):
                     tol[a + t, h * G:(h + 1) * G] = part * (np.expm1(2 * dmax) + 2.0 ** -8 + 2 * len(keys) * 2.0 ** -24) \
                         + floor + 2.0 ** -8 * np.abs(o)
