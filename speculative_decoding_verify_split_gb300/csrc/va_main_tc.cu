@@ -245,7 +245,7 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 // partial in shared memory (in the drained rings) and the cluster joins them
 // there: no work scan, no partials in global memory, no merge kernel. A CTA
 // without a tile skips the roles and meets the others at the join. Latency
-// is the bound: two sequences of 1,024 and 769 keys take 8.2 us a call (12.5
+// is the bound: two sequences of 1,024 and 769 keys take 8.2 us a call (13.8
 // split over all CTAs), a chain of the launch, the lengths, the block table and
 // the first tile (a round trip each), one tile's QK, softmax and PV, the
 // epilogue, and the join between two cluster barriers.
@@ -260,6 +260,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kT = C::kT;
   constexpr int kSBufs = C::kSBufs;
   constexpr int kPBufs = C::kPBufs;
+  // A tile's fp32 work two values at a time, where the softmax bounds the kernel
+  // (long context with a soft cap 145.3 -> 140.5 us) or its latency does (two
+  // sequences in clusters 8.38 -> 8.18); where the loads do it is slower (long
+  // context 130.7 -> 133.3). The same roundings.
+  constexpr bool kPairs = VAR || CLU;
   constexpr float kShift = FP8 ? 0.f : kPShift;  // O and l are sums of 2^(s - m_ref + kShift)
   constexpr int kPagesPerTile = C::kPagesPerTile;
   constexpr int kKpt = C::kKpt;
@@ -879,8 +884,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarSFree + b));
               }
+              if constexpr (kPairs) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(vh[i]) + __uint_as_float(vl[i]);
+                for (int i = 0; i < 32; i += 2)
+                  unpack2(add2(pack2(__uint_as_float(vh[i]), __uint_as_float(vh[i + 1])),
+                               pack2(__uint_as_float(vl[i]), __uint_as_float(vl[i + 1]))), x[i], x[i + 1]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(vh[i]) + __uint_as_float(vl[i]);
+              }
             } else {
               uint32_t v[16];
               tmem_ld_16x32bx2_x16<16>(tmem + lane_base + kColS + b * kT + 32 * kh, v);
@@ -898,7 +910,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // logit l by at most |l| 2^-11 log2 units (0.5 % of a key's
                 // weight at l = 10).
 #pragma unroll
-                for (int i = 0; i < kKpt; ++i) x[i] = tanh_approx(x[i] * (SCL ? rx2[i / 16] : rx));
+                for (int i = 0; i < kKpt; i += 2) {
+                  const float f = SCL ? rx2[i / 16] : rx;
+                  unpack2(mul2(pack2(x[i], x[i + 1]), pack2(f, f)), x[i], x[i + 1]);
+                  x[i] = tanh_approx(x[i]);
+                  x[i + 1] = tanh_approx(x[i + 1]);
+                }
               }
             }
             const int key0 = lt * kT + kKpt * qtr;
@@ -987,8 +1004,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t ph[8], pl[8];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float a = ex2(fmaf(x[2 * i], xs2[i / 8], off2[i / 8]));
-              const float bb = ex2(fmaf(x[2 * i + 1], xs2[i / 8], off2[i / 8]));
+              float a, bb;
+              if constexpr (kPairs) {
+                unpack2(fma2(pack2(x[2 * i], x[2 * i + 1]), pack2(xs2[i / 8], xs2[i / 8]), pack2(off2[i / 8], off2[i / 8])), a, bb);
+              } else {
+                a = fmaf(x[2 * i], xs2[i / 8], off2[i / 8]);
+                bb = fmaf(x[2 * i + 1], xs2[i / 8], off2[i / 8]);
+              }
+              a = ex2(a);
+              bb = ex2(bb);
               if (i < 8)
                 ls0 += a + bb;
               else
