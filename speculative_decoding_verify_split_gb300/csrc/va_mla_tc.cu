@@ -174,15 +174,16 @@ __device__ __forceinline__ int core_off(int m, int k, int row_bytes) {
 // GQA kernel it multiplies the page's logits, and as the value's scale joins
 // the weight, P = 2^(s + log2 scale - e), with l summing P / scale. A
 // thread's 16 keys of a tile are one page. The producers bring the scales
-// with the ring slot. 64 sequences of 8K to 32K keys (733 MB), 16 heads: 154 us
-// with 3 draft tokens, 137 with one, 70 and 81 % of the measured copy bandwidth;
-// of the 154 the merge kernel is 11.
+// with the ring slot. 64 sequences of 8K to 32K keys (733 MB), 16 heads: 153 us
+// with 3 draft tokens, 135 with one, 71 and 82 % of the measured copy bandwidth;
+// of the 153 the merge kernel is 11.
 // CLU: one cluster of CTAs per item, as in the GQA kernel: two sequences of
-// 1,024 and 769 keys 10.6 us a call (23.3 split over all CTAs).
+// 1,024 and 769 keys 10.4 to 10.9 us a call (22.1 split over all CTAs).
 // NAR: at most 32 packed rows. P's two terms are then stacked in the N of P V
 // (rows r and nar + r of P^T, columns r and nar + r of O^T, added up in the
 // epilogue): half its instructions, and N = 32 for 16 rows (64 sequences of 8K
-// to 32K, one token: N = 64 135.9 us, N = 32 132.5).
+// to 32K, one token: N = 64 135.9 us, N = 32 132.5). P's exponents are packed fp32
+// FMAs, two keys an instruction (137.8 -> 135.2; at 64 rows 201 -> 204).
 template <bool SCL, bool CLU, bool NAR>
 __global__ void __launch_bounds__(kThreads, 1)
     va_mla_tc_kernel(const Params p, const __grid_constant__ CUtensorMap tm_kv,
@@ -857,8 +858,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float off2 = lv - e;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float a = ex2(fmaf(x[2 * i], xs, off2));
-            const float bb = ex2(fmaf(x[2 * i + 1], xs, off2));
+            float a, bb;
+            if constexpr (NAR) {
+              unpack2(fma2(pack2(x[2 * i], x[2 * i + 1]), pack2(xs, xs), pack2(off2, off2)), a, bb);
+            } else {
+              a = fmaf(x[2 * i], xs, off2);
+              bb = fmaf(x[2 * i + 1], xs, off2);
+            }
+            a = ex2(a);
+            bb = ex2(bb);
             ls += a + bb;
             uint32_t h2, l2;
             split_weights(a, bb, h2, l2);
