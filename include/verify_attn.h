@@ -554,7 +554,10 @@ va_status verify_attn_append_mla(const va_tensor* q_pe, const va_tensor* latent,
  *  num_splits   0: the library's choice, which for small batches is one cluster of
  *               up to 8 CTAs per (sequence, KV head) that joins its partial results
  *               on chip, without a merge kernel; > 0 forces the split over that many
- *               CTAs. With VA_LIBRARY_STATUS added a wait that runs out is reported
+ *               CTAs. The choice goes by max_seqlen_k, the lengths being on the
+ *               device: with a bound far above them (the capacity, 32K and more for
+ *               two sequences of 1K keys) it is the split, 42 us where clusters take
+ *               8.2 (latent 45 and 10). With VA_LIBRARY_STATUS added a wait that runs out is reported
  *               by verify_attn_last_device_error(NULL, ...) instead of the
  *               workspace's status word: for a workspace that is given back behind
  *               the call.
@@ -571,6 +574,9 @@ va_status verify_attn_append_mla(const va_tensor* q_pe, const va_tensor* latent,
  *  - Logits below 2^20 in magnitude (fp32 holds them to 2^-4 there).
  * verify_attn, its variants and verify_attn_mla over e4m3 caches are the same, with
  * one V scale for all pages.
+ * Page-scaled caches are read by these two entry points alone: not by
+ * verify_attn_partial (and so not over context-parallel shards),
+ * verify_attn_noalloc or the draft-extend pass.
  * Errors as verify_attn_opt; VA_ERR_NULL without scales, VA_ERR_DTYPE for a
  * BF16 cache or scales that are not fp32, VA_ERR_SHAPE for scales of another
  * shape, VA_ERR_LAYOUT for a zero stride or an address off 4 bytes.
@@ -587,8 +593,8 @@ va_status verify_attn_scaled(const va_tensor* q, const va_tensor* k_cache, const
  * verify_attn_mla_scaled - verify_attn_mla over a page-scaled e4m3 latent
  * cache: scales [num_blocks, 1] fp32, one scale a page for its whole rows, as
  * key and as value (verify_attn_append_mla writes such a cache). Workspace as
- * verify_attn_mla (NULL is refused during stream capture); scales as
- * verify_attn_scaled.
+ * verify_attn_mla (NULL is refused during stream capture); scales, num_splits and
+ * accuracy as verify_attn_scaled.
  */
 va_status verify_attn_mla_scaled(const va_tensor* q, const va_tensor* kv_cache, const va_tensor* scales,
                                  const va_tensor* block_table, const va_tensor* cu_seqlens_q,

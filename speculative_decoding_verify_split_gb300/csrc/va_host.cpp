@@ -152,19 +152,22 @@ static int64_t tiles_upper_bound(int64_t B, int64_t hkv, int32_t max_q, int32_t 
 //    and the merge kernel cost, and a quarter tile for each segment past eight
 //    (24 tiles at most) that the merge would have to fold per item; for items
 //    that are as large as their bound on average with a window (`even`), and
-//    half as large without. Over 216 shapes of each kind (1 to 152 items of 8 to
-//    512 tiles, of one size, from half of it and from an eighth of it) the
-//    choice loses 0.6 % to the better of the two on average, and clusters alone
-//    or the split alone 12 and 19 % (GQA), 5 and 29 % (latent).
+//    half as large without. Over the 216 shapes of each kind that the figures are
+//    fitted on (1 to 152 items of 8 to 512 tiles, of one size, from half of it and
+//    from an eighth of it) the choice loses 0.6 % to the better of the two on
+//    average, and clusters alone or the split alone 12 and 19 % (GQA), 5 and 29 %
+//    (latent).
+//  * T is the caller's bound on the lengths, which are on the device: a loose one
+//    makes the largest item look large, and the split is taken.
 // Measured, us per call in graphs of calls, split over all CTAs against
 // clusters (16 query heads per KV head unless noted):
-//   2 x 1,024 keys, 4 tokens 12.5 / 8.3; 32 x 2,000, 1 token 17.8 / 12.9;
-//   64 x 1,000, 2 tokens, 8 heads 19.1 / 13.7; 1 x 8,000, 4 tokens 21.3 / 16.4;
-//   1 x 20,000, 1 token 47.2 / 30.8; 16 x 3,000, 2 tokens 17.5 / 15.3;
-//   1 x 40,000 49.7 / 54.4 (split); 32 x 2 heads, window of 1,023 24.0 / 17.9.
-//   Latent cache: 2 x 1,024, 4 tokens 23.3 / 10.6; 32 x 2,000, 1 token
-//   25.9 / 18.6; 76 x 1,500, 4 tokens 52.8 / 36.9; 100 x 600, 1 token
-//   27.6 / 21.3; 8 x 16,384 at most, 2 tokens 33.8 / 42.8 (split).
+//   2 x 1,024 keys, 4 tokens 13.8 / 8.2; 32 x 2,000, 1 token 17.6 / 12.5;
+//   64 x 1,000, 2 tokens, 8 heads 18.8 / 13.3; 1 x 8,000, 4 tokens 21.5 / 16.4;
+//   1 x 20,000, 1 token 47.5 / 30.9; 16 x 3,000, 2 tokens 17.2 / 15.0;
+//   1 x 40,000 49.7 / 54.4 (split); 32 x 2 heads, window of 1,023 24.0 / 17.8.
+//   Latent cache: 2 x 1,024, 4 tokens 22.1 / 10.4; 32 x 2,000, 1 token
+//   23.2 / 16.1; 76 x 1,500, 4 tokens 46.7 / 32.6; 100 x 600, 1 token
+//   25.5 / 19.4; 8 x 16,384 at most, 2 tokens 33.8 / 42.8 (split).
 static bool cluster_plan(int64_t J, int64_t T, int32_t tile_keys, int64_t group, int32_t max_q,
                          const int32_t* caps, int32_t num_sms, bool even, int32_t* cluster, int32_t* share) {
   if (J < 1 || T < 1) return false;
