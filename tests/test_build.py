@@ -11,7 +11,7 @@ from speculative_decoding_verify_split_gb300 import build
 
 @pytest.fixture(scope="module", autouse=True)
 def built():
-    build.build_library()
+    build.build_library(force=not all(os.path.exists(os.path.join(build.BUILD, f + ".o")) for f in build.SOURCES))
 
 
 def test_another_torch_or_interpreter_makes_the_extension_stale(monkeypatch):
