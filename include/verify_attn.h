@@ -604,6 +604,66 @@ va_status verify_attn_mla_scaled(const va_tensor* q, const va_tensor* kv_cache, 
                                  void* stream);
 
 /*
+ * verify_attn_chunk - attention of chunks of new tokens over the paged cache:
+ * whole prompts, pieces of prompts behind cached tokens, single tokens, mixed in
+ * a batch. The operation of verify_attn and of its variants for any number of
+ * new tokens and query heads a KV head: with L = cu_seqlens_q[b+1] -
+ * cu_seqlens_q[b] new tokens of sequence b and S = seqused_k[b] cached ones (the
+ * new ones counted, stored before), token t is at position i = S - L + t and
+ * head h of it reads KV head h / (Hq/Hkv):
+ *
+ *   s_j = softmax_scale * k_descale * q . K_j        (then the soft cap)
+ *   out[cu[b]+t, h, :] = v_descale * sum_j softmax(s)_j V_j  over j in [0, i], or
+ *                        with a window over j in [i - window_left, i] and
+ *                        j < min(first_tokens, i + 1)
+ *
+ *  q, out       [total_q, Hq, 256] BF16; out is written (rows of sequences; rows
+ *               behind the last sequence are left as they were) and may not
+ *               overlap an input or itself. A row that sees no key is 0.
+ *  k_cache, v_cache  [num_blocks, 16, Hkv, 256] FP8_E4M3 or BF16, as verify_attn.
+ *  k_scales, v_scales  [num_blocks, Hkv] fp32: a page-scaled e4m3 cache, as
+ *               verify_attn_scaled reads it (no descales); or both NULL.
+ *  block_table, cu_seqlens_q, seqused_k, k_descale, v_descale  as verify_attn.
+ *               A page none of whose keys is seen is not read, so a
+ *               sliding-window page table need not map it. Lengths past the
+ *               table's width are read as the width, page ids outside
+ *               [0, num_blocks) as pages of zeros.
+ *  opts         NULL: no window, soft cap or sinks (verify_attn_opt).
+ *  first_tokens with a window: the sequence's first tokens that stay visible
+ *               (attention sinks that are tokens); without one they are anyhow.
+ *  workspace    verify_attn_chunk_workspace_size() bytes of device memory,
+ *               256-byte aligned, first 4 bytes its status word, as
+ *               verify_attn_ex; or NULL to use the library's own, whose calls
+ *               must be ordered on one stream (refused during stream capture,
+ *               VA_ERR_WORKSPACE).
+ *  num_splits   0: the library's choice; > 0: the CTA pairs that share the work
+ *               (at most what the device holds). VA_LIBRARY_STATUS as
+ *               verify_attn_scaled.
+ *
+ * Two launches (the second one joins what pairs shared), asynchronous on
+ * stream, capturable; nothing depends on host bounds of the lengths.
+ * Accuracy: Q K^T and P V on the tensor cores in 16 bits with fp32 sums. BF16
+ * caches: P is rounded to bf16. E4M3 caches: codes are taken as f16 (exact), P is
+ * rounded to f16, with steps of 2^-24 * 2^-7 below 2^-21 of the row's reference
+ * (within 2^8 of its largest weight), Q exactly down to 2^-31 of a row's largest.
+ * The normaliser, the references and the joined sums are fp32.
+ * A value that is NaN or infinite at a key in [0, S) may reach rows of the same
+ * sequence that do not see the key; keys may be anything where they are not seen.
+ * Errors before launching, as verify_attn_append_kv; VA_ERR_UNSUPPORTED also for
+ * first_tokens < 0, descales beside page scales, or total_q * Hq / Hkv past 2^31.
+ */
+va_status verify_attn_chunk(const va_tensor* q, const va_tensor* k_cache, const va_tensor* v_cache,
+                            const va_tensor* k_scales, const va_tensor* v_scales, const va_tensor* block_table,
+                            const va_tensor* cu_seqlens_q, const va_tensor* seqused_k, float softmax_scale,
+                            const va_tensor* k_descale, const va_tensor* v_descale, va_tensor* out,
+                            const va_options* opts, int32_t first_tokens, void* workspace, size_t workspace_bytes,
+                            int32_t num_splits, void* stream);
+
+/* Workspace bytes of verify_attn_chunk on the current device, for any shapes (0
+ * on error). */
+size_t verify_attn_chunk_workspace_size(void);
+
+/*
  * verify_attn_last_device_error - reads and clears the device status word of
  * a workspace. This turns the pages' gates and asserts (sglang PR 36330 digest,
  * "Key code excerpts") into something a caller can check after launch: a

@@ -35,7 +35,7 @@ EXPORTS = ("verify_attn", "verify_attn_ex", "verify_attn_check", "verify_attn_pl
            "verify_attn_mla_workspace_size", "verify_attn_partial", "verify_attn_merge_partials",
            "verify_attn_last_device_error", "verify_attn_set_wait_limit",
            "verify_attn_append_kv", "verify_attn_append_mla", "verify_attn_scaled",
-           "verify_attn_mla_scaled")
+           "verify_attn_mla_scaled", "verify_attn_chunk", "verify_attn_chunk_workspace_size")
 
 # Absorbed-MLA latent cache: row = [latent (MLA_NOPE) | rope key (MLA_PE)].
 MLA_NOPE, MLA_PE = 512, 64
@@ -139,6 +139,11 @@ def _lib():
                                                          ctypes.c_float, P, V, ctypes.c_size_t,
                                                          ctypes.c_int32, V, V]
         lib.verify_attn_mla_scaled.restype = ctypes.c_int32
+        lib.verify_attn_chunk.argtypes = [P] * 8 + [ctypes.c_float, P, P, P, ctypes.POINTER(VaOptions),
+                                                    ctypes.c_int32, V, ctypes.c_size_t, ctypes.c_int32, V]
+        lib.verify_attn_chunk.restype = ctypes.c_int32
+        lib.verify_attn_chunk_workspace_size.argtypes = []
+        lib.verify_attn_chunk_workspace_size.restype = ctypes.c_size_t
         lib.verify_attn_status_string.argtypes = [ctypes.c_int32]
         lib.verify_attn_status_string.restype = ctypes.c_char_p
         _LIB = lib
@@ -627,3 +632,33 @@ def verify_attn_mla_scaled(q, kv_cache, scales, block_table, cu_seqlens_q, sequs
     if s != VA_OK:
         raise VerifyAttnError(s, "verify_attn_mla_scaled")
     return out
+
+
+def verify_attn_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, softmax_scale: float,
+                      k_descale=None, v_descale=None, k_scales=None, v_scales=None, out=None,
+                      window_left: int = -1, first_tokens: int = 0, softcap: float = 0.0, sinks=None,
+                      workspace: Optional[torch.Tensor] = None, num_splits: int = 0, stream=None):
+    """Attention of chunks of new tokens (prompts, pieces of prompts, single
+    tokens) over the paged cache that ``append_kv`` wrote them to (see
+    include/verify_attn.h): any number of tokens a sequence; bf16, e4m3 with
+    descales or, with k_scales / v_scales, page-scaled. With a window the
+    sequence's first ``first_tokens`` tokens stay visible. ``workspace`` (a
+    uint8 device tensor of ``chunk_workspace_size()`` bytes) as for
+    ``verify_attn_scaled``."""
+    if out is None:
+        out = _empty(q.shape, q, stream)
+    s = _native().attn_chunk(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_seqlens_q, seqused_k,
+                             k_descale, v_descale, out, sinks, softmax_scale, window_left, softcap,
+                             first_tokens, workspace, num_splits, _handle(stream))
+    if s != VA_OK:
+        raise VerifyAttnError(s, "verify_attn_chunk")
+    return out
+
+
+def chunk_workspace_size(device=None) -> int:
+    """Bytes of a ``verify_attn_chunk`` workspace tensor, alignment included."""
+    with torch.cuda.device(device):
+        n = _lib().verify_attn_chunk_workspace_size()
+    if n == 0:
+        raise VerifyAttnError(6, "verify_attn_chunk_workspace_size")
+    return int(n) + 256

@@ -1,6 +1,6 @@
 // The compiled half of the Python binding for the calls of a verify step that
 // a decoder makes back to back (append_kv, append_mla, verify_attn_scaled,
-// verify_attn_mla_scaled): reads torch tensors into va_tensor descriptors and
+// verify_attn_mla_scaled, verify_attn_chunk): reads torch tensors into va_tensor descriptors and
 // calls the C ABI. Marshalling fifteen tensors through ctypes takes 20 us on a
 // Grace core, several times what the kernels of a small step take; here it
 // takes well under one.
@@ -235,7 +235,7 @@ struct Tail {
 
   bool read(PyObject* workspace, PyObject* num_splits, PyObject* ev, PyObject* st, c10::Device device) {
     if (!read_int(num_splits, &splits) || !read_stream(st, device, &stream)) return false;
-    event = PyLong_AsVoidPtr(ev);
+    if (ev) event = PyLong_AsVoidPtr(ev);
     if (PyErr_Occurred()) return false;
     if (workspace == Py_None) return true;
     if (!THPVariable_Check(workspace)) {
@@ -322,12 +322,41 @@ PyObject* attn_mla_scaled(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// attn_chunk(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_seqlens_q, seqused_k, k_descale, v_descale, out, sinks,
+//            softmax_scale, window_left, softcap, first_tokens, workspace, num_splits, stream)
+PyObject* attn_chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (!arity(n, 19)) return nullptr;
+    Args args;
+    va_tensor* t[12];
+    for (int i = 0; i < 12; ++i)
+      if (!args.add(a[i], &t[i])) return nullptr;
+    int32_t first_tokens;
+    float scale;
+    va_options opt;
+    Tail tail;
+    if (!read_float(a[12], &scale) || !read_int(a[13], &opt.window_left) || !read_float(a[14], &opt.softcap) ||
+        !read_int(a[15], &first_tokens) || !args.on_cuda("verify_attn_chunk") ||
+        !tail.read(a[16], a[17], nullptr, a[18], args.device))
+      return nullptr;
+    opt.sinks = t[11];
+    c10::cuda::CUDAGuard guard(args.device);
+    const size_t need = tail.ws ? 0 : verify_attn_chunk_workspace_size();
+    const CallWorkspace own(need, tail.stream);
+    return status_of(args.device, [&] {
+      return verify_attn_chunk(t[0], t[1], t[2], t[3], t[4], t[5], t[6], t[7], scale, t[8], t[9], t[10], &opt, first_tokens,
+                               tail.ws ? tail.ws : own.get(), tail.ws ? tail.bytes : need, tail.splits_arg(), tail.stream);
+    });
+  });
+}
+
 PyMethodDef kMethods[] = {
     {"append_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_kv)), METH_FASTCALL, nullptr},
     {"append_mla", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_mla)), METH_FASTCALL, nullptr},
     {"attn_scaled", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn_scaled)), METH_FASTCALL, nullptr},
     {"attn_mla_scaled", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn_mla_scaled)), METH_FASTCALL,
      nullptr},
+    {"attn_chunk", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn_chunk)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "va_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,990 @@
+// Attention of chunks of new tokens over the paged cache, on pairs of CTAs.
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "va_chunk.h"
+#include "va_fp8.cuh"
+#include "va_ptx.cuh"
+
+namespace va {
+namespace {
+
+using namespace ptx;
+
+constexpr int kKeys = kChunkKeys;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ---- the split of the work ----------------------------------------------------------
+
+struct Seq {
+  int S, L, q0;  // cached tokens, new tokens, first row of q; clamped to the buffers
+};
+
+__device__ __forceinline__ Seq chunk_seq(const ChunkParams& p, int b) {
+  const int a = p.cu_q[b], e = p.cu_q[b + 1];
+  Seq s;
+  s.q0 = a;
+  s.L = a < 0 || e <= a ? 0 : e - a;
+  const int room = p.total_q - a;
+  if (s.L > room) s.L = room < 0 ? 0 : room;
+  s.S = p.seqused_k[b];
+  const int cap = p.num_blocks > 0 ? p.bt_width * kPageSize : 0;
+  s.S = s.S < 0 ? 0 : s.S > cap ? cap : s.S;
+  return s;
+}
+
+__device__ __forceinline__ int row_tiles(const ChunkParams& p, const Seq& s) {
+  return (int)(((int64_t)s.L * p.group + kChunkRows - 1) / kChunkRows);
+}
+
+// Units of the split: a tile is 128 G of them. Row tile m costs
+//   min(max(0, (S - L) G + 256 (m + 1)), cap) + kChunkItemCost * 128 G,
+// about G times the keys that its rows see, so that the sum over a sequence's
+// row tiles has a closed form and a share's start is found without walking them.
+// The sum of tiles that an item really has (window and first tokens start and
+// end inside tiles) is at most 3 above keys / 128.
+__device__ __forceinline__ int64_t unit_cap(const ChunkParams& p) {
+  if (p.window_left < 0) return INT64_MAX / 4;
+  return ((int64_t)p.window_left + 2 + p.first_tokens) * p.group + kChunkRows;
+}
+
+__device__ __forceinline__ int64_t chunk_cost(const ChunkParams& p, const Seq& s, int m) {
+  const int64_t x = (int64_t)(s.S - s.L) * p.group + (int64_t)kChunkRows * (m + 1);
+  const int64_t cap = unit_cap(p);
+  return (x < 0 ? 0 : x > cap ? cap : x) + (int64_t)kChunkItemCost * kKeys * p.group;
+}
+
+// Units of row tiles [0, m).
+__device__ __forceinline__ int64_t chunk_prefix(const ChunkParams& p, const Seq& s, int64_t m) {
+  const int64_t x0 = (int64_t)(s.S - s.L) * p.group, cap = unit_cap(p);
+  int64_t a = x0 < 0 ? -x0 / kChunkRows : 0;           // tiles below a cost nothing but their start
+  int64_t b = cap <= x0 ? 0 : (cap - x0) / kChunkRows;  // tiles from b on cost cap
+  a = a > m ? m : a;
+  b = b > m ? m : b < a ? a : b;
+  return m * ((int64_t)kChunkItemCost * kKeys * p.group) + (b - a) * x0 + kChunkRows / 2 * (b * (b + 1) - a * (a + 1)) +
+         (m > b ? (m - b) * cap : 0);
+}
+
+// The keys that an item's rows see: [0, khi), or with a window [klo, khi) and the
+// first tokens; its tiles: nf from 0 on, then those from w0 on, n in all.
+struct Span {
+  int klo, khi, nf, w0, n;
+};
+
+__device__ __forceinline__ Span item_span(const ChunkParams& p, const Seq& s, int m) {
+  const int t0 = (int)((int64_t)kChunkRows * m / p.group);
+  int t1 = (int)(((int64_t)kChunkRows * m + kChunkRows - 1) / p.group);
+  t1 = t1 < s.L - 1 ? t1 : s.L - 1;
+  Span x;
+  x.khi = s.S - s.L + t1 + 1;
+  x.khi = x.khi < 0 ? 0 : x.khi;
+  x.klo = 0;
+  if (p.window_left >= 0) {
+    const int64_t lo = (int64_t)s.S - s.L + t0 - p.window_left;
+    x.klo = lo < 0 ? 0 : (int)lo;
+  }
+  x.w0 = x.klo / kKeys;
+  x.nf = 0;
+  if (p.window_left >= 0 && p.first_tokens > 0) {
+    x.nf = (int)(((int64_t)p.first_tokens + kKeys - 1) / kKeys);
+    x.nf = x.nf < x.w0 ? x.nf : x.w0;
+  }
+  x.n = x.khi > 0 ? x.nf + (x.khi + kKeys - 1) / kKeys - x.w0 : 0;
+  return x;
+}
+
+__device__ __forceinline__ int64_t share_begin(int64_t total, int c, int used) { return total * c / used; }
+
+__device__ __forceinline__ int64_t ceil_units(int64_t x, int64_t unit) { return x <= 0 ? 0 : (x + unit - 1) / unit; }
+
+// Walks the items from a share's start on.
+struct Walk {
+  int b, h, m, tiles;
+  int64_t off;
+  Seq s;
+};
+
+__device__ __forceinline__ Walk start_walk(const ChunkParams& p, const ChunkStart& st) {
+  Walk w;
+  w.b = st.b;
+  w.h = st.h;
+  w.m = st.m;
+  w.off = st.off;
+  w.s = chunk_seq(p, st.b);
+  w.tiles = row_tiles(p, w.s);
+  return w;
+}
+
+// An item's part in a share: tiles [i0, i1) of its n.
+struct Piece {
+  int b, h, m, i0, i1;
+  Seq s;
+  Span x;
+  bool direct;  // the whole item: its rows are written to out
+};
+
+__device__ __forceinline__ bool next_piece(const ChunkParams& p, int64_t t0, int64_t t1, Walk& w, Piece& pc) {
+  const int64_t unit = (int64_t)kKeys * p.group;
+  while (w.off < t1) {
+    if (w.m >= w.tiles) {
+      w.m = 0;
+      if (w.tiles == 0 || ++w.h == p.hkv) {
+        w.h = 0;
+        if (++w.b >= p.num_seqs) return false;
+        w.s = chunk_seq(p, w.b);
+        w.tiles = row_tiles(p, w.s);
+      }
+      continue;
+    }
+    pc.b = w.b;
+    pc.h = w.h;
+    pc.m = w.m;
+    pc.s = w.s;
+    pc.x = item_span(p, w.s, w.m);
+    const int64_t off = w.off;
+    w.off += chunk_cost(p, w.s, w.m);
+    ++w.m;
+    const int64_t i0 = ceil_units(t0 - off, unit), i1 = ceil_units(t1 - off, unit);
+    pc.i0 = (int)(i0 < pc.x.n ? i0 : pc.x.n);
+    pc.i1 = (int)(i1 < pc.x.n ? i1 : pc.x.n);
+    pc.direct = pc.i0 == 0 && pc.i1 == pc.x.n;
+    if (pc.i0 < pc.i1 || (pc.x.n == 0 && off >= t0)) return true;
+  }
+  return false;
+}
+
+__device__ __forceinline__ int tile_of(const Span& x, int i) { return i < x.nf ? i : x.w0 + (i - x.nf); }
+
+// ---- the main kernel -----------------------------------------------------------------
+
+enum Kind { kBf16 = 0, kE4m3 = 1, kPageScaled = 2 };
+
+constexpr int kSoftmaxWarps = 4, kLoadWarps = 4;
+constexpr int kThreads = 32 * (kSoftmaxWarps + kLoadWarps + 2);
+constexpr int kWarpProducer = 8, kWarpMma = 9;
+
+template <int KIND>
+struct Cfg {
+  static constexpr bool kFp8 = KIND != kBf16;
+  static constexpr int kOpBytes = 32768;                    // a CTA's half of a K or V tile, 16 bits
+  static constexpr int kOpSlots = kFp8 ? 3 : 5;
+  static constexpr int kRawBytes = kFp8 ? 16384 : kOpBytes;  // what TMA brings
+  static constexpr int kRawSlots = kFp8 ? 4 : kOpSlots;
+  static constexpr int kOffQ = 0;  // [4 d chunks][128 rows][128 bytes]
+  static constexpr int kOffOp = 65536;
+  static constexpr int kOffRaw = kFp8 ? kOffOp + kOpSlots * kOpBytes : kOffOp;
+  static constexpr int kOffMisc = kFp8 ? kOffRaw + kRawSlots * kRawBytes : kOffOp + kOpSlots * kOpBytes;
+  static constexpr int kSmemBytes = kOffMisc + 3072;
+  static_assert(kSmemBytes <= 232448, "shared memory");
+  // instruction descriptors: f16 (0) or bf16 (1) operands, M = 256
+  static constexpr uint32_t kFmt = kFp8 ? 0u : 1u;
+  static constexpr uint32_t kIdQK = instr_desc(kFmt, kFmt, false, kKeys, 256);
+  static constexpr uint32_t kIdPV = instr_desc(kFmt, kFmt, true, kHeadDim, 256);
+};
+
+// misc area: barriers, scratch of the work scan, row factors, page scales
+constexpr int kMaxRaw = 5, kMaxOp = 5, kScaleTiles = 8;
+enum : int {
+  kBarRawFull = 0,
+  kBarRawEmpty = kBarRawFull + kMaxRaw,
+  kBarOpFull = kBarRawEmpty + kMaxRaw,
+  kBarOpEmpty = kBarOpFull + kMaxOp,
+  kBarSFull = kBarOpEmpty + kMaxOp,
+  kBarPFull = kBarSFull + 2,
+  kBarPvDone = kBarPFull + 2,
+  kBarQFull = kBarPvDone + 2,
+  kBarQFree,
+  kBarOFree,
+  kBarDrain,
+  kBarScales,
+  kNumBars = kBarScales + kScaleTiles
+};
+constexpr int kOffTmem = 8 * kNumBars, kOffAbort = kOffTmem + 4;
+constexpr int kOffScratch = (kOffAbort + 4 + 15) / 16 * 16;     // 32 x 8 bytes
+constexpr int kOffStart = kOffScratch + 256;                     // ChunkStart
+constexpr int kOffRow = (kOffStart + 48 + 15) / 16 * 16;         // [2][128] floats
+constexpr int kOffScale = kOffRow + 1024;                        // [kScaleTiles][8] (K scale, log2 V scale)
+static_assert(kOffScale + kScaleTiles * 64 <= 3072, "misc area");
+
+constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
+
+// P = 2^(s - m_ref + shift): m_ref moves when a tile's max passes it by more than
+// kMove (O and l are rescaled then). bf16 keeps 8 bits at any size; f16 holds up to
+// 2^15 with shift 7 and all its 11 bits down to 2^-21 of 2^m_ref.
+constexpr float kMove = 8.f;
+
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_b16x2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kThreads, 1)
+    va_chunk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+  using C = Cfg<KIND>;
+  constexpr bool kFp8 = C::kFp8;
+  constexpr bool kScl = KIND == kPageScaled;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw;
+  unsigned char* misc = sm + C::kOffMisc;
+  const uint32_t sbase = smem_addr(sm);
+  const uint32_t mbase = sbase + C::kOffMisc;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + kOffAbort);
+  long long* scratch = reinterpret_cast<long long*>(misc + kOffScratch);
+  ChunkStart* start = reinterpret_cast<ChunkStart*>(misc + kOffStart);
+  float* row_factor = reinterpret_cast<float*>(misc + kOffRow);
+  float2* page_scale = reinterpret_cast<float2*>(misc + kOffScale);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank();
+  const int c = blockIdx.x >> 1;
+  auto bar = [&](int i) { return mbase + 8 * i; };
+  auto lead = [&](int i) { return cluster_addr(mbase + 8 * i, 0); };  // the issuing CTA's barrier
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    for (int i = 0; i < C::kRawSlots; ++i) {
+      mbar_init(bar(kBarRawFull + i), 1);
+      mbar_init(bar(kBarRawEmpty + i), kFp8 ? kLoadWarps : 1);
+    }
+    for (int i = 0; i < C::kOpSlots; ++i) {
+      mbar_init(bar(kBarOpFull + i), kFp8 ? 2 * kLoadWarps : 2);
+      mbar_init(bar(kBarOpEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarSFull + i), 1);
+      mbar_init(bar(kBarPFull + i), 2 * kSoftmaxWarps);
+      mbar_init(bar(kBarPvDone + i), 1);
+    }
+    mbar_init(bar(kBarQFull), 2 * kLoadWarps);
+    mbar_init(bar(kBarQFree), 1);
+    mbar_init(bar(kBarOFree), 2 * kSoftmaxWarps);
+    mbar_init(bar(kBarDrain), 1);
+    for (int i = 0; i < kScaleTiles; ++i) mbar_init(bar(kBarScales + i), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc_pair(mbase + kOffTmem, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  if (warp == kWarpProducer && lane == 0 && p.num_blocks > 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_arrive();  // barriers are set up before the other CTA arrives on them
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc + kOffTmem);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- this pair's share
+  int64_t t0 = 0, t1 = 0;
+  {
+    const int64_t unit = (int64_t)kKeys * p.group;
+    int64_t total = 0, mine = 0, ex = 0;
+    Seq s{};
+    if (p.num_seqs <= kThreads) {
+      if (tid < p.num_seqs) {
+        s = chunk_seq(p, tid);
+        mine = p.hkv * chunk_prefix(p, s, row_tiles(p, s));
+      }
+      long long tot;
+      ex = block_exclusive_scan<kThreads>(mine, scratch, &tot);
+      total = tot;
+    } else {
+      for (int b0 = 0; b0 < p.num_seqs; b0 += kThreads) {
+        int64_t v = 0;
+        if (b0 + tid < p.num_seqs) {
+          const Seq q = chunk_seq(p, b0 + tid);
+          v = p.hkv * chunk_prefix(p, q, row_tiles(p, q));
+        }
+        long long tot;
+        block_exclusive_scan<kThreads>(v, scratch, &tot);
+        total += tot;
+      }
+    }
+    int64_t used = p.force > 0 ? p.force : total / (4 * unit);
+    used = used < 1 ? 1 : used > p.pairs ? p.pairs : used;
+    if (total == 0) used = 0;
+    if (c < used) {
+      t0 = share_begin(total, c, (int)used);
+      t1 = share_begin(total, c + 1, (int)used);
+      int64_t running = 0;
+      for (int b0 = 0; b0 < p.num_seqs; b0 += kThreads) {
+        if (p.num_seqs > kThreads) {
+          mine = 0;
+          if (b0 + tid < p.num_seqs) {
+            s = chunk_seq(p, b0 + tid);
+            mine = p.hkv * chunk_prefix(p, s, row_tiles(p, s));
+          }
+          long long tot;
+          ex = block_exclusive_scan<kThreads>(mine, scratch, &tot);
+          ex += running;
+          running += tot;
+        }
+        if (mine > 0 && ex <= t0 && t0 < ex + mine) {
+          const int tiles = row_tiles(p, s);
+          const int64_t per = chunk_prefix(p, s, tiles);
+          const int64_t h = (t0 - ex) / per, at = t0 - ex - h * per;
+          int lo = 0, hi = tiles;  // the largest m with prefix(m) <= at
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (chunk_prefix(p, s, mid) <= at)
+              lo = mid;
+            else
+              hi = mid;
+          }
+          start->b = b0 + tid;
+          start->h = (int)h;
+          start->m = lo;
+          start->off = ex + h * per + chunk_prefix(p, s, lo);
+          start->total = total;
+          start->used = (int)used;
+        }
+      }
+      __syncthreads();
+      if (tid == 0 && rank == 0) p.ws_start[c] = *start;
+    } else if (c == 0 && tid == 0 && rank == 0) {
+      p.ws_start[0].used = 0;
+    }
+  }
+  __syncwarp();
+  cluster_wait();
+
+  auto give_up = [&](int code) {
+    *abort_flag = 1;
+    st_cluster_u32(cluster_addr(mbase + kOffAbort, (uint32_t)(rank ^ 1)), 1u);
+    if (p.ws_status) atomicOr(p.ws_status, code);
+  };
+  // Waits of a whole warp: warp-uniform, false once anything has given up.
+  bool ok = true;
+  auto wait_for = [&](int b, int use, int code, bool cluster = false) {
+    if (!ok) return false;
+    const uint32_t par = (uint32_t)use & 1u;
+    const bool got = cluster ? mbar_wait_cluster(bar(b), par, abort_flag, p.wait_limit_ns)
+                             : mbar_wait(bar(b), par, abort_flag, p.wait_limit_ns);
+    if (!__all_sync(0xffffffffu, got)) {
+      if (lane == 0) give_up(code);
+      ok = false;
+    }
+    return ok;
+  };
+
+  if (t0 < t1) {
+    Walk w = start_walk(p, *start);
+    Piece pc;
+    int seq = 0;  // K and V tiles so far: a piece's K0, K1, V0, K2, V1, .., K(n-1), V(n-2), V(n-1)
+    if (warp == kWarpProducer) {
+      // ======================= TMA producer ==========================================
+      // One 2 KB box (a page's 16 tokens x 128 bytes) a lane: this CTA's half of K's
+      // keys, or of V's columns. Pages that no row of the item sees are not mapped
+      // perhaps: they are read past the cache's last page, which TMA fills with zeros.
+      constexpr int kDim = kFp8 ? 2 : 4;            // 128-byte chunks of a row
+      constexpr int kVCh = kDim / 2;                // .. of V's half
+      const int k_page = lane / kDim + 4 * rank, k_ch = lane % kDim;
+      const int v_page = lane / kVCh, v_ch = lane % kVCh;
+      constexpr int kEl = kFp8 ? 128 : 64;          // elements of a chunk
+      const bool k_on = lane < 4 * kDim, v_on = lane < 8 * kVCh;
+      int tiles = 0;  // tiles so far (page scales)
+      while (ok && next_piece(p, t0, t1, w, pc)) {
+        const int n = pc.i1 - pc.i0;
+        const int* bt = p.block_table + (int64_t)pc.b * p.bt_s0;
+        auto page_id = [&](int page) {
+          const int key = page * kPageSize;
+          const bool seen = key < pc.x.khi && (key + kPageSize > pc.x.klo || key < p.first_tokens);
+          const int id = seen ? bt[(int64_t)page * p.bt_s1] : -1;
+          return (unsigned)id < (unsigned)p.num_blocks ? id : p.num_blocks;
+        };
+        auto step = [&](int off, bool& is_k, int& i) {
+          is_k = off == 0 || (off != 2 * n - 1 && (off & 1));
+          i = off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1;
+        };
+        auto page_of = [&](int off) {
+          bool is_k;
+          int i;
+          step(off, is_k, i);
+          return tile_of(pc.x, pc.i0 + i) * (kKeys / kPageSize) + (is_k ? k_page : v_page);
+        };
+        auto fetch = [&](int off) {
+          bool is_k;
+          int i;
+          step(off, is_k, i);
+          return (is_k ? k_on : v_on) ? page_id(page_of(off)) : p.num_blocks;
+        };
+        // page scales of tile i: lanes 24..31, loaded a tile ahead
+        float ks = 1.f, vs = 1.f;
+        auto scales_of = [&](int i) {
+          if (kScl && lane >= 24 && i < n) {
+            const int id = page_id(tile_of(pc.x, pc.i0 + i) * (kKeys / kPageSize) + lane - 24);
+            ks = vs = 1.f;
+            if (id < p.num_blocks) {
+              ks = __ldg(p.k_scales + (int64_t)id * p.ks_s0 + (int64_t)pc.h * p.ks_s1);
+              vs = __ldg(p.v_scales + (int64_t)id * p.vs_s0 + (int64_t)pc.h * p.vs_s1);
+            }
+          }
+        };
+        if (n > 0) scales_of(0);
+        int next = n > 0 ? fetch(0) : 0;
+        for (int off = 0; off < 2 * n && ok; ++off, ++seq) {
+          bool is_k;
+          int i;
+          step(off, is_k, i);
+          const int id = next;
+          if (off + 1 < 2 * n) next = fetch(off + 1);
+          const int slot = seq % C::kRawSlots, use = seq / C::kRawSlots;
+          if (use > 0 && !wait_for(kBarRawEmpty + slot, use - 1, 1)) break;
+          if (kScl && is_k) {
+            if (lane >= 24) {
+              const float k1 = fminf(fmaxf(ks, kMinPageScale), kMaxPageScale);
+              const float v1 = fminf(fmaxf(vs, kMinPageScale), kMaxPageScale);
+              page_scale[((tiles + i) % kScaleTiles) * 8 + lane - 24] = make_float2(k1, log2f(v1));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarScales + (tiles + i) % kScaleTiles));
+            scales_of(i + 1);
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(kBarRawFull + slot), C::kRawBytes);
+          __syncwarp();
+          const uint32_t dst = sbase + C::kOffRaw + slot * C::kRawBytes;
+          if (is_k) {
+            if (k_on)
+              tma_load_4d(dst + k_ch * (64 * 128) + (lane / kDim) * 2048, &tm_k, k_ch * kEl, pc.h, 0, id,
+                          bar(kBarRawFull + slot));
+          } else if (v_on) {
+            tma_load_4d(dst + v_ch * (128 * 128) + v_page * 2048, &tm_v, (rank * kVCh + v_ch) * kEl, pc.h, 0, id,
+                        bar(kBarRawFull + slot));
+          }
+          __syncwarp();
+        }
+        tiles += n;
+      }
+      // copies in flight land before the CTA ends, also when another role gave up
+      if (lane == 0)
+        for (int k = seq > C::kRawSlots ? seq - C::kRawSlots : 0; k < seq; ++k)
+          mbar_wait_drain(bar(kBarRawFull + k % C::kRawSlots), (uint32_t)(k / C::kRawSlots) & 1u, kDrainLimitNs);
+      __syncwarp();
+    } else if (warp == kWarpMma) {
+      // ======================= MMA issuer (the even CTA) ===============================
+      if (rank == 0) {
+        int tiles = 0, piece = 0;
+        while (ok && next_piece(p, t0, t1, w, pc)) {
+          const int n = pc.i1 - pc.i0;
+          if (n == 0) continue;
+          if (!wait_for(kBarQFull, piece, 2, true)) break;
+          for (int off = 0; off < 2 * n && ok; ++off, ++seq) {
+            const bool is_k = off == 0 || (off != 2 * n - 1 && (off & 1));
+            const int i = off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1;
+            const int slot = seq % C::kOpSlots, use = seq / C::kOpSlots;
+            const int b = (tiles + i) & 1;
+            if (!wait_for(kBarOpFull + slot, use, 4, true)) break;
+            if (!is_k) {
+              if (!wait_for(kBarPFull + b, (tiles + i) >> 1, 8, true)) break;
+              if (i == 0 && piece > 0 && !wait_for(kBarOFree, piece - 1, 16, true)) break;
+            }
+            tc_fence_after();
+            const uint32_t src = sbase + C::kOffOp + slot * C::kOpBytes;
+            if (elect_one()) {
+              if (is_k) {
+#pragma unroll
+                for (int k = 0; k < kHeadDim / 16; ++k) {
+                  const uint32_t ko = (uint32_t)((k & 3) * 32);
+                  mma_f16_pair(tmem + kColS + b * kKeys, smem_desc(sbase + C::kOffQ + (k >> 2) * (128 * 128) + ko, 16, 1024, kLayoutSw128),
+                               smem_desc(src + (k >> 2) * (64 * 128) + ko, 16, 1024, kLayoutSw128), C::kIdQK, k ? 1u : 0u);
+                }
+                mma_commit_pair(bar(kBarSFull + b));
+              } else {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                  mma_f16_pair_ta(tmem + kColO, tmem + kColS + b * kKeys + 8 * k,
+                                  smem_desc(src + k * 2048, 128 * 128, 1024, kLayoutSw128), C::kIdPV, i || k ? 1u : 0u);
+                mma_commit_pair(bar(kBarPvDone + b));
+              }
+              mma_commit_pair(bar((kFp8 ? kBarOpEmpty : kBarRawEmpty) + slot));
+              if (is_k && i == n - 1) mma_commit_pair(bar(kBarQFree));
+            }
+            __syncwarp();
+          }
+          tiles += n;
+          ++piece;
+        }
+        // every MMA has finished before the pair frees its memory
+        if (elect_one()) {
+          mma_commit_pair(bar(kBarDrain));
+          mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
+        }
+        __syncwarp();
+      }
+    } else if (warp >= kSoftmaxWarps) {
+      // ======================= loaders ================================================
+      // Q of an item, and K and V tiles on their way from TMA to the MMAs: e4m3 codes
+      // become f16 (exactly), V rows past the last key that a row sees become zeros (0
+      // times what a slot behind the sequence's last token holds would reach O).
+      const int lw = warp - kSoftmaxWarps;
+      const float kd = p.k_descale ? *p.k_descale : 1.f;
+      const bool neg = p.scale_log2 * kd < 0.f;
+      int piece = 0;
+      while (next_piece(p, t0, t1, w, pc)) {
+        const int n = pc.i1 - pc.i0;
+        if (n == 0) continue;
+        if (piece > 0 && !wait_for(kBarQFree, piece - 1, 32)) break;
+        // Q: rows lw, lw + 4, .. of this CTA's 128, eight at a time
+#pragma unroll 1
+        for (int r0 = lw; r0 < 128; r0 += 32) {
+          uint4 raw[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int64_t row = (int64_t)pc.m * kChunkRows + rank * 128 + r0 + 4 * k;
+            raw[k] = make_uint4(0, 0, 0, 0);
+            if (row < (int64_t)pc.s.L * p.group) {
+              const int t = (int)row / p.group, g = (int)row - t * p.group;
+              raw[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(pc.s.q0 + t) * p.q_s0 +
+                                                       (int64_t)(pc.h * p.group + g) * p.q_s1 + 8 * lane);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = r0 + 4 * k;
+            uint4 v = raw[k];
+            if constexpr (kFp8) {
+              // f16 of q times a power of two that brings the row's largest into [2^14,
+              // 2^15): exact for values down to 2^-31 of it
+              uint32_t x[4] = {v.x, v.y, v.z, v.w};
+              float mx = 0.f;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xFFFF0000u))));
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              int e = 0;
+              if (mx > 0.f && mx < INFINITY) {
+                e = 14 - ((int)(__float_as_uint(mx) >> 23) - 127);
+                e = e > 120 ? 120 : e < -120 ? -120 : e;
+              }
+              const float up = __uint_as_float((uint32_t)(e + 127) << 23) * (neg ? -1.f : 1.f);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                x[j] = pack_f16x2(__uint_as_float(x[j] << 16) * up, __uint_as_float(x[j] & 0xFFFF0000u) * up);
+              v = make_uint4(x[0], x[1], x[2], x[3]);
+              if (lane == 0) row_factor[(piece & 1) * 128 + r] = __uint_as_float((uint32_t)(127 - e) << 23);
+            } else if (neg) {
+              v = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
+            }
+            *reinterpret_cast<uint4*>(sm + C::kOffQ + (lane >> 3) * (128 * 128) + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = v;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead(kBarQFull));
+        ++piece;
+        if (!kFp8 && lw > 0) continue;  // one warp hands the tiles on
+        for (int off = 0; off < 2 * n && ok; ++off, ++seq) {
+          const bool is_k = off == 0 || (off != 2 * n - 1 && (off & 1));
+          const int i = off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1;
+          const int rs = seq % C::kRawSlots, os = seq % C::kOpSlots;
+          if (!wait_for(kBarRawFull + rs, seq / C::kRawSlots, 64)) break;
+          // V rows from this one on are seen by no row
+          const int valid = is_k ? kKeys : pc.x.khi - tile_of(pc.x, pc.i0 + i) * kKeys;
+          if constexpr (kFp8) {
+            if (seq >= C::kOpSlots && !wait_for(kBarOpEmpty + os, seq / C::kOpSlots - 1, 128)) break;
+            const unsigned char* raw = sm + C::kOffRaw + rs * C::kRawBytes;
+            unsigned char* op = sm + C::kOffOp + os * C::kOpBytes;
+            const int u = lane & 7;
+            // 16 codes a thread and step: unit u of row-chunk rc (K: 2 chunks of 64 rows, V: 128 rows)
+            uint4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int rc = k * 16 + lw * 4 + (lane >> 3);
+              x[k] = *reinterpret_cast<const uint4*>(raw + rc * 128 + ((u ^ (rc & 7)) << 4));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int rc = k * 16 + lw * 4 + (lane >> 3);
+              const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+              uint32_t h[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+                h[j] = (uint32_t)v.x | ((uint32_t)v.y << 16);
+              }
+              const int row = is_k ? rc & 63 : rc;
+              const int region = is_k ? 2 * (rc >> 6) + (u >> 2) : u >> 2;
+              const bool zero = !is_k && rc >= valid;
+              const uint4 lo = zero ? make_uint4(0, 0, 0, 0) : make_uint4(h[0], h[1], h[2], h[3]);
+              const uint4 hi = zero ? make_uint4(0, 0, 0, 0) : make_uint4(h[4], h[5], h[6], h[7]);
+              unsigned char* dst = op + region * (is_k ? 64 * 128 : 128 * 128) + row * 128;
+              // the lanes of the upper region write their second unit first: a row's
+              // eight lanes then reach eight different units
+              const int first = u >> 2;
+              *reinterpret_cast<uint4*>(dst + (((2 * (u & 3) + first) ^ (row & 7)) << 4)) = first ? hi : lo;
+              *reinterpret_cast<uint4*>(dst + (((2 * (u & 3) + (first ^ 1)) ^ (row & 7)) << 4)) = first ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(kBarRawEmpty + rs));
+              mbar_arrive_cluster(lead(kBarOpFull + os));
+            }
+          } else {
+            if (valid < kKeys) {
+              unsigned char* op = sm + C::kOffOp + os * C::kOpBytes;
+              const int z0 = valid < 0 ? 0 : valid;
+              for (int k = z0 * 16 + lane; k < kKeys * 16; k += 32)
+                *reinterpret_cast<uint4*>(op + (k & 15) / 8 * (128 * 128) + (k >> 4) * 128 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_cluster(lead(kBarOpFull + os));
+          }
+        }
+        if (!ok) break;
+      }
+    } else {
+      // ======================= softmax / epilogue =====================================
+      const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+      const int r = 32 * warp + lane;  // this CTA's row
+      const float kd = p.k_descale ? *p.k_descale : 1.f;
+      const float vd = p.v_descale ? *p.v_descale : 1.f;
+      const float cscale = fmaxf(fabsf(p.scale_log2 * kd), 1e-30f);  // the sign is Q's
+      constexpr float kShift = kFp8 ? 7.f : 0.f;
+      int tiles = 0, piece = 0;
+      while (ok && next_piece(p, t0, t1, w, pc)) {
+        const int n = pc.i1 - pc.i0;
+        const int64_t row = (int64_t)pc.m * kChunkRows + rank * 128 + r;
+        const int64_t rows = (int64_t)pc.s.L * p.group;
+        const bool row_ok = row < rows;
+        const bool idle = (int64_t)pc.m * kChunkRows + rank * 128 + 32 * warp >= rows;  // no row of the warp's
+        const int t = row_ok ? (int)row / p.group : 0, g = row_ok ? (int)row - t * p.group : 0;
+        // keys that this row sees: up to vis_end, from vis_lo on or below first_tokens
+        const int vis_end = row_ok ? pc.s.S - pc.s.L + t : -1;
+        const int64_t vis_lo = p.window_left >= 0 ? (int64_t)vis_end - p.window_left : 0;
+        // tiles with keys past end_min, or before lo_max, are masked
+        const int end_min = pc.s.S - pc.s.L + (int)((int64_t)pc.m * kChunkRows / p.group);
+        const int64_t lo_max = p.window_left >= 0 ? (int64_t)pc.x.khi - 1 - p.window_left : 0;
+        float m_ref = -INFINITY, l = 0.f, rs = cscale;
+        for (int i = 0; i < n && ok; ++i) {
+          const int cur = tiles + i, b = cur & 1;
+          if (kScl && !wait_for(kBarScales + cur % kScaleTiles, cur / kScaleTiles, 512)) break;
+          if (!wait_for(kBarSFull + b, cur >> 1, 256)) break;
+          // (S was free, so it is; the wait keeps the barrier within a phase of the
+          // one that the rescale and the epilogue wait for)
+          if (cur > 1 && !wait_for(kBarPvDone + b, (cur - 2) >> 1, 1024)) break;
+          tc_fence_after();
+          if (!idle) {
+            if (kFp8 && i == 0) rs = fmaxf(cscale * row_factor[(piece & 1) * 128 + r], 1.2e-38f);
+            float x[kKeys];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(tmem + lane_base + kColS + b * kKeys + 32 * q, v);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[32 * q + k] = __uint_as_float(v[k]);
+            }
+            tmem_wait_ld();
+            float xs = rs;
+            if (p.softcap_log2 > 0.f && !kScl) {
+              // c tanh(s / c) = c (1 - 2 / (e^(2 s / c) + 1)), kept without the factor c
+              const float f = rs * (2.f * kLog2e) / p.softcap_log2;
+#pragma unroll
+              for (int k = 0; k < kKeys; ++k) x[k] = 1.f - __fdividef(2.f, ex2(x[k] * f) + 1.f);
+              xs = p.softcap_log2;
+            }
+            const int key0 = tile_of(pc.x, pc.i0 + i) * kKeys;
+            float xs8[8], lv8[8];
+            if constexpr (kScl) {
+              const float4* sc = reinterpret_cast<const float4*>(page_scale + (cur % kScaleTiles) * 8);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float4 v = sc[q];
+                xs8[2 * q] = rs * v.x;
+                lv8[2 * q] = v.y;
+                xs8[2 * q + 1] = rs * v.z;
+                lv8[2 * q + 1] = v.w;
+              }
+              if (p.softcap_log2 > 0.f) {
+#pragma unroll
+                for (int k = 0; k < kKeys; ++k)
+                  x[k] = 1.f - __fdividef(2.f, ex2(x[k] * (xs8[k / 16] * (2.f * kLog2e) / p.softcap_log2)) + 1.f);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) xs8[q] = p.softcap_log2;
+              }
+#pragma unroll
+              for (int q = 0; q < 8; ++q) xs8[q] = fmaxf(xs8[q], 1.2e-38f);  // a masked key's -inf stays that
+            }
+            if (key0 + kKeys - 1 > end_min) {
+#pragma unroll
+              for (int k = 0; k < kKeys; ++k)
+                if (key0 + k > vis_end) x[k] = -INFINITY;
+            }
+            if (key0 < lo_max) {
+#pragma unroll
+              for (int k = 0; k < kKeys; ++k)
+                if (key0 + k < vis_lo && key0 + k >= p.first_tokens) x[k] = -INFINITY;
+            }
+            float top = -INFINITY;
+            if constexpr (kScl) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                float u = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) u = fmax3(u, x[16 * q + k], x[16 * q + k + 1]);
+                top = fmaxf(top, fmaf(u, xs8[q], lv8[q]));
+              }
+            } else {
+              float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int k = 0; k < kKeys; k += 2) u[(k >> 1) & 3] = fmax3(u[(k >> 1) & 3], x[k], x[k + 1]);
+              top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * xs;
+            }
+            const bool need = top > m_ref + kMove || (m_ref == -INFINITY && top > -INFINITY);
+            const float m_new = need ? top : m_ref;
+            const float alpha = need && m_ref != -INFINITY ? ex2(m_ref - m_new) : 1.f;
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+              // O holds earlier tiles (of this piece: m_ref is not -inf)
+              if (!wait_for(kBarPvDone + (b ^ 1), (cur - 1) >> 1, 2048)) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int q = 0; q < kHeadDim / 32; ++q) {
+                uint32_t o[32];
+                const uint32_t ta = tmem + lane_base + kColO + 32 * q;
+                tmem_ld_32x32b_x32(ta, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st_32x32b_x32(ta, o);
+              }
+              l *= alpha;
+            }
+            m_ref = m_new;
+            // (a row without a visible key yet: P = 0)
+            const float ref = m_ref == -INFINITY ? INFINITY : m_ref - kShift;
+            uint64_t ls[2] = {0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t pw[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const int j = 32 * q + 2 * k;
+                const float f = kScl ? xs8[j / 16] : xs, off = kScl ? lv8[j / 16] - ref : -ref;
+                float a, d;
+                unpack2(fma2(pack2(x[j], x[j + 1]), pack2(f, f), pack2(off, off)), a, d);
+                a = ex2(a);
+                d = ex2(d);
+                ls[k & 1] = add2(ls[k & 1], pack2(a, d));
+                pw[k] = kFp8 ? pack_f16x2(a, d) : pack_b16x2(a, d);
+                if (kScl && k % 8 == 7) {  // a page's end: its weights without the V scale
+                  float s0, s1, s2, s3;
+                  unpack2(ls[0], s0, s1);
+                  unpack2(ls[1], s2, s3);
+                  l = fmaf((s0 + s1) + (s2 + s3), ex2(-lv8[j / 16]), l);
+                  ls[0] = ls[1] = 0;
+                }
+              }
+              tmem_st_32x32b_x16(tmem + lane_base + kColS + b * kKeys + 16 * q, pw);
+            }
+            if (!kScl) {
+              float s0, s1, s2, s3;
+              unpack2(ls[0], s0, s1);
+              unpack2(ls[1], s2, s3);
+              l += (s0 + s1) + (s2 + s3);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead(kBarPFull + b));
+        }
+        if (!ok) break;
+        // -- epilogue
+        tiles += n;
+        if (n > 0) {
+          if (!wait_for(kBarPvDone + ((tiles - 1) & 1), (tiles - 1) >> 1, 4096)) break;
+          tc_fence_after();
+        }
+        if (!idle) {
+          if (p.sinks && pc.direct && row_ok && m_ref != -INFINITY)
+            l += ex2(p.sinks[pc.h * p.group + g] * kLog2e - (m_ref - kShift));
+          const float inv = l > 0.f || l != l ? vd / l : 0.f;
+          const int64_t slot = 2 * (int64_t)c + (pc.i0 == 0 ? 1 : 0);
+          const int pr = rank * 128 + r;
+          uint16_t* dst = p.out + (int64_t)(pc.s.q0 + t) * p.o_s0 + (int64_t)(pc.h * p.group + g) * p.o_s1;
+          float* acc = p.ws_acc + (slot * kChunkRows + pr) * kHeadDim;
+          const bool nothing = m_ref == -INFINITY && l == l;  // (all of them NaN: NaN)
+#pragma unroll 1
+          for (int q = 0; q < kHeadDim / 32; ++q) {
+            uint32_t o[32];
+            if (n > 0) {
+              tmem_ld_32x32b_x32(tmem + lane_base + kColO + 32 * q, o);
+              tmem_wait_ld();
+            }
+            if (!row_ok) continue;
+            if (pc.direct) {
+              uint32_t v[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                v[k] = nothing ? 0u : pack_b16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+              if (p.out_v8) {
+                st_global_v8(dst + 32 * q, v);
+                st_global_v8(dst + 32 * q + 16, v + 8);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  reinterpret_cast<uint4*>(dst + 32 * q)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) st_global_v8(acc + 32 * q + 8 * k, o + 8 * k);
+            }
+          }
+          if (!pc.direct && row_ok)
+            *reinterpret_cast<float2*>(p.ws_ml + (slot * kChunkRows + pr) * 2) =
+                make_float2(nothing ? -INFINITY : m_ref == -INFINITY ? 0.f : m_ref - kShift, l);
+        }
+        if (n > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead(kBarOFree));
+          ++piece;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // (the odd CTA's copy of the last commit: no arrival is under way when it ends)
+  if (t0 < t1 && rank == 1 && tid == 0) mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
+  __syncwarp();
+  // both CTAs are done with each other's barriers and tensor memory
+  cluster_arrive();
+  __syncwarp();
+  cluster_wait();
+  if (warp == kWarpMma) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// ---- the merge -------------------------------------------------------------------------
+//
+// CTA x takes the item that the share of pair x + 1 starts in, if it starts inside it
+// and pair x holds the item's first tile: sums the pairs' partials in their order.
+constexpr int kMergeThreads = 256, kMergeRows = kMergeThreads / (kHeadDim / 4);
+
+__global__ void __launch_bounds__(kMergeThreads) va_chunk_merge_kernel(const ChunkParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int c = blockIdx.x + 1;
+  const int used = p.ws_start[0].used;
+  if (c >= used) return;
+  const ChunkStart st = p.ws_start[c];
+  const int64_t unit = (int64_t)kKeys * p.group;
+  const int64_t begin = share_begin(st.total, c, used);
+  if (st.off >= begin || share_begin(st.total, c - 1, used) > st.off) return;
+  const Seq s = chunk_seq(p, st.b);
+  const Span x = item_span(p, s, st.m);
+  if (ceil_units(begin - st.off, unit) >= x.n) return;  // pair c - 1 held it all
+  const int r = blockIdx.y * kMergeRows + threadIdx.x / (kHeadDim / 4), col = threadIdx.x % (kHeadDim / 4);
+  const int64_t row = (int64_t)st.m * kChunkRows + r;
+  if (row >= (int64_t)s.L * p.group) return;
+  float M = -INFINITY, den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = c - 1; k < used; ++k) {
+    int64_t slot = 2 * (int64_t)k;
+    if (k == c - 1) {
+      ++slot;
+    } else {
+      const int64_t i0 = ceil_units(share_begin(st.total, k, used) - st.off, unit);
+      const int64_t i1 = ceil_units(share_begin(st.total, k + 1, used) - st.off, unit);
+      if (i0 >= x.n) break;
+      if (i0 >= i1) continue;
+    }
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + (slot * kChunkRows + r) * 2));
+    const float4 a = __ldcg(reinterpret_cast<const float4*>(p.ws_acc + (slot * kChunkRows + r) * kHeadDim) + col);
+    if (ml.x == -INFINITY) continue;
+    const float mc = fmaxf(M, ml.x);
+    const float w0 = M == -INFINITY ? 0.f : exp2f(M - mc), w1 = exp2f(ml.x - mc);
+    den = den * w0 + ml.y * w1;
+    acc.x = acc.x * w0 + a.x * w1;
+    acc.y = acc.y * w0 + a.y * w1;
+    acc.z = acc.z * w0 + a.z * w1;
+    acc.w = acc.w * w0 + a.w * w1;
+    M = mc;
+  }
+  const int t = (int)row / p.group, g = (int)row - t * p.group;
+  if (p.sinks && M != -INFINITY) den += exp2f(p.sinks[st.h * p.group + g] * kLog2e - M);
+  const float vd = p.v_descale ? *p.v_descale : 1.f;
+  const float inv = M != -INFINITY ? vd / den : 0.f;
+  uint16_t* dst = p.out + (int64_t)(s.q0 + t) * p.o_s0 + (int64_t)(st.h * p.group + g) * p.o_s1 + 4 * col;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_b16x2(acc.x * inv, acc.y * inv), pack_b16x2(acc.z * inv, acc.w * inv));
+}
+
+template <int KIND>
+cudaError_t prepare_one(int32_t* max_pairs) {
+  cudaError_t e = cudaFuncSetAttribute(va_chunk_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<KIND>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<KIND>::kSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, va_chunk_kernel<KIND>, &cfg);
+  if (n < *max_pairs) *max_pairs = n;
+  return e;
+}
+
+}  // namespace
+
+cudaError_t prepare_chunk(int32_t* max_pairs) {
+  *max_pairs = 1 << 20;
+  cudaError_t e = prepare_one<kBf16>(max_pairs);
+  if (e == cudaSuccess) e = prepare_one<kE4m3>(max_pairs);
+  if (e == cudaSuccess) e = prepare_one<kPageScaled>(max_pairs);
+  return e;
+}
+
+cudaError_t launch_chunk(const ChunkParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream) {
+  // programmatic dependents of the stream's previous kernel, as the verify kernels
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cfg.stream = stream;
+  cfg.gridDim = dim3(2 * p.pairs);
+  cfg.blockDim = dim3(kThreads);
+  cudaError_t e;
+  if (p.k_scales) {
+    cfg.dynamicSmemBytes = Cfg<kPageScaled>::kSmemBytes;
+    e = cudaLaunchKernelEx(&cfg, va_chunk_kernel<kPageScaled>, p, tm_k, tm_v);
+  } else if (p.kv_fp8) {
+    cfg.dynamicSmemBytes = Cfg<kE4m3>::kSmemBytes;
+    e = cudaLaunchKernelEx(&cfg, va_chunk_kernel<kE4m3>, p, tm_k, tm_v);
+  } else {
+    cfg.dynamicSmemBytes = Cfg<kBf16>::kSmemBytes;
+    e = cudaLaunchKernelEx(&cfg, va_chunk_kernel<kBf16>, p, tm_k, tm_v);
+  }
+  if (e != cudaSuccess || p.pairs < 2) return e;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(p.pairs - 1, kChunkRows / kMergeRows);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, va_chunk_merge_kernel, p);
+}
+
+}  // namespace va

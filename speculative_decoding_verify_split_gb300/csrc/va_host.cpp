@@ -8,6 +8,7 @@
 
 #include <cuda_runtime.h>
 
+#include "va_chunk.h"
 #include "va_host_impl.h"
 
 namespace va_host_impl {
@@ -259,7 +260,7 @@ static EncodeTiledFn encode_tiled() {
 // 4-D map over a cache [num_blocks, 16, Hkv, 256]: box = one page of one KV
 // head, 128 bytes of the head dim (16 tokens x 128 bytes), 128-byte swizzle,
 // so each box lands as two 1 KB swizzle atoms.
-static bool make_kv_map(CUtensorMap* m, const va_tensor* t, int64_t nb, int64_t hkv) {
+bool make_kv_map(CUtensorMap* m, const va_tensor* t, int64_t nb, int64_t hkv) {
   EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   const int64_t es_bytes = elem_size(t->dtype);
@@ -290,6 +291,7 @@ struct DeviceState {
   // clusters of 2^i CTAs that run at once (main kernel, latent main kernel)
   int32_t clusters[kMaxClusterLog2 + 1] = {};
   int32_t mla_clusters[kMaxClusterLog2 + 1] = {};
+  int32_t chunk_pairs = 0;  // CTA pairs of the chunk kernels that run at once
   void* ws = nullptr;
   size_t ws_bytes = 0;
   int32_t* status = nullptr;  // g_status on this device
@@ -312,8 +314,9 @@ static va_status device_state(DeviceState** out) {
     if (cudaDeviceGetAttribute(&st.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return VA_ERR_CUDA;
     if (prepare_main_tc() != cudaSuccess || prepare_mla_tc() != cudaSuccess ||
-        prepare_mla_bf16_tc() != cudaSuccess)
+        prepare_mla_bf16_tc() != cudaSuccess || prepare_chunk(&st.chunk_pairs) != cudaSuccess)
       return VA_ERR_CUDA;
+    if (st.chunk_pairs > st.sms / 2) st.chunk_pairs = st.sms / 2;
     main_tc_clusters(st.clusters);
     mla_tc_clusters(st.mla_clusters);
     void* word = nullptr;
@@ -650,6 +653,31 @@ static va_status refuse_capture(cudaStream_t stream) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return VA_ERR_CUDA;
   return cap == cudaStreamCaptureStatusNone ? VA_OK : VA_ERR_WORKSPACE;
+}
+
+va_status begin_call(LibraryCall* call) {
+  call->lk = std::unique_lock<std::mutex>(g_mu);
+  DeviceState* st = nullptr;
+  const va_status s = device_state(&st);
+  if (s != VA_OK) return s;
+  call->chunk_pairs = st->chunk_pairs;
+  call->status = st->status;
+  return VA_OK;
+}
+
+va_status take_workspace(LibraryCall* call, void** ws, size_t* ws_bytes, size_t need, cudaStream_t stream) {
+  if (*ws) {
+    call->lk.unlock();
+    return VA_OK;
+  }
+  va_status s = refuse_capture(stream);
+  DeviceState* st = nullptr;
+  if (s == VA_OK) s = device_state(&st);
+  if (s == VA_OK) s = library_workspace(st, need, stream);
+  if (s != VA_OK) return s;
+  *ws = st->ws;
+  *ws_bytes = st->ws_bytes;
+  return VA_OK;
 }
 
 va_status current_device_sms(int* sms) {

@@ -7,8 +7,6 @@
 #include "va_host_impl.h"
 
 namespace va_host_impl {
-namespace {
-
 using namespace va;
 
 // The metadata every append call takes: block table, prefix sums, lengths.
@@ -52,6 +50,8 @@ bool places_distinct(const va_tensor* t, int dims, int64_t width) {
 }
 
 bool rows_distinct(const va_tensor* t) { return places_distinct(t, t->ndim - 1, t->shape[t->ndim - 1]); }
+
+namespace {
 
 // The scales of a page-scaled cache that the call writes.
 va_status check_written_scales(const va_tensor* t, int64_t num_blocks, int64_t hkv) {

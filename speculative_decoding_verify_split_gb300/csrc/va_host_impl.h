@@ -1,6 +1,9 @@
 // Host helpers shared by the translation units that implement the C ABI.
 #pragma once
 
+#include <mutex>
+
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "verify_attn.h"
@@ -28,6 +31,16 @@ bool dims_ok(const va_tensor* t, int ndim);
 bool rows_16b(const va_tensor* t);
 va_status check_descale(const va_tensor* t);
 va_status check_page_scales(const va_tensor* t, int64_t num_blocks, int64_t hkv);
+
+// Whether the elements of a tensor that is written have places of their own:
+// runs of `width` elements over its first `dims` dimensions, whose strides are
+// nested in some order; and the same of its rows.
+bool places_distinct(const va_tensor* t, int dims, int64_t width);
+bool rows_distinct(const va_tensor* t);
+// Rows that are read or written in 16-byte pieces: present and aligned.
+va_status check_rows(const va_tensor* t);
+// The metadata of a batch: block table, prefix sums, lengths.
+va_status check_batch(const va_tensor* bt, const va_tensor* cu, const va_tensor* su);
 
 // Argument checks shared by every attention entry point (pure host code).
 va_status validate(const va_tensor* q, const va_tensor* k, const va_tensor* v,
@@ -70,6 +83,22 @@ va_status launch(const va_tensor* q, const va_tensor* k, const va_tensor* v, con
                  const Shapes& sh, const va_plan& plan, void* ws, size_t ws_bytes,
                  cudaEvent_t ev_mid, cudaStream_t stream, const va_options* opts = nullptr,
                  const PartialOut* part = nullptr, const PageScales* scales = nullptr);
+
+// A call on the current device: the library's state, locked until the call has
+// been launched where it uses the library's workspace.
+struct LibraryCall {
+  std::unique_lock<std::mutex> lk;
+  int32_t chunk_pairs = 0;
+  int32_t* status = nullptr;  // the status word of calls with VA_LIBRARY_STATUS
+};
+va_status begin_call(LibraryCall* call);
+// The workspace of a call: the caller's (the lock is given back), or the
+// library's, grown as needed and refused during stream capture.
+va_status take_workspace(LibraryCall* call, void** ws, size_t* ws_bytes, size_t need, cudaStream_t stream);
+
+// TMA map over a GQA cache: boxes of a page's 16 tokens x 128 bytes of one head,
+// 128-byte swizzle.
+bool make_kv_map(CUtensorMap* m, const va_tensor* t, int64_t nb, int64_t hkv);
 
 // SM count of the current device (initialises the per-device state once).
 va_status current_device_sms(int* sms);
