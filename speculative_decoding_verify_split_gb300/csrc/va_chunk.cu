@@ -162,9 +162,9 @@ __device__ __forceinline__ int tile_of(const Span& x, int i) { return i < x.nf ?
 
 enum Kind { kBf16 = 0, kE4m3 = 1, kPageScaled = 2 };
 
-constexpr int kSoftmaxWarps = 4, kLoadWarps = 4;
+constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;
 constexpr int kThreads = 32 * (kSoftmaxWarps + kLoadWarps + 2);
-constexpr int kWarpProducer = 8, kWarpMma = 9;
+constexpr int kWarpProducer = kSoftmaxWarps + kLoadWarps, kWarpMma = kWarpProducer + 1;
 
 template <int KIND>
 struct Cfg {
@@ -203,11 +203,12 @@ enum : int {
   kNumBars = kBarScales + kScaleTiles
 };
 constexpr int kOffTmem = 8 * kNumBars, kOffAbort = kOffTmem + 4;
-constexpr int kOffScratch = (kOffAbort + 4 + 15) / 16 * 16;     // 32 x 8 bytes
-constexpr int kOffStart = kOffScratch + 256;                     // ChunkStart
+constexpr int kOffStart = (kOffAbort + 4 + 15) / 16 * 16;       // ChunkStart
 constexpr int kOffRow = (kOffStart + 48 + 15) / 16 * 16;         // [2][128] floats
-constexpr int kOffScale = kOffRow + 1024;                        // [kScaleTiles][8] (K scale, log2 V scale)
-static_assert(kOffScale + kScaleTiles * 64 <= 3072, "misc area");
+constexpr int kOffXch = kOffRow + 1024;                          // [2][128] floats; before: 32 x 8 bytes of the scan
+constexpr int kOffScale = kOffXch + 1024;                        // [kScaleTiles][8] (K scale, log2 V scale)
+constexpr int kMiscBytes = kOffScale + kScaleTiles * 64;
+static_assert(kMiscBytes <= 3072, "misc area");
 
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
@@ -237,9 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_addr(sm);
   const uint32_t mbase = sbase + C::kOffMisc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + kOffAbort);
-  long long* scratch = reinterpret_cast<long long*>(misc + kOffScratch);
+  long long* scratch = reinterpret_cast<long long*>(misc + kOffXch);
   ChunkStart* start = reinterpret_cast<ChunkStart*>(misc + kOffStart);
   float* row_factor = reinterpret_cast<float*>(misc + kOffRow);
+  float* xch = reinterpret_cast<float*>(misc + kOffXch);
   float2* page_scale = reinterpret_cast<float2*>(misc + kOffScale);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -367,12 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // Waits of a whole warp: warp-uniform, false once anything has given up.
   bool ok = true;
-  auto wait_for = [&](int b, int use, int code, bool cluster = false) {
+  auto wait_for = [&](int b, int use, int code) {
     if (!ok) return false;
-    const uint32_t par = (uint32_t)use & 1u;
-    const bool got = cluster ? mbar_wait_cluster(bar(b), par, abort_flag, p.wait_limit_ns)
-                             : mbar_wait(bar(b), par, abort_flag, p.wait_limit_ns);
-    if (!__all_sync(0xffffffffu, got)) {
+    if (!__all_sync(0xffffffffu, mbar_wait(bar(b), (uint32_t)use & 1u, abort_flag, p.wait_limit_ns))) {
       if (lane == 0) give_up(code);
       ok = false;
     }
@@ -479,16 +478,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && next_piece(p, t0, t1, w, pc)) {
           const int n = pc.i1 - pc.i0;
           if (n == 0) continue;
-          if (!wait_for(kBarQFull, piece, 2, true)) break;
+          if (!wait_for(kBarQFull, piece, 2)) break;
           for (int off = 0; off < 2 * n && ok; ++off, ++seq) {
             const bool is_k = off == 0 || (off != 2 * n - 1 && (off & 1));
             const int i = off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1;
             const int slot = seq % C::kOpSlots, use = seq / C::kOpSlots;
             const int b = (tiles + i) & 1;
-            if (!wait_for(kBarOpFull + slot, use, 4, true)) break;
+            if (!wait_for(kBarOpFull + slot, use, 4)) break;
             if (!is_k) {
-              if (!wait_for(kBarPFull + b, (tiles + i) >> 1, 8, true)) break;
-              if (i == 0 && piece > 0 && !wait_for(kBarOFree, piece - 1, 16, true)) break;
+              if (!wait_for(kBarPFull + b, (tiles + i) >> 1, 8)) break;
+              if (i == 0 && piece > 0 && !wait_for(kBarOFree, piece - 1, 16)) break;
             }
             tc_fence_after();
             const uint32_t src = sbase + C::kOffOp + slot * C::kOpBytes;
@@ -649,180 +648,200 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ======================= softmax / epilogue =====================================
-      const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
-      const int r = 32 * warp + lane;  // this CTA's row
+      // Two warps share a lane quadrant: warp half kh takes keys [64 kh, +64) of a tile
+      // and columns [128 kh, +128) of O, a thread one row. They vote on whether some row's
+      // reference moves, around the quadrant's named barrier; the maxima are exchanged
+      // only then. After a failure a warp walks on without waits and work, so that the
+      // two still meet at every barrier.
+      const int q = warp & 3, kh = warp >> 2;
+      const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+      const int r = 32 * q + lane;  // this CTA's row
       const float kd = p.k_descale ? *p.k_descale : 1.f;
       const float vd = p.v_descale ? *p.v_descale : 1.f;
       const float cscale = fmaxf(fabsf(p.scale_log2 * kd), 1e-30f);  // the sign is Q's
       constexpr float kShift = kFp8 ? 7.f : 0.f;
+      constexpr int kMine = kKeys / 2, kPg = kMine / kPageSize;
       int tiles = 0, piece = 0;
-      while (ok && next_piece(p, t0, t1, w, pc)) {
+      // the row's value of both halves
+      auto exchange = [&](float v, bool is_max) {
+        xch[kh * 128 + r] = v;
+        named_bar(1 + q, 64);
+        const float o = xch[(kh ^ 1) * 128 + r];
+        named_bar(1 + q, 64);
+        return is_max ? fmaxf(v, o) : v + o;
+      };
+      while (next_piece(p, t0, t1, w, pc)) {
         const int n = pc.i1 - pc.i0;
         const int64_t row = (int64_t)pc.m * kChunkRows + rank * 128 + r;
         const int64_t rows = (int64_t)pc.s.L * p.group;
         const bool row_ok = row < rows;
-        const bool idle = (int64_t)pc.m * kChunkRows + rank * 128 + 32 * warp >= rows;  // no row of the warp's
+        const bool idle = (int64_t)pc.m * kChunkRows + rank * 128 + 32 * q >= rows;  // no row of the quadrant's
         const int t = row_ok ? (int)row / p.group : 0, g = row_ok ? (int)row - t * p.group : 0;
         // keys that this row sees: up to vis_end, from vis_lo on or below first_tokens
         const int vis_end = row_ok ? pc.s.S - pc.s.L + t : -1;
-        const int64_t vis_lo = p.window_left >= 0 ? (int64_t)vis_end - p.window_left : 0;
+        const int64_t vis_lo64 = p.window_left >= 0 ? (int64_t)vis_end - p.window_left : 0;
+        const int vis_lo = vis_lo64 < 0 ? 0 : (int)vis_lo64;
         // tiles with keys past end_min, or before lo_max, are masked
         const int end_min = pc.s.S - pc.s.L + (int)((int64_t)pc.m * kChunkRows / p.group);
         const int64_t lo_max = p.window_left >= 0 ? (int64_t)pc.x.khi - 1 - p.window_left : 0;
         float m_ref = -INFINITY, l = 0.f, rs = cscale;
-        for (int i = 0; i < n && ok; ++i) {
+        for (int i = 0; i < n; ++i) {
           const int cur = tiles + i, b = cur & 1;
-          if (kScl && !wait_for(kBarScales + cur % kScaleTiles, cur / kScaleTiles, 512)) break;
-          if (!wait_for(kBarSFull + b, cur >> 1, 256)) break;
-          // (S was free, so it is; the wait keeps the barrier within a phase of the
-          // one that the rescale and the epilogue wait for)
-          if (cur > 1 && !wait_for(kBarPvDone + b, (cur - 2) >> 1, 1024)) break;
+          if (kScl) wait_for(kBarScales + cur % kScaleTiles, cur / kScaleTiles, 512);
+          wait_for(kBarSFull + b, cur >> 1, 256);
           tc_fence_after();
           if (!idle) {
-            if (kFp8 && i == 0) rs = fmaxf(cscale * row_factor[(piece & 1) * 128 + r], 1.2e-38f);
-            float x[kKeys];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t v[32];
-              tmem_ld_32x32b_x32(tmem + lane_base + kColS + b * kKeys + 32 * q, v);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) x[32 * q + k] = __uint_as_float(v[k]);
-            }
-            tmem_wait_ld();
-            float xs = rs;
-            if (p.softcap_log2 > 0.f && !kScl) {
-              // c tanh(s / c) = c (1 - 2 / (e^(2 s / c) + 1)), kept without the factor c
-              const float f = rs * (2.f * kLog2e) / p.softcap_log2;
-#pragma unroll
-              for (int k = 0; k < kKeys; ++k) x[k] = 1.f - __fdividef(2.f, ex2(x[k] * f) + 1.f);
-              xs = p.softcap_log2;
-            }
-            const int key0 = tile_of(pc.x, pc.i0 + i) * kKeys;
-            float xs8[8], lv8[8];
-            if constexpr (kScl) {
-              const float4* sc = reinterpret_cast<const float4*>(page_scale + (cur % kScaleTiles) * 8);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float4 v = sc[q];
-                xs8[2 * q] = rs * v.x;
-                lv8[2 * q] = v.y;
-                xs8[2 * q + 1] = rs * v.z;
-                lv8[2 * q + 1] = v.w;
-              }
-              if (p.softcap_log2 > 0.f) {
-#pragma unroll
-                for (int k = 0; k < kKeys; ++k)
-                  x[k] = 1.f - __fdividef(2.f, ex2(x[k] * (xs8[k / 16] * (2.f * kLog2e) / p.softcap_log2)) + 1.f);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) xs8[q] = p.softcap_log2;
-              }
-#pragma unroll
-              for (int q = 0; q < 8; ++q) xs8[q] = fmaxf(xs8[q], 1.2e-38f);  // a masked key's -inf stays that
-            }
-            if (key0 + kKeys - 1 > end_min) {
-#pragma unroll
-              for (int k = 0; k < kKeys; ++k)
-                if (key0 + k > vis_end) x[k] = -INFINITY;
-            }
-            if (key0 < lo_max) {
-#pragma unroll
-              for (int k = 0; k < kKeys; ++k)
-                if (key0 + k < vis_lo && key0 + k >= p.first_tokens) x[k] = -INFINITY;
-            }
+            float x[kMine];
+            float xs = rs, xs4[kPg], lv4[kPg];
             float top = -INFINITY;
-            if constexpr (kScl) {
+            if (ok) {
+              if (kFp8 && i == 0) xs = rs = fmaxf(cscale * row_factor[(piece & 1) * 128 + r], 1.2e-38f);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                float u = -INFINITY;
+              for (int j = 0; j < kMine / 32; ++j) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem + lane_base + kColS + b * kKeys + kMine * kh + 32 * j, v);
 #pragma unroll
-                for (int k = 0; k < 16; k += 2) u = fmax3(u, x[16 * q + k], x[16 * q + k + 1]);
-                top = fmaxf(top, fmaf(u, xs8[q], lv8[q]));
+                for (int k = 0; k < 32; ++k) x[32 * j + k] = __uint_as_float(v[k]);
               }
-            } else {
-              float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              tmem_wait_ld();
+              if constexpr (kScl) {
+                const float4* sc = reinterpret_cast<const float4*>(page_scale + (cur % kScaleTiles) * 8 + kPg * kh);
 #pragma unroll
-              for (int k = 0; k < kKeys; k += 2) u[(k >> 1) & 3] = fmax3(u[(k >> 1) & 3], x[k], x[k + 1]);
-              top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * xs;
-            }
-            const bool need = top > m_ref + kMove || (m_ref == -INFINITY && top > -INFINITY);
-            const float m_new = need ? top : m_ref;
-            const float alpha = need && m_ref != -INFINITY ? ex2(m_ref - m_new) : 1.f;
-            if (__any_sync(0xffffffffu, alpha != 1.f)) {
-              // O holds earlier tiles (of this piece: m_ref is not -inf)
-              if (!wait_for(kBarPvDone + (b ^ 1), (cur - 1) >> 1, 2048)) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int q = 0; q < kHeadDim / 32; ++q) {
-                uint32_t o[32];
-                const uint32_t ta = tmem + lane_base + kColO + 32 * q;
-                tmem_ld_32x32b_x32(ta, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                tmem_st_32x32b_x32(ta, o);
-              }
-              l *= alpha;
-            }
-            m_ref = m_new;
-            // (a row without a visible key yet: P = 0)
-            const float ref = m_ref == -INFINITY ? INFINITY : m_ref - kShift;
-            uint64_t ls[2] = {0, 0};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t pw[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const int j = 32 * q + 2 * k;
-                const float f = kScl ? xs8[j / 16] : xs, off = kScl ? lv8[j / 16] - ref : -ref;
-                float a, d;
-                unpack2(fma2(pack2(x[j], x[j + 1]), pack2(f, f), pack2(off, off)), a, d);
-                a = ex2(a);
-                d = ex2(d);
-                ls[k & 1] = add2(ls[k & 1], pack2(a, d));
-                pw[k] = kFp8 ? pack_f16x2(a, d) : pack_b16x2(a, d);
-                if (kScl && k % 8 == 7) {  // a page's end: its weights without the V scale
-                  float s0, s1, s2, s3;
-                  unpack2(ls[0], s0, s1);
-                  unpack2(ls[1], s2, s3);
-                  l = fmaf((s0 + s1) + (s2 + s3), ex2(-lv8[j / 16]), l);
-                  ls[0] = ls[1] = 0;
+                for (int j = 0; j < kPg / 2; ++j) {
+                  const float4 v = sc[j];
+                  xs4[2 * j] = rs * v.x;
+                  lv4[2 * j] = v.y;
+                  xs4[2 * j + 1] = rs * v.z;
+                  lv4[2 * j + 1] = v.w;
                 }
               }
-              tmem_st_32x32b_x16(tmem + lane_base + kColS + b * kKeys + 16 * q, pw);
+              if (p.softcap_log2 > 0.f) {
+                // c tanh(s / c) = c (1 - 2 / (e^(2 s / c) + 1)), kept without the factor c
+                const float f = (2.f * kLog2e) / p.softcap_log2;
+#pragma unroll
+                for (int k = 0; k < kMine; ++k)
+                  x[k] = 1.f - __fdividef(2.f, ex2(x[k] * (f * (kScl ? xs4[k / kPageSize] : rs))) + 1.f);
+                xs = p.softcap_log2;
+#pragma unroll
+                for (int j = 0; j < kPg; ++j) xs4[j] = xs;
+              }
+              if constexpr (kScl) {
+#pragma unroll
+                for (int j = 0; j < kPg; ++j) xs4[j] = fmaxf(xs4[j], 1.2e-38f);  // a masked key's -inf stays that
+              }
+              const int key0 = tile_of(pc.x, pc.i0 + i) * kKeys + kMine * kh;
+              if (key0 + kMine - 1 > end_min) {
+#pragma unroll
+                for (int k = 0; k < kMine; ++k)
+                  if (key0 + k > vis_end) x[k] = -INFINITY;
+              }
+              if (key0 < lo_max) {
+#pragma unroll
+                for (int k = 0; k < kMine; ++k)
+                  if (key0 + k < vis_lo && key0 + k >= p.first_tokens) x[k] = -INFINITY;
+              }
+              if constexpr (kScl) {
+#pragma unroll
+                for (int j = 0; j < kPg; ++j) {
+                  float u = -INFINITY;
+#pragma unroll
+                  for (int k = 0; k < kPageSize; k += 2) u = fmax3(u, x[kPageSize * j + k], x[kPageSize * j + k + 1]);
+                  top = fmaxf(top, fmaf(u, xs4[j], lv4[j]));
+                }
+              } else {
+                float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < kMine; k += 2) u[(k >> 1) & 3] = fmax3(u[(k >> 1) & 3], x[k], x[k + 1]);
+                top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * xs;
+              }
             }
-            if (!kScl) {
-              float s0, s1, s2, s3;
-              unpack2(ls[0], s0, s1);
-              unpack2(ls[1], s2, s3);
-              l += (s0 + s1) + (s2 + s3);
+            // (an item's first tile sets the references: no vote)
+            if (i == 0 || named_bar_or(1 + q, 64, top > m_ref + kMove)) {
+              top = exchange(top, true);
+              const float m_new = top > m_ref + kMove ? top : m_ref;
+              const float alpha = m_new != m_ref && m_ref != -INFINITY ? ex2(m_ref - m_new) : 1.f;
+              if (__any_sync(0xffffffffu, alpha != 1.f) && wait_for(kBarPvDone + (b ^ 1), (cur - 1) >> 1, 2048)) {
+                // O holds earlier tiles (of this piece: m_ref is not -inf)
+                tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < kHeadDim / 32; ++j) {
+                  uint32_t o[16];
+                  const uint32_t ta = tmem + lane_base + kColO + 128 * kh + 16 * j;
+                  tmem_ld_32x32b_x16(ta, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                  tmem_st_32x32b_x16(ta, o);
+                }
+                l *= alpha;
+              }
+              m_ref = m_new;
             }
-            tmem_wait_st();
+            if (ok) {
+              // (a row without a visible key yet: P = 0)
+              const float ref = m_ref == -INFINITY ? INFINITY : m_ref - kShift;
+              uint64_t ls[2] = {0, 0};
+#pragma unroll
+              for (int j = 0; j < kMine / 32; ++j) {
+                uint32_t pw[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const int y = 32 * j + 2 * k;
+                  const float f = kScl ? xs4[y / kPageSize] : xs, off = kScl ? lv4[y / kPageSize] - ref : -ref;
+                  float a, d;
+                  unpack2(fma2(pack2(x[y], x[y + 1]), pack2(f, f), pack2(off, off)), a, d);
+                  a = ex2(a);
+                  d = ex2(d);
+                  ls[k & 1] = add2(ls[k & 1], pack2(a, d));
+                  pw[k] = kFp8 ? pack_f16x2(a, d) : pack_b16x2(a, d);
+                  if (kScl && k % 8 == 7) {  // a page's end: its weights without the V scale
+                    float s0, s1, s2, s3;
+                    unpack2(ls[0], s0, s1);
+                    unpack2(ls[1], s2, s3);
+                    l = fmaf((s0 + s1) + (s2 + s3), ex2(-lv4[y / kPageSize]), l);
+                    ls[0] = ls[1] = 0;
+                  }
+                }
+                // over S: both warps have loaded their parts of it (the barriers above)
+                tmem_st_32x32b_x16(tmem + lane_base + kColS + b * kKeys + kMine / 2 * kh + 16 * j, pw);
+              }
+              if (!kScl) {
+                float s0, s1, s2, s3;
+                unpack2(ls[0], s0, s1);
+                unpack2(ls[1], s2, s3);
+                l += (s0 + s1) + (s2 + s3);
+              }
+              tmem_wait_st();
+            }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead(kBarPFull + b));
+          if (ok) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead(kBarPFull + b));
+          }
         }
-        if (!ok) break;
         // -- epilogue
         tiles += n;
+        if (!idle) l = exchange(l, false);
         if (n > 0) {
-          if (!wait_for(kBarPvDone + ((tiles - 1) & 1), (tiles - 1) >> 1, 4096)) break;
+          wait_for(kBarPvDone + ((tiles - 1) & 1), (tiles - 1) >> 1, 4096);
           tc_fence_after();
         }
+        if (!ok) continue;
         if (!idle) {
           if (p.sinks && pc.direct && row_ok && m_ref != -INFINITY)
             l += ex2(p.sinks[pc.h * p.group + g] * kLog2e - (m_ref - kShift));
           const float inv = l > 0.f || l != l ? vd / l : 0.f;
           const int64_t slot = 2 * (int64_t)c + (pc.i0 == 0 ? 1 : 0);
           const int pr = rank * 128 + r;
-          uint16_t* dst = p.out + (int64_t)(pc.s.q0 + t) * p.o_s0 + (int64_t)(pc.h * p.group + g) * p.o_s1;
-          float* acc = p.ws_acc + (slot * kChunkRows + pr) * kHeadDim;
+          uint16_t* dst = p.out + (int64_t)(pc.s.q0 + t) * p.o_s0 + (int64_t)(pc.h * p.group + g) * p.o_s1 + 128 * kh;
+          float* acc = p.ws_acc + (slot * kChunkRows + pr) * kHeadDim + 128 * kh;
           const bool nothing = m_ref == -INFINITY && l == l;  // (all of them NaN: NaN)
 #pragma unroll 1
-          for (int q = 0; q < kHeadDim / 32; ++q) {
+          for (int j = 0; j < kHeadDim / 64; ++j) {
             uint32_t o[32];
             if (n > 0) {
-              tmem_ld_32x32b_x32(tmem + lane_base + kColO + 32 * q, o);
+              tmem_ld_32x32b_x32(tmem + lane_base + kColO + 128 * kh + 32 * j, o);
               tmem_wait_ld();
             }
             if (!row_ok) continue;
@@ -832,19 +851,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 16; ++k)
                 v[k] = nothing ? 0u : pack_b16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
               if (p.out_v8) {
-                st_global_v8(dst + 32 * q, v);
-                st_global_v8(dst + 32 * q + 16, v + 8);
+                st_global_v8(dst + 32 * j, v);
+                st_global_v8(dst + 32 * j + 16, v + 8);
               } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  reinterpret_cast<uint4*>(dst + 32 * q)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                  reinterpret_cast<uint4*>(dst + 32 * j)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
               }
             } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) st_global_v8(acc + 32 * q + 8 * k, o + 8 * k);
+              for (int k = 0; k < 4; ++k) st_global_v8(acc + 32 * j + 8 * k, o + 8 * k);
             }
           }
-          if (!pc.direct && row_ok)
+          if (!pc.direct && row_ok && kh == 0)
             *reinterpret_cast<float2*>(p.ws_ml + (slot * kChunkRows + pr) * 2) =
                 make_float2(nothing ? -INFINITY : m_ref == -INFINITY ? 0.f : m_ref - kShift, l);
         }
