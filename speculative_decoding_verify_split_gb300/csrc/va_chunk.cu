@@ -118,12 +118,13 @@ __device__ __forceinline__ Walk start_walk(const ChunkParams& p, const ChunkStar
   return w;
 }
 
-// An item's part in a share: tiles [i0, i1) of its n.
+// An item's part in a share: tiles [i0, i0 + n) of the item's.
 struct Piece {
-  int b, h, m, i0, i1;
-  Seq s;
+  int n;                    // -1: no further piece
+  int h, m, i0;
+  int S, L, q0, b;
   Span x;
-  bool direct;  // the whole item: its rows are written to out
+  int direct;               // the whole item: its rows are written to out
 };
 
 __device__ __forceinline__ bool next_piece(const ChunkParams& p, int64_t t0, int64_t t1, Walk& w, Piece& pc) {
@@ -142,16 +143,20 @@ __device__ __forceinline__ bool next_piece(const ChunkParams& p, int64_t t0, int
     pc.b = w.b;
     pc.h = w.h;
     pc.m = w.m;
-    pc.s = w.s;
+    pc.S = w.s.S;
+    pc.L = w.s.L;
+    pc.q0 = w.s.q0;
     pc.x = item_span(p, w.s, w.m);
     const int64_t off = w.off;
     w.off += chunk_cost(p, w.s, w.m);
     ++w.m;
-    const int64_t i0 = ceil_units(t0 - off, unit), i1 = ceil_units(t1 - off, unit);
-    pc.i0 = (int)(i0 < pc.x.n ? i0 : pc.x.n);
-    pc.i1 = (int)(i1 < pc.x.n ? i1 : pc.x.n);
-    pc.direct = pc.i0 == 0 && pc.i1 == pc.x.n;
-    if (pc.i0 < pc.i1 || (pc.x.n == 0 && off >= t0)) return true;
+    int64_t i0 = ceil_units(t0 - off, unit), i1 = ceil_units(t1 - off, unit);
+    i0 = i0 < pc.x.n ? i0 : pc.x.n;
+    i1 = i1 < pc.x.n ? i1 : pc.x.n;
+    pc.i0 = (int)i0;
+    pc.n = (int)(i1 - i0);
+    pc.direct = i0 == 0 && i1 == pc.x.n;
+    if (pc.n > 0 || (pc.x.n == 0 && off >= t0)) return true;
   }
   return false;
 }
@@ -163,8 +168,9 @@ __device__ __forceinline__ int tile_of(const Span& x, int i) { return i < x.nf ?
 enum Kind { kBf16 = 0, kE4m3 = 1, kPageScaled = 2 };
 
 constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;
-constexpr int kThreads = 32 * (kSoftmaxWarps + kLoadWarps + 2);
-constexpr int kWarpProducer = kSoftmaxWarps + kLoadWarps, kWarpMma = kWarpProducer + 1;
+constexpr int kThreads = 32 * (kSoftmaxWarps + kLoadWarps + 3);
+constexpr int kWarpProducer = kSoftmaxWarps + kLoadWarps, kWarpMma = kWarpProducer + 1, kWarpPlan = kWarpMma + 1;
+constexpr int kPieces = 4;  // places of the queue of pieces
 
 template <int KIND>
 struct Cfg {
@@ -186,7 +192,10 @@ struct Cfg {
 };
 
 // misc area: barriers, scratch of the work scan, row factors, page scales
-constexpr int kMaxRaw = 5, kMaxOp = 5, kScaleTiles = 8;
+constexpr int kMaxRaw = 5, kMaxOp = 5;
+// Tiles whose page scales are kept: the producer, up to 7 of the rings' K and V tiles
+// ahead of the MMAs, writes tile i's once the softmax is through with tile i - 5.
+constexpr int kScaleTiles = 6;
 enum : int {
   kBarRawFull = 0,
   kBarRawEmpty = kBarRawFull + kMaxRaw,
@@ -200,15 +209,17 @@ enum : int {
   kBarOFree,
   kBarDrain,
   kBarScales,
-  kNumBars = kBarScales + kScaleTiles
+  kBarPieceFull = kBarScales + kScaleTiles,
+  kBarPieceEmpty = kBarPieceFull + kPieces,
+  kNumBars = kBarPieceEmpty + kPieces
 };
 constexpr int kOffTmem = 8 * kNumBars, kOffAbort = kOffTmem + 4;
-constexpr int kOffStart = (kOffAbort + 4 + 15) / 16 * 16;       // ChunkStart
-constexpr int kOffRow = (kOffStart + 48 + 15) / 16 * 16;         // [2][128] floats
+constexpr int kOffPieces = (kOffAbort + 4 + 15) / 16 * 16;      // [kPieces] Piece; before: ChunkStart
+constexpr int kOffRow = kOffPieces + kPieces * 64;               // [2][128] floats
 constexpr int kOffXch = kOffRow + 1024;                          // [2][128] floats; before: 32 x 8 bytes of the scan
 constexpr int kOffScale = kOffXch + 1024;                        // [kScaleTiles][8] (K scale, log2 V scale)
 constexpr int kMiscBytes = kOffScale + kScaleTiles * 64;
-static_assert(kMiscBytes <= 3072, "misc area");
+static_assert(kMiscBytes <= 3072 && sizeof(Piece) <= 64, "misc area");
 
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
@@ -226,7 +237,8 @@ __device__ __forceinline__ uint32_t pack_b16x2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int KIND>
+// VAR: with the code of the window and the soft cap.
+template <int KIND, bool VAR>
 __global__ void __launch_bounds__(kThreads, 1)
     va_chunk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<KIND>;
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t mbase = sbase + C::kOffMisc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + kOffAbort);
   long long* scratch = reinterpret_cast<long long*>(misc + kOffXch);
-  ChunkStart* start = reinterpret_cast<ChunkStart*>(misc + kOffStart);
+  ChunkStart* start = reinterpret_cast<ChunkStart*>(misc + kOffPieces);
   float* row_factor = reinterpret_cast<float*>(misc + kOffRow);
   float* xch = reinterpret_cast<float*>(misc + kOffXch);
   float2* page_scale = reinterpret_cast<float2*>(misc + kOffScale);
@@ -270,6 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(kBarOFree), 2 * kSoftmaxWarps);
     mbar_init(bar(kBarDrain), 1);
     for (int i = 0; i < kScaleTiles; ++i) mbar_init(bar(kBarScales + i), 1);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(bar(kBarPieceFull + i), 1);
+      mbar_init(bar(kBarPieceEmpty + i), kSoftmaxWarps + kLoadWarps + 1 + (rank == 0 ? 1 : 0));
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -379,10 +395,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (t0 < t1) {
-    Walk w = start_walk(p, *start);
-    Piece pc;
+    // The pieces of the share, walked by one warp for all roles. A role's warp takes the
+    // next one (`at` counts them) and gives it back when it is through with it.
+    volatile Piece* pieces = reinterpret_cast<volatile Piece*>(misc + kOffPieces);
+    int at = 0;
+    auto take = [&]() -> const volatile Piece* {
+      const volatile Piece* pc = pieces + at % kPieces;
+      return wait_for(kBarPieceFull + at % kPieces, at / kPieces, 8192) && pc->n >= 0 ? pc : nullptr;
+    };
+    auto give_back = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarPieceEmpty + at % kPieces));
+      ++at;
+    };
     int seq = 0;  // K and V tiles so far: a piece's K0, K1, V0, K2, V1, .., K(n-1), V(n-2), V(n-1)
-    if (warp == kWarpProducer) {
+    if (warp == kWarpPlan) {
+      Walk w = start_walk(p, *start);
+      __syncwarp();  // (the pieces take start's place)
+      Piece pc;
+      for (bool more = true; more && ok; ++at) {
+        more = next_piece(p, t0, t1, w, pc);
+        if (!more) pc.n = -1;
+        if (at >= kPieces && !wait_for(kBarPieceEmpty + at % kPieces, at / kPieces - 1, 16384)) break;
+        if (lane == 0) *reinterpret_cast<Piece*>(misc + kOffPieces + at % kPieces * sizeof(Piece)) = pc;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPieceFull + at % kPieces));
+      }
+    } else if (warp == kWarpProducer) {
       // ======================= TMA producer ==========================================
       // One 2 KB box (a page's 16 tokens x 128 bytes) a lane: this CTA's half of K's
       // keys, or of V's columns. Pages that no row of the item sees are not mapped
@@ -394,12 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kEl = kFp8 ? 128 : 64;          // elements of a chunk
       const bool k_on = lane < 4 * kDim, v_on = lane < 8 * kVCh;
       int tiles = 0;  // tiles so far (page scales)
-      while (ok && next_piece(p, t0, t1, w, pc)) {
-        const int n = pc.i1 - pc.i0;
-        const int* bt = p.block_table + (int64_t)pc.b * p.bt_s0;
+      while (const volatile Piece* pc_ = take()) {
+        const Span x{pc_->x.klo, pc_->x.khi, pc_->x.nf, pc_->x.w0, 0};
+        const int n = pc_->n, i0 = pc_->i0, h = pc_->h;
+        const int* bt = p.block_table + (int64_t)pc_->b * p.bt_s0;
+        give_back();
         auto page_id = [&](int page) {
           const int key = page * kPageSize;
-          const bool seen = key < pc.x.khi && (key + kPageSize > pc.x.klo || key < p.first_tokens);
+          const bool seen = key < x.khi && (key + kPageSize > x.klo || key < p.first_tokens);
           const int id = seen ? bt[(int64_t)page * p.bt_s1] : -1;
           return (unsigned)id < (unsigned)p.num_blocks ? id : p.num_blocks;
         };
@@ -411,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool is_k;
           int i;
           step(off, is_k, i);
-          return tile_of(pc.x, pc.i0 + i) * (kKeys / kPageSize) + (is_k ? k_page : v_page);
+          return tile_of(x, i0 + i) * (kKeys / kPageSize) + (is_k ? k_page : v_page);
         };
         auto fetch = [&](int off) {
           bool is_k;
@@ -423,11 +464,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float ks = 1.f, vs = 1.f;
         auto scales_of = [&](int i) {
           if (kScl && lane >= 24 && i < n) {
-            const int id = page_id(tile_of(pc.x, pc.i0 + i) * (kKeys / kPageSize) + lane - 24);
+            const int id = page_id(tile_of(x, i0 + i) * (kKeys / kPageSize) + lane - 24);
             ks = vs = 1.f;
             if (id < p.num_blocks) {
-              ks = __ldg(p.k_scales + (int64_t)id * p.ks_s0 + (int64_t)pc.h * p.ks_s1);
-              vs = __ldg(p.v_scales + (int64_t)id * p.vs_s0 + (int64_t)pc.h * p.vs_s1);
+              ks = __ldg(p.k_scales + (int64_t)id * p.ks_s0 + (int64_t)h * p.ks_s1);
+              vs = __ldg(p.v_scales + (int64_t)id * p.vs_s0 + (int64_t)h * p.vs_s1);
             }
           }
         };
@@ -456,10 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t dst = sbase + C::kOffRaw + slot * C::kRawBytes;
           if (is_k) {
             if (k_on)
-              tma_load_4d(dst + k_ch * (64 * 128) + (lane / kDim) * 2048, &tm_k, k_ch * kEl, pc.h, 0, id,
+              tma_load_4d(dst + k_ch * (64 * 128) + (lane / kDim) * 2048, &tm_k, k_ch * kEl, h, 0, id,
                           bar(kBarRawFull + slot));
           } else if (v_on) {
-            tma_load_4d(dst + v_ch * (128 * 128) + v_page * 2048, &tm_v, (rank * kVCh + v_ch) * kEl, pc.h, 0, id,
+            tma_load_4d(dst + v_ch * (128 * 128) + v_page * 2048, &tm_v, (rank * kVCh + v_ch) * kEl, h, 0, id,
                         bar(kBarRawFull + slot));
           }
           __syncwarp();
@@ -475,8 +516,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ======================= MMA issuer (the even CTA) ===============================
       if (rank == 0) {
         int tiles = 0, piece = 0;
-        while (ok && next_piece(p, t0, t1, w, pc)) {
-          const int n = pc.i1 - pc.i0;
+        while (const volatile Piece* pc = take()) {
+          const int n = pc->n;
+          give_back();
           if (n == 0) continue;
           if (!wait_for(kBarQFull, piece, 2)) break;
           for (int off = 0; off < 2 * n && ok; ++off, ++seq) {
@@ -531,8 +573,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float kd = p.k_descale ? *p.k_descale : 1.f;
       const bool neg = p.scale_log2 * kd < 0.f;
       int piece = 0;
-      while (next_piece(p, t0, t1, w, pc)) {
-        const int n = pc.i1 - pc.i0;
+      while (const volatile Piece* pc = take()) {
+        const int n = pc->n, i0 = pc->i0, h = pc->h, m = pc->m, L = pc->L, q0 = pc->q0;
+        const Span x{pc->x.klo, pc->x.khi, pc->x.nf, pc->x.w0, 0};
+        give_back();
         if (n == 0) continue;
         if (piece > 0 && !wait_for(kBarQFree, piece - 1, 32)) break;
         // Q: rows lw, lw + 4, .. of this CTA's 128, eight at a time
@@ -541,12 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 raw[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int64_t row = (int64_t)pc.m * kChunkRows + rank * 128 + r0 + 4 * k;
+            const int64_t row = (int64_t)m * kChunkRows + rank * 128 + r0 + 4 * k;
             raw[k] = make_uint4(0, 0, 0, 0);
-            if (row < (int64_t)pc.s.L * p.group) {
+            if (row < (int64_t)L * p.group) {
               const int t = (int)row / p.group, g = (int)row - t * p.group;
-              raw[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(pc.s.q0 + t) * p.q_s0 +
-                                                       (int64_t)(pc.h * p.group + g) * p.q_s1 + 8 * lane);
+              raw[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(q0 + t) * p.q_s0 +
+                                                       (int64_t)(h * p.group + g) * p.q_s1 + 8 * lane);
             }
           }
 #pragma unroll
@@ -556,11 +600,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kFp8) {
               // f16 of q times a power of two that brings the row's largest into [2^14,
               // 2^15): exact for values down to 2^-31 of it
-              uint32_t x[4] = {v.x, v.y, v.z, v.w};
+              uint32_t w4[4] = {v.x, v.y, v.z, v.w};
               float mx = 0.f;
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xFFFF0000u))));
+                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w4[j] << 16)), fabsf(__uint_as_float(w4[j] & 0xFFFF0000u))));
 #pragma unroll
               for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
               int e = 0;
@@ -571,8 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float up = __uint_as_float((uint32_t)(e + 127) << 23) * (neg ? -1.f : 1.f);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                x[j] = pack_f16x2(__uint_as_float(x[j] << 16) * up, __uint_as_float(x[j] & 0xFFFF0000u) * up);
-              v = make_uint4(x[0], x[1], x[2], x[3]);
+                w4[j] = pack_f16x2(__uint_as_float(w4[j] << 16) * up, __uint_as_float(w4[j] & 0xFFFF0000u) * up);
+              v = make_uint4(w4[0], w4[1], w4[2], w4[3]);
               if (lane == 0) row_factor[(piece & 1) * 128 + r] = __uint_as_float((uint32_t)(127 - e) << 23);
             } else if (neg) {
               v = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
@@ -591,23 +635,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int rs = seq % C::kRawSlots, os = seq % C::kOpSlots;
           if (!wait_for(kBarRawFull + rs, seq / C::kRawSlots, 64)) break;
           // V rows from this one on are seen by no row
-          const int valid = is_k ? kKeys : pc.x.khi - tile_of(pc.x, pc.i0 + i) * kKeys;
+          const int valid = is_k ? kKeys : x.khi - tile_of(x, i0 + i) * kKeys;
           if constexpr (kFp8) {
             if (seq >= C::kOpSlots && !wait_for(kBarOpEmpty + os, seq / C::kOpSlots - 1, 128)) break;
             const unsigned char* raw = sm + C::kOffRaw + rs * C::kRawBytes;
             unsigned char* op = sm + C::kOffOp + os * C::kOpBytes;
             const int u = lane & 7;
             // 16 codes a thread and step: unit u of row-chunk rc (K: 2 chunks of 64 rows, V: 128 rows)
-            uint4 x[8];
+            uint4 in8[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int rc = k * 16 + lw * 4 + (lane >> 3);
-              x[k] = *reinterpret_cast<const uint4*>(raw + rc * 128 + ((u ^ (rc & 7)) << 4));
+              in8[k] = *reinterpret_cast<const uint4*>(raw + rc * 128 + ((u ^ (rc & 7)) << 4));
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int rc = k * 16 + lw * 4 + (lane >> 3);
-              const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+              const uint32_t in[4] = {in8[k].x, in8[k].y, in8[k].z, in8[k].w};
               uint32_t h[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
@@ -670,22 +714,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar(1 + q, 64);
         return is_max ? fmaxf(v, o) : v + o;
       };
-      while (next_piece(p, t0, t1, w, pc)) {
-        const int n = pc.i1 - pc.i0;
-        const int64_t row = (int64_t)pc.m * kChunkRows + rank * 128 + r;
-        const int64_t rows = (int64_t)pc.s.L * p.group;
-        const bool row_ok = row < rows;
-        const bool idle = (int64_t)pc.m * kChunkRows + rank * 128 + 32 * q >= rows;  // no row of the quadrant's
-        const int t = row_ok ? (int)row / p.group : 0, g = row_ok ? (int)row - t * p.group : 0;
-        // keys that this row sees: up to vis_end, from vis_lo on or below first_tokens
-        const int vis_end = row_ok ? pc.s.S - pc.s.L + t : -1;
-        const int64_t vis_lo64 = p.window_left >= 0 ? (int64_t)vis_end - p.window_left : 0;
-        const int vis_lo = vis_lo64 < 0 ? 0 : (int)vis_lo64;
+      while (true) {
+        const volatile Piece* pc = take();
+        if (named_bar_or(1 + q, 64, pc == nullptr)) break;  // (the two warps leave together)
+        const int n = pc->n;
+        const int row0 = pc->m * kChunkRows + rank * 128;  // this CTA's first row
+        const bool idle = row0 + 32 * q >= pc->L * p.group;  // no row of the quadrant's
+        const int t_r = (row0 + r) / p.group;  // the row's token
+        // keys that this row sees: up to vis_end, from vis_lo on or below first_tokens;
         // tiles with keys past end_min, or before lo_max, are masked
-        const int end_min = pc.s.S - pc.s.L + (int)((int64_t)pc.m * kChunkRows / p.group);
-        const int64_t lo_max = p.window_left >= 0 ? (int64_t)pc.x.khi - 1 - p.window_left : 0;
+        const int vis_end = t_r < pc->L ? pc->S - pc->L + t_r : -1;
+        const int end_min = pc->S - pc->L + pc->m * kChunkRows / p.group;
+        int vis_lo = 0, lo_max = 0;
+        if (VAR && p.window_left >= 0) {
+          const int64_t lo = (int64_t)vis_end - p.window_left, hi = (int64_t)pc->x.khi - 1 - p.window_left;
+          vis_lo = lo < 0 ? 0 : (int)lo;
+          lo_max = hi < 0 ? 0 : (int)hi;
+        }
+        int tile = pc->i0;
+        const int jump = VAR ? pc->x.nf : 0, jump_to = VAR ? pc->x.w0 : 0;
         float m_ref = -INFINITY, l = 0.f, rs = cscale;
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < n; ++i, ++tile) {
           const int cur = tiles + i, b = cur & 1;
           if (kScl) wait_for(kBarScales + cur % kScaleTiles, cur / kScaleTiles, 512);
           wait_for(kBarSFull + b, cur >> 1, 256);
@@ -715,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   lv4[2 * j + 1] = v.w;
                 }
               }
-              if (p.softcap_log2 > 0.f) {
+              if (VAR && p.softcap_log2 > 0.f) {
                 // c tanh(s / c) = c (1 - 2 / (e^(2 s / c) + 1)), kept without the factor c
                 const float f = (2.f * kLog2e) / p.softcap_log2;
 #pragma unroll
@@ -729,13 +778,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kPg; ++j) xs4[j] = fmaxf(xs4[j], 1.2e-38f);  // a masked key's -inf stays that
               }
-              const int key0 = tile_of(pc.x, pc.i0 + i) * kKeys + kMine * kh;
+              const int key0 = (VAR && tile >= jump ? tile - jump + jump_to : tile) * kKeys + kMine * kh;
               if (key0 + kMine - 1 > end_min) {
 #pragma unroll
                 for (int k = 0; k < kMine; ++k)
                   if (key0 + k > vis_end) x[k] = -INFINITY;
               }
-              if (key0 < lo_max) {
+              if (VAR && key0 < lo_max) {
 #pragma unroll
                 for (int k = 0; k < kMine; ++k)
                   if (key0 + k < vis_lo && key0 + k >= p.first_tokens) x[k] = -INFINITY;
@@ -827,14 +876,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_for(kBarPvDone + ((tiles - 1) & 1), (tiles - 1) >> 1, 4096);
           tc_fence_after();
         }
-        if (!ok) continue;
-        if (!idle) {
-          if (p.sinks && pc.direct && row_ok && m_ref != -INFINITY)
-            l += ex2(p.sinks[pc.h * p.group + g] * kLog2e - (m_ref - kShift));
+        if (ok && !idle) {
+          const bool row_ok = row0 + r < pc->L * p.group, direct = pc->direct;
+          const int g = row0 + r - t_r * p.group;
+          if (p.sinks && direct && row_ok && m_ref != -INFINITY)
+            l += ex2(p.sinks[pc->h * p.group + g] * kLog2e - (m_ref - kShift));
           const float inv = l > 0.f || l != l ? vd / l : 0.f;
-          const int64_t slot = 2 * (int64_t)c + (pc.i0 == 0 ? 1 : 0);
+          const int64_t slot = 2 * (int64_t)c + (pc->i0 == 0 ? 1 : 0);
           const int pr = rank * 128 + r;
-          uint16_t* dst = p.out + (int64_t)(pc.s.q0 + t) * p.o_s0 + (int64_t)(pc.h * p.group + g) * p.o_s1 + 128 * kh;
+          uint16_t* dst = p.out + (int64_t)(pc->q0 + t_r) * p.o_s0 + (int64_t)(pc->h * p.group + g) * p.o_s1 + 128 * kh;
           float* acc = p.ws_acc + (slot * kChunkRows + pr) * kHeadDim + 128 * kh;
           const bool nothing = m_ref == -INFINITY && l == l;  // (all of them NaN: NaN)
 #pragma unroll 1
@@ -845,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_ld();
             }
             if (!row_ok) continue;
-            if (pc.direct) {
+            if (direct) {
               uint32_t v[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k)
@@ -863,16 +913,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 4; ++k) st_global_v8(acc + 32 * j + 8 * k, o + 8 * k);
             }
           }
-          if (!pc.direct && row_ok && kh == 0)
+          if (!direct && row_ok && kh == 0)
             *reinterpret_cast<float2*>(p.ws_ml + (slot * kChunkRows + pr) * 2) =
                 make_float2(nothing ? -INFINITY : m_ref == -INFINITY ? 0.f : m_ref - kShift, l);
         }
-        if (n > 0) {
+        if (ok && n > 0) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(lead(kBarOFree));
-          ++piece;
         }
+        if (n > 0) ++piece;
+        give_back();
       }
     }
   }
@@ -943,9 +994,9 @@ __global__ void __launch_bounds__(kMergeThreads) va_chunk_merge_kernel(const Chu
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_b16x2(acc.x * inv, acc.y * inv), pack_b16x2(acc.z * inv, acc.w * inv));
 }
 
-template <int KIND>
+template <int KIND, bool VAR>
 cudaError_t prepare_one(int32_t* max_pairs) {
-  cudaError_t e = cudaFuncSetAttribute(va_chunk_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<KIND>::kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(va_chunk_kernel<KIND, VAR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<KIND>::kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
@@ -958,7 +1009,7 @@ cudaError_t prepare_one(int32_t* max_pairs) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, va_chunk_kernel<KIND>, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&n, va_chunk_kernel<KIND, VAR>, &cfg);
   if (n < *max_pairs) *max_pairs = n;
   return e;
 }
@@ -967,10 +1018,20 @@ cudaError_t prepare_one(int32_t* max_pairs) {
 
 cudaError_t prepare_chunk(int32_t* max_pairs) {
   *max_pairs = 1 << 20;
-  cudaError_t e = prepare_one<kBf16>(max_pairs);
-  if (e == cudaSuccess) e = prepare_one<kE4m3>(max_pairs);
-  if (e == cudaSuccess) e = prepare_one<kPageScaled>(max_pairs);
+  cudaError_t e = prepare_one<kBf16, false>(max_pairs);
+  if (e == cudaSuccess) e = prepare_one<kBf16, true>(max_pairs);
+  if (e == cudaSuccess) e = prepare_one<kE4m3, false>(max_pairs);
+  if (e == cudaSuccess) e = prepare_one<kE4m3, true>(max_pairs);
+  if (e == cudaSuccess) e = prepare_one<kPageScaled, false>(max_pairs);
+  if (e == cudaSuccess) e = prepare_one<kPageScaled, true>(max_pairs);
   return e;
+}
+
+template <int KIND>
+static cudaError_t launch_main(cudaLaunchConfig_t& cfg, const ChunkParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v) {
+  cfg.dynamicSmemBytes = Cfg<KIND>::kSmemBytes;
+  return p.window_left >= 0 || p.softcap_log2 > 0.f ? cudaLaunchKernelEx(&cfg, va_chunk_kernel<KIND, true>, p, tm_k, tm_v)
+                                                    : cudaLaunchKernelEx(&cfg, va_chunk_kernel<KIND, false>, p, tm_k, tm_v);
 }
 
 cudaError_t launch_chunk(const ChunkParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream) {
@@ -987,17 +1048,9 @@ cudaError_t launch_chunk(const ChunkParams& p, const CUtensorMap& tm_k, const CU
   cfg.stream = stream;
   cfg.gridDim = dim3(2 * p.pairs);
   cfg.blockDim = dim3(kThreads);
-  cudaError_t e;
-  if (p.k_scales) {
-    cfg.dynamicSmemBytes = Cfg<kPageScaled>::kSmemBytes;
-    e = cudaLaunchKernelEx(&cfg, va_chunk_kernel<kPageScaled>, p, tm_k, tm_v);
-  } else if (p.kv_fp8) {
-    cfg.dynamicSmemBytes = Cfg<kE4m3>::kSmemBytes;
-    e = cudaLaunchKernelEx(&cfg, va_chunk_kernel<kE4m3>, p, tm_k, tm_v);
-  } else {
-    cfg.dynamicSmemBytes = Cfg<kBf16>::kSmemBytes;
-    e = cudaLaunchKernelEx(&cfg, va_chunk_kernel<kBf16>, p, tm_k, tm_v);
-  }
+  const cudaError_t e = p.k_scales ? launch_main<kPageScaled>(cfg, p, tm_k, tm_v)
+                        : p.kv_fp8 ? launch_main<kE4m3>(cfg, p, tm_k, tm_v)
+                                   : launch_main<kBf16>(cfg, p, tm_k, tm_v);
   if (e != cudaSuccess || p.pairs < 2) return e;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(p.pairs - 1, kChunkRows / kMergeRows);
