@@ -167,10 +167,23 @@ __device__ __forceinline__ int tile_of(const Span& x, int i) { return i < x.nf ?
 
 enum Kind { kBf16 = 0, kE4m3 = 1, kPageScaled = 2 };
 
-constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;
-constexpr int kThreads = 32 * (kSoftmaxWarps + kLoadWarps + 3);
-constexpr int kWarpProducer = kSoftmaxWarps + kLoadWarps, kWarpMma = kWarpProducer + 1, kWarpPlan = kWarpMma + 1;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kLoadGroups = 2, kLoadWarps = 4 * kLoadGroups;  // a group of four warps takes every other tile
+constexpr int kProducers = 2;                                 // K's and V's
+constexpr int kWarpProducer = kSoftmaxWarps + kLoadWarps, kWarpMma = kWarpProducer + kProducers, kWarpPlan = kWarpMma + 1;
+constexpr int kThreads = 32 * (kWarpPlan + 1);
 constexpr int kPieces = 4;  // places of the queue of pieces
+
+// Tiles (K and V, in the order of their use) go to two warps or groups in turn, those of
+// even and of odd number. A barrier tells two phases apart and no more, so a waiter has to
+// meet every phase of it: where the slots are odd in number, a slot's users take turns,
+// and each gets the arrivals that free the slot for it on a barrier of its own. Tile
+// `seq` waits for use empty_use(seq) of barrier empty_bar(seq); the end of tile `seq`
+// arrives for the slot's next user, on empty_bar(seq + slots).
+template <int SLOTS>
+__device__ __forceinline__ int empty_bar(int seq) { return seq % (2 * SLOTS); }
+template <int SLOTS>
+__device__ __forceinline__ int empty_use(int seq) { return seq / (2 * SLOTS) - (seq % (2 * SLOTS) < SLOTS ? 1 : 0); }
 
 template <int KIND>
 struct Cfg {
@@ -185,6 +198,8 @@ struct Cfg {
   static constexpr int kOffMisc = kFp8 ? kOffRaw + kRawSlots * kRawBytes : kOffOp + kOpSlots * kOpBytes;
   static constexpr int kSmemBytes = kOffMisc + 3072;
   static_assert(kSmemBytes <= 232448, "shared memory");
+  static_assert(!kFp8 || kRawSlots % 2 == 0, "a raw slot belongs to one producer and one group");
+  static_assert(kOpSlots % 2 == 1, "empty_bar");
   // instruction descriptors: f16 (0) or bf16 (1) operands, M = 256
   static constexpr uint32_t kFmt = kFp8 ? 0u : 1u;
   static constexpr uint32_t kIdQK = instr_desc(kFmt, kFmt, false, kKeys, 256);
@@ -198,10 +213,10 @@ constexpr int kMaxRaw = 5, kMaxOp = 5;
 constexpr int kScaleTiles = 6;
 enum : int {
   kBarRawFull = 0,
-  kBarRawEmpty = kBarRawFull + kMaxRaw,
-  kBarOpFull = kBarRawEmpty + kMaxRaw,
-  kBarOpEmpty = kBarOpFull + kMaxOp,
-  kBarSFull = kBarOpEmpty + kMaxOp,
+  kBarOpFull = kBarRawFull + kMaxRaw,
+  kBarEmpty = kBarOpFull + kMaxOp,   // what the MMAs are through with: twice the operand slots (empty_bar)
+  kBarRawEmpty = kBarEmpty + 6,      // e4m3: what has been converted
+  kBarSFull = kBarEmpty + 2 * kMaxOp,
   kBarPFull = kBarSFull + 2,
   kBarPvDone = kBarPFull + 2,
   kBarQFull = kBarPvDone + 2,
@@ -214,7 +229,8 @@ enum : int {
   kNumBars = kBarPieceEmpty + kPieces
 };
 constexpr int kOffTmem = 8 * kNumBars, kOffAbort = kOffTmem + 4;
-constexpr int kOffPieces = (kOffAbort + 4 + 15) / 16 * 16;      // [kPieces] Piece; before: ChunkStart
+constexpr int kOffIssued = kOffAbort + 4;  // the last tile that went into each raw slot, or -1
+constexpr int kOffPieces = (kOffIssued + 4 * kMaxRaw + 15) / 16 * 16;      // [kPieces] Piece; before: ChunkStart
 constexpr int kOffRow = kOffPieces + kPieces * 64;               // [2][128] floats
 constexpr int kOffXch = kOffRow + 1024;                          // [2][128] floats; before: 32 x 8 bytes of the scan
 constexpr int kOffScale = kOffXch + 1024;                        // [kScaleTiles][8] (K scale, log2 V scale)
@@ -252,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + kOffAbort);
   long long* scratch = reinterpret_cast<long long*>(misc + kOffXch);
   ChunkStart* start = reinterpret_cast<ChunkStart*>(misc + kOffPieces);
+  volatile int* issued = reinterpret_cast<volatile int*>(misc + kOffIssued);
   float* row_factor = reinterpret_cast<float*>(misc + kOffRow);
   float* xch = reinterpret_cast<float*>(misc + kOffXch);
   float2* page_scale = reinterpret_cast<float2*>(misc + kOffScale);
@@ -266,15 +283,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::kRawSlots; ++i) {
       mbar_init(bar(kBarRawFull + i), 1);
-      mbar_init(bar(kBarRawEmpty + i), kFp8 ? kLoadWarps : 1);
+      if (kFp8) mbar_init(bar(kBarRawEmpty + i), 4);
     }
-    for (int i = 0; i < C::kOpSlots; ++i) {
-      mbar_init(bar(kBarOpFull + i), kFp8 ? 2 * kLoadWarps : 2);
-      mbar_init(bar(kBarOpEmpty + i), 1);
-    }
+    for (int i = 0; i < C::kOpSlots; ++i) mbar_init(bar(kBarOpFull + i), kFp8 ? 2 * 4 : 2);
+    for (int i = 0; i < 2 * C::kOpSlots; ++i) mbar_init(bar(kBarEmpty + i), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarSFull + i), 1);
-      mbar_init(bar(kBarPFull + i), 2 * kSoftmaxWarps);
+      mbar_init(bar(kBarPFull + i), kSoftmaxWarps);  // a group's four warps of each CTA
       mbar_init(bar(kBarPvDone + i), 1);
     }
     mbar_init(bar(kBarQFull), 2 * kLoadWarps);
@@ -284,9 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kScaleTiles; ++i) mbar_init(bar(kBarScales + i), 1);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(bar(kBarPieceFull + i), 1);
-      mbar_init(bar(kBarPieceEmpty + i), kSoftmaxWarps + kLoadWarps + 1 + (rank == 0 ? 1 : 0));
+      mbar_init(bar(kBarPieceEmpty + i), kSoftmaxWarps + kLoadWarps + kProducers + (rank == 0 ? 1 : 0));
     }
     *abort_flag = 0;
+    for (int i = 0; i < kMaxRaw; ++i) issued[i] = -1;
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
@@ -409,167 +425,261 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++at;
     };
     int seq = 0;  // K and V tiles so far: a piece's K0, K1, V0, K2, V1, .., K(n-1), V(n-2), V(n-1)
-    if (warp == kWarpPlan) {
-      Walk w = start_walk(p, *start);
-      __syncwarp();  // (the pieces take start's place)
-      Piece pc;
-      for (bool more = true; more && ok; ++at) {
-        more = next_piece(p, t0, t1, w, pc);
-        if (!more) pc.n = -1;
-        if (at >= kPieces && !wait_for(kBarPieceEmpty + at % kPieces, at / kPieces - 1, 16384)) break;
-        if (lane == 0) *reinterpret_cast<Piece*>(misc + kOffPieces + at % kPieces * sizeof(Piece)) = pc;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPieceFull + at % kPieces));
-      }
-    } else if (warp == kWarpProducer) {
-      // ======================= TMA producer ==========================================
-      // One 2 KB box (a page's 16 tokens x 128 bytes) a lane: this CTA's half of K's
-      // keys, or of V's columns. Pages that no row of the item sees are not mapped
-      // perhaps: they are read past the cache's last page, which TMA fills with zeros.
-      constexpr int kDim = kFp8 ? 2 : 4;            // 128-byte chunks of a row
-      constexpr int kVCh = kDim / 2;                // .. of V's half
-      const int k_page = lane / kDim + 4 * rank, k_ch = lane % kDim;
-      const int v_page = lane / kVCh, v_ch = lane % kVCh;
-      constexpr int kEl = kFp8 ? 128 : 64;          // elements of a chunk
-      const bool k_on = lane < 4 * kDim, v_on = lane < 8 * kVCh;
-      int tiles = 0;  // tiles so far (page scales)
-      while (const volatile Piece* pc_ = take()) {
-        const Span x{pc_->x.klo, pc_->x.khi, pc_->x.nf, pc_->x.w0, 0};
-        const int n = pc_->n, i0 = pc_->i0, h = pc_->h;
-        const int* bt = p.block_table + (int64_t)pc_->b * p.bt_s0;
-        give_back();
-        auto page_id = [&](int page) {
-          const int key = page * kPageSize;
-          const bool seen = key < x.khi && (key + kPageSize > x.klo || key < p.first_tokens);
-          const int id = seen ? bt[(int64_t)page * p.bt_s1] : -1;
-          return (unsigned)id < (unsigned)p.num_blocks ? id : p.num_blocks;
-        };
-        auto step = [&](int off, bool& is_k, int& i) {
-          is_k = off == 0 || (off != 2 * n - 1 && (off & 1));
-          i = off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1;
-        };
-        auto page_of = [&](int off) {
-          bool is_k;
-          int i;
-          step(off, is_k, i);
-          return tile_of(x, i0 + i) * (kKeys / kPageSize) + (is_k ? k_page : v_page);
-        };
-        auto fetch = [&](int off) {
-          bool is_k;
-          int i;
-          step(off, is_k, i);
-          return (is_k ? k_on : v_on) ? page_id(page_of(off)) : p.num_blocks;
-        };
-        // page scales of tile i: lanes 24..31, loaded a tile ahead
-        float ks = 1.f, vs = 1.f;
-        auto scales_of = [&](int i) {
-          if (kScl && lane >= 24 && i < n) {
-            const int id = page_id(tile_of(x, i0 + i) * (kKeys / kPageSize) + lane - 24);
-            ks = vs = 1.f;
-            if (id < p.num_blocks) {
-              ks = __ldg(p.k_scales + (int64_t)id * p.ks_s0 + (int64_t)h * p.ks_s1);
-              vs = __ldg(p.v_scales + (int64_t)id * p.vs_s0 + (int64_t)h * p.vs_s1);
-            }
-          }
-        };
-        if (n > 0) scales_of(0);
-        int next = n > 0 ? fetch(0) : 0;
-        for (int off = 0; off < 2 * n && ok; ++off, ++seq) {
-          bool is_k;
-          int i;
-          step(off, is_k, i);
-          const int id = next;
-          if (off + 1 < 2 * n) next = fetch(off + 1);
-          const int slot = seq % C::kRawSlots, use = seq / C::kRawSlots;
-          if (use > 0 && !wait_for(kBarRawEmpty + slot, use - 1, 1)) break;
-          if (kScl && is_k) {
-            if (lane >= 24) {
-              const float k1 = fminf(fmaxf(ks, kMinPageScale), kMaxPageScale);
-              const float v1 = fminf(fmaxf(vs, kMinPageScale), kMaxPageScale);
-              page_scale[((tiles + i) % kScaleTiles) * 8 + lane - 24] = make_float2(k1, log2f(v1));
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarScales + (tiles + i) % kScaleTiles));
-            scales_of(i + 1);
-          }
-          if (lane == 0) mbar_arrive_expect_tx(bar(kBarRawFull + slot), C::kRawBytes);
-          __syncwarp();
-          const uint32_t dst = sbase + C::kOffRaw + slot * C::kRawBytes;
-          if (is_k) {
-            if (k_on)
-              tma_load_4d(dst + k_ch * (64 * 128) + (lane / kDim) * 2048, &tm_k, k_ch * kEl, h, 0, id,
-                          bar(kBarRawFull + slot));
-          } else if (v_on) {
-            tma_load_4d(dst + v_ch * (128 * 128) + v_page * 2048, &tm_v, (rank * kVCh + v_ch) * kEl, h, 0, id,
-                        bar(kBarRawFull + slot));
-          }
-          __syncwarp();
+    if (warp < kSoftmaxWarps) {
+      // ======================= softmax / epilogue =====================================
+      // Two groups of four warps, a thread a row: group 0 takes the tiles in S buffer 0,
+      // group 1 those in buffer 1, so that one tile's chain of latencies (load, maximum,
+      // powers, store) runs beside the next one's. A row's reference goes from tile to
+      // tile, and so from group to group, through shared memory as soon as the tile's
+      // maximum is known; l stays with the group. In the epilogue a group writes half of
+      // O's columns. After a failure a warp walks on without waits and work, so that the
+      // two warps of a quadrant still meet at every named barrier (1 + q: to group 0,
+      // 5 + q: to group 1, 9 + q: both).
+      const int q = warp & 3, grp = warp >> 2;
+      const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+      const int r = 32 * q + lane;  // this CTA's row
+      const float kd = p.k_descale ? *p.k_descale : 1.f;
+      const float vd = p.v_descale ? *p.v_descale : 1.f;
+      const float cscale = fmaxf(fabsf(p.scale_log2 * kd), 1e-30f);  // the sign is Q's
+      constexpr float kShift = kFp8 ? 7.f : 0.f;
+      int tiles = 0, piece = 0;
+      while (true) {
+        const volatile Piece* pc = take();
+        if (named_bar_or(9 + q, 64, pc == nullptr)) break;  // (the two warps leave together)
+        const int n = pc->n;
+        const int row0 = pc->m * kChunkRows + rank * 128;  // this CTA's first row
+        const bool idle = row0 + 32 * q >= pc->L * p.group;  // no row of the quadrant's
+        const int t_r = (row0 + r) / p.group;  // the row's token
+        // keys that this row sees: up to vis_end, from vis_lo on or below first_tokens;
+        // tiles with keys past end_min, or before lo_max, are masked
+        const int vis_end = t_r < pc->L ? pc->S - pc->L + t_r : -1;
+        const int end_min = pc->S - pc->L + pc->m * kChunkRows / p.group;
+        int vis_lo = 0, lo_max = 0;
+        if (VAR && p.window_left >= 0) {
+          const int64_t lo = (int64_t)vis_end - p.window_left, hi = (int64_t)pc->x.khi - 1 - p.window_left;
+          vis_lo = lo < 0 ? 0 : (int)lo;
+          lo_max = hi < 0 ? 0 : (int)hi;
         }
-        tiles += n;
-      }
-      // copies in flight land before the CTA ends, also when another role gave up
-      if (lane == 0)
-        for (int k = seq > C::kRawSlots ? seq - C::kRawSlots : 0; k < seq; ++k)
-          mbar_wait_drain(bar(kBarRawFull + k % C::kRawSlots), (uint32_t)(k / C::kRawSlots) & 1u, kDrainLimitNs);
-      __syncwarp();
-    } else if (warp == kWarpMma) {
-      // ======================= MMA issuer (the even CTA) ===============================
-      if (rank == 0) {
-        int tiles = 0, piece = 0;
-        while (const volatile Piece* pc = take()) {
-          const int n = pc->n;
-          give_back();
-          if (n == 0) continue;
-          if (!wait_for(kBarQFull, piece, 2)) break;
-          for (int off = 0; off < 2 * n && ok; ++off, ++seq) {
-            const bool is_k = off == 0 || (off != 2 * n - 1 && (off & 1));
-            const int i = off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1;
-            const int slot = seq % C::kOpSlots, use = seq / C::kOpSlots;
-            const int b = (tiles + i) & 1;
-            if (!wait_for(kBarOpFull + slot, use, 4)) break;
-            if (!is_k) {
-              if (!wait_for(kBarPFull + b, (tiles + i) >> 1, 8)) break;
-              if (i == 0 && piece > 0 && !wait_for(kBarOFree, piece - 1, 16)) break;
-            }
-            tc_fence_after();
-            const uint32_t src = sbase + C::kOffOp + slot * C::kOpBytes;
-            if (elect_one()) {
-              if (is_k) {
+        const int tile0 = pc->i0;
+        const int jump = VAR ? pc->x.nf : 0, jump_to = VAR ? pc->x.w0 : 0;
+        float m_ref = -INFINITY, l = 0.f, rs = cscale;
+        bool first = true;  // of this group's tiles
+        for (int i = (tiles & 1) ^ grp; i < n; i += 2) {
+          const int cur = tiles + i;
+          if (kScl) wait_for(kBarScales + cur % kScaleTiles, cur / kScaleTiles, 512);
+          wait_for(kBarSFull + grp, cur >> 1, 256);
+          tc_fence_after();
+          const uint32_t ts = tmem + lane_base + kColS + grp * kKeys;
+          const int tile = tile0 + i;
+          const int key0 = (VAR && tile >= jump ? tile - jump + jump_to : tile) * kKeys;
+          const bool mask_hi = key0 + kKeys - 1 > end_min, mask_lo = VAR && key0 < lo_max;
+          const float2* scales = page_scale + (cur % kScaleTiles) * 8;
+          const bool cap = VAR && p.softcap_log2 > 0.f;
+          // S is read twice, 32 keys at a time: for the row's maximum and for P (its 128
+          // values would leave a thread no registers, and half the block no threads; a
+          // read takes 100 cycles)
+          auto load = [&](int part, uint32_t (&x)[32]) {
+            tmem_ld_32x32b_x32(ts + 32 * part, x);
+            tmem_wait_ld();
+          };
+          constexpr uint32_t kHidden = 0xFF800000u;  // -inf
+          auto mask = [&](int part, uint32_t (&x)[32]) {
+            if (mask_hi) {
+              const int end = vis_end - key0 - 32 * part;
 #pragma unroll
-                for (int k = 0; k < kHeadDim / 16; ++k) {
-                  const uint32_t ko = (uint32_t)((k & 3) * 32);
-                  mma_f16_pair(tmem + kColS + b * kKeys, smem_desc(sbase + C::kOffQ + (k >> 2) * (128 * 128) + ko, 16, 1024, kLayoutSw128),
-                               smem_desc(src + (k >> 2) * (64 * 128) + ko, 16, 1024, kLayoutSw128), C::kIdQK, k ? 1u : 0u);
+              for (int k = 0; k < 32; ++k)
+                if (k > end) x[k] = kHidden;
+            }
+            if (mask_lo) {
+              const int lo = vis_lo - key0 - 32 * part, keep = p.first_tokens - key0 - 32 * part;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (k < lo && k >= keep) x[k] = kHidden;
+            }
+          };
+          // a key's logit (log2 units) is x times this; positive and normal, so that a masked
+          // key's -inf stays that
+          auto factor = [&](float ks) { return cap ? p.softcap_log2 : fmaxf(rs * ks, 1.2e-38f); };
+          float top = -INFINITY;
+          if (ok && !idle) {
+            if (kFp8 && first) rs = fmaxf(cscale * row_factor[(piece & 1) * 128 + r], 1.2e-38f);
+#pragma unroll
+            for (int part = 0; part < 4; ++part) {
+              uint32_t x[32];
+              load(part, x);
+              if (cap) {
+                // c tanh(s / c) = c (1 - 2 / (e^(2 s / c) + 1)), kept without the factor c
+                // in S's place
+                const float f = rs * ((2.f * kLog2e) / p.softcap_log2);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                  const float y = __uint_as_float(x[k]) * (kScl ? f * scales[2 * part + k / kPageSize].x : f);
+                  x[k] = __float_as_uint(1.f - __fdividef(2.f, ex2(y) + 1.f));
                 }
-                mma_commit_pair(bar(kBarSFull + b));
+                tmem_st_32x32b_x32(ts + 32 * part, x);
+              }
+              mask(part, x);
+              float u[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+              for (int k = 0; k < 32; k += 2)
+                u[k / kPageSize] = fmax3(u[k / kPageSize], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+              if constexpr (kScl) {
+                const float4 sc = *reinterpret_cast<const float4*>(scales + 2 * part);
+                top = fmax3(top, fmaf(u[0], factor(sc.x), sc.y), fmaf(u[1], factor(sc.z), sc.w));
+              } else {
+                top = fmax3(top, u[0], u[1]);
+              }
+            }
+            if (!kScl) top *= factor(1.f);
+            if (cap) tmem_wait_st();
+          }
+          // the reference of the tile before, the other group's
+          float m_old = -INFINITY;
+          if (i > 0) {
+            named_bar(1 + 4 * grp + q, 64);
+            m_old = xch[r];
+          }
+          const float m_new = top > m_old + kMove ? top : m_old;
+          if (i + 1 < n) {
+            xch[r] = m_new;
+            named_arrive(1 + 4 * (grp ^ 1) + q, 64);
+          }
+          if (ok && !idle) {
+            if (m_new != m_ref) {
+              if (m_ref != -INFINITY) l *= ex2(m_ref - m_new);
+              m_ref = m_new;
+            }
+            const float alpha = m_new != m_old && m_old != -INFINITY ? ex2(m_old - m_new) : 1.f;
+            if (__any_sync(0xffffffffu, alpha != 1.f) && wait_for(kBarPvDone + (grp ^ 1), (cur - 1) >> 1, 2048)) {
+              // O holds earlier tiles (of this piece: m_old is not -inf)
+              tc_fence_after();
+#pragma unroll 1
+              for (int j = 0; j < kHeadDim / 32; ++j) {
+                uint32_t o[32];
+                const uint32_t ta = tmem + lane_base + kColO + 32 * j;
+                tmem_ld_32x32b_x32(ta, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st_32x32b_x32(ta, o);
+              }
+            }
+            // (a row without a visible key yet: P = 0)
+            const float ref = m_ref == -INFINITY ? INFINITY : m_ref - kShift;
+            uint64_t ls[2] = {0, 0};
+#pragma unroll
+            for (int part = 0; part < 4; ++part) {
+              uint32_t x[32], pw[16];
+              load(part, x);
+              mask(part, x);
+              const float4 sc = kScl ? *reinterpret_cast<const float4*>(scales + 2 * part) : make_float4(1.f, 0.f, 1.f, 0.f);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float f = factor(k < 8 ? sc.x : sc.z), off = (k < 8 ? sc.y : sc.w) - ref;
+                float a, d;
+                unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), pack2(f, f), pack2(off, off)), a, d);
+                a = ex2(a);
+                d = ex2(d);
+                ls[k & 1] = add2(ls[k & 1], pack2(a, d));
+                pw[k] = kFp8 ? pack_f16x2(a, d) : pack_b16x2(a, d);
+                if (kScl && k % 8 == 7) {  // a page's end: its weights without the V scale
+                  float s0, s1, s2, s3;
+                  unpack2(ls[0], s0, s1);
+                  unpack2(ls[1], s2, s3);
+                  l = fmaf((s0 + s1) + (s2 + s3), ex2(-(k < 8 ? sc.y : sc.w)), l);
+                  ls[0] = ls[1] = 0;
+                }
+              }
+              // over S: this thread has loaded the columns
+              tmem_st_32x32b_x16(ts + 16 * part, pw);
+            }
+            if (!kScl) {
+              float s0, s1, s2, s3;
+              unpack2(ls[0], s0, s1);
+              unpack2(ls[1], s2, s3);
+              l += (s0 + s1) + (s2 + s3);
+            }
+            tmem_wait_st();
+          }
+          first = false;
+          if (ok) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(lead(kBarPFull + grp));
+          }
+        }
+        // -- epilogue: both groups' (reference, sum); O's is the larger reference
+        tiles += n;
+        named_bar(9 + q, 64);
+        xch[128 * grp + r] = m_ref;
+        named_bar(9 + q, 64);
+        const float m_row = fmaxf(m_ref, xch[128 * (grp ^ 1) + r]);
+        if (m_ref != m_row) l = m_ref == -INFINITY ? 0.f : l * ex2(m_ref - m_row);
+        named_bar(9 + q, 64);
+        xch[128 * grp + r] = l;
+        named_bar(9 + q, 64);
+        l += xch[128 * (grp ^ 1) + r];
+        m_ref = m_row;
+        if (n > 0) {
+          wait_for(kBarPvDone + ((tiles - 1) & 1), (tiles - 1) >> 1, 4096);
+          tc_fence_after();
+        }
+        if (ok && !idle) {
+          const bool row_ok = row0 + r < pc->L * p.group, direct = pc->direct;
+          const int g = row0 + r - t_r * p.group;
+          if (p.sinks && direct && row_ok && m_ref != -INFINITY)
+            l += ex2(p.sinks[pc->h * p.group + g] * kLog2e - (m_ref - kShift));
+          const float inv = l > 0.f || l != l ? vd / l : 0.f;
+          const int64_t slot = 2 * (int64_t)c + (pc->i0 == 0 ? 1 : 0);
+          const int pr = rank * 128 + r;
+          uint16_t* dst = p.out + (int64_t)(pc->q0 + t_r) * p.o_s0 + (int64_t)(pc->h * p.group + g) * p.o_s1 + 128 * grp;
+          float* acc = p.ws_acc + (slot * kChunkRows + pr) * kHeadDim + 128 * grp;
+          const bool nothing = m_ref == -INFINITY && l == l;  // (all of them NaN: NaN)
+#pragma unroll 1
+          for (int j = 0; j < kHeadDim / 64; ++j) {
+            uint32_t o[32];
+            if (n > 0) {
+              tmem_ld_32x32b_x32(tmem + lane_base + kColO + 128 * grp + 32 * j, o);
+              tmem_wait_ld();
+            }
+            if (!row_ok) continue;
+            if (direct) {
+              uint32_t v[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                v[k] = nothing ? 0u : pack_b16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+              if (p.out_v8) {
+                st_global_v8(dst + 32 * j, v);
+                st_global_v8(dst + 32 * j + 16, v + 8);
               } else {
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                  mma_f16_pair_ta(tmem + kColO, tmem + kColS + b * kKeys + 8 * k,
-                                  smem_desc(src + k * 2048, 128 * 128, 1024, kLayoutSw128), C::kIdPV, i || k ? 1u : 0u);
-                mma_commit_pair(bar(kBarPvDone + b));
+                for (int k = 0; k < 4; ++k)
+                  reinterpret_cast<uint4*>(dst + 32 * j)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
               }
-              mma_commit_pair(bar((kFp8 ? kBarOpEmpty : kBarRawEmpty) + slot));
-              if (is_k && i == n - 1) mma_commit_pair(bar(kBarQFree));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) st_global_v8(acc + 32 * j + 8 * k, o + 8 * k);
             }
-            __syncwarp();
           }
-          tiles += n;
-          ++piece;
+          if (!direct && row_ok && grp == 0)
+            *reinterpret_cast<float2*>(p.ws_ml + (slot * kChunkRows + pr) * 2) =
+                make_float2(nothing ? -INFINITY : m_ref == -INFINITY ? 0.f : m_ref - kShift, l);
         }
-        // every MMA has finished before the pair frees its memory
-        if (elect_one()) {
-          mma_commit_pair(bar(kBarDrain));
-          mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
+        if (ok && n > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead(kBarOFree));
         }
-        __syncwarp();
+        if (n > 0) ++piece;
+        give_back();
       }
-    } else if (warp >= kSoftmaxWarps) {
+    } else if (warp < kSoftmaxWarps + kLoadWarps) {
       // ======================= loaders ================================================
       // Q of an item, and K and V tiles on their way from TMA to the MMAs: e4m3 codes
       // become f16 (exactly), V rows past the last key that a row sees become zeros (0
       // times what a slot behind the sequence's last token holds would reach O).
-      const int lw = warp - kSoftmaxWarps;
+      const int lw = warp - kSoftmaxWarps;        // rows of Q
+      const int lg = lw >> 2, lq = lw & 3;        // group, and warp of it
       const float kd = p.k_descale ? *p.k_descale : 1.f;
       const bool neg = p.scale_log2 * kd < 0.f;
       int piece = 0;
@@ -579,13 +689,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         give_back();
         if (n == 0) continue;
         if (piece > 0 && !wait_for(kBarQFree, piece - 1, 32)) break;
-        // Q: rows lw, lw + 4, .. of this CTA's 128, eight at a time
+        // Q: rows lw, lw + 8, .. of this CTA's 128, four at a time
 #pragma unroll 1
-        for (int r0 = lw; r0 < 128; r0 += 32) {
-          uint4 raw[8];
+        for (int r0 = lw; r0 < 128; r0 += 4 * kLoadWarps) {
+          uint4 raw[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int64_t row = (int64_t)m * kChunkRows + rank * 128 + r0 + 4 * k;
+          for (int k = 0; k < 4; ++k) {
+            const int64_t row = (int64_t)m * kChunkRows + rank * 128 + r0 + kLoadWarps * k;
             raw[k] = make_uint4(0, 0, 0, 0);
             if (row < (int64_t)L * p.group) {
               const int t = (int)row / p.group, g = (int)row - t * p.group;
@@ -594,8 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = r0 + 4 * k;
+          for (int k = 0; k < 4; ++k) {
+            const int r = r0 + kLoadWarps * k;
             uint4 v = raw[k];
             if constexpr (kFp8) {
               // f16 of q times a power of two that brings the row's largest into [2^14,
@@ -633,11 +743,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool is_k = off == 0 || (off != 2 * n - 1 && (off & 1));
           const int i = off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1;
           const int rs = seq % C::kRawSlots, os = seq % C::kOpSlots;
+          if (kFp8 && (seq & 1) != lg) continue;
           if (!wait_for(kBarRawFull + rs, seq / C::kRawSlots, 64)) break;
           // V rows from this one on are seen by no row
           const int valid = is_k ? kKeys : x.khi - tile_of(x, i0 + i) * kKeys;
           if constexpr (kFp8) {
-            if (seq >= C::kOpSlots && !wait_for(kBarOpEmpty + os, seq / C::kOpSlots - 1, 128)) break;
+            if (seq >= C::kOpSlots && !wait_for(kBarEmpty + empty_bar<C::kOpSlots>(seq), empty_use<C::kOpSlots>(seq), 128)) break;
             const unsigned char* raw = sm + C::kOffRaw + rs * C::kRawBytes;
             unsigned char* op = sm + C::kOffOp + os * C::kOpBytes;
             const int u = lane & 7;
@@ -645,12 +756,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 in8[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const int rc = k * 16 + lw * 4 + (lane >> 3);
+              const int rc = k * 16 + lq * 4 + (lane >> 3);
               in8[k] = *reinterpret_cast<const uint4*>(raw + rc * 128 + ((u ^ (rc & 7)) << 4));
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const int rc = k * 16 + lw * 4 + (lane >> 3);
+              const int rc = k * 16 + lq * 4 + (lane >> 3);
               const uint32_t in[4] = {in8[k].x, in8[k].y, in8[k].z, in8[k].w};
               uint32_t h[8];
 #pragma unroll
@@ -691,247 +802,162 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
     } else {
-      // ======================= softmax / epilogue =====================================
-      // Two warps share a lane quadrant: warp half kh takes keys [64 kh, +64) of a tile
-      // and columns [128 kh, +128) of O, a thread one row. They vote on whether some row's
-      // reference moves, around the quadrant's named barrier; the maxima are exchanged
-      // only then. After a failure a warp walks on without waits and work, so that the
-      // two still meet at every barrier.
-      const int q = warp & 3, kh = warp >> 2;
-      const uint32_t lane_base = (uint32_t)(32 * q) << 16;
-      const int r = 32 * q + lane;  // this CTA's row
-      const float kd = p.k_descale ? *p.k_descale : 1.f;
-      const float vd = p.v_descale ? *p.v_descale : 1.f;
-      const float cscale = fmaxf(fabsf(p.scale_log2 * kd), 1e-30f);  // the sign is Q's
-      constexpr float kShift = kFp8 ? 7.f : 0.f;
-      constexpr int kMine = kKeys / 2, kPg = kMine / kPageSize;
-      int tiles = 0, piece = 0;
-      // the row's value of both halves
-      auto exchange = [&](float v, bool is_max) {
-        xch[kh * 128 + r] = v;
-        named_bar(1 + q, 64);
-        const float o = xch[(kh ^ 1) * 128 + r];
-        named_bar(1 + q, 64);
-        return is_max ? fmaxf(v, o) : v + o;
-      };
-      while (true) {
-        const volatile Piece* pc = take();
-        if (named_bar_or(1 + q, 64, pc == nullptr)) break;  // (the two warps leave together)
-        const int n = pc->n;
-        const int row0 = pc->m * kChunkRows + rank * 128;  // this CTA's first row
-        const bool idle = row0 + 32 * q >= pc->L * p.group;  // no row of the quadrant's
-        const int t_r = (row0 + r) / p.group;  // the row's token
-        // keys that this row sees: up to vis_end, from vis_lo on or below first_tokens;
-        // tiles with keys past end_min, or before lo_max, are masked
-        const int vis_end = t_r < pc->L ? pc->S - pc->L + t_r : -1;
-        const int end_min = pc->S - pc->L + pc->m * kChunkRows / p.group;
-        int vis_lo = 0, lo_max = 0;
-        if (VAR && p.window_left >= 0) {
-          const int64_t lo = (int64_t)vis_end - p.window_left, hi = (int64_t)pc->x.khi - 1 - p.window_left;
-          vis_lo = lo < 0 ? 0 : (int)lo;
-          lo_max = hi < 0 ? 0 : (int)hi;
-        }
-        int tile = pc->i0;
-        const int jump = VAR ? pc->x.nf : 0, jump_to = VAR ? pc->x.w0 : 0;
-        float m_ref = -INFINITY, l = 0.f, rs = cscale;
-        for (int i = 0; i < n; ++i, ++tile) {
-          const int cur = tiles + i, b = cur & 1;
-          if (kScl) wait_for(kBarScales + cur % kScaleTiles, cur / kScaleTiles, 512);
-          wait_for(kBarSFull + b, cur >> 1, 256);
-          tc_fence_after();
-          if (!idle) {
-            float x[kMine];
-            float xs = rs, xs4[kPg], lv4[kPg];
-            float top = -INFINITY;
-            if (ok) {
-              if (kFp8 && i == 0) xs = rs = fmaxf(cscale * row_factor[(piece & 1) * 128 + r], 1.2e-38f);
-#pragma unroll
-              for (int j = 0; j < kMine / 32; ++j) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tmem + lane_base + kColS + b * kKeys + kMine * kh + 32 * j, v);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) x[32 * j + k] = __uint_as_float(v[k]);
-              }
-              tmem_wait_ld();
-              if constexpr (kScl) {
-                const float4* sc = reinterpret_cast<const float4*>(page_scale + (cur % kScaleTiles) * 8 + kPg * kh);
-#pragma unroll
-                for (int j = 0; j < kPg / 2; ++j) {
-                  const float4 v = sc[j];
-                  xs4[2 * j] = rs * v.x;
-                  lv4[2 * j] = v.y;
-                  xs4[2 * j + 1] = rs * v.z;
-                  lv4[2 * j + 1] = v.w;
-                }
-              }
-              if (VAR && p.softcap_log2 > 0.f) {
-                // c tanh(s / c) = c (1 - 2 / (e^(2 s / c) + 1)), kept without the factor c
-                const float f = (2.f * kLog2e) / p.softcap_log2;
-#pragma unroll
-                for (int k = 0; k < kMine; ++k)
-                  x[k] = 1.f - __fdividef(2.f, ex2(x[k] * (f * (kScl ? xs4[k / kPageSize] : rs))) + 1.f);
-                xs = p.softcap_log2;
-#pragma unroll
-                for (int j = 0; j < kPg; ++j) xs4[j] = xs;
-              }
-              if constexpr (kScl) {
-#pragma unroll
-                for (int j = 0; j < kPg; ++j) xs4[j] = fmaxf(xs4[j], 1.2e-38f);  // a masked key's -inf stays that
-              }
-              const int key0 = (VAR && tile >= jump ? tile - jump + jump_to : tile) * kKeys + kMine * kh;
-              if (key0 + kMine - 1 > end_min) {
-#pragma unroll
-                for (int k = 0; k < kMine; ++k)
-                  if (key0 + k > vis_end) x[k] = -INFINITY;
-              }
-              if (VAR && key0 < lo_max) {
-#pragma unroll
-                for (int k = 0; k < kMine; ++k)
-                  if (key0 + k < vis_lo && key0 + k >= p.first_tokens) x[k] = -INFINITY;
-              }
-              if constexpr (kScl) {
-#pragma unroll
-                for (int j = 0; j < kPg; ++j) {
-                  float u = -INFINITY;
-#pragma unroll
-                  for (int k = 0; k < kPageSize; k += 2) u = fmax3(u, x[kPageSize * j + k], x[kPageSize * j + k + 1]);
-                  top = fmaxf(top, fmaf(u, xs4[j], lv4[j]));
-                }
-              } else {
-                float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < kMine; k += 2) u[(k >> 1) & 3] = fmax3(u[(k >> 1) & 3], x[k], x[k + 1]);
-                top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * xs;
-              }
-            }
-            // (an item's first tile sets the references: no vote)
-            if (i == 0 || named_bar_or(1 + q, 64, top > m_ref + kMove)) {
-              top = exchange(top, true);
-              const float m_new = top > m_ref + kMove ? top : m_ref;
-              const float alpha = m_new != m_ref && m_ref != -INFINITY ? ex2(m_ref - m_new) : 1.f;
-              if (__any_sync(0xffffffffu, alpha != 1.f) && wait_for(kBarPvDone + (b ^ 1), (cur - 1) >> 1, 2048)) {
-                // O holds earlier tiles (of this piece: m_ref is not -inf)
-                tc_fence_after();
-#pragma unroll 1
-                for (int j = 0; j < kHeadDim / 32; ++j) {
-                  uint32_t o[16];
-                  const uint32_t ta = tmem + lane_base + kColO + 128 * kh + 16 * j;
-                  tmem_ld_32x32b_x16(ta, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                  tmem_st_32x32b_x16(ta, o);
-                }
-                l *= alpha;
-              }
-              m_ref = m_new;
-            }
-            if (ok) {
-              // (a row without a visible key yet: P = 0)
-              const float ref = m_ref == -INFINITY ? INFINITY : m_ref - kShift;
-              uint64_t ls[2] = {0, 0};
-#pragma unroll
-              for (int j = 0; j < kMine / 32; ++j) {
-                uint32_t pw[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const int y = 32 * j + 2 * k;
-                  const float f = kScl ? xs4[y / kPageSize] : xs, off = kScl ? lv4[y / kPageSize] - ref : -ref;
-                  float a, d;
-                  unpack2(fma2(pack2(x[y], x[y + 1]), pack2(f, f), pack2(off, off)), a, d);
-                  a = ex2(a);
-                  d = ex2(d);
-                  ls[k & 1] = add2(ls[k & 1], pack2(a, d));
-                  pw[k] = kFp8 ? pack_f16x2(a, d) : pack_b16x2(a, d);
-                  if (kScl && k % 8 == 7) {  // a page's end: its weights without the V scale
-                    float s0, s1, s2, s3;
-                    unpack2(ls[0], s0, s1);
-                    unpack2(ls[1], s2, s3);
-                    l = fmaf((s0 + s1) + (s2 + s3), ex2(-lv4[y / kPageSize]), l);
-                    ls[0] = ls[1] = 0;
-                  }
-                }
-                // over S: both warps have loaded their parts of it (the barriers above)
-                tmem_st_32x32b_x16(tmem + lane_base + kColS + b * kKeys + kMine / 2 * kh + 16 * j, pw);
-              }
-              if (!kScl) {
-                float s0, s1, s2, s3;
-                unpack2(ls[0], s0, s1);
-                unpack2(ls[1], s2, s3);
-                l += (s0 + s1) + (s2 + s3);
-              }
-              tmem_wait_st();
-            }
-          }
-          if (ok) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead(kBarPFull + b));
-          }
-        }
-        // -- epilogue
-        tiles += n;
-        if (!idle) l = exchange(l, false);
-        if (n > 0) {
-          wait_for(kBarPvDone + ((tiles - 1) & 1), (tiles - 1) >> 1, 4096);
-          tc_fence_after();
-        }
-        if (ok && !idle) {
-          const bool row_ok = row0 + r < pc->L * p.group, direct = pc->direct;
-          const int g = row0 + r - t_r * p.group;
-          if (p.sinks && direct && row_ok && m_ref != -INFINITY)
-            l += ex2(p.sinks[pc->h * p.group + g] * kLog2e - (m_ref - kShift));
-          const float inv = l > 0.f || l != l ? vd / l : 0.f;
-          const int64_t slot = 2 * (int64_t)c + (pc->i0 == 0 ? 1 : 0);
-          const int pr = rank * 128 + r;
-          uint16_t* dst = p.out + (int64_t)(pc->q0 + t_r) * p.o_s0 + (int64_t)(pc->h * p.group + g) * p.o_s1 + 128 * kh;
-          float* acc = p.ws_acc + (slot * kChunkRows + pr) * kHeadDim + 128 * kh;
-          const bool nothing = m_ref == -INFINITY && l == l;  // (all of them NaN: NaN)
-#pragma unroll 1
-          for (int j = 0; j < kHeadDim / 64; ++j) {
-            uint32_t o[32];
-            if (n > 0) {
-              tmem_ld_32x32b_x32(tmem + lane_base + kColO + 128 * kh + 32 * j, o);
-              tmem_wait_ld();
-            }
-            if (!row_ok) continue;
-            if (direct) {
-              uint32_t v[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                v[k] = nothing ? 0u : pack_b16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-              if (p.out_v8) {
-                st_global_v8(dst + 32 * j, v);
-                st_global_v8(dst + 32 * j + 16, v + 8);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  reinterpret_cast<uint4*>(dst + 32 * j)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) st_global_v8(acc + 32 * j + 8 * k, o + 8 * k);
-            }
-          }
-          if (!direct && row_ok && kh == 0)
-            *reinterpret_cast<float2*>(p.ws_ml + (slot * kChunkRows + pr) * 2) =
-                make_float2(nothing ? -INFINITY : m_ref == -INFINITY ? 0.f : m_ref - kShift, l);
-        }
-        if (ok && n > 0) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead(kBarOFree));
-        }
-        if (n > 0) ++piece;
-        give_back();
+    if (warp == kWarpPlan) {
+      Walk w = start_walk(p, *start);
+      __syncwarp();  // (the pieces take start's place)
+      Piece pc;
+      for (bool more = true; more && ok; ++at) {
+        more = next_piece(p, t0, t1, w, pc);
+        if (!more) pc.n = -1;
+        if (at >= kPieces && !wait_for(kBarPieceEmpty + at % kPieces, at / kPieces - 1, 16384)) break;
+        if (lane == 0) *reinterpret_cast<Piece*>(misc + kOffPieces + at % kPieces * sizeof(Piece)) = pc;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPieceFull + at % kPieces));
       }
+    } else if (warp < kWarpMma) {
+      // ======================= TMA producers =========================================
+      // Two warps, for the tiles of even and of odd number. One 2 KB box (a page's 16
+      // tokens x 128 bytes) a lane: this CTA's half of K's keys, or of V's columns. Pages
+      // that no row of the item sees are not mapped perhaps: they are read past the cache's
+      // last page, which TMA fills with zeros. Page ids are loaded two tiles ahead.
+      constexpr int kDim = kFp8 ? 2 : 4;    // 128-byte chunks of a row
+      constexpr int kEl = kFp8 ? 128 : 64;  // elements of a chunk
+      const int mine = warp - kWarpProducer;
+      const bool scl = kScl && lane >= 24;  // lanes that bring the page scales of K's tile
+      int tiles = 0;
+      while (const volatile Piece* pc = take()) {
+        const Span x{pc->x.klo, pc->x.khi, pc->x.nf, pc->x.w0, 0};
+        const int n = pc->n, i0 = pc->i0, h = pc->h;
+        const int* bt = p.block_table + (int64_t)pc->b * p.bt_s0;
+        give_back();
+        auto is_k = [&](int off) { return off == 0 || (off != 2 * n - 1 && (off & 1)); };
+        auto tile_at = [&](int off) { return off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1; };
+        auto page_id = [&](int off) {
+          const bool k = is_k(off);
+          const int of = k ? (scl ? lane - 24 : lane / kDim + 4 * rank) : lane / (kDim / 2);
+          const bool on = k ? scl || lane < 4 * kDim : lane < 8 * (kDim / 2);
+          const int page = tile_of(x, i0 + tile_at(off)) * (kKeys / kPageSize) + of, key = page * kPageSize;
+          const bool seen = off < 2 * n && on && key < x.khi && (key + kPageSize > x.klo || key < p.first_tokens);
+          return seen ? bt[(int64_t)page * p.bt_s1] : -1;
+        };
+        float ks = 1.f, vs = 1.f;
+        auto scales_of = [&](int id) {
+          ks = vs = 1.f;
+          if (scl && (unsigned)id < (unsigned)p.num_blocks) {
+            ks = __ldg(p.k_scales + (int64_t)id * p.ks_s0 + (int64_t)h * p.ks_s1);
+            vs = __ldg(p.v_scales + (int64_t)id * p.vs_s0 + (int64_t)h * p.vs_s1);
+          }
+        };
+        int off = (seq ^ mine) & 1;  // this warp's first tile of the piece
+        int id = page_id(off), id1 = page_id(off + 2);
+        if (kScl) scales_of(id);
+        for (; off < 2 * n && ok; off += 2) {
+          const int s = seq + off, slot = s % C::kRawSlots;
+          if (kFp8) {
+            if (s >= C::kRawSlots && !wait_for(kBarRawEmpty + slot, s / C::kRawSlots - 1, 1)) break;
+          } else {
+            if (s >= C::kOpSlots && !wait_for(kBarEmpty + empty_bar<C::kOpSlots>(s), empty_use<C::kOpSlots>(s), 1)) break;
+          }
+          const bool k = is_k(off);
+          if (kScl && k) {
+            const int t = (tiles + tile_at(off)) % kScaleTiles;
+            if (scl) {
+              const float k1 = fminf(fmaxf(ks, kMinPageScale), kMaxPageScale);
+              const float v1 = fminf(fmaxf(vs, kMinPageScale), kMaxPageScale);
+              page_scale[t * 8 + lane - 24] = make_float2(k1, log2f(v1));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarScales + t));
+          }
+          if (kScl) scales_of(id1);
+          if (lane == 0) {
+            issued[slot] = s;
+            mbar_arrive_expect_tx(bar(kBarRawFull + slot), C::kRawBytes);
+          }
+          __syncwarp();
+          const uint32_t dst = sbase + C::kOffRaw + slot * C::kRawBytes;
+          const int page = (unsigned)id < (unsigned)p.num_blocks ? id : p.num_blocks;
+          if (k) {
+            if (lane < 4 * kDim)
+              tma_load_4d(dst + lane % kDim * (64 * 128) + lane / kDim * 2048, &tm_k, lane % kDim * kEl, h, 0, page,
+                          bar(kBarRawFull + slot));
+          } else if (lane < 8 * (kDim / 2)) {
+            const int ch = lane % (kDim / 2);
+            tma_load_4d(dst + ch * (128 * 128) + lane / (kDim / 2) * 2048, &tm_v, (rank * (kDim / 2) + ch) * kEl, h, 0, page,
+                        bar(kBarRawFull + slot));
+          }
+          __syncwarp();
+          id = id1;
+          id1 = page_id(off + 4);
+        }
+        seq += 2 * n;
+        tiles += n;
+      }
+    } else if (warp == kWarpMma) {
+      // ======================= MMA issuer (the even CTA) ===============================
+      if (rank == 0) {
+        int tiles = 0, piece = 0;
+        while (const volatile Piece* pc = take()) {
+          const int n = pc->n;
+          give_back();
+          if (n == 0) continue;
+          if (!wait_for(kBarQFull, piece, 2)) break;
+          for (int off = 0; off < 2 * n && ok; ++off, ++seq) {
+            const bool is_k = off == 0 || (off != 2 * n - 1 && (off & 1));
+            const int i = off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1;
+            const int slot = seq % C::kOpSlots, use = seq / C::kOpSlots;
+            const int b = (tiles + i) & 1;
+            if (!wait_for(kBarOpFull + slot, use, 4)) break;
+            if (!is_k) {
+              if (!wait_for(kBarPFull + b, (tiles + i) >> 1, 8)) break;
+              if (i == 0 && piece > 0 && !wait_for(kBarOFree, piece - 1, 16)) break;
+            }
+            tc_fence_after();
+            const uint32_t src = sbase + C::kOffOp + slot * C::kOpBytes;
+            if (elect_one()) {
+              if (is_k) {
+#pragma unroll
+                for (int k = 0; k < kHeadDim / 16; ++k) {
+                  const uint32_t ko = (uint32_t)((k & 3) * 32);
+                  mma_f16_pair(tmem + kColS + b * kKeys, smem_desc(sbase + C::kOffQ + (k >> 2) * (128 * 128) + ko, 16, 1024, kLayoutSw128),
+                               smem_desc(src + (k >> 2) * (64 * 128) + ko, 16, 1024, kLayoutSw128), C::kIdQK, k ? 1u : 0u);
+                }
+                mma_commit_pair(bar(kBarSFull + b));
+              } else {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                  mma_f16_pair_ta(tmem + kColO, tmem + kColS + b * kKeys + 8 * k,
+                                  smem_desc(src + k * 2048, 128 * 128, 1024, kLayoutSw128), C::kIdPV, i || k ? 1u : 0u);
+                mma_commit_pair(bar(kBarPvDone + b));
+              }
+              mma_commit_pair(bar(kBarEmpty + empty_bar<C::kOpSlots>(seq + C::kOpSlots)));
+              if (is_k && i == n - 1) mma_commit_pair(bar(kBarQFree));
+            }
+            __syncwarp();
+          }
+          tiles += n;
+          ++piece;
+        }
+        // every MMA has finished before the pair frees its memory
+        if (elect_one()) {
+          mma_commit_pair(bar(kBarDrain));
+          mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
+        }
+        __syncwarp();
+      }
+    }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // (the odd CTA's copy of the last commit: no arrival is under way when it ends)
-  if (t0 < t1 && rank == 1 && tid == 0) mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
+  if (t0 < t1 && tid == 0) {
+    // copies in flight land before the CTA ends, also when a role gave up; and the odd
+    // CTA's copy of the last commit, so that no arrival is under way
+    for (int i = 0; i < C::kRawSlots; ++i)
+      if (issued[i] >= 0) mbar_wait_drain(bar(kBarRawFull + i), (uint32_t)(issued[i] / C::kRawSlots) & 1u, kDrainLimitNs);
+    if (rank == 1) mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
+  }
   __syncwarp();
   // both CTAs are done with each other's barriers and tensor memory
   cluster_arrive();

@@ -467,6 +467,11 @@ __device__ __forceinline__ void named_bar(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
+// Arrives on a named barrier without waiting.
+__device__ __forceinline__ void named_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // Named barrier that also ORs a predicate over its `count` threads.
 __device__ __forceinline__ bool named_bar_or(int id, int count, bool pred) {
   uint32_t r;
@@ -528,6 +533,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // waits for every store of the thread, 1,600 cycles where 100 do).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The same without release: what is handed over is tensor memory alone, ordered by
+// tcgen05's fences on both sides.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
