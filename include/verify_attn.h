@@ -643,9 +643,10 @@ va_status verify_attn_mla_scaled(const va_tensor* q, const va_tensor* kv_cache, 
  * Two launches (the second one joins what pairs shared), asynchronous on
  * stream, capturable; nothing depends on host bounds of the lengths.
  * Accuracy: Q K^T and P V on the tensor cores in 16 bits with fp32 sums. BF16
- * caches: P is rounded to bf16. E4M3 caches: codes are taken as f16 (exact), P is
- * rounded to f16, with steps of 2^-24 * 2^-7 below 2^-21 of the row's reference
- * (within 2^8 of its largest weight), Q exactly down to 2^-31 of a row's largest.
+ * caches: P is rounded to bf16. E4M3 caches: Q enters as two e4m3 terms, bf16's 8
+ * bits in steps of at most 2^-16 of the row's largest; V's codes are taken as f16
+ * (exact) and P is rounded to f16, in steps of 2^-31 below 2^-21 of the row's
+ * reference (within 2^8 of its largest weight).
  * The normaliser, the references and the joined sums are fp32.
  * A value that is NaN or infinite at a key in [0, S) may reach rows of the same
  * sequence that do not see the key; keys may be anything where they are not seen.

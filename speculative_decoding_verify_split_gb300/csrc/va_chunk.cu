@@ -172,51 +172,48 @@ constexpr int kLoadGroups = 2, kLoadWarps = 4 * kLoadGroups;  // a group of four
 constexpr int kProducers = 2;                                 // K's and V's
 constexpr int kWarpProducer = kSoftmaxWarps + kLoadWarps, kWarpMma = kWarpProducer + kProducers, kWarpPlan = kWarpMma + 1;
 constexpr int kThreads = 32 * (kWarpPlan + 1);
-constexpr int kPieces = 4;  // places of the queue of pieces
+constexpr int kPieces = 3;  // places of the queue of pieces
 
-// Tiles (K and V, in the order of their use) go to two warps or groups in turn, those of
-// even and of odd number. A barrier tells two phases apart and no more, so a waiter has to
-// meet every phase of it: where the slots are odd in number, a slot's users take turns,
-// and each gets the arrivals that free the slot for it on a barrier of its own. Tile
-// `seq` waits for use empty_use(seq) of barrier empty_bar(seq); the end of tile `seq`
-// arrives for the slot's next user, on empty_bar(seq + slots).
-template <int SLOTS>
-__device__ __forceinline__ int empty_bar(int seq) { return seq % (2 * SLOTS); }
-template <int SLOTS>
-__device__ __forceinline__ int empty_use(int seq) { return seq / (2 * SLOTS) - (seq % (2 * SLOTS) < SLOTS ? 1 : 0); }
-
+// Shared memory: Q, then K's ring and V's. K goes to the MMAs as TMA brings it. So does a
+// bf16 V; e4m3 codes of V become f16 on the way, from a ring of their own. A waiter meets
+// every phase of its barriers: a ring has one producer, and a slot one user (e4m3 V:
+// two slots for two groups, tile by tile in turn).
 template <int KIND>
 struct Cfg {
   static constexpr bool kFp8 = KIND != kBf16;
-  static constexpr int kOpBytes = 32768;                    // a CTA's half of a K or V tile, 16 bits
-  static constexpr int kOpSlots = kFp8 ? 3 : 5;
-  static constexpr int kRawBytes = kFp8 ? 16384 : kOpBytes;  // what TMA brings
-  static constexpr int kRawSlots = kFp8 ? 4 : kOpSlots;
-  static constexpr int kOffQ = 0;  // [4 d chunks][128 rows][128 bytes]
-  static constexpr int kOffOp = 65536;
-  static constexpr int kOffRaw = kFp8 ? kOffOp + kOpSlots * kOpBytes : kOffOp;
-  static constexpr int kOffMisc = kFp8 ? kOffRaw + kRawSlots * kRawBytes : kOffOp + kOpSlots * kOpBytes;
+  static constexpr int kKBytes = kFp8 ? 16384 : 32768;  // a CTA's half of a K tile: 64 keys
+  static constexpr int kVBytes = 32768;                 // .. of a V tile, 16 bits: 128 columns
+  static constexpr int kRawBytes = 16384;               // .. as e4m3
+  static constexpr int kKSlots = kFp8 ? 4 : 2, kVSlots = kFp8 ? 2 : 3, kRawSlots = kFp8 ? 2 : 0;
+  static constexpr int kOffQ = 0;  // [4][128 rows][128 bytes]: d chunks (bf16), or two of each e4m3 term
+  static constexpr int kOffK = 65536;
+  static constexpr int kOffV = kOffK + kKSlots * kKBytes;
+  static constexpr int kOffRaw = kOffV + kVSlots * kVBytes;
+  static constexpr int kOffMisc = kOffRaw + kRawSlots * kRawBytes;
   static constexpr int kSmemBytes = kOffMisc + 3072;
   static_assert(kSmemBytes <= 232448, "shared memory");
-  static_assert(!kFp8 || kRawSlots % 2 == 0, "a raw slot belongs to one producer and one group");
-  static_assert(kOpSlots % 2 == 1, "empty_bar");
-  // instruction descriptors: f16 (0) or bf16 (1) operands, M = 256
-  static constexpr uint32_t kFmt = kFp8 ? 0u : 1u;
-  static constexpr uint32_t kIdQK = instr_desc(kFmt, kFmt, false, kKeys, 256);
-  static constexpr uint32_t kIdPV = instr_desc(kFmt, kFmt, true, kHeadDim, 256);
+  // what TMA fills: V's own ring, or the codes'
+  static constexpr int kTmaVSlots = kFp8 ? kRawSlots : kVSlots;
+  static constexpr int kTmaVBytes = kFp8 ? kRawBytes : kVBytes, kOffTmaV = kFp8 ? kOffRaw : kOffV;
+  // instruction descriptors, M = 256: bf16 (1) or e4m3 (0), and f16 (0)
+  static constexpr uint32_t kIdQK = instr_desc(kFp8 ? 0u : 1u, kFp8 ? 0u : 1u, false, kKeys, 256);
+  static constexpr uint32_t kIdPV = instr_desc(kFp8 ? 0u : 1u, kFp8 ? 0u : 1u, true, kHeadDim, 256);
 };
 
-// misc area: barriers, scratch of the work scan, row factors, page scales
-constexpr int kMaxRaw = 5, kMaxOp = 5;
-// Tiles whose page scales are kept: the producer, up to 7 of the rings' K and V tiles
-// ahead of the MMAs, writes tile i's once the softmax is through with tile i - 5.
+// misc area: barriers, pieces, row factors, page scales
+constexpr int kMaxK = 4, kMaxV = 3;
+// Tiles whose page scales are kept: the producer, up to four K tiles ahead of the MMAs,
+// writes tile i's once the softmax is through with tile i - 6.
 constexpr int kScaleTiles = 6;
 enum : int {
-  kBarRawFull = 0,
-  kBarOpFull = kBarRawFull + kMaxRaw,
-  kBarEmpty = kBarOpFull + kMaxOp,   // what the MMAs are through with: twice the operand slots (empty_bar)
-  kBarRawEmpty = kBarEmpty + 6,      // e4m3: what has been converted
-  kBarSFull = kBarEmpty + 2 * kMaxOp,
+  kBarKFull = 0,                      // this CTA's half has landed
+  kBarKPeer = kBarKFull + kMaxK,      // .. the odd CTA's (in the even one)
+  kBarKEmpty = kBarKPeer + kMaxK,
+  kBarVLanded = kBarKEmpty + kMaxK,   // what TMA brought of V
+  kBarRawEmpty = kBarVLanded + kMaxV,  // e4m3: converted
+  kBarVFull = kBarRawEmpty + 2,       // V as the MMAs take it, both CTAs' halves
+  kBarVEmpty = kBarVFull + kMaxV,
+  kBarSFull = kBarVEmpty + kMaxV,
   kBarPFull = kBarSFull + 2,
   kBarPvDone = kBarPFull + 2,
   kBarQFull = kBarPvDone + 2,
@@ -229,8 +226,8 @@ enum : int {
   kNumBars = kBarPieceEmpty + kPieces
 };
 constexpr int kOffTmem = 8 * kNumBars, kOffAbort = kOffTmem + 4;
-constexpr int kOffIssued = kOffAbort + 4;  // the last tile that went into each raw slot, or -1
-constexpr int kOffPieces = (kOffIssued + 4 * kMaxRaw + 15) / 16 * 16;      // [kPieces] Piece; before: ChunkStart
+constexpr int kOffIssued = kOffAbort + 4;  // K tiles and V tiles that TMA has been told to bring
+constexpr int kOffPieces = (kOffIssued + 8 + 15) / 16 * 16;      // [kPieces] Piece; before: ChunkStart
 constexpr int kOffRow = kOffPieces + kPieces * 64;               // [2][128] floats
 constexpr int kOffXch = kOffRow + 1024;                          // [2][128] floats; before: 32 x 8 bytes of the scan
 constexpr int kOffScale = kOffXch + 1024;                        // [kScaleTiles][8] (K scale, log2 V scale)
@@ -281,12 +278,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
-    for (int i = 0; i < C::kRawSlots; ++i) {
-      mbar_init(bar(kBarRawFull + i), 1);
-      if (kFp8) mbar_init(bar(kBarRawEmpty + i), 4);
+    for (int i = 0; i < C::kKSlots; ++i) {
+      mbar_init(bar(kBarKFull + i), 1);
+      mbar_init(bar(kBarKPeer + i), 1);
+      mbar_init(bar(kBarKEmpty + i), 1);
     }
-    for (int i = 0; i < C::kOpSlots; ++i) mbar_init(bar(kBarOpFull + i), kFp8 ? 2 * 4 : 2);
-    for (int i = 0; i < 2 * C::kOpSlots; ++i) mbar_init(bar(kBarEmpty + i), 1);
+    for (int i = 0; i < C::kTmaVSlots; ++i) mbar_init(bar(kBarVLanded + i), 1);
+    for (int i = 0; i < C::kRawSlots; ++i) mbar_init(bar(kBarRawEmpty + i), 4);
+    for (int i = 0; i < C::kVSlots; ++i) {
+      mbar_init(bar(kBarVFull + i), kFp8 ? 2 * 4 : 2);
+      mbar_init(bar(kBarVEmpty + i), 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarSFull + i), 1);
       mbar_init(bar(kBarPFull + i), kSoftmaxWarps);  // a group's four warps of each CTA
@@ -299,10 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kScaleTiles; ++i) mbar_init(bar(kBarScales + i), 1);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(bar(kBarPieceFull + i), 1);
-      mbar_init(bar(kBarPieceEmpty + i), kSoftmaxWarps + kLoadWarps + kProducers + (rank == 0 ? 1 : 0));
+      mbar_init(bar(kBarPieceEmpty + i), kWarpPlan);  // every warp before it
     }
     *abort_flag = 0;
-    for (int i = 0; i < kMaxRaw; ++i) issued[i] = -1;
+    issued[0] = issued[1] = 0;
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
@@ -424,7 +426,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(kBarPieceEmpty + at % kPieces));
       ++at;
     };
-    int seq = 0;  // K and V tiles so far: a piece's K0, K1, V0, K2, V1, .., K(n-1), V(n-2), V(n-1)
     if (warp < kSoftmaxWarps) {
       // ======================= softmax / epilogue =====================================
       // Two groups of four warps, a thread a row: group 0 takes the tiles in S buffer 0,
@@ -675,14 +676,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp < kSoftmaxWarps + kLoadWarps) {
       // ======================= loaders ================================================
-      // Q of an item, and K and V tiles on their way from TMA to the MMAs: e4m3 codes
-      // become f16 (exactly), V rows past the last key that a row sees become zeros (0
+      // Q of an item, and V's tiles on their way from TMA to the MMAs: e4m3 codes become
+      // f16 (exactly), rows past the last key that a row of the item sees become zeros (0
       // times what a slot behind the sequence's last token holds would reach O).
-      const int lw = warp - kSoftmaxWarps;        // rows of Q
-      const int lg = lw >> 2, lq = lw & 3;        // group, and warp of it
+      const int lw = warp - kSoftmaxWarps;  // rows of Q
+      const int lg = lw >> 2, lq = lw & 3;  // group, and warp of it
       const float kd = p.k_descale ? *p.k_descale : 1.f;
       const bool neg = p.scale_log2 * kd < 0.f;
-      int piece = 0;
+      int piece = 0, tiles = 0;
       while (const volatile Piece* pc = take()) {
         const int n = pc->n, i0 = pc->i0, h = pc->h, m = pc->m, L = pc->L, q0 = pc->q0;
         const Span x{pc->x.klo, pc->x.khi, pc->x.nf, pc->x.w0, 0};
@@ -695,10 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 raw[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int64_t row = (int64_t)m * kChunkRows + rank * 128 + r0 + kLoadWarps * k;
+            const int row = m * kChunkRows + rank * 128 + r0 + kLoadWarps * k;
             raw[k] = make_uint4(0, 0, 0, 0);
-            if (row < (int64_t)L * p.group) {
-              const int t = (int)row / p.group, g = (int)row - t * p.group;
+            if (row < L * p.group) {
+              const int t = row / p.group, g = row - t * p.group;
               raw[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(q0 + t) * p.q_s0 +
                                                        (int64_t)(h * p.group + g) * p.q_s1 + 8 * lane);
             }
@@ -706,32 +707,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int r = r0 + kLoadWarps * k;
-            uint4 v = raw[k];
             if constexpr (kFp8) {
-              // f16 of q times a power of two that brings the row's largest into [2^14,
-              // 2^15): exact for values down to 2^-31 of it
-              uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+              // two e4m3 terms of q times a power of two that brings the row's largest into
+              // [2^7, 2^8): bf16's 8 bits, in steps of at most 2^-16 of the largest
+              const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
               float mx = 0.f;
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w4[j] << 16)), fabsf(__uint_as_float(w4[j] & 0xFFFF0000u))));
+                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
 #pragma unroll
               for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
               int e = 0;
               if (mx > 0.f && mx < INFINITY) {
-                e = 14 - ((int)(__float_as_uint(mx) >> 23) - 127);
+                e = 7 - ((int)(__float_as_uint(mx) >> 23) - 127);
                 e = e > 120 ? 120 : e < -120 ? -120 : e;
               }
               const float up = __uint_as_float((uint32_t)(e + 127) << 23) * (neg ? -1.f : 1.f);
+              uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w4[j] = pack_f16x2(__uint_as_float(w4[j] << 16) * up, __uint_as_float(w4[j] & 0xFFFF0000u) * up);
-              v = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              for (int j = 0; j < 4; ++j) {
+                const float a = __uint_as_float(w[j] << 16) * up, d = __uint_as_float(w[j] & 0xFFFF0000u) * up;
+                const uint32_t h8 = pack_fp8x2(a, d);
+                const float2 f = unpack_fp8x2(h8);
+                hi[j >> 1] |= h8 << (16 * (j & 1));
+                lo[j >> 1] |= pack_fp8x2(a - f.x, d - f.y) << (16 * (j & 1));
+              }
               if (lane == 0) row_factor[(piece & 1) * 128 + r] = __uint_as_float((uint32_t)(127 - e) << 23);
-            } else if (neg) {
-              v = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
+              unsigned char* dst = sm + C::kOffQ + (lane >> 4) * (128 * 128) + r * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + 8 * (lane & 1);
+              *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(dst + 2 * 128 * 128) = make_uint2(lo[0], lo[1]);
+            } else {
+              const uint32_t flip = neg ? 0x80008000u : 0u;
+              *reinterpret_cast<uint4*>(sm + C::kOffQ + (lane >> 3) * (128 * 128) + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(raw[k].x ^ flip, raw[k].y ^ flip, raw[k].z ^ flip, raw[k].w ^ flip);
             }
-            *reinterpret_cast<uint4*>(sm + C::kOffQ + (lane >> 3) * (128 * 128) + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = v;
           }
         }
         fence_proxy_async_smem();
@@ -739,43 +748,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_cluster(lead(kBarQFull));
         ++piece;
         if (!kFp8 && lw > 0) continue;  // one warp hands the tiles on
-        for (int off = 0; off < 2 * n && ok; ++off, ++seq) {
-          const bool is_k = off == 0 || (off != 2 * n - 1 && (off & 1));
-          const int i = off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1;
-          const int rs = seq % C::kRawSlots, os = seq % C::kOpSlots;
-          if (kFp8 && (seq & 1) != lg) continue;
-          if (!wait_for(kBarRawFull + rs, seq / C::kRawSlots, 64)) break;
-          // V rows from this one on are seen by no row
-          const int valid = is_k ? kKeys : x.khi - tile_of(x, i0 + i) * kKeys;
+        for (int i = 0; i < n && ok; ++i) {
+          const int cur = tiles + i;
+          if (kFp8 && (cur & 1) != lg) continue;
+          // rows of V from this one on are seen by no row
+          const int valid = x.khi - tile_of(x, i0 + i) * kKeys;
           if constexpr (kFp8) {
-            if (seq >= C::kOpSlots && !wait_for(kBarEmpty + empty_bar<C::kOpSlots>(seq), empty_use<C::kOpSlots>(seq), 128)) break;
-            const unsigned char* raw = sm + C::kOffRaw + rs * C::kRawBytes;
-            unsigned char* op = sm + C::kOffOp + os * C::kOpBytes;
+            if (!wait_for(kBarVLanded + lg, cur >> 1, 64)) break;
+            if (cur > 1 && !wait_for(kBarVEmpty + lg, (cur >> 1) - 1, 128)) break;
+            const unsigned char* raw = sm + C::kOffRaw + lg * C::kRawBytes;
+            unsigned char* op = sm + C::kOffV + lg * C::kVBytes;
             const int u = lane & 7;
-            // 16 codes a thread and step: unit u of row-chunk rc (K: 2 chunks of 64 rows, V: 128 rows)
+            // 16 codes a thread and step: unit u (16 columns) of row k * 16 + ..
             uint4 in8[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const int rc = k * 16 + lq * 4 + (lane >> 3);
-              in8[k] = *reinterpret_cast<const uint4*>(raw + rc * 128 + ((u ^ (rc & 7)) << 4));
+              const int row = k * 16 + lq * 4 + (lane >> 3);
+              in8[k] = *reinterpret_cast<const uint4*>(raw + row * 128 + ((u ^ (row & 7)) << 4));
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const int rc = k * 16 + lq * 4 + (lane >> 3);
+              const int row = k * 16 + lq * 4 + (lane >> 3);
               const uint32_t in[4] = {in8[k].x, in8[k].y, in8[k].z, in8[k].w};
               uint32_t h[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
-                h[j] = (uint32_t)v.x | ((uint32_t)v.y << 16);
+                h[j] = row < valid ? (uint32_t)v.x | ((uint32_t)v.y << 16) : 0u;
               }
-              const int row = is_k ? rc & 63 : rc;
-              const int region = is_k ? 2 * (rc >> 6) + (u >> 2) : u >> 2;
-              const bool zero = !is_k && rc >= valid;
-              const uint4 lo = zero ? make_uint4(0, 0, 0, 0) : make_uint4(h[0], h[1], h[2], h[3]);
-              const uint4 hi = zero ? make_uint4(0, 0, 0, 0) : make_uint4(h[4], h[5], h[6], h[7]);
-              unsigned char* dst = op + region * (is_k ? 64 * 128 : 128 * 128) + row * 128;
-              // the lanes of the upper region write their second unit first: a row's
+              const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+              unsigned char* dst = op + (u >> 2) * (128 * 128) + row * 128;
+              // the lanes of the upper 64 columns write their second unit first: a row's
               // eight lanes then reach eight different units
               const int first = u >> 2;
               *reinterpret_cast<uint4*>(dst + (((2 * (u & 3) + first) ^ (row & 7)) << 4)) = first ? hi : lo;
@@ -784,21 +787,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(bar(kBarRawEmpty + rs));
-              mbar_arrive_cluster(lead(kBarOpFull + os));
+              mbar_arrive(bar(kBarRawEmpty + lg));
+              mbar_arrive_cluster(lead(kBarVFull + lg));
             }
           } else {
+            const int slot = cur % C::kVSlots;
+            if (!wait_for(kBarVLanded + slot, cur / C::kVSlots, 64)) break;
             if (valid < kKeys) {
-              unsigned char* op = sm + C::kOffOp + os * C::kOpBytes;
-              const int z0 = valid < 0 ? 0 : valid;
-              for (int k = z0 * 16 + lane; k < kKeys * 16; k += 32)
+              unsigned char* op = sm + C::kOffV + slot * C::kVBytes;
+              for (int k = (valid < 0 ? 0 : valid) * 16 + lane; k < kKeys * 16; k += 32)
                 *reinterpret_cast<uint4*>(op + (k & 15) / 8 * (128 * 128) + (k >> 4) * 128 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
               fence_proxy_async_smem();
               __syncwarp();
             }
-            if (lane == 0) mbar_arrive_cluster(lead(kBarOpFull + os));
+            if (lane == 0) mbar_arrive_cluster(lead(kBarVFull + slot));
           }
         }
+        tiles += n;
         if (!ok) break;
       }
     } else {
@@ -816,28 +821,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp < kWarpMma) {
       // ======================= TMA producers =========================================
-      // Two warps, for the tiles of even and of odd number. One 2 KB box (a page's 16
-      // tokens x 128 bytes) a lane: this CTA's half of K's keys, or of V's columns. Pages
-      // that no row of the item sees are not mapped perhaps: they are read past the cache's
-      // last page, which TMA fills with zeros. Page ids are loaded two tiles ahead.
+      // One warp for K's tiles, one for V's. One 2 KB box (a page's 16 tokens x 128
+      // bytes) a lane: this CTA's half of K's keys, or of V's columns. Pages that no row of
+      // the item sees are not mapped perhaps: they are read past the cache's last page,
+      // which TMA fills with zeros. Page ids are loaded two tiles ahead.
+      const bool is_k = warp == kWarpProducer;
       constexpr int kDim = kFp8 ? 2 : 4;    // 128-byte chunks of a row
       constexpr int kEl = kFp8 ? 128 : 64;  // elements of a chunk
-      const int mine = warp - kWarpProducer;
-      const bool scl = kScl && lane >= 24;  // lanes that bring the page scales of K's tile
+      const int chunks = is_k ? kDim : kDim / 2;
+      const int box_page = lane / chunks + (is_k ? 4 * rank : 0), box_ch = lane % chunks;
+      const bool on = lane < (is_k ? 4 : 8) * chunks;
+      const uint32_t ring = sbase + (is_k ? C::kOffK : C::kOffTmaV);
+      const int bytes = is_k ? C::kKBytes : C::kTmaVBytes, slots = is_k ? C::kKSlots : C::kTmaVSlots;
+      const uint32_t box = ring + (is_k ? box_ch * (64 * 128) + lane / chunks * 2048 : box_ch * (128 * 128) + box_page * 2048);
+      const int el = is_k ? box_ch * kEl : (rank * (kDim / 2) + box_ch) * kEl;
+      const int full = is_k ? kBarKFull : kBarVLanded, empty = is_k ? kBarKEmpty : kFp8 ? kBarRawEmpty : kBarVEmpty;
+      const bool scl = kScl && is_k && lane >= 24;  // lanes that bring the tile's page scales
+      const int page_of = scl ? lane - 24 : box_page;
       int tiles = 0;
       while (const volatile Piece* pc = take()) {
         const Span x{pc->x.klo, pc->x.khi, pc->x.nf, pc->x.w0, 0};
         const int n = pc->n, i0 = pc->i0, h = pc->h;
         const int* bt = p.block_table + (int64_t)pc->b * p.bt_s0;
         give_back();
-        auto is_k = [&](int off) { return off == 0 || (off != 2 * n - 1 && (off & 1)); };
-        auto tile_at = [&](int off) { return off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1; };
-        auto page_id = [&](int off) {
-          const bool k = is_k(off);
-          const int of = k ? (scl ? lane - 24 : lane / kDim + 4 * rank) : lane / (kDim / 2);
-          const bool on = k ? scl || lane < 4 * kDim : lane < 8 * (kDim / 2);
-          const int page = tile_of(x, i0 + tile_at(off)) * (kKeys / kPageSize) + of, key = page * kPageSize;
-          const bool seen = off < 2 * n && on && key < x.khi && (key + kPageSize > x.klo || key < p.first_tokens);
+        auto page_id = [&](int i) {
+          const int page = tile_of(x, i0 + i) * (kKeys / kPageSize) + page_of, key = page * kPageSize;
+          const bool seen = i < n && (on || scl) && key < x.khi && (key + kPageSize > x.klo || key < p.first_tokens);
           return seen ? bt[(int64_t)page * p.bt_s1] : -1;
         };
         float ks = 1.f, vs = 1.f;
@@ -848,103 +857,105 @@ __global__ void __launch_bounds__(kThreads, 1)
             vs = __ldg(p.v_scales + (int64_t)id * p.vs_s0 + (int64_t)h * p.vs_s1);
           }
         };
-        int off = (seq ^ mine) & 1;  // this warp's first tile of the piece
-        int id = page_id(off), id1 = page_id(off + 2);
+        int id = page_id(0), id1 = page_id(1);
         if (kScl) scales_of(id);
-        for (; off < 2 * n && ok; off += 2) {
-          const int s = seq + off, slot = s % C::kRawSlots;
-          if (kFp8) {
-            if (s >= C::kRawSlots && !wait_for(kBarRawEmpty + slot, s / C::kRawSlots - 1, 1)) break;
-          } else {
-            if (s >= C::kOpSlots && !wait_for(kBarEmpty + empty_bar<C::kOpSlots>(s), empty_use<C::kOpSlots>(s), 1)) break;
-          }
-          const bool k = is_k(off);
-          if (kScl && k) {
-            const int t = (tiles + tile_at(off)) % kScaleTiles;
+        for (int i = 0; i < n && ok; ++i) {
+          const int cur = tiles + i, slot = cur % slots;
+          if (cur >= slots && !wait_for(empty + slot, cur / slots - 1, 1)) break;
+          if (kScl && is_k) {
             if (scl) {
               const float k1 = fminf(fmaxf(ks, kMinPageScale), kMaxPageScale);
               const float v1 = fminf(fmaxf(vs, kMinPageScale), kMaxPageScale);
-              page_scale[t * 8 + lane - 24] = make_float2(k1, log2f(v1));
+              page_scale[cur % kScaleTiles * 8 + lane - 24] = make_float2(k1, log2f(v1));
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarScales + t));
+            if (lane == 0) mbar_arrive(bar(kBarScales + cur % kScaleTiles));
+            scales_of(id1);
           }
-          if (kScl) scales_of(id1);
           if (lane == 0) {
-            issued[slot] = s;
-            mbar_arrive_expect_tx(bar(kBarRawFull + slot), C::kRawBytes);
+            issued[is_k ? 0 : 1] = cur + 1;
+            mbar_arrive_expect_tx(bar(full + slot), bytes);
           }
           __syncwarp();
-          const uint32_t dst = sbase + C::kOffRaw + slot * C::kRawBytes;
-          const int page = (unsigned)id < (unsigned)p.num_blocks ? id : p.num_blocks;
-          if (k) {
-            if (lane < 4 * kDim)
-              tma_load_4d(dst + lane % kDim * (64 * 128) + lane / kDim * 2048, &tm_k, lane % kDim * kEl, h, 0, page,
-                          bar(kBarRawFull + slot));
-          } else if (lane < 8 * (kDim / 2)) {
-            const int ch = lane % (kDim / 2);
-            tma_load_4d(dst + ch * (128 * 128) + lane / (kDim / 2) * 2048, &tm_v, (rank * (kDim / 2) + ch) * kEl, h, 0, page,
-                        bar(kBarRawFull + slot));
-          }
+          if (on)
+            tma_load_4d(box + slot * bytes, is_k ? &tm_k : &tm_v, el, h, 0,
+                        (unsigned)id < (unsigned)p.num_blocks ? id : p.num_blocks, bar(full + slot));
           __syncwarp();
           id = id1;
-          id1 = page_id(off + 4);
+          id1 = page_id(i + 2);
         }
-        seq += 2 * n;
         tiles += n;
       }
     } else if (warp == kWarpMma) {
       // ======================= MMA issuer (the even CTA) ===============================
-      if (rank == 0) {
-        int tiles = 0, piece = 0;
-        while (const volatile Piece* pc = take()) {
-          const int n = pc->n;
-          give_back();
-          if (n == 0) continue;
-          if (!wait_for(kBarQFull, piece, 2)) break;
-          for (int off = 0; off < 2 * n && ok; ++off, ++seq) {
-            const bool is_k = off == 0 || (off != 2 * n - 1 && (off & 1));
-            const int i = off == 0 ? 0 : off == 2 * n - 1 ? n - 1 : (off & 1) ? (off + 1) / 2 : off / 2 - 1;
-            const int slot = seq % C::kOpSlots, use = seq / C::kOpSlots;
-            const int b = (tiles + i) & 1;
-            if (!wait_for(kBarOpFull + slot, use, 4)) break;
-            if (!is_k) {
-              if (!wait_for(kBarPFull + b, (tiles + i) >> 1, 8)) break;
-              if (i == 0 && piece > 0 && !wait_for(kBarOFree, piece - 1, 16)) break;
-            }
+      // Q K^T of tile i + 1, then P V of tile i. The odd CTA's warp tells it that its half
+      // of a K tile has landed.
+      int tiles = 0, piece = 0;
+      while (const volatile Piece* pc = take()) {
+        const int n = pc->n;
+        give_back();
+        if (n == 0) continue;
+        if (rank == 1) {
+          for (int i = 0; i < n; ++i) {
+            const int slot = (tiles + i) % C::kKSlots;
+            if (!wait_for(kBarKFull + slot, (tiles + i) / C::kKSlots, 4)) break;
+            if (lane == 0) mbar_arrive_cluster(lead(kBarKPeer + slot));
+          }
+          tiles += n;
+          continue;
+        }
+        if (!wait_for(kBarQFull, piece, 2)) break;
+        for (int i = 0; i <= n && ok; ++i) {
+          if (i < n) {
+            const int cur = tiles + i, slot = cur % C::kKSlots, use = cur / C::kKSlots;
+            if (!wait_for(kBarKFull + slot, use, 4) || !wait_for(kBarKPeer + slot, use, 4)) break;
             tc_fence_after();
-            const uint32_t src = sbase + C::kOffOp + slot * C::kOpBytes;
+            const uint32_t src = sbase + C::kOffK + slot * C::kKBytes;
             if (elect_one()) {
-              if (is_k) {
 #pragma unroll
-                for (int k = 0; k < kHeadDim / 16; ++k) {
-                  const uint32_t ko = (uint32_t)((k & 3) * 32);
-                  mma_f16_pair(tmem + kColS + b * kKeys, smem_desc(sbase + C::kOffQ + (k >> 2) * (128 * 128) + ko, 16, 1024, kLayoutSw128),
-                               smem_desc(src + (k >> 2) * (64 * 128) + ko, 16, 1024, kLayoutSw128), C::kIdQK, k ? 1u : 0u);
-                }
-                mma_commit_pair(bar(kBarSFull + b));
-              } else {
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                  mma_f16_pair_ta(tmem + kColO, tmem + kColS + b * kKeys + 8 * k,
-                                  smem_desc(src + k * 2048, 128 * 128, 1024, kLayoutSw128), C::kIdPV, i || k ? 1u : 0u);
-                mma_commit_pair(bar(kBarPvDone + b));
+              for (int k = 0; k < 16; ++k) {
+                // bf16: 16 columns of d; e4m3: 32, of Q's first term, then of its second
+                const uint32_t ko = (uint32_t)((k & 3) * 32);
+                const uint64_t a = smem_desc(sbase + C::kOffQ + (k >> 2) * (128 * 128) + ko, 16, 1024, kLayoutSw128);
+                const uint64_t b = smem_desc(src + (kFp8 ? (k >> 2) & 1 : k >> 2) * (64 * 128) + ko, 16, 1024, kLayoutSw128);
+                if constexpr (kFp8)
+                  mma_f8f6f4_pair(tmem + kColS + (cur & 1) * kKeys, a, b, C::kIdQK, k ? 1u : 0u);
+                else
+                  mma_f16_pair(tmem + kColS + (cur & 1) * kKeys, a, b, C::kIdQK, k ? 1u : 0u);
               }
-              mma_commit_pair(bar(kBarEmpty + empty_bar<C::kOpSlots>(seq + C::kOpSlots)));
-              if (is_k && i == n - 1) mma_commit_pair(bar(kBarQFree));
+              mma_commit_pair(bar(kBarSFull + (cur & 1)));
+              mma_commit_pair(bar(kBarKEmpty + slot));
+              if (i == n - 1) mma_commit_pair(bar(kBarQFree));
             }
             __syncwarp();
           }
-          tiles += n;
-          ++piece;
+          if (i > 0) {
+            const int cur = tiles + i - 1, slot = cur % C::kVSlots;
+            if (!wait_for(kBarVFull + slot, cur / C::kVSlots, 4)) break;
+            if (!wait_for(kBarPFull + (cur & 1), cur >> 1, 8)) break;
+            if (i == 1 && piece > 0 && !wait_for(kBarOFree, piece - 1, 16)) break;
+            tc_fence_after();
+            const uint32_t src = sbase + C::kOffV + slot * C::kVBytes;
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                mma_f16_pair_ta(tmem + kColO, tmem + kColS + (cur & 1) * kKeys + 8 * k,
+                                smem_desc(src + k * 2048, 128 * 128, 1024, kLayoutSw128), C::kIdPV, i > 1 || k ? 1u : 0u);
+              mma_commit_pair(bar(kBarPvDone + (cur & 1)));
+              mma_commit_pair(bar(kBarVEmpty + slot));
+            }
+            __syncwarp();
+          }
         }
-        // every MMA has finished before the pair frees its memory
-        if (elect_one()) {
-          mma_commit_pair(bar(kBarDrain));
-          mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
-        }
-        __syncwarp();
+        tiles += n;
+        ++piece;
       }
+      // every MMA has finished before the pair frees its memory
+      if (rank == 0 && elect_one()) {
+        mma_commit_pair(bar(kBarDrain));
+        mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
+      }
+      __syncwarp();
     }
     }
   }
@@ -954,8 +965,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (t0 < t1 && tid == 0) {
     // copies in flight land before the CTA ends, also when a role gave up; and the odd
     // CTA's copy of the last commit, so that no arrival is under way
-    for (int i = 0; i < C::kRawSlots; ++i)
-      if (issued[i] >= 0) mbar_wait_drain(bar(kBarRawFull + i), (uint32_t)(issued[i] / C::kRawSlots) & 1u, kDrainLimitNs);
+    for (int k = issued[0] > C::kKSlots ? issued[0] - C::kKSlots : 0; k < issued[0]; ++k)
+      mbar_wait_drain(bar(kBarKFull + k % C::kKSlots), (uint32_t)(k / C::kKSlots) & 1u, kDrainLimitNs);
+    for (int k = issued[1] > C::kTmaVSlots ? issued[1] - C::kTmaVSlots : 0; k < issued[1]; ++k)
+      mbar_wait_drain(bar(kBarVLanded + k % C::kTmaVSlots), (uint32_t)(k / C::kTmaVSlots) & 1u, kDrainLimitNs);
     if (rank == 1) mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
   }
   __syncwarp();

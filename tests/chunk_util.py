@@ -90,6 +90,10 @@ def tolerance(b, want, size, softcap=0.0):
     q, k = np.abs(decode(b.q)), np.abs(b.values(0))
     bound = abs(b.scale) * q.sum(axis=2).max(initial=0.0) * k.max(initial=0.0)  # of |s|, and of sum|q_d k_d| |scale|
     logit = 256 * 2.0 ** -24 * bound + 2.0 ** -21 * 1.45 * bound + 2.0 ** -21
+    if b.kind != "bf16":
+        # q as two e4m3 terms of q 2^e, the row's largest in [2^7, 2^8): the second is
+        # exact, or off by half of e4m3's smallest step, 2^-10: 2^-17 of the row's largest
+        logit += abs(b.scale) * 2.0 ** -17 * q.max(initial=0.0) * k.sum(axis=3).max(initial=0.0)
     if softcap:
         # tanh by 2^x and a quotient: 2^-20 of it and of 1, times the cap
         logit += 2.0 ** -20 * softcap
