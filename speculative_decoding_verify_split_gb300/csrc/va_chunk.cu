@@ -75,8 +75,9 @@ struct Span {
 };
 
 __device__ __forceinline__ Span item_span(const ChunkParams& p, const Seq& s, int m) {
-  const int t0 = (int)((int64_t)kChunkRows * m / p.group);
-  int t1 = (int)(((int64_t)kChunkRows * m + kChunkRows - 1) / p.group);
+  const uint32_t row0 = (uint32_t)kChunkRows * m, group = (uint32_t)p.group;  // (rows fit an int)
+  const int t0 = (int)(row0 / group);
+  int t1 = (int)((row0 + kChunkRows - 1) / group);
   t1 = t1 < s.L - 1 ? t1 : s.L - 1;
   Span x;
   x.khi = s.S - s.L + t1 + 1;
@@ -167,11 +168,7 @@ __device__ __forceinline__ int tile_of(const Span& x, int i) { return i < x.nf ?
 
 enum Kind { kBf16 = 0, kE4m3 = 1, kPageScaled = 2 };
 
-constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadGroups = 2, kLoadWarps = 4 * kLoadGroups;  // a group of four warps takes every other tile
-constexpr int kProducers = 2;                                 // K's and V's
-constexpr int kWarpProducer = kSoftmaxWarps + kLoadWarps, kWarpMma = kWarpProducer + kProducers, kWarpPlan = kWarpMma + 1;
-constexpr int kThreads = 32 * (kWarpPlan + 1);
+constexpr int kSoftmaxWarps = 16;
 constexpr int kPieces = 3;  // places of the queue of pieces
 
 // Shared memory: Q, then K's ring and V's. K goes to the MMAs as TMA brings it. So does a
@@ -181,6 +178,15 @@ constexpr int kPieces = 3;  // places of the queue of pieces
 template <int KIND>
 struct Cfg {
   static constexpr bool kFp8 = KIND != kBf16;
+  // Warps: softmax, loaders, two producers, the MMA's and the planner. The groups of four
+  // loaders convert e4m3 V in turn. Registers a thread: the softmax takes what the others
+  // give up of the launch's (their sum by warpgroup is at most the launch's).
+  static constexpr int kLoadGroups = 2, kLoadWarps = 4 * kLoadGroups;
+  static constexpr int kWarpProducer = kSoftmaxWarps + kLoadWarps, kWarpMma = kWarpProducer + 2, kWarpPlan = kWarpMma + 1;
+  static constexpr int kThreads = 32 * (kWarpPlan + 1);
+  static constexpr int kLaunchRegs = 72, kSoftmaxRegs = 80, kOtherRegs = 56;
+  static_assert(4 * kSoftmaxRegs + (kLoadGroups + 1) * kOtherRegs <= (5 + kLoadGroups) * kLaunchRegs, "registers");
+  static_assert(kThreads * kLaunchRegs <= 65536, "registers");
   static constexpr int kKBytes = kFp8 ? 16384 : 32768;  // a CTA's half of a K tile: 64 keys
   static constexpr int kVBytes = 32768;                 // .. of a V tile, 16 bits: 128 columns
   static constexpr int kRawBytes = 16384;               // .. as e4m3
@@ -228,9 +234,10 @@ enum : int {
 constexpr int kOffTmem = 8 * kNumBars, kOffAbort = kOffTmem + 4;
 constexpr int kOffIssued = kOffAbort + 4;  // K tiles and V tiles that TMA has been told to bring
 constexpr int kOffPieces = (kOffIssued + 8 + 15) / 16 * 16;      // [kPieces] Piece; before: ChunkStart
-constexpr int kOffRow = kOffPieces + kPieces * 64;               // [2][128] floats
-constexpr int kOffXch = kOffRow + 1024;                          // [2][128] floats; before: 32 x 8 bytes of the scan
-constexpr int kOffScale = kOffXch + 1024;                        // [kScaleTiles][8] (K scale, log2 V scale)
+constexpr int kOffRow = kOffPieces + kPieces * 64;               // [2][128] exponents of Q's rows (bytes)
+constexpr int kOffXch = kOffRow + 256;                           // [2][128] floats; before: 32 x 8 bytes of the scan
+constexpr int kOffRef = kOffXch + 1024;                          // [128] floats: the rows' references
+constexpr int kOffScale = kOffRef + 512;                         // [kScaleTiles][8] (K scale, log2 V scale)
 constexpr int kMiscBytes = kOffScale + kScaleTiles * 64;
 static_assert(kMiscBytes <= 3072 && sizeof(Piece) <= 64, "misc area");
 
@@ -252,11 +259,13 @@ __device__ __forceinline__ uint32_t pack_b16x2(float a, float b) {
 
 // VAR: with the code of the window and the soft cap.
 template <int KIND, bool VAR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
     va_chunk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<KIND>;
   constexpr bool kFp8 = C::kFp8;
   constexpr bool kScl = KIND == kPageScaled;
+  constexpr int kThreads = C::kThreads, kLoadWarps = C::kLoadWarps;
+  constexpr int kWarpProducer = C::kWarpProducer, kWarpMma = C::kWarpMma, kWarpPlan = C::kWarpPlan;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw;
   unsigned char* misc = sm + C::kOffMisc;
@@ -266,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long* scratch = reinterpret_cast<long long*>(misc + kOffXch);
   ChunkStart* start = reinterpret_cast<ChunkStart*>(misc + kOffPieces);
   volatile int* issued = reinterpret_cast<volatile int*>(misc + kOffIssued);
-  float* row_factor = reinterpret_cast<float*>(misc + kOffRow);
+  unsigned char* row_exp = misc + kOffRow;
+  float* refs = reinterpret_cast<float*>(misc + kOffRef);
   float* xch = reinterpret_cast<float*>(misc + kOffXch);
   float2* page_scale = reinterpret_cast<float2*>(misc + kOffScale);
 
@@ -291,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarSFull + i), 1);
-      mbar_init(bar(kBarPFull + i), kSoftmaxWarps);  // a group's four warps of each CTA
+      mbar_init(bar(kBarPFull + i), kSoftmaxWarps);  // a group's eight warps of each CTA
       mbar_init(bar(kBarPvDone + i), 1);
     }
     mbar_init(bar(kBarQFull), 2 * kLoadWarps);
@@ -427,16 +437,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++at;
     };
     if (warp < kSoftmaxWarps) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
       // ======================= softmax / epilogue =====================================
-      // Two groups of four warps, a thread a row: group 0 takes the tiles in S buffer 0,
-      // group 1 those in buffer 1, so that one tile's chain of latencies (load, maximum,
-      // powers, store) runs beside the next one's. A row's reference goes from tile to
-      // tile, and so from group to group, through shared memory as soon as the tile's
-      // maximum is known; l stays with the group. In the epilogue a group writes half of
-      // O's columns. After a failure a warp walks on without waits and work, so that the
-      // two warps of a quadrant still meet at every named barrier (1 + q: to group 0,
-      // 5 + q: to group 1, 9 + q: both).
-      const int q = warp & 3, grp = warp >> 2;
+      // Two groups of eight warps: group 0 takes the tiles in S buffer 0, group 1 those in
+      // buffer 1, so that one tile's chain of latencies (load, maximum, powers, store) runs
+      // beside the next one's. Two warps of a group share a lane quadrant, a thread one
+      // row and 64 keys. A row's reference goes from tile to tile, and so from group to
+      // group, as soon as the tile's maximum is known; l stays with the thread. In the
+      // epilogue a warp writes a quarter of O's columns. After a failure a warp walks on
+      // without waits and work, so that they still meet at every named barrier (1 + q: a
+      // group's two warps, whose turn the reference's way grants; 5 + q and 9 + q: that way
+      // to group 0 and to group 1; 13: all).
+      const int q = warp & 3, kh = (warp >> 2) & 1, grp = warp >> 3;
       const uint32_t lane_base = (uint32_t)(32 * q) << 16;
       const int r = 32 * q + lane;  // this CTA's row
       const float kd = p.k_descale ? *p.k_descale : 1.f;
@@ -446,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tiles = 0, piece = 0;
       while (true) {
         const volatile Piece* pc = take();
-        if (named_bar_or(9 + q, 64, pc == nullptr)) break;  // (the two warps leave together)
+        if (named_bar_or(13, 32 * kSoftmaxWarps, pc == nullptr)) break;  // (all leave together)
         const int n = pc->n;
         const int row0 = pc->m * kChunkRows + rank * 128;  // this CTA's first row
         const bool idle = row0 + 32 * q >= pc->L * p.group;  // no row of the quadrant's
@@ -470,11 +482,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kScl) wait_for(kBarScales + cur % kScaleTiles, cur / kScaleTiles, 512);
           wait_for(kBarSFull + grp, cur >> 1, 256);
           tc_fence_after();
-          const uint32_t ts = tmem + lane_base + kColS + grp * kKeys;
+          const uint32_t ts = tmem + lane_base + kColS + grp * kKeys + 64 * kh;  // this warp's keys
           const int tile = tile0 + i;
-          const int key0 = (VAR && tile >= jump ? tile - jump + jump_to : tile) * kKeys;
-          const bool mask_hi = key0 + kKeys - 1 > end_min, mask_lo = VAR && key0 < lo_max;
-          const float2* scales = page_scale + (cur % kScaleTiles) * 8;
+          const int key0 = (VAR && tile >= jump ? tile - jump + jump_to : tile) * kKeys + 64 * kh;
+          const bool mask_hi = key0 + 63 > end_min, mask_lo = VAR && key0 < lo_max;
+          const float2* scales = page_scale + (cur % kScaleTiles) * 8 + 4 * kh;
           const bool cap = VAR && p.softcap_log2 > 0.f;
           // S is read twice, 32 keys at a time: for the row's maximum and for P (its 128
           // values would leave a thread no registers, and half the block no threads; a
@@ -503,9 +515,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto factor = [&](float ks) { return cap ? p.softcap_log2 : fmaxf(rs * ks, 1.2e-38f); };
           float top = -INFINITY;
           if (ok && !idle) {
-            if (kFp8 && first) rs = fmaxf(cscale * row_factor[(piece & 1) * 128 + r], 1.2e-38f);
+            if (kFp8 && first) rs = fmaxf(cscale * __uint_as_float((uint32_t)row_exp[(piece & 1) * 128 + r] << 23), 1.2e-38f);
 #pragma unroll
-            for (int part = 0; part < 4; ++part) {
+            for (int part = 0; part < 2; ++part) {
               uint32_t x[32];
               load(part, x);
               if (cap) {
@@ -534,30 +546,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!kScl) top *= factor(1.f);
             if (cap) tmem_wait_st();
           }
-          // the reference of the tile before, the other group's
+          // the reference of the tile before, the other group's; the maximum of the row's
+          // other keys
           float m_old = -INFINITY;
           if (i > 0) {
-            named_bar(1 + 4 * grp + q, 64);
-            m_old = xch[r];
+            named_bar(5 + 4 * grp + q, 128);
+            m_old = refs[r];
           }
+          xch[128 * kh + r] = top;
+          named_bar(1 + q, 64);
+          top = fmaxf(top, xch[128 * (kh ^ 1) + r]);
           const float m_new = top > m_old + kMove ? top : m_old;
           if (i + 1 < n) {
-            xch[r] = m_new;
-            named_arrive(1 + 4 * (grp ^ 1) + q, 64);
+            if (kh == 0) refs[r] = m_new;
+            named_arrive(5 + 4 * (grp ^ 1) + q, 128);
           }
           if (ok && !idle) {
             if (m_new != m_ref) {
               if (m_ref != -INFINITY) l *= ex2(m_ref - m_new);
               m_ref = m_new;
             }
-            const float alpha = m_new != m_old && m_old != -INFINITY ? ex2(m_old - m_new) : 1.f;
-            if (__any_sync(0xffffffffu, alpha != 1.f) && wait_for(kBarPvDone + (grp ^ 1), (cur - 1) >> 1, 2048)) {
+            const bool move = m_new != m_old && m_old != -INFINITY;
+            if (__any_sync(0xffffffffu, move) && wait_for(kBarPvDone + (grp ^ 1), (cur - 1) >> 1, 2048)) {
+              const float alpha = move ? ex2(m_old - m_new) : 1.f;
               // O holds earlier tiles (of this piece: m_old is not -inf)
               tc_fence_after();
 #pragma unroll 1
-              for (int j = 0; j < kHeadDim / 32; ++j) {
+              for (int j = 0; j < kHeadDim / 64; ++j) {
                 uint32_t o[32];
-                const uint32_t ta = tmem + lane_base + kColO + 32 * j;
+                const uint32_t ta = tmem + lane_base + kColO + 128 * kh + 32 * j;
                 tmem_ld_32x32b_x32(ta, o);
                 tmem_wait_ld();
 #pragma unroll
@@ -569,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float ref = m_ref == -INFINITY ? INFINITY : m_ref - kShift;
             uint64_t ls[2] = {0, 0};
 #pragma unroll
-            for (int part = 0; part < 4; ++part) {
+            for (int part = 0; part < 2; ++part) {
               uint32_t x[32], pw[16];
               load(part, x);
               mask(part, x);
@@ -609,39 +626,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_relaxed(lead(kBarPFull + grp));
           }
         }
-        // -- epilogue: both groups' (reference, sum); O's is the larger reference
+        // -- epilogue: the groups' references (O's is the larger) and the four sums
         tiles += n;
-        named_bar(9 + q, 64);
-        xch[128 * grp + r] = m_ref;
-        named_bar(9 + q, 64);
-        const float m_row = fmaxf(m_ref, xch[128 * (grp ^ 1) + r]);
+        named_bar(13, 32 * kSoftmaxWarps);
+        if (kh == 0) xch[128 * grp + r] = m_ref;
+        named_bar(13, 32 * kSoftmaxWarps);
+        const float m_row = fmaxf(xch[r], xch[128 + r]);
         if (m_ref != m_row) l = m_ref == -INFINITY ? 0.f : l * ex2(m_ref - m_row);
-        named_bar(9 + q, 64);
-        xch[128 * grp + r] = l;
-        named_bar(9 + q, 64);
-        l += xch[128 * (grp ^ 1) + r];
         m_ref = m_row;
+        named_bar(13, 32 * kSoftmaxWarps);
+        if (kh == 1) xch[128 * grp + r] = l;
+        named_bar(13, 32 * kSoftmaxWarps);
+        if (kh == 0) xch[128 * grp + r] = l + xch[128 * grp + r];
+        named_bar(13, 32 * kSoftmaxWarps);
+        l = xch[r] + xch[128 + r];
         if (n > 0) {
           wait_for(kBarPvDone + ((tiles - 1) & 1), (tiles - 1) >> 1, 4096);
           tc_fence_after();
         }
-        if (ok && !idle) {
-          const bool row_ok = row0 + r < pc->L * p.group, direct = pc->direct;
-          const int g = row0 + r - t_r * p.group;
-          if (p.sinks && direct && row_ok && m_ref != -INFINITY)
-            l += ex2(p.sinks[pc->h * p.group + g] * kLog2e - (m_ref - kShift));
+        const bool row_ok = row0 + r < pc->L * p.group, direct = pc->direct;
+        const int g = row0 + r - t_r * p.group, head = pc->h * p.group + g;
+        const int64_t slot = 2 * (int64_t)c + (pc->i0 == 0 ? 1 : 0);
+        uint16_t* dst = p.out + (int64_t)(pc->q0 + t_r) * p.o_s0 + (int64_t)head * p.o_s1 + 128 * grp + 64 * kh;
+        give_back();  // (ahead of the stores, which an arrival would wait for)
+        if (ok) {
+          if (p.sinks && direct && row_ok && m_ref != -INFINITY) l += ex2(p.sinks[head] * kLog2e - (m_ref - kShift));
           const float inv = l > 0.f || l != l ? vd / l : 0.f;
-          const int64_t slot = 2 * (int64_t)c + (pc->i0 == 0 ? 1 : 0);
-          const int pr = rank * 128 + r;
-          uint16_t* dst = p.out + (int64_t)(pc->q0 + t_r) * p.o_s0 + (int64_t)(pc->h * p.group + g) * p.o_s1 + 128 * grp;
-          float* acc = p.ws_acc + (slot * kChunkRows + pr) * kHeadDim + 128 * grp;
           const bool nothing = m_ref == -INFINITY && l == l;  // (all of them NaN: NaN)
-#pragma unroll 1
-          for (int j = 0; j < kHeadDim / 64; ++j) {
+          const int64_t acc_row = slot * kChunkRows + rank * 128 + r;
+          float* acc = p.ws_acc + acc_row * kHeadDim + 128 * grp + 64 * kh;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
             uint32_t o[32];
-            if (n > 0) {
-              tmem_ld_32x32b_x32(tmem + lane_base + kColO + 128 * grp + 32 * j, o);
+            if (n > 0 && !idle) {
+              tmem_ld_32x32b_x32(tmem + lane_base + kColO + 128 * grp + 64 * kh + 32 * j, o);
               tmem_wait_ld();
+            }
+            if (n > 0 && j == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_relaxed(lead(kBarOFree));
             }
             if (!row_ok) continue;
             if (direct) {
@@ -662,19 +686,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 4; ++k) st_global_v8(acc + 32 * j + 8 * k, o + 8 * k);
             }
           }
-          if (!direct && row_ok && grp == 0)
-            *reinterpret_cast<float2*>(p.ws_ml + (slot * kChunkRows + pr) * 2) =
+          if (!direct && row_ok && grp == 0 && kh == 0)
+            *reinterpret_cast<float2*>(p.ws_ml + acc_row * 2) =
                 make_float2(nothing ? -INFINITY : m_ref == -INFINITY ? 0.f : m_ref - kShift, l);
         }
-        if (ok && n > 0) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead(kBarOFree));
-        }
         if (n > 0) ++piece;
-        give_back();
       }
     } else if (warp < kSoftmaxWarps + kLoadWarps) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
       // ======================= loaders ================================================
       // Q of an item, and V's tiles on their way from TMA to the MMAs: e4m3 codes become
       // f16 (exactly), rows past the last key that a row of the item sees become zeros (0
@@ -690,26 +709,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         give_back();
         if (n == 0) continue;
         if (piece > 0 && !wait_for(kBarQFree, piece - 1, 32)) break;
-        // Q: rows lw, lw + 8, .. of this CTA's 128, four at a time
+        // Q: rows lw, lw + 8, .. of this CTA's 128
+        const int rows = L * p.group, row0 = m * kChunkRows + rank * 128;
+        auto q_row = [&](int r) {  // this lane's eight columns of row r
+          const int t = (row0 + r) / p.group, g = row0 + r - t * p.group;
+          return p.q + (int64_t)(q0 + t) * p.q_s0 + (int64_t)(h * p.group + g) * p.q_s1 + 8 * lane;
+        };
+        if constexpr (!kFp8) {
+          // straight into place, all rows under way at once; rows behind the last are zeros
+          auto place = [&](int r) { return C::kOffQ + (lane >> 3) * (128 * 128) + r * 128 + (((lane & 7) ^ (r & 7)) << 4); };
 #pragma unroll 1
-        for (int r0 = lw; r0 < 128; r0 += 4 * kLoadWarps) {
-          uint4 raw[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int row = m * kChunkRows + rank * 128 + r0 + kLoadWarps * k;
-            raw[k] = make_uint4(0, 0, 0, 0);
-            if (row < L * p.group) {
-              const int t = row / p.group, g = row - t * p.group;
-              raw[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(q0 + t) * p.q_s0 +
-                                                       (int64_t)(h * p.group + g) * p.q_s1 + 8 * lane);
+          for (int r = lw; r < 128; r += kLoadWarps) {
+            const bool on = row0 + r < rows;
+            cp_async_16(sbase + place(r), on ? q_row(r) : p.q, on);
+          }
+          cp_async_wait_all();
+          if (neg) {
+#pragma unroll 1
+            for (int r = lw; r < 128; r += kLoadWarps) {
+              uint4* v = reinterpret_cast<uint4*>(sm + place(r));
+              *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u, v->w ^ 0x80008000u);
             }
           }
+        } else {
+          // as two e4m3 terms of q times a power of two that brings the row's largest into
+          // [2^7, 2^8): bf16's 8 bits, in steps of at most 2^-16 of the largest. Four rows at a
+          // time.
+#pragma unroll 1
+          for (int r0 = lw; r0 < 128; r0 += 4 * kLoadWarps) {
+            uint4 raw[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = r0 + kLoadWarps * k;
-            if constexpr (kFp8) {
-              // two e4m3 terms of q times a power of two that brings the row's largest into
-              // [2^7, 2^8): bf16's 8 bits, in steps of at most 2^-16 of the largest
+            for (int k = 0; k < 4; ++k) {
+              const int r = r0 + kLoadWarps * k;
+              raw[k] = row0 + r < rows ? *reinterpret_cast<const uint4*>(q_row(r)) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = r0 + kLoadWarps * k;
               const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
               float mx = 0.f;
 #pragma unroll
@@ -732,14 +768,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 hi[j >> 1] |= h8 << (16 * (j & 1));
                 lo[j >> 1] |= pack_fp8x2(a - f.x, d - f.y) << (16 * (j & 1));
               }
-              if (lane == 0) row_factor[(piece & 1) * 128 + r] = __uint_as_float((uint32_t)(127 - e) << 23);
-              unsigned char* dst = sm + C::kOffQ + (lane >> 4) * (128 * 128) + r * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + 8 * (lane & 1);
-              *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(dst + 2 * 128 * 128) = make_uint2(lo[0], lo[1]);
-            } else {
-              const uint32_t flip = neg ? 0x80008000u : 0u;
-              *reinterpret_cast<uint4*>(sm + C::kOffQ + (lane >> 3) * (128 * 128) + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
-                  make_uint4(raw[k].x ^ flip, raw[k].y ^ flip, raw[k].z ^ flip, raw[k].w ^ flip);
+              if (lane == 0) row_exp[(piece & 1) * 128 + r] = (unsigned char)(127 - e);
+              unsigned char* to = sm + C::kOffQ + (lane >> 4) * (128 * 128) + r * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + 8 * (lane & 1);
+              *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(to + 2 * 128 * 128) = make_uint2(lo[0], lo[1]);
             }
           }
         }
@@ -807,6 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
     } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == kWarpPlan) {
       Walk w = start_walk(p, *start);
       __syncwarp();  // (the pieces take start's place)
@@ -939,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k)
-                mma_f16_pair_ta(tmem + kColO, tmem + kColS + (cur & 1) * kKeys + 8 * k,
+                mma_f16_pair_ta(tmem + kColO, tmem + kColS + (cur & 1) * kKeys + 64 * (k >> 2) + 8 * (k & 3),
                                 smem_desc(src + k * 2048, 128 * 128, 1024, kLayoutSw128), C::kIdPV, i > 1 || k ? 1u : 0u);
               mma_commit_pair(bar(kBarPvDone + (cur & 1)));
               mma_commit_pair(bar(kBarVEmpty + slot));
@@ -983,54 +1016,94 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // CTA x takes the item that the share of pair x + 1 starts in, if it starts inside it
 // and pair x holds the item's first tile: sums the pairs' partials in their order.
-constexpr int kMergeThreads = 256, kMergeRows = kMergeThreads / (kHeadDim / 4);
+constexpr int kMergeThreads = 256, kMergeRows = 32;  // rows of a CTA, four at a time
+constexpr int kMaxPairs = 256;
 
 __global__ void __launch_bounds__(kMergeThreads) va_chunk_merge_kernel(const ChunkParams p) {
+  __shared__ int s_slots[kMaxPairs];
+  __shared__ int s_n;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int c = blockIdx.x + 1;
   const int used = p.ws_start[0].used;
   if (c >= used) return;
   const ChunkStart st = p.ws_start[c];
-  const int64_t unit = (int64_t)kKeys * p.group;
-  const int64_t begin = share_begin(st.total, c, used);
-  if (st.off >= begin || share_begin(st.total, c - 1, used) > st.off) return;
   const Seq s = chunk_seq(p, st.b);
-  const Span x = item_span(p, s, st.m);
-  if (ceil_units(begin - st.off, unit) >= x.n) return;  // pair c - 1 held it all
-  const int r = blockIdx.y * kMergeRows + threadIdx.x / (kHeadDim / 4), col = threadIdx.x % (kHeadDim / 4);
-  const int64_t row = (int64_t)st.m * kChunkRows + r;
-  if (row >= (int64_t)s.L * p.group) return;
-  float M = -INFINITY, den = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = c - 1; k < used; ++k) {
-    int64_t slot = 2 * (int64_t)k;
-    if (k == c - 1) {
-      ++slot;
-    } else {
-      const int64_t i0 = ceil_units(share_begin(st.total, k, used) - st.off, unit);
-      const int64_t i1 = ceil_units(share_begin(st.total, k + 1, used) - st.off, unit);
-      if (i0 >= x.n) break;
-      if (i0 >= i1) continue;
+  const int row0 = st.m * kChunkRows + blockIdx.y * kMergeRows, rows = s.L * p.group;
+  if (row0 >= rows) return;
+  if (threadIdx.x < 32) {
+    // the slots of the item's parts, in the pairs' order
+    const int lane = threadIdx.x;
+    const int64_t unit = (int64_t)kKeys * p.group;
+    int n = 0;
+    if (st.off < share_begin(st.total, c, used) && share_begin(st.total, c - 1, used) <= st.off) {
+      const int tiles = item_span(p, s, st.m).n;
+      for (int k0 = c - 1; k0 < used; k0 += 32) {
+        const int k = k0 + lane;
+        int64_t i0 = 0, i1 = 0;
+        if (k < used) {
+          i0 = ceil_units(share_begin(st.total, k, used) - st.off, unit);
+          i1 = ceil_units(share_begin(st.total, k + 1, used) - st.off, unit);
+          i1 = i1 < tiles ? i1 : tiles;
+        }
+        const unsigned has = __ballot_sync(0xffffffffu, i0 < i1);
+        if (i0 < i1) s_slots[n + __popc(has & ((1u << lane) - 1))] = 2 * k + (i0 == 0 ? 1 : 0);
+        n += __popc(has);
+        if (has == 0) break;
+      }
     }
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + (slot * kChunkRows + r) * 2));
-    const float4 a = __ldcg(reinterpret_cast<const float4*>(p.ws_acc + (slot * kChunkRows + r) * kHeadDim) + col);
-    if (ml.x == -INFINITY) continue;
-    const float mc = fmaxf(M, ml.x);
-    const float w0 = M == -INFINITY ? 0.f : exp2f(M - mc), w1 = exp2f(ml.x - mc);
-    den = den * w0 + ml.y * w1;
-    acc.x = acc.x * w0 + a.x * w1;
-    acc.y = acc.y * w0 + a.y * w1;
-    acc.z = acc.z * w0 + a.z * w1;
-    acc.w = acc.w * w0 + a.w * w1;
-    M = mc;
+    if (lane == 0) s_n = n;
   }
-  const int t = (int)row / p.group, g = (int)row - t * p.group;
-  if (p.sinks && M != -INFINITY) den += exp2f(p.sinks[st.h * p.group + g] * kLog2e - M);
+  __syncthreads();
+  const int n = s_n;
+  if (n < 2) return;  // no item is split here, or an earlier pair's CTA joins it
   const float vd = p.v_descale ? *p.v_descale : 1.f;
-  const float inv = M != -INFINITY ? vd / den : 0.f;
-  uint16_t* dst = p.out + (int64_t)(s.q0 + t) * p.o_s0 + (int64_t)(st.h * p.group + g) * p.o_s1 + 4 * col;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_b16x2(acc.x * inv, acc.y * inv), pack_b16x2(acc.z * inv, acc.w * inv));
+  const int col = threadIdx.x % (kHeadDim / 4);
+#pragma unroll 2
+  for (int i = threadIdx.x / (kHeadDim / 4); i < kMergeRows; i += kMergeThreads / (kHeadDim / 4)) {
+    const int row = row0 + i, r = blockIdx.y * kMergeRows + i;
+    if (row >= rows) break;
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < n; k0 += 4) {
+      float2 ml[4];
+      float4 a[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + k < n) {
+          const int64_t at = (int64_t)s_slots[k0 + k] * kChunkRows + r;
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml + at * 2));
+          a[k] = __ldcg(reinterpret_cast<const float4*>(p.ws_acc + at * kHeadDim) + col);
+        }
+      }
+      const float mc = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+      if (mc == -INFINITY) continue;
+      const float w = M == -INFINITY ? 0.f : exp2f(M - mc);
+      den *= w;
+      acc.x *= w;
+      acc.y *= w;
+      acc.z *= w;
+      acc.w *= w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (ml[k].x == -INFINITY) continue;  // no visible key: its partial holds nothing
+        const float u = exp2f(ml[k].x - mc);
+        den = fmaf(ml[k].y, u, den);
+        acc.x = fmaf(a[k].x, u, acc.x);
+        acc.y = fmaf(a[k].y, u, acc.y);
+        acc.z = fmaf(a[k].z, u, acc.z);
+        acc.w = fmaf(a[k].w, u, acc.w);
+      }
+      M = mc;
+    }
+    const int t = row / p.group, g = row - t * p.group;
+    if (p.sinks && M != -INFINITY) den += exp2f(p.sinks[st.h * p.group + g] * kLog2e - M);
+    const float inv = M != -INFINITY ? vd / den : 0.f;
+    uint16_t* dst = p.out + (int64_t)(s.q0 + t) * p.o_s0 + (int64_t)(st.h * p.group + g) * p.o_s1 + 4 * col;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_b16x2(acc.x * inv, acc.y * inv), pack_b16x2(acc.z * inv, acc.w * inv));
+  }
 }
 
 template <int KIND, bool VAR>
@@ -1039,7 +1112,7 @@ cudaError_t prepare_one(int32_t* max_pairs) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Cfg<KIND>::kThreads);
   cfg.dynamicSmemBytes = Cfg<KIND>::kSmemBytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1050,6 +1123,7 @@ cudaError_t prepare_one(int32_t* max_pairs) {
   int n = 0;
   e = cudaOccupancyMaxActiveClusters(&n, va_chunk_kernel<KIND, VAR>, &cfg);
   if (n < *max_pairs) *max_pairs = n;
+  if (*max_pairs > kMaxPairs) *max_pairs = kMaxPairs;
   return e;
 }
 
@@ -1068,6 +1142,7 @@ cudaError_t prepare_chunk(int32_t* max_pairs) {
 
 template <int KIND>
 static cudaError_t launch_main(cudaLaunchConfig_t& cfg, const ChunkParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v) {
+  cfg.blockDim = dim3(Cfg<KIND>::kThreads);
   cfg.dynamicSmemBytes = Cfg<KIND>::kSmemBytes;
   return p.window_left >= 0 || p.softcap_log2 > 0.f ? cudaLaunchKernelEx(&cfg, va_chunk_kernel<KIND, true>, p, tm_k, tm_v)
                                                     : cudaLaunchKernelEx(&cfg, va_chunk_kernel<KIND, false>, p, tm_k, tm_v);
@@ -1086,7 +1161,6 @@ cudaError_t launch_chunk(const ChunkParams& p, const CUtensorMap& tm_k, const CU
   cfg.numAttrs = 2;
   cfg.stream = stream;
   cfg.gridDim = dim3(2 * p.pairs);
-  cfg.blockDim = dim3(kThreads);
   const cudaError_t e = p.k_scales ? launch_main<kPageScaled>(cfg, p, tm_k, tm_v)
                         : p.kv_fp8 ? launch_main<kE4m3>(cfg, p, tm_k, tm_v)
                                    : launch_main<kBf16>(cfg, p, tm_k, tm_v);
