@@ -17,6 +17,12 @@ using namespace ptx;
 constexpr int kKeys = kChunkKeys;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// n / p.group for 0 <= n < 2^31: with s = ceil(log2 d) and m = floor(2^(31 + s) / d) + 1,
+// n m / 2^(31 + s) is above n / d by less than 1 / d (0 < m d - 2^(31 + s) <= d <= 2^s).
+__device__ __forceinline__ int by_group(const ChunkParams& p, int n) {
+  return p.group == 1 ? n : (int)(__umulhi((uint32_t)n, p.group_m) >> p.group_s);
+}
+
 // ---- the split of the work ----------------------------------------------------------
 
 struct Seq {
@@ -75,9 +81,9 @@ struct Span {
 };
 
 __device__ __forceinline__ Span item_span(const ChunkParams& p, const Seq& s, int m) {
-  const uint32_t row0 = (uint32_t)kChunkRows * m, group = (uint32_t)p.group;  // (rows fit an int)
-  const int t0 = (int)(row0 / group);
-  int t1 = (int)((row0 + kChunkRows - 1) / group);
+  const int row0 = kChunkRows * m;  // (rows fit an int)
+  const int t0 = by_group(p, row0);
+  int t1 = by_group(p, row0 + kChunkRows - 1);
   t1 = t1 < s.L - 1 ? t1 : s.L - 1;
   Span x;
   x.khi = s.S - s.L + t1 + 1;
@@ -178,14 +184,15 @@ constexpr int kPieces = 3;  // places of the queue of pieces
 template <int KIND>
 struct Cfg {
   static constexpr bool kFp8 = KIND != kBf16;
-  // Warps: softmax, loaders, two producers, the MMA's and the planner. The groups of four
-  // loaders convert e4m3 V in turn. Registers a thread: the softmax takes what the others
-  // give up of the launch's (their sum by warpgroup is at most the launch's).
+  // Warps: softmax, loaders (two groups of four, which convert e4m3 V in turn), two
+  // producers, the MMA's and the planner. Registers a thread: each warpgroup trades its
+  // share of the launch's 72; the last one, with the MMA issuer, is the one that pays
+  // most for a spill (80 / 56 / 56: bf16 1,190 us where this takes 1,138).
   static constexpr int kLoadGroups = 2, kLoadWarps = 4 * kLoadGroups;
   static constexpr int kWarpProducer = kSoftmaxWarps + kLoadWarps, kWarpMma = kWarpProducer + 2, kWarpPlan = kWarpMma + 1;
   static constexpr int kThreads = 32 * (kWarpPlan + 1);
-  static constexpr int kLaunchRegs = 72, kSoftmaxRegs = 80, kOtherRegs = 56;
-  static_assert(4 * kSoftmaxRegs + (kLoadGroups + 1) * kOtherRegs <= (5 + kLoadGroups) * kLaunchRegs, "registers");
+  static constexpr int kLaunchRegs = 72, kSoftmaxRegs = 80, kLoadRegs = 48, kOtherRegs = 88;
+  static_assert(4 * kSoftmaxRegs + kLoadGroups * kLoadRegs + kOtherRegs <= (5 + kLoadGroups) * kLaunchRegs, "registers");
   static_assert(kThreads * kLaunchRegs <= 65536, "registers");
   static constexpr int kKBytes = kFp8 ? 16384 : 32768;  // a CTA's half of a K tile: 64 keys
   static constexpr int kVBytes = 32768;                 // .. of a V tile, 16 bits: 128 columns
@@ -452,7 +459,6 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
       const uint32_t lane_base = (uint32_t)(32 * q) << 16;
       const int r = 32 * q + lane;  // this CTA's row
       const float kd = p.k_descale ? *p.k_descale : 1.f;
-      const float vd = p.v_descale ? *p.v_descale : 1.f;
       const float cscale = fmaxf(fabsf(p.scale_log2 * kd), 1e-30f);  // the sign is Q's
       constexpr float kShift = kFp8 ? 7.f : 0.f;
       int tiles = 0, piece = 0;
@@ -462,11 +468,11 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
         const int n = pc->n;
         const int row0 = pc->m * kChunkRows + rank * 128;  // this CTA's first row
         const bool idle = row0 + 32 * q >= pc->L * p.group;  // no row of the quadrant's
-        const int t_r = (row0 + r) / p.group;  // the row's token
+        const int t_r = by_group(p, row0 + r);  // the row's token
         // keys that this row sees: up to vis_end, from vis_lo on or below first_tokens;
         // tiles with keys past end_min, or before lo_max, are masked
         const int vis_end = t_r < pc->L ? pc->S - pc->L + t_r : -1;
-        const int end_min = pc->S - pc->L + pc->m * kChunkRows / p.group;
+        const int end_min = pc->S - pc->L + by_group(p, pc->m * kChunkRows);
         int vis_lo = 0, lo_max = 0;
         if (VAR && p.window_left >= 0) {
           const int64_t lo = (int64_t)vis_end - p.window_left, hi = (int64_t)pc->x.khi - 1 - p.window_left;
@@ -651,6 +657,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
         give_back();  // (ahead of the stores, which an arrival would wait for)
         if (ok) {
           if (p.sinks && direct && row_ok && m_ref != -INFINITY) l += ex2(p.sinks[head] * kLog2e - (m_ref - kShift));
+          const float vd = p.v_descale ? *p.v_descale : 1.f;
           const float inv = l > 0.f || l != l ? vd / l : 0.f;
           const bool nothing = m_ref == -INFINITY && l == l;  // (all of them NaN: NaN)
           const int64_t acc_row = slot * kChunkRows + rank * 128 + r;
@@ -693,7 +700,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
         if (n > 0) ++piece;
       }
     } else if (warp < kSoftmaxWarps + kLoadWarps) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLoadRegs));
       // ======================= loaders ================================================
       // Q of an item, and V's tiles on their way from TMA to the MMAs: e4m3 codes become
       // f16 (exactly), rows past the last key that a row of the item sees become zeros (0
@@ -712,13 +719,13 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
         // Q: rows lw, lw + 8, .. of this CTA's 128
         const int rows = L * p.group, row0 = m * kChunkRows + rank * 128;
         auto q_row = [&](int r) {  // this lane's eight columns of row r
-          const int t = (row0 + r) / p.group, g = row0 + r - t * p.group;
+          const int t = by_group(p, row0 + r), g = row0 + r - t * p.group;
           return p.q + (int64_t)(q0 + t) * p.q_s0 + (int64_t)(h * p.group + g) * p.q_s1 + 8 * lane;
         };
         if constexpr (!kFp8) {
           // straight into place, all rows under way at once; rows behind the last are zeros
           auto place = [&](int r) { return C::kOffQ + (lane >> 3) * (128 * 128) + r * 128 + (((lane & 7) ^ (r & 7)) << 4); };
-#pragma unroll 1
+#pragma unroll 4
           for (int r = lw; r < 128; r += kLoadWarps) {
             const bool on = row0 + r < rows;
             cp_async_16(sbase + place(r), on ? q_row(r) : p.q, on);
@@ -791,30 +798,33 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
             const unsigned char* raw = sm + C::kOffRaw + lg * C::kRawBytes;
             unsigned char* op = sm + C::kOffV + lg * C::kVBytes;
             const int u = lane & 7;
-            // 16 codes a thread and step: unit u (16 columns) of row k * 16 + ..
-            uint4 in8[8];
+            // 16 codes a thread and step: unit u (16 columns) of a row
+#pragma unroll 1
+            for (int k0 = 0; k0 < 8; k0 += 2) {
+              uint4 in8[2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int row = k * 16 + lq * 4 + (lane >> 3);
-              in8[k] = *reinterpret_cast<const uint4*>(raw + row * 128 + ((u ^ (row & 7)) << 4));
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int row = k * 16 + lq * 4 + (lane >> 3);
-              const uint32_t in[4] = {in8[k].x, in8[k].y, in8[k].z, in8[k].w};
-              uint32_t h[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
-                h[j] = row < valid ? (uint32_t)v.x | ((uint32_t)v.y << 16) : 0u;
+              for (int k = 0; k < 2; ++k) {
+                const int row = (k0 + k) * 16 + lq * 4 + (lane >> 3);
+                in8[k] = *reinterpret_cast<const uint4*>(raw + row * 128 + ((u ^ (row & 7)) << 4));
               }
-              const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-              unsigned char* dst = op + (u >> 2) * (128 * 128) + row * 128;
-              // the lanes of the upper 64 columns write their second unit first: a row's
-              // eight lanes then reach eight different units
-              const int first = u >> 2;
-              *reinterpret_cast<uint4*>(dst + (((2 * (u & 3) + first) ^ (row & 7)) << 4)) = first ? hi : lo;
-              *reinterpret_cast<uint4*>(dst + (((2 * (u & 3) + (first ^ 1)) ^ (row & 7)) << 4)) = first ? lo : hi;
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int row = (k0 + k) * 16 + lq * 4 + (lane >> 3);
+                const uint32_t in[4] = {in8[k].x, in8[k].y, in8[k].z, in8[k].w};
+                uint32_t h[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+                  h[j] = row < valid ? (uint32_t)v.x | ((uint32_t)v.y << 16) : 0u;
+                }
+                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                unsigned char* dst = op + (u >> 2) * (128 * 128) + row * 128;
+                // the lanes of the upper 64 columns write their second unit first: a row's
+                // eight lanes then reach eight different units
+                const int first = u >> 2;
+                *reinterpret_cast<uint4*>(dst + (((2 * (u & 3) + first) ^ (row & 7)) << 4)) = first ? hi : lo;
+                *reinterpret_cast<uint4*>(dst + (((2 * (u & 3) + (first ^ 1)) ^ (row & 7)) << 4)) = first ? lo : hi;
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -839,7 +849,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
         if (!ok) break;
       }
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == kWarpPlan) {
       Walk w = start_walk(p, *start);
       __syncwarp();  // (the pieces take start's place)
@@ -1098,7 +1108,7 @@ __global__ void __launch_bounds__(kMergeThreads) va_chunk_merge_kernel(const Chu
       }
       M = mc;
     }
-    const int t = row / p.group, g = row - t * p.group;
+    const int t = by_group(p, row), g = row - t * p.group;
     if (p.sinks && M != -INFINITY) den += exp2f(p.sinks[st.h * p.group + g] * kLog2e - M);
     const float inv = M != -INFINITY ? vd / den : 0.f;
     uint16_t* dst = p.out + (int64_t)(s.q0 + t) * p.o_s0 + (int64_t)(st.h * p.group + g) * p.o_s1 + 4 * col;

@@ -35,6 +35,7 @@ struct ChunkParams {
   int64_t o_s0, o_s1;
   int32_t out_v8;          // 32-byte stores fit out
   int32_t num_seqs, hq, hkv, group, num_blocks, total_q;
+  uint32_t group_m, group_s;  // division by group (by_group)
   int32_t kv_fp8;
   float scale_log2;        // softmax_scale * log2(e)
   float softcap_log2;      // 0: none

@@ -129,6 +129,12 @@ VA_EXPORT va_status verify_attn_chunk(const va_tensor* q, const va_tensor* k_cac
   p.hq = (int32_t)sh.hq;
   p.hkv = (int32_t)sh.hkv;
   p.group = (int32_t)(sh.hq / sh.hkv);
+  if (p.group > 1) {
+    int log2 = 1;
+    while ((1ll << log2) < p.group) ++log2;
+    p.group_m = (uint32_t)((1ull << (31 + log2)) / (uint32_t)p.group + 1);
+    p.group_s = (uint32_t)(log2 - 1);
+  }
   p.num_blocks = (int32_t)sh.num_blocks;
   p.total_q = (int32_t)sh.total_q;
   p.kv_fp8 = sh.kv_dtype == VA_FP8_E4M3;
