@@ -506,6 +506,37 @@ va_status verify_attn_append_kv(const va_tensor* q, const va_tensor* k, const va
                                 va_tensor* k_cache, va_tensor* v_cache, void* stream);
 
 /*
+ * va_norm - norms of queries and keys over each head's 256 columns, ahead of the
+ * rotation: x becomes x / sqrt(mean(x^2) + eps) * (weight + offset), in fp32, not
+ * rounded before the rotation.
+ *  q_weight, k_weight  [256] bf16 or fp32, contiguous, 16-byte aligned; NULL: queries
+ *               (keys) are not normalised.
+ *  eps          >= 0, finite.   offset  finite: 1 for weights stored as their
+ *               difference from 1, else 0.
+ */
+typedef struct va_norm {
+  const va_tensor* q_weight;
+  const va_tensor* k_weight;
+  float eps;
+  float offset;
+} va_norm;
+
+/*
+ * verify_attn_append_kv_norm - verify_attn_append_kv with norms of the queries and
+ * keys in the same pass: q_out, the keys stored and a page's scale of keys are those of
+ * the normalised and rotated values. norm NULL: verify_attn_append_kv. With a q_weight,
+ * rope may be NULL (queries normalised only); a q_weight without q is VA_ERR_NULL. Errors
+ * of the weights: VA_ERR_DTYPE, VA_ERR_SHAPE, VA_ERR_LAYOUT, VA_ERR_NULL; VA_ERR_UNSUPPORTED
+ * for eps or offset out of range. Otherwise as verify_attn_append_kv, in one launch.
+ */
+va_status verify_attn_append_kv_norm(const va_tensor* q, const va_tensor* k, const va_tensor* v,
+                                     const va_tensor* block_table, const va_tensor* cu_seqlens_q,
+                                     const va_tensor* seqused_k, const va_norm* norm, const va_rope* rope,
+                                     const va_tensor* k_descale, const va_tensor* v_descale, va_tensor* k_scales,
+                                     va_tensor* v_scales, va_tensor* q_out, va_tensor* k_cache,
+                                     va_tensor* v_cache, void* stream);
+
+/*
  * verify_attn_append_mla - the same for a latent cache (verify_attn_mla): new
  * token t's row is [latent | rotated k_pe].
  *

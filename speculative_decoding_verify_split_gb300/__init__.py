@@ -35,7 +35,8 @@ EXPORTS = ("verify_attn", "verify_attn_ex", "verify_attn_check", "verify_attn_pl
            "verify_attn_mla_workspace_size", "verify_attn_partial", "verify_attn_merge_partials",
            "verify_attn_last_device_error", "verify_attn_set_wait_limit",
            "verify_attn_append_kv", "verify_attn_append_mla", "verify_attn_scaled",
-           "verify_attn_mla_scaled", "verify_attn_chunk", "verify_attn_chunk_workspace_size")
+           "verify_attn_mla_scaled", "verify_attn_chunk", "verify_attn_chunk_workspace_size",
+           "verify_attn_append_kv_norm")
 
 # Absorbed-MLA latent cache: row = [latent (MLA_NOPE) | rope key (MLA_PE)].
 MLA_NOPE, MLA_PE = 512, 64
@@ -67,6 +68,11 @@ class VaOptions(ctypes.Structure):
 class VaRope(ctypes.Structure):
     _fields_ = [("cos_sin", ctypes.POINTER(VaTensor)), ("positions", ctypes.POINTER(VaTensor)),
                 ("interleaved", ctypes.c_int32)]
+
+
+class VaNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.POINTER(VaTensor)), ("k_weight", ctypes.POINTER(VaTensor)),
+                ("eps", ctypes.c_float), ("offset", ctypes.c_float)]
 
 
 class VerifyAttnError(RuntimeError):
@@ -129,6 +135,8 @@ def _lib():
         R, V = ctypes.POINTER(VaRope), ctypes.c_void_p
         lib.verify_attn_append_kv.argtypes = [P] * 6 + [R] + [P] * 7 + [V]
         lib.verify_attn_append_kv.restype = ctypes.c_int32
+        lib.verify_attn_append_kv_norm.argtypes = [P] * 6 + [ctypes.POINTER(VaNorm), R] + [P] * 7 + [V]
+        lib.verify_attn_append_kv_norm.restype = ctypes.c_int32
         lib.verify_attn_append_mla.argtypes = [P] * 6 + [R] + [P] * 4 + [V]
         lib.verify_attn_append_mla.restype = ctypes.c_int32
         lib.verify_attn_scaled.argtypes = [P] * 8 + [ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
@@ -560,18 +568,26 @@ def merge_partials(parts, out=None, stream=None):
 
 def append_kv(k, v, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, q=None, q_out=None,
               cos_sin=None, positions=None, interleaved: bool = False, k_descale=None,
-              v_descale=None, k_scales=None, v_scales=None, stream=None):
+              v_descale=None, k_scales=None, v_scales=None, stream=None, q_norm=None, k_norm=None,
+              norm_eps: float = 1e-6, norm_offset: float = 0.0):
     """Rotates a batch's new queries and keys and stores its new keys and
     values in the paged cache (see include/verify_attn.h): what runs before
     ``verify_attn`` on the same block_table, cu_seqlens_q and seqused_k, or,
     with k_scales / v_scales [num_blocks, Hkv] fp32, before
-    ``verify_attn_scaled``. Caches and scales are written in place. Returns
+    ``verify_attn_scaled``, or before ``verify_attn_chunk``. With q_norm / k_norm
+    ([256], bf16 or fp32) queries / keys are first normalised head by head: x / sqrt(mean(x^2) +
+    norm_eps) * (weight + norm_offset). Caches and scales are written in place. Returns
     ``q_out`` (created if q is given without it; it may be q itself), or None."""
     if q is not None and q_out is None:
         q_out = _empty(q.shape, q, stream)
-    s = _native().append_kv(q, k, v, block_table, cu_seqlens_q, seqused_k, k_descale, v_descale,
-                            k_scales, v_scales, q_out, k_cache, v_cache, cos_sin, positions,
-                            interleaved, _handle(stream))
+    if q_norm is None and k_norm is None:
+        s = _native().append_kv(q, k, v, block_table, cu_seqlens_q, seqused_k, k_descale, v_descale,
+                                k_scales, v_scales, q_out, k_cache, v_cache, cos_sin, positions,
+                                interleaved, _handle(stream))
+    else:
+        s = _native().append_kv_norm(q, k, v, block_table, cu_seqlens_q, seqused_k, k_descale, v_descale,
+                                     k_scales, v_scales, q_out, k_cache, v_cache, cos_sin, positions,
+                                     interleaved, q_norm, k_norm, norm_eps, norm_offset, _handle(stream))
     if s != VA_OK:
         raise VerifyAttnError(s, "verify_attn_append_kv")
     return q_out

@@ -20,6 +20,10 @@
 // multiply-add), so the stored bytes are those of the same formula in any
 // fp32 arithmetic.
 //
+// With norms a head's row is first multiplied by 1 / sqrt(mean x^2 + eps) and its
+// columns' weights: a warp holds the row anyway, so the sum takes five shuffles, for four
+// rows side by side.
+//
 // Every byte is read and written once, so the bound is memory: the prompts of
 // 8 sequences (14,274 tokens, 32 query and 2 KV heads, page scales, 526 MB)
 // take 83.4 us, 93 % of the measured copy bandwidth; latent prompts of 39,119
@@ -264,12 +268,53 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// The sums of four values over the warp's lanes, in every lane.
+__device__ __forceinline__ void warp_sum4(float* v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+}
+
+// The norm's weights of a lane's eight columns, the offset added.
+__device__ __forceinline__ void norm_weights(const void* w, bool fp32, float offset, const Lane& col, float* x) {
+  if (fp32) {
+    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + col.o1);
+    const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + col.o2);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    unpack4(*reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + col.o1), x);
+    unpack4(*reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + col.o2), x + 4);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] += offset;
+}
+
+// Four rows of 256, eight columns of each a lane, times 1 / sqrt(mean x^2 + eps) and w.
+__device__ __forceinline__ void normalise4(float (&x)[4][8], const float* w, float eps) {
+  float s[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    s[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[k] = fmaf(x[k][i], x[k][i], s[k]);
+  }
+  warp_sum4(s);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float r = rsqrtf(fmaf(s[k], 1.f / kHeadDim, eps));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[k][i] = x[k][i] * r * w[i];
+  }
+}
+
 // ---- keys, values and queries of a GQA cache -----------------------------------
 //
 // blockIdx.y < 2 hkv: the page's K rows (even) or V rows (odd) of one KV head,
 // four slots of the page per warp. Above: the same tokens' rows of
-// kHeadsPerCta query heads, a token per warp.
-template <int KIND, bool INTER>
+// kHeadsPerCta query heads, a token per warp. NORM: with the norms' code.
+template <int KIND, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kKvThreads, 8) va_append_kernel(const AppendParams p) {
   constexpr int kWarps = kKvThreads / 32;
   __shared__ UnitShared sh;
@@ -300,11 +345,30 @@ __global__ void __launch_bounds__(kKvThreads, 8) va_append_kernel(const AppendPa
         sn = *reinterpret_cast<const float4*>(cs + p.rot / 2);
       }
       uint16_t* out = p.q_out + (int64_t)tok * p.qo_s0;
+      float xn[4][8];
+      if constexpr (NORM) {
+        static_assert(kHeadsPerCta == 4, "normalise4");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          unpack4(w1[i], xn[i]);
+          unpack4(w2[i], xn[i] + 4);
+        }
+        if (p.q_norm) {
+          float w[8];
+          norm_weights(p.q_norm, p.q_norm_fp32, p.norm_offset, col, w);
+          normalise4(xn, w, p.norm_eps);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < kHeadsPerCta; ++i) {
         float x[8];
-        unpack4(w1[i], x);
-        unpack4(w2[i], x + 4);
+        if constexpr (NORM) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = xn[i][k];
+        } else {
+          unpack4(w1[i], x);
+          unpack4(w2[i], x + 4);
+        }
         if (col.turn) rotate8<INTER>(x, c, sn);
         if (hb + i < p.hq) {
           uint16_t* dst = out + (int64_t)(hb + i) * p.qo_s1;
@@ -376,6 +440,16 @@ __global__ void __launch_bounds__(kKvThreads, 8) va_append_kernel(const AppendPa
   for (int k = 0; k < 4; ++k) {
     unpack4(w1[k], x[k]);
     unpack4(w2[k], x[k] + 4);
+  }
+  if constexpr (NORM) {
+    if (is_k && p.k_norm) {
+      float w[8];
+      norm_weights(p.k_norm, p.k_norm_fp32, p.norm_offset, col, w);
+      normalise4(x, w, p.norm_eps);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
     if (turn) rotate8<INTER>(x[k], cs[k], sn[k]);
     if (KIND == kPageScaled) {
 #pragma unroll
@@ -587,9 +661,10 @@ __global__ void __launch_bounds__(kMlaThreads, 4) va_append_mla_kernel(const App
 using KernelFn = void (*)(const AppendParams);
 
 template <int KIND>
-KernelFn pick(bool mla, bool inter) {
+KernelFn pick(bool mla, bool inter, bool norm) {
   if (mla) return inter ? va_append_mla_kernel<KIND, true> : va_append_mla_kernel<KIND, false>;
-  return inter ? va_append_kernel<KIND, true> : va_append_kernel<KIND, false>;
+  if (norm) return inter ? va_append_kernel<KIND, true, true> : va_append_kernel<KIND, false, true>;
+  return inter ? va_append_kernel<KIND, true, false> : va_append_kernel<KIND, false, false>;
 }
 
 }  // namespace
@@ -602,9 +677,10 @@ int64_t append_roles(bool mla, const AppendParams& p) {
 cudaError_t launch_append(const AppendParams& p, bool mla, cudaStream_t stream) {
   const int64_t units = p.total_q / kPageSize + 2 * (int64_t)p.num_seqs;
   const int64_t roles = append_roles(mla, p);
-  const KernelFn fn = p.kc.scales ? pick<kPageScaled>(mla, p.interleaved)
-                      : p.kc.fp8  ? pick<kE4m3>(mla, p.interleaved)
-                                  : pick<kBf16>(mla, p.interleaved);
+  const bool norm = p.q_norm || p.k_norm;
+  const KernelFn fn = p.kc.scales ? pick<kPageScaled>(mla, p.interleaved, norm)
+                      : p.kc.fp8  ? pick<kE4m3>(mla, p.interleaved, norm)
+                                  : pick<kBf16>(mla, p.interleaved, norm);
   // a programmatic dependent of the stream's previous kernel, as the
   // attention kernels are: it touches memory only after that kernel
   cudaLaunchConfig_t cfg = {};

@@ -40,6 +40,12 @@ struct AppendParams {
   int64_t max_pos;
   int32_t rot;
   int32_t interleaved;
+  // Norms of queries and keys (verify_attn_append_kv_norm): the weights of a head's 256
+  // columns, bf16 bits or fp32, plus norm_offset; null: not normalised
+  const void* q_norm;
+  const void* k_norm;
+  int32_t q_norm_fp32, k_norm_fp32;
+  float norm_eps, norm_offset;
   const float* k_descale;    // nullable
   const float* v_descale;    // nullable
   int32_t num_seqs, total_q, hq, hkv, num_blocks;

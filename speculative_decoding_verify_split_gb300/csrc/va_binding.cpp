@@ -25,7 +25,7 @@ namespace {
 
 // The descriptors of one call, and the device they share.
 struct Args {
-  static constexpr int kMax = 16;
+  static constexpr int kMax = 20;
   va_tensor d[kMax];
   int n = 0;
   bool any = false;
@@ -177,6 +177,31 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return status_of(args.device, [&] {
       return verify_attn_append_kv(t[0], t[1], t[2], t[3], t[4], t[5], r, t[6], t[7], t[8], t[9], t[10], t[11], t[12],
                                    stream);
+    });
+  });
+}
+
+// append_kv_norm(append_kv's first 16, q_weight, k_weight, eps, offset, stream)
+PyObject* append_kv_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (!arity(n, 21)) return nullptr;
+    Args args;
+    va_tensor *t[13], *w[2];
+    for (int i = 0; i < 13; ++i)
+      if (!args.add(a[i], &t[i])) return nullptr;
+    va_rope rope;
+    const va_rope* r;
+    va_norm norm;
+    cudaStream_t stream;
+    if (!read_rope(args, a[13], a[14], a[15], &rope, &r) || !args.add(a[16], &w[0]) || !args.add(a[17], &w[1]) ||
+        !read_float(a[18], &norm.eps) || !read_float(a[19], &norm.offset) || !args.on_cuda("append_kv") ||
+        !read_stream(a[20], args.device, &stream))
+      return nullptr;
+    norm.q_weight = w[0];
+    norm.k_weight = w[1];
+    return status_of(args.device, [&] {
+      return verify_attn_append_kv_norm(t[0], t[1], t[2], t[3], t[4], t[5], &norm, r, t[6], t[7], t[8], t[9], t[10], t[11],
+                                        t[12], stream);
     });
   });
 }
@@ -352,6 +377,7 @@ PyObject* attn_chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 PyMethodDef kMethods[] = {
     {"append_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_kv)), METH_FASTCALL, nullptr},
+    {"append_kv_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_kv_norm)), METH_FASTCALL, nullptr},
     {"append_mla", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_mla)), METH_FASTCALL, nullptr},
     {"attn_scaled", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn_scaled)), METH_FASTCALL, nullptr},
     {"attn_mla_scaled", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn_mla_scaled)), METH_FASTCALL,

@@ -1,6 +1,7 @@
 // Host side of the append entry points (include/verify_attn.h): argument
 // validation and the launch.
 #include <climits>
+#include <cmath>
 #include <cstring>
 
 #include "va_append.h"
@@ -109,11 +110,41 @@ void set_batch(AppendParams* p, const va_tensor* bt, const va_tensor* cu, const 
   p->num_seqs = (int32_t)su->shape[0];
 }
 
-// q and q_out [total_q, hq, width]: both or neither, and only with a rotation.
+// The weights of a norm over a head's columns.
+va_status check_norm_weight(const va_tensor* t) {
+  if (!t) return VA_OK;
+  if (t->dtype != VA_BF16 && t->dtype != VA_FP32) return VA_ERR_DTYPE;
+  if (!dims_ok(t, 1) || t->shape[0] != kHeadDim) return VA_ERR_SHAPE;
+  if (t->stride[0] != 1) return VA_ERR_LAYOUT;
+  if (!t->data) return VA_ERR_NULL;
+  return aligned16(t->data) ? VA_OK : VA_ERR_LAYOUT;
+}
+
+va_status check_norm(const va_norm* n, AppendParams* p) {
+  if (!n) return VA_OK;
+  va_status s = check_norm_weight(n->q_weight);
+  if (s == VA_OK) s = check_norm_weight(n->k_weight);
+  if (s != VA_OK) return s;
+  if (!(n->eps >= 0.f) || !std::isfinite(n->eps) || !std::isfinite(n->offset)) return VA_ERR_UNSUPPORTED;
+  p->norm_eps = n->eps;
+  p->norm_offset = n->offset;
+  if (n->q_weight) {
+    p->q_norm = n->q_weight->data;
+    p->q_norm_fp32 = n->q_weight->dtype == VA_FP32;
+  }
+  if (n->k_weight) {
+    p->k_norm = n->k_weight->data;
+    p->k_norm_fp32 = n->k_weight->dtype == VA_FP32;
+  }
+  return VA_OK;
+}
+
+// q and q_out [total_q, hq, width]: both or neither, and only with something to do
+// (a rotation, a norm).
 va_status check_queries(const va_tensor* q, const va_tensor* q_out, int64_t total_q, int64_t width,
-                        const va_rope* rope, AppendParams* p) {
+                        bool work, AppendParams* p) {
   if (!q && !q_out) return VA_OK;
-  if (!q || !q_out || !rope) return VA_ERR_NULL;
+  if (!q || !q_out || !work) return VA_ERR_NULL;
   if (!dims_ok(q, 3) || !dims_ok(q_out, 3)) return VA_ERR_SHAPE;
   if (q->dtype != VA_BF16 || q_out->dtype != VA_BF16) return VA_ERR_DTYPE;
   if (q->shape[2] != width) return VA_ERR_UNSUPPORTED;
@@ -163,6 +194,16 @@ VA_EXPORT va_status verify_attn_append_kv(const va_tensor* q, const va_tensor* k
                                           const va_tensor* k_descale, const va_tensor* v_descale,
                                           va_tensor* k_scales, va_tensor* v_scales, va_tensor* q_out,
                                           va_tensor* k_cache, va_tensor* v_cache, void* stream) {
+  return verify_attn_append_kv_norm(q, k, v, block_table, cu_seqlens_q, seqused_k, nullptr, rope, k_descale, v_descale,
+                                    k_scales, v_scales, q_out, k_cache, v_cache, stream);
+}
+
+VA_EXPORT va_status verify_attn_append_kv_norm(const va_tensor* q, const va_tensor* k, const va_tensor* v,
+                                               const va_tensor* block_table, const va_tensor* cu_seqlens_q,
+                                               const va_tensor* seqused_k, const va_norm* norm, const va_rope* rope,
+                                               const va_tensor* k_descale, const va_tensor* v_descale,
+                                               va_tensor* k_scales, va_tensor* v_scales, va_tensor* q_out,
+                                               va_tensor* k_cache, va_tensor* v_cache, void* stream) {
   if (!k || !v || !block_table || !cu_seqlens_q || !seqused_k || !k_cache || !v_cache) return VA_ERR_NULL;
   if (!dims_ok(k, 3) || !dims_ok(v, 3) || !dims_ok(k_cache, 4) || !dims_ok(v_cache, 4)) return VA_ERR_SHAPE;
   if (k->dtype != VA_BF16 || v->dtype != VA_BF16) return VA_ERR_DTYPE;
@@ -199,7 +240,9 @@ VA_EXPORT va_status verify_attn_append_kv(const va_tensor* q, const va_tensor* k
   va::AppendParams p;
   std::memset(&p, 0, sizeof(p));
   s = check_rope(rope, total_q, va::kHeadDim, &p);
-  if (s == VA_OK) s = check_queries(q, q_out, total_q, va::kHeadDim, rope, &p);
+  if (s == VA_OK) s = check_norm(norm, &p);
+  if (s == VA_OK) s = check_queries(q, q_out, total_q, va::kHeadDim, rope || p.q_norm, &p);
+  if (s == VA_OK && p.q_norm && !q) s = VA_ERR_NULL;
   if (s != VA_OK) return s;
   p.k = static_cast<const uint16_t*>(k->data);
   p.k_s0 = k->stride[0];
@@ -250,7 +293,7 @@ VA_EXPORT va_status verify_attn_append_mla(const va_tensor* q_pe, const va_tenso
   std::memset(&p, 0, sizeof(p));
   s = check_rope(rope, total_q, va::kMlaPe, &p);
   if (s == VA_OK && rope && p.rot != va::kMlaPe) s = VA_ERR_UNSUPPORTED;  // the whole rope part turns
-  if (s == VA_OK) s = check_queries(q_pe, q_pe_out, total_q, va::kMlaPe, rope, &p);
+  if (s == VA_OK) s = check_queries(q_pe, q_pe_out, total_q, va::kMlaPe, rope != nullptr, &p);
   if (s != VA_OK) return s;
   p.k = static_cast<const uint16_t*>(latent->data);
   p.k_s0 = latent->stride[0];
