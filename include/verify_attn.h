@@ -635,6 +635,88 @@ va_status verify_attn_mla_scaled(const va_tensor* q, const va_tensor* kv_cache, 
                                  void* stream);
 
 /*
+ * The page pool: sequences that share pages of their caches (a prompt's pages under
+ * several candidates). Beside the block table [B, W] and seqused_k [B], both as the
+ * attention calls take them, two int32 arrays in device memory:
+ *  page_count  [B]: pages that row b holds, entries [0, page_count[b]) of its row; at
+ *              least ceil(seqused_k[b] / 16), more where room was reserved.
+ *  refs        [num_blocks]: rows that hold the page; 0: it is free. A page that no row
+ *              may get (a padding page) has any other count.
+ * All caches of a model share one pool: the table's calls run once, verify_attn_copy_pages
+ * once a cache. The calls below are asynchronous on stream, capturable, one launch each,
+ * without a workspace or host reads; they decide from the arrays as they are when the
+ * call starts, and their results depend on nothing else. Lists are contiguous int32
+ * device tensors. `status` (nullable): one int32 that VA_PG_* bits are ORed into, never
+ * cleared. What a bit reports is left undone, for that sequence or entry alone:
+ *  VA_PG_BAD_SEQ    a listed index outside [0, B); a child listed twice (the first counts)
+ *                   or listed as a parent too
+ *  VA_PG_IN_USE     a child whose row holds pages (free it first)
+ *  VA_PG_NO_PAGES   not enough free pages
+ *  VA_PG_ROW_FULL   more tokens than a row of the table has places for
+ *  VA_PG_BAD_TABLE  a count below its tokens or past the row, a page outside the pool, or
+ *                   one freed more often than it was held (its count stays 0)
+ * Errors before launching: VA_ERR_NULL, VA_ERR_SHAPE, VA_ERR_DTYPE (all int32),
+ * VA_ERR_LAYOUT (strided vectors; a block table whose entries overlap).
+ */
+#define VA_PG_BAD_SEQ 1
+#define VA_PG_IN_USE 2
+#define VA_PG_NO_PAGES 4
+#define VA_PG_ROW_FULL 8
+#define VA_PG_BAD_TABLE 16
+
+/*
+ * verify_attn_free_pages - takes the rows of the listed sequences out of the pool: their
+ * pages' refs fall by one, page_count and seqused_k become 0 (the row's entries stay as
+ * they were). A sequence listed twice is freed once.
+ */
+va_status verify_attn_free_pages(const va_tensor* block_table, va_tensor* seqused_k, va_tensor* page_count,
+                                 va_tensor* refs, const va_tensor* seqs, int32_t* status, void* stream);
+
+/*
+ * verify_attn_fork_pages - children[i], whose row holds no page, becomes a copy of
+ * parents[i]: seqused_k and the pages that hold its tokens, whose refs grow by one (the
+ * parent's reserved room is not shared). Nothing is copied until one of them writes: see
+ * verify_attn_reserve_pages. A parent may be listed any number of times.
+ */
+va_status verify_attn_fork_pages(va_tensor* block_table, va_tensor* seqused_k, va_tensor* page_count,
+                                 va_tensor* refs, const va_tensor* parents, const va_tensor* children,
+                                 int32_t* status, void* stream);
+
+/*
+ * verify_attn_reserve_pages - pages of its own for the next new_tokens[b] tokens of every
+ * sequence (0 or less: none): what runs before append. With S = seqused_k[b] and want =
+ * ceil((S + new_tokens[b]) / 16), the places [S / 16, want) of row b end up holding
+ * pages with refs 1: one that other rows held too is replaced (its refs fall by one, also
+ * where every one of its rows replaces it), places behind page_count[b] are filled, and
+ * page_count[b] becomes want if that is more. The k-th page that the call needs, in the
+ * order of sequences and of places, is the k-th page with refs 0 (VA_PG_NO_PAGES: a sequence
+ * gets all or none of its pages, and none if the sum up to it exceeds the free ones).
+ *  src, dst   [B], written: the page whose contents sequence b's caches need copied
+ *             (verify_attn_copy_pages takes the two lists), -1 for none.
+ *  room       [B], written: tokens that row b has places for now, 16 * page_count[b].
+ * VA_ERR_UNSUPPORTED for more than 8,192 sequences or 4,194,304 pages.
+ */
+va_status verify_attn_reserve_pages(va_tensor* block_table, const va_tensor* seqused_k, va_tensor* page_count,
+                                    va_tensor* refs, const va_tensor* new_tokens, va_tensor* src, va_tensor* dst,
+                                    va_tensor* room, int32_t* status, void* stream);
+
+/*
+ * verify_attn_copy_pages - page dst[i] of a cache becomes a copy of page src[i], for K and V,
+ * with their page scales.
+ *  k_cache, v_cache  [num_blocks, 16, H, D] BF16 or FP8_E4M3, D a multiple of 16 bytes,
+ *               strides as verify_attn; v_cache NULL: one cache (a latent one).
+ *  k_scales, v_scales  [num_blocks, H] fp32 of e4m3 caches, or NULL.
+ *  src, dst     [n]. A pair with an index outside [0, num_blocks) (-1), or of one page
+ *               twice, copies nothing. A page may be copied any number of times; one that is
+ *               written twice, or written and read, has unspecified contents.
+ * Errors: VA_ERR_NULL, VA_ERR_SHAPE, VA_ERR_DTYPE (scales over a BF16 cache), VA_ERR_LAYOUT
+ * (elements on top of each other, K and V in one place), VA_ERR_UNSUPPORTED (pages other
+ * than 16, other widths, pages past 16 M elements a token row).
+ */
+va_status verify_attn_copy_pages(va_tensor* k_cache, va_tensor* v_cache, va_tensor* k_scales, va_tensor* v_scales,
+                                 const va_tensor* src, const va_tensor* dst, void* stream);
+
+/*
  * verify_attn_chunk - attention of chunks of new tokens over the paged cache:
  * whole prompts, pieces of prompts behind cached tokens, single tokens, mixed in
  * a batch. The operation of verify_attn and of its variants for any number of

@@ -36,13 +36,17 @@ EXPORTS = ("verify_attn", "verify_attn_ex", "verify_attn_check", "verify_attn_pl
            "verify_attn_last_device_error", "verify_attn_set_wait_limit",
            "verify_attn_append_kv", "verify_attn_append_mla", "verify_attn_scaled",
            "verify_attn_mla_scaled", "verify_attn_chunk", "verify_attn_chunk_workspace_size",
-           "verify_attn_append_kv_norm")
+           "verify_attn_append_kv_norm", "verify_attn_copy_pages", "verify_attn_free_pages",
+           "verify_attn_fork_pages", "verify_attn_reserve_pages")
 
 # Absorbed-MLA latent cache: row = [latent (MLA_NOPE) | rope key (MLA_PE)].
 MLA_NOPE, MLA_PE = 512, 64
 
 # Status bits of verify_attn_block_table_from_indptr.
 BT_BAD_PAGE, BT_TRUNCATED, BT_BAD_INDPTR = 1, 2, 4
+
+# Status bits of free_pages, fork_pages and reserve_pages.
+PG_BAD_SEQ, PG_IN_USE, PG_NO_PAGES, PG_ROW_FULL, PG_BAD_TABLE = 1, 2, 4, 8, 16
 
 # Size of the library's built-in partials array used by verify_attn_noalloc.
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -152,6 +156,14 @@ def _lib():
         lib.verify_attn_chunk.restype = ctypes.c_int32
         lib.verify_attn_chunk_workspace_size.argtypes = []
         lib.verify_attn_chunk_workspace_size.restype = ctypes.c_size_t
+        lib.verify_attn_copy_pages.argtypes = [P] * 6 + [V]
+        lib.verify_attn_copy_pages.restype = ctypes.c_int32
+        lib.verify_attn_free_pages.argtypes = [P] * 5 + [V, V]
+        lib.verify_attn_free_pages.restype = ctypes.c_int32
+        lib.verify_attn_fork_pages.argtypes = [P] * 6 + [V, V]
+        lib.verify_attn_fork_pages.restype = ctypes.c_int32
+        lib.verify_attn_reserve_pages.argtypes = [P] * 8 + [V, V]
+        lib.verify_attn_reserve_pages.restype = ctypes.c_int32
         lib.verify_attn_status_string.argtypes = [ctypes.c_int32]
         lib.verify_attn_status_string.restype = ctypes.c_char_p
         _LIB = lib
@@ -203,15 +215,15 @@ def _native():
     return _NATIVE
 
 
-def _empty(shape, like, stream):
+def _empty(shape, like, stream, dtype=torch.bfloat16):
     """An output that the call creates: from the allocator's pool of the stream
     that writes it, so that memory freed by its owner is not reused under it."""
     if stream is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _handle(stream):
@@ -678,3 +690,48 @@ def chunk_workspace_size(device=None) -> int:
     if n == 0:
         raise VerifyAttnError(6, "verify_attn_chunk_workspace_size")
     return int(n) + 256
+
+
+def free_pages(block_table, seqused_k, page_count, refs, seqs, status=None, stream=None):
+    """Gives back the pages of the listed sequences' rows (see the page pool in
+    include/verify_attn.h): ``page_count`` [B] and ``refs`` [num_blocks] are int32
+    device tensors; ``status``, if given, a one-element int32 tensor that PG_* bits
+    are ORed into."""
+    s = _native().free_pages(block_table, seqused_k, page_count, refs, seqs, status, _handle(stream))
+    if s != VA_OK:
+        raise VerifyAttnError(s, "verify_attn_free_pages")
+
+
+def fork_pages(block_table, seqused_k, page_count, refs, parents, children, status=None, stream=None):
+    """Makes the empty rows ``children`` copies of ``parents`` that share their pages
+    (see include/verify_attn.h); ``reserve_pages`` separates them where they write on."""
+    s = _native().fork_pages(block_table, seqused_k, page_count, refs, parents, children, status, _handle(stream))
+    if s != VA_OK:
+        raise VerifyAttnError(s, "verify_attn_fork_pages")
+
+
+def reserve_pages(block_table, seqused_k, page_count, refs, new_tokens, src=None, dst=None, room=None,
+                  status=None, stream=None):
+    """Pages of its own for the next ``new_tokens`` [B] tokens of every sequence (see
+    include/verify_attn.h), before ``append_kv``. Returns (src, dst, room), int32 [B]
+    each: the pages that ``copy_pages`` has to copy, and the tokens that rows have
+    places for."""
+    if src is None or dst is None or room is None:
+        made = _empty((3, block_table.shape[0]), block_table, stream, torch.int32)
+        src = made[0] if src is None else src
+        dst = made[1] if dst is None else dst
+        room = made[2] if room is None else room
+    s = _native().reserve_pages(block_table, seqused_k, page_count, refs, new_tokens, src, dst, room, status,
+                                _handle(stream))
+    if s != VA_OK:
+        raise VerifyAttnError(s, "verify_attn_reserve_pages")
+    return src, dst, room
+
+
+def copy_pages(k_cache, v_cache, src, dst, k_scales=None, v_scales=None, stream=None):
+    """Copies pages ``src`` of K and V caches (v_cache None: one cache) to pages
+    ``dst``, with their page scales (see include/verify_attn.h); int32 lists, -1 for
+    nothing to copy."""
+    s = _native().copy_pages(k_cache, v_cache, k_scales, v_scales, src, dst, None, _handle(stream))
+    if s != VA_OK:
+        raise VerifyAttnError(s, "verify_attn_copy_pages")

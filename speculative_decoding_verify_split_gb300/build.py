@@ -27,8 +27,9 @@ BINDING = os.path.join(LIBDIR, "va_binding.so")
 BINDING_SOURCE = "va_binding.cpp"
 BINDING_STAMP = os.path.join(LIBDIR, "va_binding.abi")  # the torch and Python that BINDING was built for
 
-SOURCES = ["va_host.cpp", "va_host_append.cpp", "va_host_chunk.cpp", "va_main_tc.cu", "va_mla_tc.cu", "va_mla_bf16_tc.cu", "va_merge.cu",
-           "va_noalloc.cu", "va_pagetable.cu", "va_append.cu", "va_chunk.cu"]
+SOURCES = ["va_host.cpp", "va_host_append.cpp", "va_host_chunk.cpp", "va_host_pages.cpp", "va_main_tc.cu", "va_mla_tc.cu", "va_mla_bf16_tc.cu", "va_merge.cu",
+           "va_noalloc.cu", "va_pagetable.cu", "va_append.cu", "va_chunk.cu",
+           "va_pages.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",

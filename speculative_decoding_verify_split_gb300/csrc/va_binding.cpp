@@ -1,6 +1,6 @@
 // The compiled half of the Python binding for the calls of a verify step that
 // a decoder makes back to back (append_kv, append_mla, verify_attn_scaled,
-// verify_attn_mla_scaled, verify_attn_chunk): reads torch tensors into va_tensor descriptors and
+// verify_attn_mla_scaled, verify_attn_chunk, the page pool's): reads torch tensors into va_tensor descriptors and
 // calls the C ABI. Marshalling fifteen tensors through ctypes takes 20 us on a
 // Grace core, several times what the kernels of a small step take; here it
 // takes well under one.
@@ -375,6 +375,67 @@ PyObject* attn_chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The address of a one-element int32 status tensor, or null.
+bool read_status(PyObject* o, const Args& args, int32_t** out) {
+  *out = nullptr;
+  if (o == Py_None) return true;
+  if (!THPVariable_Check(o)) {
+    PyErr_SetString(PyExc_TypeError, "status: a tensor or None");
+    return false;
+  }
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (t.device() != args.device || t.scalar_type() != at::kInt || t.numel() < 1) {
+    PyErr_SetString(PyExc_ValueError, "status: an int32 tensor on the call's device");
+    return false;
+  }
+  *out = static_cast<int32_t*>(t.data_ptr());
+  return true;
+}
+
+// The pool's calls: `N` tensors in the C call's order, status, stream.
+template <int N, class F>
+PyObject* pool_call(const char* where, PyObject* const* a, Py_ssize_t n, F call) {
+  return guarded([&]() -> PyObject* {
+    if (!arity(n, N + 2)) return nullptr;
+    Args args;
+    va_tensor* t[N];
+    for (int i = 0; i < N; ++i)
+      if (!args.add(a[i], &t[i])) return nullptr;
+    int32_t* status;
+    cudaStream_t stream;
+    if (!args.on_cuda(where) || !read_status(a[N], args, &status) || !read_stream(a[N + 1], args.device, &stream)) return nullptr;
+    return status_of(args.device, [&] { return call(t, status, stream); });
+  });
+}
+
+// free_pages(block_table, seqused_k, page_count, refs, seqs, status, stream)
+PyObject* free_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return pool_call<5>("free_pages", a, n, [](va_tensor** t, int32_t* status, cudaStream_t stream) {
+    return verify_attn_free_pages(t[0], t[1], t[2], t[3], t[4], status, stream);
+  });
+}
+
+// fork_pages(block_table, seqused_k, page_count, refs, parents, children, status, stream)
+PyObject* fork_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return pool_call<6>("fork_pages", a, n, [](va_tensor** t, int32_t* status, cudaStream_t stream) {
+    return verify_attn_fork_pages(t[0], t[1], t[2], t[3], t[4], t[5], status, stream);
+  });
+}
+
+// reserve_pages(block_table, seqused_k, page_count, refs, new_tokens, src, dst, room, status, stream)
+PyObject* reserve_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return pool_call<8>("reserve_pages", a, n, [](va_tensor** t, int32_t* status, cudaStream_t stream) {
+    return verify_attn_reserve_pages(t[0], t[1], t[2], t[3], t[4], t[5], t[6], t[7], status, stream);
+  });
+}
+
+// copy_pages(k_cache, v_cache, k_scales, v_scales, src, dst, None, stream)
+PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return pool_call<6>("copy_pages", a, n, [](va_tensor** t, int32_t*, cudaStream_t stream) {
+    return verify_attn_copy_pages(t[0], t[1], t[2], t[3], t[4], t[5], stream);
+  });
+}
+
 PyMethodDef kMethods[] = {
     {"append_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_kv)), METH_FASTCALL, nullptr},
     {"append_kv_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_kv_norm)), METH_FASTCALL, nullptr},
@@ -383,6 +444,10 @@ PyMethodDef kMethods[] = {
     {"attn_mla_scaled", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn_mla_scaled)), METH_FASTCALL,
      nullptr},
     {"attn_chunk", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn_chunk)), METH_FASTCALL, nullptr},
+    {"free_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(free_pages)), METH_FASTCALL, nullptr},
+    {"fork_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fork_pages)), METH_FASTCALL, nullptr},
+    {"reserve_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(reserve_pages)), METH_FASTCALL, nullptr},
+    {"copy_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(copy_pages)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "va_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
