@@ -215,15 +215,15 @@ def _native():
     return _NATIVE
 
 
-def _empty(shape, like, stream, dtype=torch.bfloat16):
+def _empty(shape, like, stream):
     """An output that the call creates: from the allocator's pool of the stream
     that writes it, so that memory freed by its owner is not reused under it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
 
 
 def _handle(stream):
@@ -716,11 +716,10 @@ def reserve_pages(block_table, seqused_k, page_count, refs, new_tokens, src=None
     include/verify_attn.h), before ``append_kv``. Returns (src, dst, room), int32 [B]
     each: the pages that ``copy_pages`` has to copy, and the tokens that rows have
     places for."""
-    if src is None or dst is None or room is None:
-        made = _empty((3, block_table.shape[0]), block_table, stream, torch.int32)
-        src = made[0] if src is None else src
-        dst = made[1] if dst is None else dst
-        room = made[2] if room is None else room
+    if src is None and dst is None and room is None:
+        src, dst, room = _native().int_outputs(block_table, block_table.shape[0], _handle(stream))
+    elif src is None or dst is None or room is None:
+        raise ValueError("src, dst and room: all three or none")
     s = _native().reserve_pages(block_table, seqused_k, page_count, refs, new_tokens, src, dst, room, status,
                                 _handle(stream))
     if s != VA_OK:

@@ -14,6 +14,7 @@
 #include <exception>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -429,6 +430,30 @@ PyObject* reserve_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// int_outputs(like, n, stream): three int32 vectors of n on like's device, from the
+// allocator's pool of the stream that will write them. (Made in Python they take 7 us,
+// three times the call that they are for.)
+PyObject* int_outputs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (!arity(n, 3)) return nullptr;
+    Args args;
+    va_tensor* like;
+    int32_t size;
+    cudaStream_t stream;
+    if (!args.add(a[0], &like) || !read_int(a[1], &size) || !args.on_cuda("reserve_pages") ||
+        !read_stream(a[2], args.device, &stream))
+      return nullptr;
+    const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(stream, args.device.index()));
+    PyObject* out = PyTuple_New(3);
+    for (int i = 0; out && i < 3; ++i) {
+      PyObject* t = THPVariable_Wrap(at::empty({size}, at::TensorOptions(at::kInt).device(args.device)));
+      if (!t) Py_CLEAR(out);
+      else PyTuple_SET_ITEM(out, i, t);
+    }
+    return out;
+  });
+}
+
 // copy_pages(k_cache, v_cache, k_scales, v_scales, src, dst, None, stream)
 PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return pool_call<6>("copy_pages", a, n, [](va_tensor** t, int32_t*, cudaStream_t stream) {
@@ -447,6 +472,7 @@ PyMethodDef kMethods[] = {
     {"free_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(free_pages)), METH_FASTCALL, nullptr},
     {"fork_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fork_pages)), METH_FASTCALL, nullptr},
     {"reserve_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(reserve_pages)), METH_FASTCALL, nullptr},
+    {"int_outputs", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(int_outputs)), METH_FASTCALL, nullptr},
     {"copy_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(copy_pages)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

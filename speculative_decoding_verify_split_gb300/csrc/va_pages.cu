@@ -148,9 +148,9 @@ __global__ void __launch_bounds__(kRowThreads) va_fork_pages_kernel(const PoolPa
 // between cluster barriers:
 //  1  every CTA: each sequence's needs and their prefix sums; its part of the bitmap;
 //  2  a sequence's thread marks the shared places of its row (as ~page);
-//  3  the free pages that grow rows go to their places, each from the thread that holds its
-//     word; a sequence's thread replaces its marked places by the pages of their ranks and
-//     gives up the shared ones;
+//  3  a free page's thread puts it in its place, where it grows a row, or hands it to the
+//     sequence; then a sequence's thread replaces its marked places (the first by that
+//     page, others by the pages of their ranks) and gives up the shared ones;
 //  4  counts of the rows.
 // It is latency: three dependent loads, the scans and four barriers.
 struct Want {
@@ -239,12 +239,40 @@ __global__ void __launch_bounds__(kPoolThreads, 1) va_reserve_pages_kernel(const
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // 1a: the bitmap, a warp a word (32 pages), several words under way
-#pragma unroll 4
-  for (int w = warp; w < words; w += kPoolThreads / 32) {
+  // What sequence b needs, and whether it gets anything (if not: said by the first CTA).
+  auto need_of = [&](int b, bool& ok) {
+    const Want w = wants(p, b, rank == 0);
+    ok = w.ok;
+    int64_t need = ok && w.want > w.have ? w.want - w.have : 0;
+    const int* row = p.table + (int64_t)b * p.t_s0;
+    for (int j = w.first; ok && j < w.have && j < w.want; ++j) {
+      const int page = row[(int64_t)j * p.t_s1];
+      ok = (unsigned)page < (unsigned)p.num_pages;  // (no place may look like a mark)
+      if (!ok && rank == 0) report(p, kPgBadTable);
+      need += is_shared(p, page);
+    }
+    return ok ? need : 0;
+  };
+  // 1a: the bitmap, a warp a word (32 pages); the first words' loads are under way while
+  // the first sequences' needs are found
+  constexpr int kWarps = kPoolThreads / 32, kEarly = 4;
+  auto refs_of = [&](int w) {
     const int page = page0 + 32 * w + lane;
-    const bool free_page = page < p.num_pages && p.refs[page] == 0;
-    const uint32_t bits = __ballot_sync(0xffffffffu, free_page);
+    return w < words && page < p.num_pages ? p.refs[page] : 1;
+  };
+  int early[kEarly];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k) early[k] = refs_of(warp + kWarps * k);
+  bool ok0 = false;
+  const int64_t need0 = tid < p.num_seqs ? need_of(tid, ok0) : 0;
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k) {
+    const uint32_t bits = __ballot_sync(0xffffffffu, early[k] == 0);
+    if (lane == 0 && warp + kWarps * k < words) map[warp + kWarps * k] = bits;
+  }
+#pragma unroll 4
+  for (int w = warp + kWarps * kEarly; w < words; w += kWarps) {
+    const uint32_t bits = __ballot_sync(0xffffffffu, refs_of(w) == 0);
     if (lane == 0) map[w] = bits;
   }
   __syncthreads();
@@ -265,24 +293,11 @@ __global__ void __launch_bounds__(kPoolThreads, 1) va_reserve_pages_kernel(const
     int64_t running = 0;
     for (int b0 = 0; b0 < p.num_seqs; b0 += kPoolThreads) {
       const int b = b0 + tid;
-      int64_t need = 0;
-      bool ok = false;
-      if (b < p.num_seqs) {
-        const Want w = wants(p, b, rank == 0);
-        ok = w.ok;
-        if (ok) {
-          need = w.want > w.have ? w.want - w.have : 0;
-          const int* row = p.table + (int64_t)b * p.t_s0;
-          for (int j = w.first; j < w.have && j < w.want; ++j) {
-            const int page = row[(int64_t)j * p.t_s1];
-            ok = ok && (unsigned)page < (unsigned)p.num_pages;
-            need += is_shared(p, page);
-          }
-          if (!ok) {  // no place may look like a mark
-            need = 0;
-            if (rank == 0) report(p, kPgBadTable);
-          }
-        }
+      int64_t need = need0;
+      bool ok = ok0;
+      if (b0 > 0) {
+        ok = false;
+        need = b < p.num_seqs ? need_of(b, ok) : 0;
       }
       const uint32_t no = __ballot_sync(0xffffffffu, !ok);
       if (lane == 0 && b < p.num_seqs) refused[b >> 5] = no;
@@ -338,26 +353,29 @@ __global__ void __launch_bounds__(kPoolThreads, 1) va_reserve_pages_kernel(const
 #pragma unroll
   for (int k = 0; k < kPoolCtas; ++k)
     if (k == rank) my_base = base[k];
-  for (int w = tid; w < words; w += kPoolThreads) {
-    uint32_t bits = map[w];
-    int at = my_base + ahead[w];  // rank of the word's first free page
-    for (; bits && at < granted; bits &= bits - 1, ++at) {
-      const int page = page0 + 32 * w + __ffs((int)bits) - 1;
-      p.refs[page] = 1;
-      int lo = 0, hi = p.num_seqs - 1;  // the sequence with sums[b] <= at < sums[b + 1]
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (sums[mid + 1] > at)
-          hi = mid;
-        else
-          lo = mid + 1;
-      }
-      const Want s = wants(p, lo, false);
-      const int grow = s.want > s.have ? s.want - s.have : 0;
-      const int k = at - sums[lo] - (sums[lo + 1] - sums[lo] - grow);  // behind its replaced pages
-      if (k >= 0) p.table[(int64_t)lo * p.t_s0 + (int64_t)(s.have + k) * p.t_s1] = page;
+  for (int w = warp; w < words && my_base + ahead[w] < granted; w += kPoolThreads / 32) {
+    const uint32_t bits = map[w];
+    const int at = my_base + ahead[w] + __popc(bits & ((1u << lane) - 1));  // this page's rank
+    if (!((bits >> lane) & 1) || at >= granted) continue;
+    const int page = page0 + 32 * w + lane;
+    p.refs[page] = 1;
+    int lo = 0, hi = p.num_seqs - 1;  // the sequence with sums[b] <= at < sums[b + 1]
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sums[mid + 1] > at)
+        hi = mid;
+      else
+        lo = mid + 1;
     }
+    const Want s = wants(p, lo, false);
+    const int grow = s.want > s.have ? s.want - s.have : 0;
+    const int k = at - sums[lo] - (sums[lo + 1] - sums[lo] - grow);  // behind its replaced pages
+    if (k >= 0)
+      p.table[(int64_t)lo * p.t_s0 + (int64_t)(s.have + k) * p.t_s1] = page;
+    else if (at == sums[lo])
+      p.dst[lo] = page;  // the first replaced one's, for 3b
   }
+  cluster_meet();
   // 3b: marked places
   auto page_of_rank = [&](int at) {
     int cta = 0;
@@ -387,12 +405,14 @@ __global__ void __launch_bounds__(kPoolThreads, 1) va_reserve_pages_kernel(const
     const Want w = wants(p, b, false);
     const bool ok = grants(b);
     if (ok && sums[b + 1] > sums[b]) {
+      const int first = __ldcg(p.dst + b);
       int* row = p.table + (int64_t)b * p.t_s0;
       int at = sums[b];
       for (int j = w.first; j < w.have && j < w.want; ++j) {
         const int mark = row[(int64_t)j * p.t_s1];
         if (mark >= 0) continue;
-        const int page = page_of_rank(at++);
+        const int page = at == sums[b] ? first : page_of_rank(at);
+        ++at;
         row[(int64_t)j * p.t_s1] = page;
         atomicSub(p.refs + ~mark, 1);
         if (j == w.first && p.seqused[b] % kPageSize != 0) {  // it holds tokens
