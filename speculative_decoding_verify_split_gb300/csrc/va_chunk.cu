@@ -46,6 +46,11 @@ __device__ __forceinline__ int row_tiles(const ChunkParams& p, const Seq& s) {
   return (int)(((int64_t)s.L * p.group + kChunkRows - 1) / kChunkRows);
 }
 
+// Tiles (in units) that a share has at least: small calls take fewer pairs, whose partials
+// cost more to write and to join than the tiles they save (two sequences of 40 tokens
+// over 600 keys: 20.3 us, with 4 24.8, with 8 32.0).
+constexpr int64_t kMinShare = 6;
+
 // Units of the split: a tile is 128 G of them. Row tile m costs
 //   min(max(0, (S - L) G + 256 (m + 1)), cap) + kChunkItemCost * 128 G,
 // about G times the keys that its rows see, so that the sum over a sequence's
@@ -103,9 +108,24 @@ __device__ __forceinline__ Span item_span(const ChunkParams& p, const Seq& s, in
   return x;
 }
 
-__device__ __forceinline__ int64_t share_begin(int64_t total, int c, int used) { return total * c / used; }
+// 64-bit quotients, by a 32-bit division (a tenth of the instructions) where they fit.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  return (uint64_t)x <= 0xFFFFFFFFu && (uint64_t)y <= 0xFFFFFFFFu ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
 
-__device__ __forceinline__ int64_t ceil_units(int64_t x, int64_t unit) { return x <= 0 ? 0 : (x + unit - 1) / unit; }
+// A share's units, and the first of share c's.
+__device__ __forceinline__ int64_t share_units(int64_t total, int used) { return used > 0 ? quotient(total + used - 1, used) : 0; }
+__device__ __forceinline__ int64_t share_begin(int64_t total, int64_t share, int c) {
+  const int64_t t = share * c;
+  return t < total ? t : total;
+}
+
+// Tiles of 128 G units that x units reach into.
+__device__ __forceinline__ int64_t ceil_units(const ChunkParams& p, int64_t x) {
+  if (x <= 0) return 0;
+  const int64_t t = (x + kKeys - 1) / kKeys;  // in G
+  return t + p.group <= 0x7FFFFFFF ? by_group(p, (int)(t + p.group - 1)) : (t + p.group - 1) / p.group;
+}
 
 // Walks the items from a share's start on.
 struct Walk {
@@ -135,7 +155,6 @@ struct Piece {
 };
 
 __device__ __forceinline__ bool next_piece(const ChunkParams& p, int64_t t0, int64_t t1, Walk& w, Piece& pc) {
-  const int64_t unit = (int64_t)kKeys * p.group;
   while (w.off < t1) {
     if (w.m >= w.tiles) {
       w.m = 0;
@@ -157,7 +176,7 @@ __device__ __forceinline__ bool next_piece(const ChunkParams& p, int64_t t0, int
     const int64_t off = w.off;
     w.off += chunk_cost(p, w.s, w.m);
     ++w.m;
-    int64_t i0 = ceil_units(t0 - off, unit), i1 = ceil_units(t1 - off, unit);
+    int64_t i0 = ceil_units(p, t0 - off), i1 = ceil_units(p, t1 - off);
     i0 = i0 < pc.x.n ? i0 : pc.x.n;
     i1 = i1 < pc.x.n ? i1 : pc.x.n;
     pc.i0 = (int)i0;
@@ -365,12 +384,18 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
         total += tot;
       }
     }
-    int64_t used = p.force > 0 ? p.force : total / (4 * unit);
-    used = used < 1 ? 1 : used > p.pairs ? p.pairs : used;
-    if (total == 0) used = 0;
+    // as many pairs as get at least kMinShare tiles' units each
+    int used = p.force > 0 && p.force < p.pairs ? p.force : p.pairs;
+    if (p.force <= 0 && total < kMinShare * unit * p.pairs) used = (int)quotient(total, kMinShare * unit);
+    used = total == 0 ? 0 : used < 1 ? 1 : used;
+    const int64_t share = share_units(total, used);
+    // The rounding up can leave the last pairs nothing: they are not counted, so that each
+    // counted share has a first unit and an item that it starts in. The share of the smaller
+    // count is the same: it is at least ceil(total / used), and share * count >= total.
+    if (share > 0) used = (int)quotient(total + share - 1, share);
     if (c < used) {
-      t0 = share_begin(total, c, (int)used);
-      t1 = share_begin(total, c + 1, (int)used);
+      t0 = share_begin(total, share, c);
+      t1 = share_begin(total, share, c + 1);
       int64_t running = 0;
       for (int b0 = 0; b0 < p.num_seqs; b0 += kThreads) {
         if (p.num_seqs > kThreads) {
@@ -387,7 +412,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
         if (mine > 0 && ex <= t0 && t0 < ex + mine) {
           const int tiles = row_tiles(p, s);
           const int64_t per = chunk_prefix(p, s, tiles);
-          const int64_t h = (t0 - ex) / per, at = t0 - ex - h * per;
+          const int64_t h = quotient(t0 - ex, per), at = t0 - ex - h * per;
           int lo = 0, hi = tiles;  // the largest m with prefix(m) <= at
           while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -401,7 +426,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
           start->m = lo;
           start->off = ex + h * per + chunk_prefix(p, s, lo);
           start->total = total;
-          start->used = (int)used;
+          start->used = used;
         }
       }
       __syncthreads();
@@ -1044,16 +1069,16 @@ __global__ void __launch_bounds__(kMergeThreads) va_chunk_merge_kernel(const Chu
   if (threadIdx.x < 32) {
     // the slots of the item's parts, in the pairs' order
     const int lane = threadIdx.x;
-    const int64_t unit = (int64_t)kKeys * p.group;
+    const int64_t share = share_units(st.total, used);
     int n = 0;
-    if (st.off < share_begin(st.total, c, used) && share_begin(st.total, c - 1, used) <= st.off) {
+    if (st.off < share_begin(st.total, share, c) && share_begin(st.total, share, c - 1) <= st.off) {
       const int tiles = item_span(p, s, st.m).n;
       for (int k0 = c - 1; k0 < used; k0 += 32) {
         const int k = k0 + lane;
         int64_t i0 = 0, i1 = 0;
         if (k < used) {
-          i0 = ceil_units(share_begin(st.total, k, used) - st.off, unit);
-          i1 = ceil_units(share_begin(st.total, k + 1, used) - st.off, unit);
+          i0 = ceil_units(p, share_begin(st.total, share, k) - st.off);
+          i1 = ceil_units(p, share_begin(st.total, share, k + 1) - st.off);
           i1 = i1 < tiles ? i1 : tiles;
         }
         const unsigned has = __ballot_sync(0xffffffffu, i0 < i1);
