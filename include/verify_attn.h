@@ -605,7 +605,7 @@ va_status verify_attn_append_mla(const va_tensor* q_pe, const va_tensor* latent,
  *  - Logits below 2^20 in magnitude (fp32 holds them to 2^-4 there).
  * verify_attn, its variants and verify_attn_mla over e4m3 caches are the same, with
  * one V scale for all pages.
- * Page-scaled caches are read by these two entry points alone: not by
+ * Page-scaled caches are read by these two entry points and verify_attn_chunk: not by
  * verify_attn_partial (and so not over context-parallel shards),
  * verify_attn_noalloc or the draft-extend pass.
  * Errors as verify_attn_opt; VA_ERR_NULL without scales, VA_ERR_DTYPE for a
@@ -793,11 +793,11 @@ size_t verify_attn_chunk_workspace_size(void);
  *
  *  workspace  the 256-byte-aligned workspace pointer that was passed to
  *             verify_attn_ex, verify_attn_opt, verify_attn_mla,
- *             verify_attn_partial or a page-scaled call; or NULL for the library's own scratch on
+ *             verify_attn_partial, verify_attn_chunk or a page-scaled call; or NULL for the library's own scratch on
  *             the current device: the workspace of calls made without one
  *             (verify_attn, and the others with a NULL workspace), the
  *             built-in array of verify_attn_noalloc, and the word of page-scaled
- *             calls with VA_LIBRARY_STATUS. The library's workspace
+ *             and chunk calls with VA_LIBRARY_STATUS. The library's workspace
  *             is replaced when it grows; its word then starts at 0 again.
  *  bits       host int32, written: the OR of the words read (0 = no bounded
  *             wait ran out since the last read and clear). Nonzero bits name

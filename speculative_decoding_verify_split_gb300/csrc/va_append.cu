@@ -22,7 +22,8 @@
 //
 // With norms a head's row is first multiplied by 1 / sqrt(mean x^2 + eps) and its
 // columns' weights: a warp holds the row anyway, so the sum takes five shuffles, for four
-// rows side by side.
+// rows side by side. The same prompts with norms take 88.8 us (87 %), a verify step 3.7 us
+// for two sequences and 5.8 us for 64.
 //
 // Every byte is read and written once, so the bound is memory: the prompts of
 // 8 sequences (14,274 tokens, 32 query and 2 KV heads, page scales, 526 MB)

@@ -1,4 +1,38 @@
 // Attention of chunks of new tokens over the paged cache, on pairs of CTAs.
+//
+// Token t of a sequence of S cached tokens, L of them new, sees the keys up to S - L + t
+// (with a window: those above S - L + t - W, and the first tokens), and
+//   out = sum_j 2^(s_j - m) V_j / sum_j 2^(s_j - m),   s = log2(e) softmax_scale q . k_j,
+// with soft cap and sinks as the verify kernels. One pass over the keys: O and the row's
+// sum l are kept relative to a reference m that follows the running maximum, and are
+// rescaled when a tile passes it by more than 2^8.
+//
+// The rows of a KV head are the G query heads of each token, packed: row = token G + head.
+// An item is 256 rows of a sequence and KV head, 128 to each CTA of a pair (two SMs, one
+// tcgen05 MMA of M = 256): each CTA brings half of every tile's keys and half of its values'
+// columns, so a tile of 128 keys is read from L2 once for 256 rows and a CTA's shared memory
+// holds the item's Q and two to four tiles of each kind. S and P share tensor memory
+// (P is written over S); O takes 256 columns of it, two S buffers the other 256.
+//
+// Work is split by units (about keys times rows): every pair takes an equal run of them,
+// found from closed forms, so a long prompt, a few tokens over a long cache and a ragged batch
+// all fill the machine; an item that two pairs share leaves fp32 partials, which the merge
+// kernel sums in the pairs' order (the same bits at every call).
+//
+// What bounds it: 4 * 256 flops a visible (row, key) pair on the tensor cores; over long caches
+// it runs there (2,048 tokens, 16 query heads over one KV head: bf16 over 63K keys 1.12 ms, 1.94
+// PFLOP/s, e4m3 over 129K 2.33 ms, 1.87; the cuBLAS peak measured here is 1.91). At
+// that rate a tile's MMAs take 1.3 us, in which each CTA's softmax has to be through with one
+// too: 16 warps, in two groups that take the tiles in turn (e4m3 with 8 warps 2.87 ms,
+// 2.45 when they became 16). Page scales cost the softmax a multiply
+// and a sum for each page (1.62 ms, 1.34 PFLOP/s), the soft cap an exponential and a division a logit
+// (1.86 ms, 1.16). Short calls are bound by the chain of share, Q, first tiles, epilogue and
+// merge: two sequences of 40 tokens over 600 keys 20 us. One token in each of many sequences
+// fills 16 of an item's 256 rows: 97 us for 269 MB, 2.8 TB/s.
+//
+// e4m3 caches: K's codes go to the MMA as they are (kind::f8f6f4), with Q as two e4m3 terms,
+// which holds bf16's 8 bits at the rate of one bf16 product; V's codes become f16 on the way
+// (exactly), for weights in f16.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -875,156 +909,156 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
       }
     } else {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    if (warp == kWarpPlan) {
-      Walk w = start_walk(p, *start);
-      __syncwarp();  // (the pieces take start's place)
-      Piece pc;
-      for (bool more = true; more && ok; ++at) {
-        more = next_piece(p, t0, t1, w, pc);
-        if (!more) pc.n = -1;
-        if (at >= kPieces && !wait_for(kBarPieceEmpty + at % kPieces, at / kPieces - 1, 16384)) break;
-        if (lane == 0) *reinterpret_cast<Piece*>(misc + kOffPieces + at % kPieces * sizeof(Piece)) = pc;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPieceFull + at % kPieces));
-      }
-    } else if (warp < kWarpMma) {
-      // ======================= TMA producers =========================================
-      // One warp for K's tiles, one for V's. One 2 KB box (a page's 16 tokens x 128
-      // bytes) a lane: this CTA's half of K's keys, or of V's columns. Pages that no row of
-      // the item sees are not mapped perhaps: they are read past the cache's last page,
-      // which TMA fills with zeros. Page ids are loaded two tiles ahead.
-      const bool is_k = warp == kWarpProducer;
-      constexpr int kDim = kFp8 ? 2 : 4;    // 128-byte chunks of a row
-      constexpr int kEl = kFp8 ? 128 : 64;  // elements of a chunk
-      const int chunks = is_k ? kDim : kDim / 2;
-      const int box_page = lane / chunks + (is_k ? 4 * rank : 0), box_ch = lane % chunks;
-      const bool on = lane < (is_k ? 4 : 8) * chunks;
-      const uint32_t ring = sbase + (is_k ? C::kOffK : C::kOffTmaV);
-      const int bytes = is_k ? C::kKBytes : C::kTmaVBytes, slots = is_k ? C::kKSlots : C::kTmaVSlots;
-      const uint32_t box = ring + (is_k ? box_ch * (64 * 128) + lane / chunks * 2048 : box_ch * (128 * 128) + box_page * 2048);
-      const int el = is_k ? box_ch * kEl : (rank * (kDim / 2) + box_ch) * kEl;
-      const int full = is_k ? kBarKFull : kBarVLanded, empty = is_k ? kBarKEmpty : kFp8 ? kBarRawEmpty : kBarVEmpty;
-      const bool scl = kScl && is_k && lane >= 24;  // lanes that bring the tile's page scales
-      const int page_of = scl ? lane - 24 : box_page;
-      int tiles = 0;
-      while (const volatile Piece* pc = take()) {
-        const Span x{pc->x.klo, pc->x.khi, pc->x.nf, pc->x.w0, 0};
-        const int n = pc->n, i0 = pc->i0, h = pc->h;
-        const int* bt = p.block_table + (int64_t)pc->b * p.bt_s0;
-        give_back();
-        auto page_id = [&](int i) {
-          const int page = tile_of(x, i0 + i) * (kKeys / kPageSize) + page_of, key = page * kPageSize;
-          const bool seen = i < n && (on || scl) && key < x.khi && (key + kPageSize > x.klo || key < p.first_tokens);
-          return seen ? bt[(int64_t)page * p.bt_s1] : -1;
-        };
-        float ks = 1.f, vs = 1.f;
-        auto scales_of = [&](int id) {
-          ks = vs = 1.f;
-          if (scl && (unsigned)id < (unsigned)p.num_blocks) {
-            ks = __ldg(p.k_scales + (int64_t)id * p.ks_s0 + (int64_t)h * p.ks_s1);
-            vs = __ldg(p.v_scales + (int64_t)id * p.vs_s0 + (int64_t)h * p.vs_s1);
-          }
-        };
-        int id = page_id(0), id1 = page_id(1);
-        if (kScl) scales_of(id);
-        for (int i = 0; i < n && ok; ++i) {
-          const int cur = tiles + i, slot = cur % slots;
-          if (cur >= slots && !wait_for(empty + slot, cur / slots - 1, 1)) break;
-          if (kScl && is_k) {
-            if (scl) {
-              const float k1 = fminf(fmaxf(ks, kMinPageScale), kMaxPageScale);
-              const float v1 = fminf(fmaxf(vs, kMinPageScale), kMaxPageScale);
-              page_scale[cur % kScaleTiles * 8 + lane - 24] = make_float2(k1, log2f(v1));
+      if (warp == kWarpPlan) {
+        Walk w = start_walk(p, *start);
+        __syncwarp();  // (the pieces take start's place)
+        Piece pc;
+        for (bool more = true; more && ok; ++at) {
+          more = next_piece(p, t0, t1, w, pc);
+          if (!more) pc.n = -1;
+          if (at >= kPieces && !wait_for(kBarPieceEmpty + at % kPieces, at / kPieces - 1, 16384)) break;
+          if (lane == 0) *reinterpret_cast<Piece*>(misc + kOffPieces + at % kPieces * sizeof(Piece)) = pc;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarPieceFull + at % kPieces));
+        }
+      } else if (warp < kWarpMma) {
+        // ======================= TMA producers =========================================
+        // One warp for K's tiles, one for V's. One 2 KB box (a page's 16 tokens x 128
+        // bytes) a lane: this CTA's half of K's keys, or of V's columns. Pages that no row of
+        // the item sees are not mapped perhaps: they are read past the cache's last page,
+        // which TMA fills with zeros. Page ids are loaded two tiles ahead.
+        const bool is_k = warp == kWarpProducer;
+        constexpr int kDim = kFp8 ? 2 : 4;    // 128-byte chunks of a row
+        constexpr int kEl = kFp8 ? 128 : 64;  // elements of a chunk
+        const int chunks = is_k ? kDim : kDim / 2;
+        const int box_page = lane / chunks + (is_k ? 4 * rank : 0), box_ch = lane % chunks;
+        const bool on = lane < (is_k ? 4 : 8) * chunks;
+        const uint32_t ring = sbase + (is_k ? C::kOffK : C::kOffTmaV);
+        const int bytes = is_k ? C::kKBytes : C::kTmaVBytes, slots = is_k ? C::kKSlots : C::kTmaVSlots;
+        const uint32_t box = ring + (is_k ? box_ch * (64 * 128) + lane / chunks * 2048 : box_ch * (128 * 128) + box_page * 2048);
+        const int el = is_k ? box_ch * kEl : (rank * (kDim / 2) + box_ch) * kEl;
+        const int full = is_k ? kBarKFull : kBarVLanded, empty = is_k ? kBarKEmpty : kFp8 ? kBarRawEmpty : kBarVEmpty;
+        const bool scl = kScl && is_k && lane >= 24;  // lanes that bring the tile's page scales
+        const int page_of = scl ? lane - 24 : box_page;
+        int tiles = 0;
+        while (const volatile Piece* pc = take()) {
+          const Span x{pc->x.klo, pc->x.khi, pc->x.nf, pc->x.w0, 0};
+          const int n = pc->n, i0 = pc->i0, h = pc->h;
+          const int* bt = p.block_table + (int64_t)pc->b * p.bt_s0;
+          give_back();
+          auto page_id = [&](int i) {
+            const int page = tile_of(x, i0 + i) * (kKeys / kPageSize) + page_of, key = page * kPageSize;
+            const bool seen = i < n && (on || scl) && key < x.khi && (key + kPageSize > x.klo || key < p.first_tokens);
+            return seen ? bt[(int64_t)page * p.bt_s1] : -1;
+          };
+          float ks = 1.f, vs = 1.f;
+          auto scales_of = [&](int id) {
+            ks = vs = 1.f;
+            if (scl && (unsigned)id < (unsigned)p.num_blocks) {
+              ks = __ldg(p.k_scales + (int64_t)id * p.ks_s0 + (int64_t)h * p.ks_s1);
+              vs = __ldg(p.v_scales + (int64_t)id * p.vs_s0 + (int64_t)h * p.vs_s1);
+            }
+          };
+          int id = page_id(0), id1 = page_id(1);
+          if (kScl) scales_of(id);
+          for (int i = 0; i < n && ok; ++i) {
+            const int cur = tiles + i, slot = cur % slots;
+            if (cur >= slots && !wait_for(empty + slot, cur / slots - 1, 1)) break;
+            if (kScl && is_k) {
+              if (scl) {
+                const float k1 = fminf(fmaxf(ks, kMinPageScale), kMaxPageScale);
+                const float v1 = fminf(fmaxf(vs, kMinPageScale), kMaxPageScale);
+                page_scale[cur % kScaleTiles * 8 + lane - 24] = make_float2(k1, log2f(v1));
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(kBarScales + cur % kScaleTiles));
+              scales_of(id1);
+            }
+            if (lane == 0) {
+              issued[is_k ? 0 : 1] = cur + 1;
+              mbar_arrive_expect_tx(bar(full + slot), bytes);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarScales + cur % kScaleTiles));
-            scales_of(id1);
-          }
-          if (lane == 0) {
-            issued[is_k ? 0 : 1] = cur + 1;
-            mbar_arrive_expect_tx(bar(full + slot), bytes);
-          }
-          __syncwarp();
-          if (on)
-            tma_load_4d(box + slot * bytes, is_k ? &tm_k : &tm_v, el, h, 0,
-                        (unsigned)id < (unsigned)p.num_blocks ? id : p.num_blocks, bar(full + slot));
-          __syncwarp();
-          id = id1;
-          id1 = page_id(i + 2);
-        }
-        tiles += n;
-      }
-    } else if (warp == kWarpMma) {
-      // ======================= MMA issuer (the even CTA) ===============================
-      // Q K^T of tile i + 1, then P V of tile i. The odd CTA's warp tells it that its half
-      // of a K tile has landed.
-      int tiles = 0, piece = 0;
-      while (const volatile Piece* pc = take()) {
-        const int n = pc->n;
-        give_back();
-        if (n == 0) continue;
-        if (rank == 1) {
-          for (int i = 0; i < n; ++i) {
-            const int slot = (tiles + i) % C::kKSlots;
-            if (!wait_for(kBarKFull + slot, (tiles + i) / C::kKSlots, 4)) break;
-            if (lane == 0) mbar_arrive_cluster(lead(kBarKPeer + slot));
+            if (on)
+              tma_load_4d(box + slot * bytes, is_k ? &tm_k : &tm_v, el, h, 0,
+                          (unsigned)id < (unsigned)p.num_blocks ? id : p.num_blocks, bar(full + slot));
+            __syncwarp();
+            id = id1;
+            id1 = page_id(i + 2);
           }
           tiles += n;
-          continue;
         }
-        if (!wait_for(kBarQFull, piece, 2)) break;
-        for (int i = 0; i <= n && ok; ++i) {
-          if (i < n) {
-            const int cur = tiles + i, slot = cur % C::kKSlots, use = cur / C::kKSlots;
-            if (!wait_for(kBarKFull + slot, use, 4) || !wait_for(kBarKPeer + slot, use, 4)) break;
-            tc_fence_after();
-            const uint32_t src = sbase + C::kOffK + slot * C::kKBytes;
-            if (elect_one()) {
+      } else if (warp == kWarpMma) {
+        // ======================= MMA issuer (the even CTA) ===============================
+        // Q K^T of tile i + 1, then P V of tile i. The odd CTA's warp tells it that its half
+        // of a K tile has landed.
+        int tiles = 0, piece = 0;
+        while (const volatile Piece* pc = take()) {
+          const int n = pc->n;
+          give_back();
+          if (n == 0) continue;
+          if (rank == 1) {
+            for (int i = 0; i < n; ++i) {
+              const int slot = (tiles + i) % C::kKSlots;
+              if (!wait_for(kBarKFull + slot, (tiles + i) / C::kKSlots, 4)) break;
+              if (lane == 0) mbar_arrive_cluster(lead(kBarKPeer + slot));
+            }
+            tiles += n;
+            continue;
+          }
+          if (!wait_for(kBarQFull, piece, 2)) break;
+          for (int i = 0; i <= n && ok; ++i) {
+            if (i < n) {
+              const int cur = tiles + i, slot = cur % C::kKSlots, use = cur / C::kKSlots;
+              if (!wait_for(kBarKFull + slot, use, 4) || !wait_for(kBarKPeer + slot, use, 4)) break;
+              tc_fence_after();
+              const uint32_t src = sbase + C::kOffK + slot * C::kKBytes;
+              if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                // bf16: 16 columns of d; e4m3: 32, of Q's first term, then of its second
-                const uint32_t ko = (uint32_t)((k & 3) * 32);
-                const uint64_t a = smem_desc(sbase + C::kOffQ + (k >> 2) * (128 * 128) + ko, 16, 1024, kLayoutSw128);
-                const uint64_t b = smem_desc(src + (kFp8 ? (k >> 2) & 1 : k >> 2) * (64 * 128) + ko, 16, 1024, kLayoutSw128);
-                if constexpr (kFp8)
-                  mma_f8f6f4_pair(tmem + kColS + (cur & 1) * kKeys, a, b, C::kIdQK, k ? 1u : 0u);
-                else
-                  mma_f16_pair(tmem + kColS + (cur & 1) * kKeys, a, b, C::kIdQK, k ? 1u : 0u);
+                for (int k = 0; k < 16; ++k) {
+                  // bf16: 16 columns of d; e4m3: 32, of Q's first term, then of its second
+                  const uint32_t ko = (uint32_t)((k & 3) * 32);
+                  const uint64_t a = smem_desc(sbase + C::kOffQ + (k >> 2) * (128 * 128) + ko, 16, 1024, kLayoutSw128);
+                  const uint64_t b = smem_desc(src + (kFp8 ? (k >> 2) & 1 : k >> 2) * (64 * 128) + ko, 16, 1024, kLayoutSw128);
+                  if constexpr (kFp8)
+                    mma_f8f6f4_pair(tmem + kColS + (cur & 1) * kKeys, a, b, C::kIdQK, k ? 1u : 0u);
+                  else
+                    mma_f16_pair(tmem + kColS + (cur & 1) * kKeys, a, b, C::kIdQK, k ? 1u : 0u);
+                }
+                mma_commit_pair(bar(kBarSFull + (cur & 1)));
+                mma_commit_pair(bar(kBarKEmpty + slot));
+                if (i == n - 1) mma_commit_pair(bar(kBarQFree));
               }
-              mma_commit_pair(bar(kBarSFull + (cur & 1)));
-              mma_commit_pair(bar(kBarKEmpty + slot));
-              if (i == n - 1) mma_commit_pair(bar(kBarQFree));
+              __syncwarp();
             }
-            __syncwarp();
-          }
-          if (i > 0) {
-            const int cur = tiles + i - 1, slot = cur % C::kVSlots;
-            if (!wait_for(kBarVFull + slot, cur / C::kVSlots, 4)) break;
-            if (!wait_for(kBarPFull + (cur & 1), cur >> 1, 8)) break;
-            if (i == 1 && piece > 0 && !wait_for(kBarOFree, piece - 1, 16)) break;
-            tc_fence_after();
-            const uint32_t src = sbase + C::kOffV + slot * C::kVBytes;
-            if (elect_one()) {
+            if (i > 0) {
+              const int cur = tiles + i - 1, slot = cur % C::kVSlots;
+              if (!wait_for(kBarVFull + slot, cur / C::kVSlots, 4)) break;
+              if (!wait_for(kBarPFull + (cur & 1), cur >> 1, 8)) break;
+              if (i == 1 && piece > 0 && !wait_for(kBarOFree, piece - 1, 16)) break;
+              tc_fence_after();
+              const uint32_t src = sbase + C::kOffV + slot * C::kVBytes;
+              if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                mma_f16_pair_ta(tmem + kColO, tmem + kColS + (cur & 1) * kKeys + 64 * (k >> 2) + 8 * (k & 3),
-                                smem_desc(src + k * 2048, 128 * 128, 1024, kLayoutSw128), C::kIdPV, i > 1 || k ? 1u : 0u);
-              mma_commit_pair(bar(kBarPvDone + (cur & 1)));
-              mma_commit_pair(bar(kBarVEmpty + slot));
+                for (int k = 0; k < kKeys / 16; ++k)
+                  mma_f16_pair_ta(tmem + kColO, tmem + kColS + (cur & 1) * kKeys + 64 * (k >> 2) + 8 * (k & 3),
+                                  smem_desc(src + k * 2048, 128 * 128, 1024, kLayoutSw128), C::kIdPV, i > 1 || k ? 1u : 0u);
+                mma_commit_pair(bar(kBarPvDone + (cur & 1)));
+                mma_commit_pair(bar(kBarVEmpty + slot));
+              }
+              __syncwarp();
             }
-            __syncwarp();
           }
+          tiles += n;
+          ++piece;
         }
-        tiles += n;
-        ++piece;
+        // every MMA has finished before the pair frees its memory
+        if (rank == 0 && elect_one()) {
+          mma_commit_pair(bar(kBarDrain));
+          mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
+        }
+        __syncwarp();
       }
-      // every MMA has finished before the pair frees its memory
-      if (rank == 0 && elect_one()) {
-        mma_commit_pair(bar(kBarDrain));
-        mbar_wait_drain(bar(kBarDrain), 0, kDrainLimitNs);
-      }
-      __syncwarp();
-    }
     }
   }
   tc_fence_before();
