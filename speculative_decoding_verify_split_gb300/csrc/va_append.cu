@@ -21,9 +21,10 @@
 // fp32 arithmetic.
 //
 // With norms a head's row is first multiplied by 1 / sqrt(mean x^2 + eps) and its
-// columns' weights: a warp holds the row anyway, so the sum takes five shuffles, for four
-// rows side by side. The same prompts with norms take 88.8 us (87 %), a verify step 3.7 us
-// for two sequences and 5.8 us for 64.
+// columns' weights. A warp holds the row anyway: four rows' sums take six shuffles, and their
+// roots are taken side by side. Prompts of 12.8K tokens (32 query and 2 KV heads, page
+// scales, 472 MB) take 81.0 us, 86 % of the measured copy bandwidth, bound by issue (68 % of
+// the slots where they took 88.8 us) as much as by memory; a verify step 3.8 us for two sequences, 5.7 us for 256.
 //
 // Every byte is read and written once, so the bound is memory: the prompts of
 // 8 sequences (14,274 tokens, 32 query and 2 KV heads, page scales, 526 MB)
@@ -41,9 +42,15 @@
 
 #include "va_append.h"
 #include "va_fp8.cuh"
+#include "va_ptx.cuh"
 
 namespace va {
 namespace {
+
+using ptx::fma2;
+using ptx::mul2;
+using ptx::pack2;
+using ptx::unpack2;
 
 constexpr int kKvThreads = 128;      // GQA caches: K or V rows of a page and KV head, or query heads
 constexpr int kMlaThreads = 256;     // latent caches
@@ -186,13 +193,31 @@ __device__ __forceinline__ Lane lane_columns(int lane, int rot) {
   return c;
 }
 
-template <bool INTER>
+// PACK: two products an instruction and the sums one by one, the same bits (packed sums are
+// fused with the products). It pays where the norms make instruction issue the bound, prompts
+// 83.0 -> 81.0 us, and costs 1.4 us of 84.7 without them.
+template <bool INTER, bool PACK>
 __device__ __forceinline__ void rotate8(float* x, float4 c, float4 s) {
   if (INTER) {
     rotate(x[0], x[1], c.x, s.x);
     rotate(x[2], x[3], c.y, s.y);
     rotate(x[4], x[5], c.z, s.z);
     rotate(x[6], x[7], c.w, s.w);
+  } else if (PACK) {
+    auto two = [](float* y, float c0, float c1, float s0, float s1) {
+      const uint64_t a = pack2(y[0], y[1]), b = pack2(y[4], y[5]), cc = pack2(c0, c1), ss = pack2(s0, s1);
+      float ac0, ac1, bs0, bs1, bc0, bc1, as0, as1;
+      unpack2(mul2(a, cc), ac0, ac1);
+      unpack2(mul2(b, ss), bs0, bs1);
+      unpack2(mul2(b, cc), bc0, bc1);
+      unpack2(mul2(a, ss), as0, as1);
+      y[0] = __fsub_rn(ac0, bs0);
+      y[1] = __fsub_rn(ac1, bs1);
+      y[4] = __fadd_rn(bc0, as0);
+      y[5] = __fadd_rn(bc1, as1);
+    };
+    two(x, c.x, c.y, s.x, s.y);
+    two(x + 2, c.z, c.w, s.z, s.w);
   } else {
     rotate(x[0], x[4], c.x, s.x);
     rotate(x[1], x[5], c.y, s.y);
@@ -269,12 +294,16 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// The sums of four values over the warp's lanes, in every lane.
-__device__ __forceinline__ void warp_sum4(float* v) {
+// The sums of four values over the warp's lanes: lanes 8 i to 8 i + 7 get v[i]'s. Half the
+// lanes go on with two of the values, a quarter with one: six shuffles.
+__device__ __forceinline__ float warp_sum4(const float* v, int lane) {
+  const bool up = lane & 16, odd = lane & 8;
+  float a = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+  float b = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
+  a = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  return a;
 }
 
 // The norm's weights of a lane's eight columns, the offset added.
@@ -293,20 +322,24 @@ __device__ __forceinline__ void norm_weights(const void* w, bool fp32, float off
 }
 
 // Four rows of 256, eight columns of each a lane, times 1 / sqrt(mean x^2 + eps) and w.
-__device__ __forceinline__ void normalise4(float (&x)[4][8], const float* w, float eps) {
+__device__ __forceinline__ void normalise4(float (&x)[4][8], const float* w, float eps, int lane) {
   float s[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    s[k] = 0.f;
+    uint64_t t = mul2(pack2(x[k][0], x[k][1]), pack2(x[k][0], x[k][1]));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[k] = fmaf(x[k][i], x[k][i], s[k]);
+    for (int i = 2; i < 8; i += 2) t = fma2(pack2(x[k][i], x[k][i + 1]), pack2(x[k][i], x[k][i + 1]), t);
+    float a, b;
+    unpack2(t, a, b);
+    s[k] = a + b;
   }
-  warp_sum4(s);
+  const float r = rsqrtf(fmaf(warp_sum4(s, lane), 1.f / kHeadDim, eps));
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float r = rsqrtf(fmaf(s[k], 1.f / kHeadDim, eps));
+    const float f = __shfl_sync(0xffffffffu, r, 8 * k);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[k][i] = x[k][i] * r * w[i];
+    for (int i = 0; i < 8; i += 2)
+      unpack2(mul2(mul2(pack2(x[k][i], x[k][i + 1]), pack2(f, f)), pack2(w[i], w[i + 1])), x[k][i], x[k][i + 1]);
   }
 }
 
@@ -315,8 +348,9 @@ __device__ __forceinline__ void normalise4(float (&x)[4][8], const float* w, flo
 // blockIdx.y < 2 hkv: the page's K rows (even) or V rows (odd) of one KV head,
 // four slots of the page per warp. Above: the same tokens' rows of
 // kHeadsPerCta query heads, a token per warp. NORM: with the norms' code.
+// Seven CTAs an SM with norms: 72 registers a thread (8 CTAs 83.9 us and 6 85.4 for 83.0).
 template <int KIND, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kKvThreads, 8) va_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kKvThreads, NORM ? 7 : 8) va_append_kernel(const AppendParams p) {
   constexpr int kWarps = kKvThreads / 32;
   __shared__ UnitShared sh;
   __shared__ float s_amax[kWarps];
@@ -328,6 +362,10 @@ __global__ void __launch_bounds__(kKvThreads, 8) va_append_kernel(const AppendPa
 
   if ((int)blockIdx.y >= 2 * p.hkv) {  // ---- query heads
     const int hb = ((int)blockIdx.y - 2 * p.hkv) * kHeadsPerCta;
+    [[maybe_unused]] float w[8];
+    if constexpr (NORM) {
+      if (p.q_norm) norm_weights(p.q_norm, p.q_norm_fp32, p.norm_offset, col, w);
+    }
     for (int t = warp; t < (int)(u.hi - u.lo); t += kWarps) {  // a token's heads, all their loads at once
       const int tok = u.tok0 + t;
       const uint16_t* src = p.q + (int64_t)tok * p.q_s0;
@@ -354,11 +392,7 @@ __global__ void __launch_bounds__(kKvThreads, 8) va_append_kernel(const AppendPa
           unpack4(w1[i], xn[i]);
           unpack4(w2[i], xn[i] + 4);
         }
-        if (p.q_norm) {
-          float w[8];
-          norm_weights(p.q_norm, p.q_norm_fp32, p.norm_offset, col, w);
-          normalise4(xn, w, p.norm_eps);
-        }
+        if (p.q_norm) normalise4(xn, w, p.norm_eps, lane);
       }
 #pragma unroll
       for (int i = 0; i < kHeadsPerCta; ++i) {
@@ -370,7 +404,7 @@ __global__ void __launch_bounds__(kKvThreads, 8) va_append_kernel(const AppendPa
           unpack4(w1[i], x);
           unpack4(w2[i], x + 4);
         }
-        if (col.turn) rotate8<INTER>(x, c, sn);
+        if (col.turn) rotate8<INTER, NORM>(x, c, sn);
         if (hb + i < p.hq) {
           uint16_t* dst = out + (int64_t)(hb + i) * p.qo_s1;
           *reinterpret_cast<uint2*>(dst + col.o1) = to_bf16x4(x);
@@ -446,12 +480,12 @@ __global__ void __launch_bounds__(kKvThreads, 8) va_append_kernel(const AppendPa
     if (is_k && p.k_norm) {
       float w[8];
       norm_weights(p.k_norm, p.k_norm_fp32, p.norm_offset, col, w);
-      normalise4(x, w, p.norm_eps);
+      normalise4(x, w, p.norm_eps, lane);
     }
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    if (turn) rotate8<INTER>(x[k], cs[k], sn[k]);
+    if (turn) rotate8<INTER, NORM>(x[k], cs[k], sn[k]);
     if (KIND == kPageScaled) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[k][i]));  // NaN counts as 0
@@ -539,7 +573,7 @@ __global__ void __launch_bounds__(kMlaThreads, 4) va_append_mla_kernel(const App
         float x[8];
         unpack4(w1[i], x);
         unpack4(w2[i], x + 4);
-        rotate8<INTER>(x, c, sn);
+        rotate8<INTER, false>(x, c, sn);
         if (g + 4 * i < nh) {
           uint16_t* dst = out + (int64_t)(h0 + g + 4 * i) * p.qo_s1;
           *reinterpret_cast<uint2*>(dst + o1) = to_bf16x4(x);
