@@ -656,7 +656,8 @@ va_status verify_attn_mla_scaled(const va_tensor* q, const va_tensor* kv_cache, 
  *  VA_PG_BAD_TABLE  a count below its tokens or past the row, a page outside the pool, or
  *                   one freed more often than it was held (its count stays 0)
  * Errors before launching: VA_ERR_NULL, VA_ERR_SHAPE, VA_ERR_DTYPE (all int32),
- * VA_ERR_LAYOUT (strided vectors; a block table whose entries overlap).
+ * VA_ERR_LAYOUT (strided vectors; a block table whose entries overlap; a vector that is
+ * written over another one).
  */
 #define VA_PG_BAD_SEQ 1
 #define VA_PG_IN_USE 2
@@ -711,7 +712,7 @@ va_status verify_attn_reserve_pages(va_tensor* block_table, const va_tensor* seq
  *               written twice, or written and read, has unspecified contents.
  * Errors: VA_ERR_NULL, VA_ERR_SHAPE, VA_ERR_DTYPE (scales over a BF16 cache), VA_ERR_LAYOUT
  * (elements on top of each other, K and V in one place), VA_ERR_UNSUPPORTED (pages other
- * than 16, other widths, pages past 16 M elements a token row).
+ * than 16, other widths, 16 M elements or more a token row).
  */
 va_status verify_attn_copy_pages(va_tensor* k_cache, va_tensor* v_cache, va_tensor* k_scales, va_tensor* v_scales,
                                  const va_tensor* src, const va_tensor* dst, void* stream);

@@ -42,6 +42,8 @@ va_status validate_chunk(const va_tensor* q, const va_tensor* k, const va_tensor
     if (s == VA_OK) s = check_rows(t);
   if (s != VA_OK) return s;
   if (!rows_distinct(out)) return VA_ERR_LAYOUT;
+  for (const va_tensor* t : {bt, cu, su, opts ? opts->sinks : nullptr})
+    if (t && (reinterpret_cast<uintptr_t>(t->data) & 3u) != 0) return VA_ERR_LAYOUT;
   if ((ks != nullptr) != (vs != nullptr)) return VA_ERR_NULL;
   if (ks) {
     if (k->dtype != VA_FP8_E4M3) return VA_ERR_DTYPE;

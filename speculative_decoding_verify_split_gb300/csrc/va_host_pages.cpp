@@ -2,6 +2,7 @@
 // validation and the launches.
 #include <climits>
 #include <cstring>
+#include <initializer_list>
 
 #include "va_host_impl.h"
 #include "va_pages.h"
@@ -23,6 +24,27 @@ va_status check_ints(const va_tensor* t, int64_t n) {
   if (t->shape[0] > 1 && t->stride[0] != 1) return VA_ERR_LAYOUT;
   if (t->shape[0] > 0 && !t->data) return VA_ERR_NULL;
   return (reinterpret_cast<uintptr_t>(t->data) & 3u) != 0 ? VA_ERR_LAYOUT : VA_OK;
+}
+
+// Whether a written vector has its place to itself: none of `n` others reaches into it.
+bool apart(const va_tensor* t, const va_tensor* const* others, int n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(t->data), e = a + 4 * (uintptr_t)t->shape[0];
+  for (int i = 0; i < n; ++i) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(others[i]->data), f = b + 4 * (uintptr_t)others[i]->shape[0];
+    if (a < f && b < e && a < e && b < f) return false;
+  }
+  return true;
+}
+
+// The last `fresh` of the vectors, and the first three, are written; those between are read.
+bool all_apart(std::initializer_list<const va_tensor*> v, int fresh) {
+  const int n = (int)v.size();
+  for (int i = 0; i < n; ++i) {
+    const bool written = i < 3 || i >= n - fresh;
+    const va_tensor* const* t = v.begin();
+    if (written && !(apart(t[i], t, i) && apart(t[i], t + i + 1, n - i - 1))) return false;
+  }
+  return true;
 }
 
 va_status check_pool(const va_tensor* bt, const va_tensor* su, const va_tensor* pc, const va_tensor* refs, int32_t* status,
@@ -59,7 +81,7 @@ va_status check_copied(const va_tensor* t, const va_tensor* scales, PageView* v)
   if (t->dtype != VA_BF16 && t->dtype != VA_FP8_E4M3) return VA_ERR_DTYPE;
   const int64_t es = t->dtype == VA_BF16 ? 2 : 1;
   if (t->shape[1] != kPageSize || t->shape[3] * es % 16 != 0 || t->shape[0] > INT32_MAX || t->shape[2] < 1 || t->shape[3] < 1 ||
-      t->shape[2] * t->shape[3] > (1 << 24))
+      t->shape[2] * t->shape[3] >= (1 << 24))
     return VA_ERR_UNSUPPORTED;
   va_status s = check_rows(t);
   if (s != VA_OK) return s;
@@ -125,6 +147,7 @@ VA_EXPORT va_status verify_attn_free_pages(const va_tensor* block_table, va_tens
   if (!seqs) return VA_ERR_NULL;
   s = check_ints(seqs, -1);
   if (s != VA_OK) return s;
+  if (!all_apart({seqused_k, page_count, refs, seqs}, 0)) return VA_ERR_LAYOUT;
   p.list = static_cast<const int32_t*>(seqs->data);
   p.n = (int32_t)seqs->shape[0];
   if (p.n == 0) return VA_OK;
@@ -141,6 +164,7 @@ VA_EXPORT va_status verify_attn_fork_pages(va_tensor* block_table, va_tensor* se
   s = check_ints(parents, -1);
   if (s == VA_OK) s = check_ints(children, parents->shape[0]);
   if (s != VA_OK) return s;
+  if (!all_apart({seqused_k, page_count, refs, parents, children}, 0)) return VA_ERR_LAYOUT;
   p.list = static_cast<const int32_t*>(parents->data);
   p.children = static_cast<const int32_t*>(children->data);
   p.n = (int32_t)parents->shape[0];
@@ -161,6 +185,7 @@ VA_EXPORT va_status verify_attn_reserve_pages(va_tensor* block_table, const va_t
     if (s != VA_OK) return s;
   }
   if (p.num_seqs > va::kMaxPoolSeqs || p.num_pages > va::kMaxPoolPages) return VA_ERR_UNSUPPORTED;
+  if (!all_apart({seqused_k, page_count, refs, new_tokens, src, dst, room}, 3)) return VA_ERR_LAYOUT;
   p.new_tokens = static_cast<const int32_t*>(new_tokens->data);
   p.src = static_cast<int32_t*>(src->data);
   p.dst = static_cast<int32_t*>(dst->data);

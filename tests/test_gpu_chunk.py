@@ -273,3 +273,21 @@ def test_more_splits_than_units(splits):
     b = Chunk([70], [300], 8, 1, KINDS[1], 33)
     want, size = b.expect()
     assert (np.abs(decode(b.run(num_splits=splits)) - want) <= tolerance(b, want, size)).all()
+
+
+def test_two_streams_at_once():
+    """Calls that are under way together have workspaces of their own."""
+    a, b = Chunk([300, 5], [4000, 900], 8, 1, "bf16", 34), Chunk([200], [5000], 16, 2, "scaled", 35)
+    calls = []
+    for x in (a, b):
+        kw = dict(k_scales=gpu(x.scales[0]), v_scales=gpu(x.scales[1]))
+        calls.append((x.args(), x.scale, kw, va.verify_attn_chunk(*x.args(), x.scale, **kw), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (args, scale, kw, _, stream) in enumerate(calls):
+            got[i].append(va.verify_attn_chunk(*args, scale, stream=stream, out=torch.empty_like(args[0]), **kw))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(calls[i][3], o) for o in got[i])
+    assert va.last_device_error() == 0
