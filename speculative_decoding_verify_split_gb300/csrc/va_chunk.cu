@@ -82,8 +82,8 @@ __device__ __forceinline__ int row_tiles(const ChunkParams& p, const Seq& s) {
 
 // Tiles (in units) that a share has at least: small calls take fewer pairs, whose partials
 // cost more to write and to join than the tiles they save (two sequences of 40 tokens
-// over 600 keys: 20.3 us, with 4 24.8, with 8 32.0).
-constexpr int64_t kMinShare = 6;
+// over 600 keys: 19.9 us, with 8 too, with 6 24.2, with 9 33.4).
+constexpr int64_t kMinShare = 7;
 
 // Units of the split: a tile is 128 G of them. Row tile m costs
 //   min(max(0, (S - L) G + 256 (m + 1)), cap) + kChunkItemCost * 128 G,

@@ -14,8 +14,10 @@ namespace va {
 constexpr int kChunkRows = 256;  // packed rows of a work item: 128 per CTA of the pair
 constexpr int kChunkKeys = 128;  // keys of a tile
 // Cost of an item beside its tiles, in tiles: Q's load, the pipeline's refill and the
-// epilogue; at least 3 (see chunk_cost).
-constexpr int kChunkItemCost = 3;
+// epilogue; at least 3 (see chunk_cost). A prompt of 8,192 tokens (16 query and 2 KV heads)
+// and four of 700 to 2,500: 3 tiles 379 and 126 us, 4 362 and 123, 5 333 and 117, 6 341 and
+// 119, 7 335 and 120.
+constexpr int kChunkItemCost = 5;
 
 struct ChunkParams {
   const uint16_t* q;  // [total_q, hq, 256] bf16 bits
