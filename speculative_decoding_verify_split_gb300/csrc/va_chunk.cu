@@ -20,8 +20,8 @@
 // kernel sums in the pairs' order (the same bits at every call).
 //
 // What bounds it: 4 * 256 flops a visible (row, key) pair on the tensor cores; over long caches
-// it runs there (2,048 tokens, 16 query heads over one KV head: bf16 over 63K keys 1.12 ms, 1.94
-// PFLOP/s, e4m3 over 129K 2.33 ms, 1.87; the cuBLAS peak measured here is 1.91). At
+// it runs there (2,048 tokens, 16 query heads over one KV head: bf16 over 63K keys 1.12 ms, 1.93
+// PFLOP/s, e4m3 over 129K 2.35 ms, 1.86; the cuBLAS peak measured here is 1.91). At
 // that rate a tile's MMAs take 1.3 us, in which each CTA's softmax has to be through with one
 // too: 16 warps, in two groups that take the tiles in turn (e4m3 with 8 warps 2.87 ms,
 // 2.45 when they became 16). Page scales cost the softmax a multiply
