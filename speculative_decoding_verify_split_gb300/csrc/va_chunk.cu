@@ -229,6 +229,7 @@ enum Kind { kBf16 = 0, kE4m3 = 1, kPageScaled = 2 };
 
 constexpr int kSoftmaxWarps = 16;
 constexpr int kPieces = 3;  // places of the queue of pieces
+constexpr int kMiscSize = 3 * 1024;  // barriers and small arrays behind the tiles
 
 // Shared memory: Q, then K's ring and V's. K goes to the MMAs as TMA brings it. So does a
 // bf16 V; e4m3 codes of V become f16 on the way, from a ring of their own. A waiter meets
@@ -256,7 +257,7 @@ struct Cfg {
   static constexpr int kOffV = kOffK + kKSlots * kKBytes;
   static constexpr int kOffRaw = kOffV + kVSlots * kVBytes;
   static constexpr int kOffMisc = kOffRaw + kRawSlots * kRawBytes;
-  static constexpr int kSmemBytes = kOffMisc + 3072;
+  static constexpr int kSmemBytes = kOffMisc + kMiscSize;
   static_assert(kSmemBytes <= 232448, "shared memory");
   // what TMA fills: V's own ring, or the codes'
   static constexpr int kTmaVSlots = kFp8 ? kRawSlots : kVSlots;
@@ -299,7 +300,7 @@ constexpr int kOffXch = kOffRow + 256;                           // [2][128] flo
 constexpr int kOffRef = kOffXch + 1024;                          // [128] floats: the rows' references
 constexpr int kOffScale = kOffRef + 512;                         // [kScaleTiles][8] (K scale, log2 V scale)
 constexpr int kMiscBytes = kOffScale + kScaleTiles * 64;
-static_assert(kMiscBytes <= 3072 && sizeof(Piece) <= 64, "misc area");
+static_assert(kMiscBytes <= kMiscSize && sizeof(Piece) <= 64, "misc area");
 
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
