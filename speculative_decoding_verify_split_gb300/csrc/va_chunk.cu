@@ -294,13 +294,17 @@ enum : int {
 };
 constexpr int kOffTmem = 8 * kNumBars, kOffAbort = kOffTmem + 4;
 constexpr int kOffIssued = kOffAbort + 4;  // K tiles and V tiles that TMA has been told to bring
-constexpr int kOffPieces = (kOffIssued + 8 + 15) / 16 * 16;      // [kPieces] Piece; before: ChunkStart
+// ChunkStart, in bytes of its own: it is read (for the merge, by the planner) while the
+// planner writes pieces already
+constexpr int kOffStart = (kOffIssued + 8 + 15) / 16 * 16;
+constexpr int kOffPieces = kOffStart + (sizeof(ChunkStart) + 15) / 16 * 16;  // [kPieces] Piece
 constexpr int kOffRow = kOffPieces + kPieces * 64;               // [2][128] exponents of Q's rows (bytes)
 constexpr int kOffXch = kOffRow + 256;                           // [2][128] floats; before: 32 x 8 bytes of the scan
 constexpr int kOffRef = kOffXch + 1024;                          // [128] floats: the rows' references
 constexpr int kOffScale = kOffRef + 512;                         // [kScaleTiles][8] (K scale, log2 V scale)
 constexpr int kMiscBytes = kOffScale + kScaleTiles * 64;
 static_assert(kMiscBytes <= kMiscSize && sizeof(Piece) <= 64, "misc area");
+static_assert(kOffStart + sizeof(ChunkStart) <= kOffPieces, "nothing lies over the start");
 
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
   const uint32_t mbase = sbase + C::kOffMisc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + kOffAbort);
   long long* scratch = reinterpret_cast<long long*>(misc + kOffXch);
-  ChunkStart* start = reinterpret_cast<ChunkStart*>(misc + kOffPieces);
+  ChunkStart* start = reinterpret_cast<ChunkStart*>(misc + kOffStart);
   volatile int* issued = reinterpret_cast<volatile int*>(misc + kOffIssued);
   unsigned char* row_exp = misc + kOffRow;
   float* refs = reinterpret_cast<float*>(misc + kOffRef);
@@ -912,7 +916,6 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
       if (warp == kWarpPlan) {
         Walk w = start_walk(p, *start);
-        __syncwarp();  // (the pieces take start's place)
         Piece pc;
         for (bool more = true; more && ok; ++at) {
           more = next_piece(p, t0, t1, w, pc);
