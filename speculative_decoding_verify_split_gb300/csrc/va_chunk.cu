@@ -518,7 +518,8 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
       // epilogue a warp writes a quarter of O's columns. After a failure a warp walks on
       // without waits and work, so that they still meet at every named barrier (1 + q: a
       // group's two warps, whose turn the reference's way grants; 5 + q and 9 + q: that way
-      // to group 0 and to group 1; 13: all).
+      // to group 0 and to group 1; 13: all). They want whole warps, as TMEM loads do: a warp
+      // whose lanes took different ways (row_ok, a lane's arrival) is brought together first.
       const int q = warp & 3, kh = (warp >> 2) & 1, grp = warp >> 3;
       const uint32_t lane_base = (uint32_t)(32 * q) << 16;
       const int r = 32 * q + lane;  // this CTA's row
@@ -528,6 +529,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
       int tiles = 0, piece = 0;
       while (true) {
         const volatile Piece* pc = take();
+        __syncwarp();
         if (named_bar_or(13, 32 * kSoftmaxWarps, pc == nullptr)) break;  // (all leave together)
         const int n = pc->n;
         const int row0 = pc->m * kChunkRows + rank * 128;  // this CTA's first row
@@ -641,6 +643,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
               const float alpha = move ? ex2(m_old - m_new) : 1.f;
               // O holds earlier tiles (of this piece: m_old is not -inf)
               tc_fence_after();
+              __syncwarp();
 #pragma unroll 1
               for (int j = 0; j < kHeadDim / 64; ++j) {
                 uint32_t o[32];
@@ -698,12 +701,14 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
         }
         // -- epilogue: the groups' references (O's is the larger) and the four sums
         tiles += n;
+        __syncwarp();
         named_bar(13, 32 * kSoftmaxWarps);
         if (kh == 0) xch[128 * grp + r] = m_ref;
         named_bar(13, 32 * kSoftmaxWarps);
         const float m_row = fmaxf(xch[r], xch[128 + r]);
         if (m_ref != m_row) l = m_ref == -INFINITY ? 0.f : l * ex2(m_ref - m_row);
         m_ref = m_row;
+        __syncwarp();
         named_bar(13, 32 * kSoftmaxWarps);
         if (kh == 1) xch[128 * grp + r] = l;
         named_bar(13, 32 * kSoftmaxWarps);
@@ -729,6 +734,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             uint32_t o[32];
+            __syncwarp();  // (rows behind the last one left the stores out)
             if (n > 0 && !idle) {
               tmem_ld_32x32b_x32(tmem + lane_base + kColO + 128 * grp + 64 * kh + 32 * j, o);
               tmem_wait_ld();
