@@ -195,7 +195,7 @@ __device__ __forceinline__ Lane lane_columns(int lane, int rot) {
 
 // PACK: two products an instruction and the sums one by one, the same bits (packed sums are
 // fused with the products). It pays where the norms make instruction issue the bound, prompts
-// 83.0 -> 81.0 us, and costs 1.4 us of 84.7 without them.
+// 83.0 -> 81.0 us, and changes nothing without them (83.8 us either way).
 template <bool INTER, bool PACK>
 __device__ __forceinline__ void rotate8(float* x, float4 c, float4 s) {
   if (INTER) {
@@ -471,12 +471,12 @@ __global__ void __launch_bounds__(kKvThreads, NORM ? 7 : 8) va_append_kernel(con
   }
   float x[4][8];
   float amax = 0.f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    unpack4(w1[k], x[k]);
-    unpack4(w2[k], x[k] + 4);
-  }
   if constexpr (NORM) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      unpack4(w1[k], x[k]);
+      unpack4(w2[k], x[k] + 4);
+    }
     if (is_k && p.k_norm) {
       float w[8];
       norm_weights(p.k_norm, p.k_norm_fp32, p.norm_offset, col, w);
@@ -485,6 +485,10 @@ __global__ void __launch_bounds__(kKvThreads, NORM ? 7 : 8) va_append_kernel(con
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
+    if constexpr (!NORM) {  // (row by row: all four unpacked ahead do not fit the registers)
+      unpack4(w1[k], x[k]);
+      unpack4(w2[k], x[k] + 4);
+    }
     if (turn) rotate8<INTER, NORM>(x[k], cs[k], sn[k]);
     if (KIND == kPageScaled) {
 #pragma unroll
