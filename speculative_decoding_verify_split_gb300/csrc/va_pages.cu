@@ -224,8 +224,8 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
 }
 
 // Dynamic shared memory: the words of this CTA's part of the bitmap, the free pages ahead
-// of each of them (in the part), the sequences' sums [num_seqs + 1], a bit for each that
-// gets nothing.
+// of each of them (in the part), the sequences' sums [num_seqs + 1], a bit for each that is
+// refused and one for each that needs pages (sums that saturate are equal, too).
 __global__ void __launch_bounds__(kPoolThreads, 1) va_reserve_pages_kernel(const PoolParams p, int words) {
   extern __shared__ int32_t dyn[];
   __shared__ int64_t scratch[32];
@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kPoolThreads, 1) va_reserve_pages_kernel(const
   int32_t* ahead = dyn + words;
   int32_t* sums = dyn + 2 * words;  // pages needed ahead of sequence b, saturating
   uint32_t* refused = reinterpret_cast<uint32_t*>(sums + p.num_seqs + 1);
+  uint32_t* needing = refused + (p.num_seqs + 31) / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)ptx::cluster_rank();
   const int page0 = rank * words * 32;
@@ -300,8 +301,11 @@ __global__ void __launch_bounds__(kPoolThreads, 1) va_reserve_pages_kernel(const
         ok = false;
         need = b < p.num_seqs ? need_of(b, ok) : 0;
       }
-      const uint32_t no = __ballot_sync(0xffffffffu, !ok);
-      if (lane == 0 && b < p.num_seqs) refused[b >> 5] = no;
+      const uint32_t no = __ballot_sync(0xffffffffu, !ok), some = __ballot_sync(0xffffffffu, need > 0);
+      if (lane == 0 && b < p.num_seqs) {
+        refused[b >> 5] = no;
+        needing[b >> 5] = some;
+      }
       int64_t total;
       const int64_t inc = block_inclusive(need, scratch, &total);
       if (b < p.num_seqs) sums[b + 1] = (int)(running + inc < INT32_MAX ? running + inc : INT32_MAX);
@@ -331,12 +335,11 @@ __global__ void __launch_bounds__(kPoolThreads, 1) va_reserve_pages_kernel(const
     }
     granted = sums[lo];
   }
-  auto grants = [&](int b) {
-    return !((refused[b >> 5] >> (b & 31)) & 1) && (sums[b + 1] <= all || sums[b + 1] == sums[b]);
-  };
+  auto needs = [&](int b) { return ((needing[b >> 5] >> (b & 31)) & 1) != 0; };
+  auto grants = [&](int b) { return !((refused[b >> 5] >> (b & 31)) & 1) && (sums[b + 1] <= all || !needs(b)); };
   // 2: marks
   for (int b = rank + kPoolCtas * tid; b < p.num_seqs; b += kPoolCtas * kPoolThreads) {
-    if (sums[b + 1] == sums[b]) continue;
+    if (!needs(b)) continue;
     if (!grants(b)) {
       report(p, kPgNoPages);
       continue;
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kPoolThreads, 1) va_reserve_pages_kernel(const
     int src = -1, dst = -1;
     const Want w = wants(p, b, false);
     const bool ok = grants(b);
-    if (ok && sums[b + 1] > sums[b]) {
+    if (ok && needs(b)) {
       const int first = __ldcg(p.dst + b);
       int* row = p.table + (int64_t)b * p.t_s0;
       int at = sums[b];
@@ -472,7 +475,7 @@ cudaError_t launch_fork_pages(const PoolParams& p, cudaStream_t stream) { return
 
 cudaError_t launch_reserve_pages(const PoolParams& p, cudaStream_t stream) {
   const int words = (p.num_pages + 32 * kPoolCtas - 1) / (32 * kPoolCtas);
-  const size_t smem = sizeof(int32_t) * (2 * (size_t)words + (size_t)p.num_seqs + 1 + ((size_t)p.num_seqs + 31) / 32);
+  const size_t smem = sizeof(int32_t) * (2 * (size_t)words + (size_t)p.num_seqs + 1 + 2 * (((size_t)p.num_seqs + 31) / 32));
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(va_reserve_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
     if (e != cudaSuccess) return e;
