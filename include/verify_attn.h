@@ -712,7 +712,7 @@ va_status verify_attn_reserve_pages(va_tensor* block_table, const va_tensor* seq
  *               written twice, or written and read, has unspecified contents.
  * Errors: VA_ERR_NULL, VA_ERR_SHAPE, VA_ERR_DTYPE (scales over a BF16 cache), VA_ERR_LAYOUT
  * (elements on top of each other, K and V in one place), VA_ERR_UNSUPPORTED (pages other
- * than 16, other widths, 16 M elements or more a token row).
+ * than 16, other widths, token rows of more than 65,535 * 512 bytes).
  */
 va_status verify_attn_copy_pages(va_tensor* k_cache, va_tensor* v_cache, va_tensor* k_scales, va_tensor* v_scales,
                                  const va_tensor* src, const va_tensor* dst, void* stream);

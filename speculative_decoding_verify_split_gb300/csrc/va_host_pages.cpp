@@ -81,7 +81,7 @@ va_status check_copied(const va_tensor* t, const va_tensor* scales, PageView* v)
   if (t->dtype != VA_BF16 && t->dtype != VA_FP8_E4M3) return VA_ERR_DTYPE;
   const int64_t es = t->dtype == VA_BF16 ? 2 : 1;
   if (t->shape[1] != kPageSize || t->shape[3] * es % 16 != 0 || t->shape[0] > INT32_MAX || t->shape[2] < 1 || t->shape[3] < 1 ||
-      t->shape[2] * t->shape[3] >= (1 << 24))
+      t->shape[2] > kMaxCopyRowUnits / (t->shape[3] * es / 16))
     return VA_ERR_UNSUPPORTED;
   va_status s = check_rows(t);
   if (s != VA_OK) return s;

@@ -24,8 +24,6 @@ __device__ __forceinline__ void report(const PoolParams& p, int32_t bit) {
 // A CTA moves 8 KB of one cache's page, four 16-byte units a thread, all loads ahead of
 // the stores. The bound is memory, both directions: 258 MB in 40.6 us, 94 % of the
 // measured copy bandwidth; a few pages are latency, 3.0 us.
-constexpr int kCopyThreads = 128, kCopyUnits = 4;
-
 __global__ void __launch_bounds__(kCopyThreads, 16) va_copy_pages_kernel(const CopyParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -36,6 +36,11 @@ struct PoolParams {
   int32_t* room;
 };
 
+// A CTA of the copy moves kCopyThreads * kCopyUnits 16-byte units of a page; a launch has at
+// most 65,535 of them a page, which is what a token row may hold.
+constexpr int kCopyThreads = 128, kCopyUnits = 4;
+constexpr int64_t kMaxCopyRowUnits = 65535ll * kCopyThreads * kCopyUnits / kPageSize;
+
 // One cache whose pages are copied: a page is 16 x heads rows of `units` 16-byte units.
 struct PageView {
   char* data;               // null: none

@@ -28,3 +28,15 @@ def test_more_pages_wanted_than_31_bits():
     va.reserve_pages(table, used, count, refs, add, status=status)
     torch.cuda.synchronize()
     assert count.nonzero().flatten().tolist() == [0, seqs - 1] and table[0, 0] == 0 and table[-1, :3].tolist() == [1, 2, 3]
+
+
+@pytest.mark.parametrize("dtype,heads", [(torch.bfloat16, 65535), (torch.float8_e4m3fn, 131070)])
+def test_pages_as_wide_as_a_launch_takes(dtype, heads):
+    """Token rows of 65,535 * 512 bytes: the last CTA of the launch has the page's end."""
+    k = torch.empty(3, 16, heads, 256, dtype=dtype, device="cuda")
+    bits = k.view(torch.uint8).view(3, -1)
+    bits[0] = torch.arange(bits.shape[1], device="cuda") % 251
+    bits[1:] = 253
+    va.copy_pages(k, None, torch.tensor([0], dtype=I, device="cuda"), torch.tensor([2], dtype=I, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(bits[0], bits[2]) and bool((bits[1] == 253).all())
