@@ -64,7 +64,7 @@ def reserve(table, used, count, refs, new_tokens):
             continue
         width = len(table[s])
         want, first = -(-(used[s] + add) // PAGE), used[s] // PAGE
-        if used[s] < 0 or not 0 <= count[s] <= width or (want <= width and first > count[s]):
+        if used[s] < 0 or not 0 <= count[s] <= width or (want <= width and -(-used[s] // PAGE) > count[s]):
             status |= BAD_TABLE
             continue
         if want > width:

@@ -170,7 +170,7 @@ __device__ __forceinline__ Want wants(const PoolParams& p, int b, bool tell) {
   }
   w.first = used < 0 ? 0 : used / kPageSize;
   w.want = w.ok ? (int)want : 0;
-  if (w.ok && w.first > w.have) {  // tokens without pages
+  if (w.ok && w.first + (used % kPageSize != 0) > w.have) {  // tokens without pages
     if (tell) report(p, kPgBadTable);
     w.ok = false;
     w.want = 0;
