@@ -15,7 +15,8 @@ def free(table, used, count, refs, seqs):
             continue
         if not 0 <= count[s] <= len(table[s]):
             status |= BAD_TABLE
-        for page in list(table[s])[:max(0, count[s])]:
+            continue
+        for page in list(table[s])[:count[s]]:
             if not 0 <= page < len(refs):
                 status |= BAD_TABLE
             elif refs[page] <= 0:

@@ -73,11 +73,14 @@ __global__ void __launch_bounds__(kRowThreads) va_free_pages_kernel(const PoolPa
     return;
   }
   if (threadIdx.x == 0) {
-    int n = atomicExch(p.page_count + b, 0);
-    p.seqused[b] = 0;
+    // (a count that no row has stays: nobody writes it, so every listing sees it)
+    int n = *static_cast<const volatile int*>(p.page_count + b);
     if (n < 0 || n > p.width) {
       report(p, kPgBadTable);
-      n = n < 0 ? 0 : p.width;
+      n = 0;
+    } else {
+      n = atomicExch(p.page_count + b, 0);
+      p.seqused[b] = 0;
     }
     s_count = n;
   }

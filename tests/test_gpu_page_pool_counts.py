@@ -21,3 +21,16 @@ def test_reserve_with_fewer_pages_than_tokens(used, short):
     *_, room = b.reserve([4, 30])
     assert b.bits == (va.PG_BAD_TABLE if short else 0)
     assert b.count.tolist() == [2 if short else 3, 4] and room == [32 if short else 48, 64]
+
+
+@pytest.mark.parametrize("count", [-1, -(1 << 31), 5, 9, (1 << 31) - 1])
+@pytest.mark.parametrize("seqs", [[0, 1], [1, 0, 0], [0] * 40 + [1]])
+def test_free_with_a_count_outside_the_row(seqs, count):
+    b = two_rows()
+    b.set(count=[count, 2])
+    b.free(seqs)
+    assert b.bits == va.PG_BAD_TABLE
+    assert b.count.tolist() == [count, 0] and b.used.tolist() == [20, 0] and b.refs.tolist()[:5] == [1, 1, 0, 0, 0]
+    b.set(count=[2, 0])
+    b.free(seqs)                                     # put right, it goes back as any other
+    assert b.refs.tolist() == [0] * 16

@@ -17,3 +17,10 @@ def test_reserve_with_fewer_pages_than_tokens(used, short):
     assert status == (pool.BAD_TABLE if short else 0)
     assert p["count"][1] == 3 and room[1] == 48 and (src, dst) == ([-1, -1], [-1, -1])
     assert room[0] == 16 * p["count"][0] and p["count"][0] == (2 if short else 3)
+
+
+@pytest.mark.parametrize("count", [-1, 5, 9])
+def test_free_with_a_count_outside_the_row(count):
+    p = two_rows(count=[count, 2])
+    assert pool.free(*p.values(), [0, 1, 0]) == pool.BAD_TABLE
+    assert p["count"] == [count, 0] and p["used"] == [20, 0] and p["refs"][:4] == [1, 1, 0, 0]
