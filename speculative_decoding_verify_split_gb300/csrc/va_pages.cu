@@ -72,6 +72,9 @@ __global__ void __launch_bounds__(kRowThreads) va_free_pages_kernel(const PoolPa
     if (threadIdx.x == 0) report(p, kPgBadSeq);
     return;
   }
+  const int* row = p.table + (int64_t)b * p.t_s0;
+  // the first entries are under way beside the count
+  const int early = (int)threadIdx.x < p.width ? row[(int64_t)threadIdx.x * p.t_s1] : 0;
   if (threadIdx.x == 0) {
     // (a count that no row has stays: nobody writes it, so every listing sees it)
     int n = *static_cast<const volatile int*>(p.page_count + b);
@@ -85,10 +88,9 @@ __global__ void __launch_bounds__(kRowThreads) va_free_pages_kernel(const PoolPa
     s_count = n;
   }
   __syncthreads();
-  const int* row = p.table + (int64_t)b * p.t_s0;
 #pragma unroll 4
   for (int j = threadIdx.x; j < s_count; j += kRowThreads) {
-    const int page = row[(int64_t)j * p.t_s1];
+    const int page = j < kRowThreads ? early : row[(int64_t)j * p.t_s1];
     if ((unsigned)page >= (unsigned)p.num_pages) {
       report(p, kPgBadTable);
       continue;
