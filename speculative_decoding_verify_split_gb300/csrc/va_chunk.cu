@@ -138,7 +138,7 @@ __device__ __forceinline__ Span item_span(const ChunkParams& p, const Seq& s, in
     x.nf = (int)(((int64_t)p.first_tokens + kKeys - 1) / kKeys);
     x.nf = x.nf < x.w0 ? x.nf : x.w0;
   }
-  x.n = x.khi > 0 ? x.nf + (x.khi + kKeys - 1) / kKeys - x.w0 : 0;
+  x.n = x.khi > 0 ? x.nf + (x.khi - 1) / kKeys + 1 - x.w0 : 0;  // (khi itself may end 16 below 2^31)
   return x;
 }
 
@@ -957,8 +957,10 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
           const int* bt = p.block_table + (int64_t)pc->b * p.bt_s0;
           give_back();
           auto page_id = [&](int i) {
-            const int page = tile_of(x, i0 + i) * (kKeys / kPageSize) + page_of, key = page * kPageSize;
-            const bool seen = i < n && (on || scl) && key < x.khi && (key + kPageSize > x.klo || key < p.first_tokens);
+            const int page = tile_of(x, i0 + i) * (kKeys / kPageSize) + page_of;
+            const uint32_t key = (uint32_t)page * kPageSize;
+            const bool seen = i < n && (on || scl) && key < (uint32_t)x.khi &&
+                              (key + kPageSize > (uint32_t)x.klo || key < (uint32_t)p.first_tokens);
             return seen ? bt[(int64_t)page * p.bt_s1] : -1;
           };
           float ks = 1.f, vs = 1.f;
