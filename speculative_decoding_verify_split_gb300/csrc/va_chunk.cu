@@ -17,7 +17,8 @@
 // Work is split by units (about keys times rows): every pair takes an equal run of them,
 // found from closed forms, so a long prompt, a few tokens over a long cache and a ragged batch
 // all fill the machine; an item that two pairs share leaves fp32 partials, which the merge
-// kernel sums in the pairs' order (the same bits at every call).
+// kernel sums in the pairs' order (the same bits at every call). Few and short items have a
+// pair each (kWholeTiles).
 //
 // What bounds it: 4 * 256 flops a visible (row, key) pair on the tensor cores; over long caches
 // it runs there (2,048 tokens, 16 query heads over one KV head: bf16 over 63K keys 1.12 ms, 1.93
@@ -26,8 +27,8 @@
 // too: 16 warps, in two groups that take the tiles in turn (e4m3 with 8 warps 2.87 ms,
 // 2.45 when they became 16). Page scales cost the softmax a multiply
 // and a sum for each page (1.62 ms, 1.34 PFLOP/s), the soft cap an exponential and a division a logit
-// (1.86 ms, 1.16). Short calls are bound by the chain of share, Q, first tiles, epilogue and
-// merge: two sequences of 40 tokens over 600 keys 20 us. One token in each of many sequences
+// (1.86 ms, 1.16). Short calls are bound by the chain of share, Q, tiles and epilogue: two
+// sequences of 25 and 21 tokens over 461 and 320 keys 19.0 us. One token in each of many sequences
 // fills 16 of an item's 256 rows: 97 us for 269 MB, 2.8 TB/s.
 //
 // e4m3 caches: K's codes go to the MMA as they are (kind::f8f6f4), with Q as two e4m3 terms,
@@ -80,10 +81,17 @@ __device__ __forceinline__ int row_tiles(const ChunkParams& p, const Seq& s) {
   return (int)(((int64_t)s.L * p.group + kChunkRows - 1) / kChunkRows);
 }
 
-// Tiles (in units) that a share has at least: small calls take fewer pairs, whose partials
-// cost more to write and to join than the tiles they save (two sequences of 40 tokens
-// over 600 keys: 19.9 us, with 8 too, with 6 24.2, with 9 33.4).
-constexpr int64_t kMinShare = 7;
+// Small calls. Where there are no more items than pairs, and none costs more than kWholeTiles
+// tiles (its start among them), an item has a pair to itself and nothing is joined; else a share
+// has at least kMinShare tiles, so that fewer pairs take part, whose partials cost more to
+// write and to join than the tiles they save. us a call, geometric means over 24 to 30 random
+// calls each: two sequences of 17-48 tokens over 200-1,024 keys (16 query heads over one)
+// 22.3 whole, 26.7 / 27.2 / 29.7 in shares of at least 3 / 4 / 7 tiles (2: 26.6, 5: 28.0, 10:
+// 29.8); up to three of 10-60 tokens over 900-3,500 keys 34.9 with items of up to 18 tiles
+// whole (16: 35.0, 20: 35.2, 24: 35.6, 28: 38.2); one of 100-900 tokens over 900-1,500 keys
+// 27.5 whole, 34.5 / 35.2 / 37.3 in shares of at least 3 / 4 / 7.
+constexpr int64_t kWholeTiles = 18;
+constexpr int64_t kMinShare = 3;
 
 // Units of the split: a tile is 128 G of them. Row tile m costs
 //   min(max(0, (S - L) G + 256 (m + 1)), cap) + kChunkItemCost * 128 G,
@@ -423,10 +431,31 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
         total += tot;
       }
     }
+    bool whole = false;
+    if (p.force <= 0 && p.num_seqs <= kThreads && total > 0 && total <= kWholeTiles * unit * p.pairs) {
+      const int tiles = tid < p.num_seqs ? row_tiles(p, s) : 0;  // (the last of them costs most)
+      if (!__syncthreads_or(tiles > 0 && chunk_cost(p, s, tiles - 1) > kWholeTiles * unit)) {
+        const int64_t items = (int64_t)tiles * p.hkv;
+        long long all;
+        const int64_t first = block_exclusive_scan<kThreads>(items, scratch, &all);
+        whole = all <= p.pairs;
+        if (whole && c < all) {  // pair c takes item c; its units are counted from the item's first
+          if (first <= c && c < first + items) {
+            start->b = tid;
+            start->h = (c - (int)first) / tiles;
+            start->m = (c - (int)first) % tiles;
+            start->off = 0;
+            start->total = chunk_cost(p, s, start->m);
+          }
+          __syncthreads();
+          t1 = start->total;
+        }
+      }
+    }
     // as many pairs as get at least kMinShare tiles' units each
     int used = p.force > 0 && p.force < p.pairs ? p.force : p.pairs;
     if (p.force <= 0 && total < kMinShare * unit * p.pairs) used = (int)quotient(total, kMinShare * unit);
-    used = total == 0 ? 0 : used < 1 ? 1 : used;
+    used = total == 0 || whole ? 0 : used < 1 ? 1 : used;
     const int64_t share = share_units(total, used);
     // The rounding up can leave the last pairs nothing: they are not counted, so that each
     // counted share has a first unit and an item that it starts in. The share of the smaller

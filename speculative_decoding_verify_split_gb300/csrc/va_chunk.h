@@ -53,7 +53,8 @@ struct ChunkParams {
 };
 
 // Where a pair's share of the work starts: row tile m of head h of sequence b,
-// whose first unit is `off`. total: all units; used: pairs that share them.
+// whose first unit is `off`. total: all units; used: pairs that share them (0 in the first
+// pair's: nothing to join; a pair that has an item to itself counts from the item on).
 struct ChunkStart {
   int64_t off, total;
   int32_t b, h, m, used;
