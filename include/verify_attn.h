@@ -761,7 +761,9 @@ va_status verify_attn_copy_pages(va_tensor* k_cache, va_tensor* v_cache, va_tens
  * bits in steps of at most 2^-16 of the row's largest; V's codes are taken as f16
  * (exact) and P is rounded to f16, in steps of 2^-31 below 2^-21 of the row's
  * reference (within 2^8 of its largest weight).
- * The normaliser, the references and the joined sums are fp32.
+ * The normaliser, the references and the joined sums are fp32. With page scales a weight
+ * is taken times its page's V scale, in the steps above too: the normaliser counts a key
+ * while that product is within 2^-126 of the row's largest.
  * A value that is NaN or infinite at a key in [0, S) may reach rows of the same
  * sequence that do not see the key; keys may be anything where they are not seen.
  * Errors before launching, as verify_attn_append_kv; VA_ERR_UNSUPPORTED also for
