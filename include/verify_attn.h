@@ -760,7 +760,10 @@ va_status verify_attn_copy_pages(va_tensor* k_cache, va_tensor* v_cache, va_tens
  * caches: P is rounded to bf16. E4M3 caches: Q enters as two e4m3 terms, bf16's 8
  * bits in steps of at most 2^-16 of the row's largest; V's codes are taken as f16
  * (exact) and P is rounded to f16, in steps of 2^-31 below 2^-21 of the row's
- * reference (within 2^8 of its largest weight).
+ * reference (within 2^8 of its largest weight). Beside a key whose value is 0, weights 2^-24
+ * of its own keep 7 bits, 2^-28 three, and below 2^-32 they are gone (the normaliser counts
+ * them); verify_attn_scaled and the other verify calls scale P by blocks of 32 keys and
+ * keep them.
  * The normaliser, the references and the joined sums are fp32. With page scales a weight
  * is taken times its page's V scale, in the steps above too: the normaliser counts a key
  * while that product is within 2^-126 of the row's largest.
