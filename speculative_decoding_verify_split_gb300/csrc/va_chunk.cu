@@ -29,7 +29,7 @@
 // and a sum for each page (1.62 ms, 1.34 PFLOP/s), the soft cap an exponential and a division a logit
 // (1.86 ms, 1.16). Short calls are bound by the chain of share, Q, tiles and epilogue: two
 // sequences of 25 and 21 tokens over 461 and 320 keys 19.0 us. One token in each of many sequences
-// fills 16 of an item's 256 rows: 97 us for 269 MB, 2.8 TB/s.
+// fills 16 of an item's 256 rows: 88-97 us for 269 MB, 2.8-3.1 TB/s.
 //
 // e4m3 caches: K's codes go to the MMA as they are (kind::f8f6f4), with Q as two e4m3 terms,
 // which holds bf16's 8 bits at the rate of one bf16 product; V's codes become f16 on the way
