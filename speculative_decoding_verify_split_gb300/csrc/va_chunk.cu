@@ -582,6 +582,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
           const int cur = tiles + i;
           if (kScl) wait_for(kBarScales + cur % kScaleTiles, cur / kScaleTiles, 512);
           wait_for(kBarSFull + grp, cur >> 1, 256);
+          __syncwarp();  // (a lane reports a wait that runs out)
           tc_fence_after();
           const uint32_t ts = tmem + lane_base + kColS + grp * kKeys + 64 * kh;  // this warp's keys
           const int tile = tile0 + i;
@@ -668,13 +669,14 @@ __global__ void __launch_bounds__(Cfg<KIND>::kThreads, 1)
               m_ref = m_new;
             }
             const bool move = m_new != m_old && m_old != -INFINITY;
-            if (__any_sync(0xffffffffu, move) && wait_for(kBarPvDone + (grp ^ 1), (cur - 1) >> 1, 2048)) {
+            if (__any_sync(0xffffffffu, move)) {
               const float alpha = move ? ex2(m_old - m_new) : 1.f;
               // O holds earlier tiles (of this piece: m_old is not -inf)
+              const bool settled = wait_for(kBarPvDone + (grp ^ 1), (cur - 1) >> 1, 2048);
               tc_fence_after();
               __syncwarp();
 #pragma unroll 1
-              for (int j = 0; j < kHeadDim / 64; ++j) {
+              for (int j = 0; settled && j < kHeadDim / 64; ++j) {
                 uint32_t o[32];
                 const uint32_t ta = tmem + lane_base + kColO + 128 * kh + 32 * j;
                 tmem_ld_32x32b_x32(ta, o);
