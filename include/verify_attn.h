@@ -770,7 +770,8 @@ va_status verify_attn_copy_pages(va_tensor* k_cache, va_tensor* v_cache, va_tens
  * A value that is NaN or infinite at a key in [0, S) may reach rows of the same
  * sequence that do not see the key; keys may be anything where they are not seen.
  * Errors before launching, as verify_attn_append_kv; VA_ERR_UNSUPPORTED also for
- * first_tokens < 0, descales beside page scales, or total_q * Hq / Hkv past 2^31.
+ * first_tokens < 0, descales beside page scales, total_q * Hq / Hkv past 2^31, or
+ * num_seqs * Hq * (total_q * Hq / Hkv / 256 + 1) * (16 * table width + total_q) past about 2^62.
  */
 va_status verify_attn_chunk(const va_tensor* q, const va_tensor* k_cache, const va_tensor* v_cache,
                             const va_tensor* k_scales, const va_tensor* v_scales, const va_tensor* block_table,

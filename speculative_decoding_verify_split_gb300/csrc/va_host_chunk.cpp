@@ -12,14 +12,15 @@ namespace {
 
 using namespace va;
 
-// The units of the split and the row numbers stay inside their integers.
+// The units of the split and the row numbers stay inside their integers, also where prefix
+// sums out of order give every sequence all rows of q.
 bool fits(const Shapes& sh) {
   const int64_t group = sh.hq / sh.hkv;
   if (sh.total_q > (INT32_MAX - 2 * kChunkRows) / group) return false;
   const double rows = (double)sh.total_q * group;
-  const double tiles = rows / kChunkRows + (double)sh.num_seqs;
+  const double tiles = (rows / kChunkRows + 1.0) * (double)sh.num_seqs;
   const double cost = (double)sh.width * kPageSize * group + rows + 4.0 * kChunkKeys * group * kChunkItemCost;
-  return sh.hkv * tiles * cost < 18014398509481984.0;  // 2^54, times the pairs
+  return sh.hkv * tiles * cost < 4611686018427387904.0;  // 2^62
 }
 
 va_status validate_chunk(const va_tensor* q, const va_tensor* k, const va_tensor* v, const va_tensor* ks, const va_tensor* vs,
